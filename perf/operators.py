@@ -301,12 +301,13 @@ def _plain_store(s, name, x, page, row):
     touched[page] = True
     new = torch.where(touched[:, None], torch.where(fresh[:, None], want, torch.maximum(old, want)), old)
     codes = cache.view(torch.uint8)
-    kept = s["table"].long()[torch.arange(s["kv_len"].numel(), device=x.device),
-                             (s["kv_len"].long() - torch.diff(s["q_start"].long())) // P]  # pages begun earlier
-    kept = kept[~fresh[kept]]
+    before = s["kv_len"].long() - torch.diff(s["q_start"].long())  # rows that each sequence held already
+    kept = s["table"].long()[torch.arange(before.numel(), device=x.device), before // P]
+    old_rows = torch.arange(P, device=x.device) < (before % P)[:, None]
+    old_rows, kept = old_rows[~fresh[kept]], kept[~fresh[kept]]
     step = torch.exp2((old[kept] - new[kept]).double()).float()[:, :, None, None]
     again = (cache[kept].float() * step).to(torch.float8_e4m3fn).view(torch.uint8)
-    codes[kept] = torch.where(step < 1, again, codes[kept])
+    codes[kept] = torch.where((step < 1) & old_rows[:, None, :, None], again, codes[kept])
     inverse = torch.exp2(-new[page].double())[:, :, None]
     codes[page, :, row] = (x.double() * inverse).float().to(torch.float8_e4m3fn).view(torch.uint8)
     scale.copy_((new + 127).to(torch.uint8))
@@ -460,8 +461,9 @@ def _exact_append(case, s):
                 if lo > first:
                     before = s[name + "_scale"][page].double() - 127
                     e = torch.maximum(e, before)
-                    grown = caches[name][page] * torch.exp2(before - e)[:, None, None]
-                    caches[name][page] = torch.where((e > before)[:, None, None], _e4m3(grown), caches[name][page])
+                    held = caches[name][page, :, :lo - first]
+                    grown = _e4m3(held * torch.exp2(before - e)[:, None, None])
+                    caches[name][page, :, :lo - first] = torch.where((e > before)[:, None, None], grown, held)
                 caches[name][page, :, lo - first:hi - first] = _e4m3(new * torch.exp2(-e)[:, None, None])
     r = {"q": q, "k": caches["k"], "v": caches["v"]}
     if s["k_scale"] is not None:
