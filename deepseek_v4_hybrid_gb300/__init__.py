@@ -1,6 +1,6 @@
 """DeepSeek-V4 hybrid compressed-attention decode step on one GB300 (sm_103a).
 
-Thin Python binding of libdsv4.so (include/dsv4.h).  The functions below take torch CUDA tensors,
+Thin Python binding of libdsv4.so (include/dsv4.h, include/dsv4_gqa.h).  The functions below take torch CUDA tensors,
 fill the C parameter structs and call the library on the current torch stream; every step of the
 decode path runs in the library's CUDA kernels.  There is no CPU fallback: the import fails if
 the library is not built.
@@ -10,7 +10,7 @@ from __future__ import annotations
 import torch
 
 from . import _abi
-from ._abi import BF16, F32, FP8_DS_MLA, I8_ROWSCALE, MXFP4, Dsv4Error  # noqa: F401
+from ._abi import BF16, E4M3_PAGE, F32, FP8_DS_MLA, I8_ROWSCALE, MXFP4, Dsv4Error  # noqa: F401
 
 _lib = _abi.load()
 
@@ -131,6 +131,153 @@ def dsv4_sparse_mla_decode_workspace_bytes(params) -> int:
 def dsv4_sparse_mla_decode(params, stream=None):
     """Shared-KV sparse MLA decode attention into params.out (see include/dsv4.h)."""
     _abi.check("dsv4_sparse_mla_decode", _lib.dsv4_sparse_mla_decode(params, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------------------------------------
+# grouped-query operators (include/dsv4_gqa.h).  The parameter structs are built once over fixed buffers
+# (they keep their tensors alive) and passed to any number of calls; the calls run on the tensors' device.
+# ---------------------------------------------------------------------------------------------------------
+def _need(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _need_tensor(t, name, dtypes, shape, device):
+    """t is a tensor of one of dtypes on device; shape entries of None are free; the last dim is contiguous."""
+    _need(isinstance(t, torch.Tensor) and t.dtype in dtypes, f"{name}: dtype {getattr(t, 'dtype', type(t))} is none of {dtypes}")
+    _need(t.dim() == len(shape) and all(w is None or s == w for s, w in zip(t.shape, shape)),
+          f"{name}: shape {tuple(t.shape)}, wanted {tuple('*' if w is None else w for w in shape)}")
+    _need(t.device == device, f"{name}: on {t.device}, wanted {device}")
+    _need(t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1, f"{name}: the last dimension is not contiguous")
+
+
+def _need_flat(t, name, dtype, shape, device):
+    _need_tensor(t, name, (dtype,), shape, device)
+    _need(t.is_contiguous(), f"{name}: not contiguous")
+
+
+def _gqa_common(k_cache, v_cache, k_scale, v_scale, block_table, q_start, kv_len, max_q_len):
+    """Fields that both grouped-query calls share."""
+    dev = k_cache.device
+    _need(dev.type == "cuda", f"k_cache: on {dev}, wanted a CUDA device")
+    e4m3 = (torch.uint8, torch.float8_e4m3fn)
+    scaled = k_cache.dtype in e4m3
+    _need_tensor(k_cache, "k_cache", e4m3 if scaled else (torch.bfloat16,), (None,) * 4, dev)
+    pages, heads, page_size, dim = k_cache.shape
+    _need_tensor(v_cache, "v_cache", e4m3 if scaled else (torch.bfloat16,), (pages, heads, page_size, dim), dev)
+    _need((k_scale is not None) == scaled and (v_scale is not None) == scaled,
+          "k_scale and v_scale go with an e4m3 cache, and only with one")
+    if scaled:
+        _need_flat(k_scale, "k_scale", torch.uint8, (pages, heads), dev)
+        _need_flat(v_scale, "v_scale", torch.uint8, (pages, heads), dev)
+    _need_flat(kv_len, "kv_len", torch.int32, (None,), dev)
+    B = kv_len.shape[0]
+    _need_flat(q_start, "q_start", torch.int32, (B + 1,), dev)
+    _need_flat(block_table, "block_table", torch.int32, (B, None), dev)
+    ks, vs = k_cache.stride(), v_cache.stride()
+    return dev, dict(k_cache=_ptr(k_cache), v_cache=_ptr(v_cache), k_page_stride=ks[0], k_cache_head_stride=ks[1],
+                     k_row_stride=ks[2], v_page_stride=vs[0], v_cache_head_stride=vs[1], v_row_stride=vs[2],
+                     k_exp=_ptr(k_scale), v_exp=_ptr(v_scale), cache_dtype=E4M3_PAGE if scaled else BF16, B=B,
+                     kv_heads=heads, head_dim=dim, page_size=page_size, num_pages=pages,
+                     block_table=_ptr(block_table), max_pages_per_seq=block_table.shape[1], q_start=_ptr(q_start),
+                     kv_len=_ptr(kv_len), max_q_len=max_q_len)
+
+
+def gqa_append_params(k_new, v_new, k_cache, v_cache, block_table, q_start, kv_len, max_q_len, k_scale=None,
+                      v_scale=None, cos_sin=None, rope_first=0, rope_halves=False, q=None, q_out=None):
+    """Parameter struct of dsv4_gqa_append.  k_new, v_new [T, kv_heads, dim] and q, q_out [T, q_heads, dim] bf16,
+    rows of any strides (slices of a fused projection); caches [pages, kv_heads, page_size, dim] in any order
+    of the first three, bf16, or e4m3 codes (uint8 or float8_e4m3fn) with k_scale, v_scale [pages, kv_heads] of
+    UE8M0 bytes; q_start [B + 1], kv_len [B] (rows including the new ones), block_table [B, n] int32;
+    cos_sin [max_pos, rope_dim] fp32 rotates keys and queries (rope_halves: pairs (i, i + rope_dim / 2))."""
+    dev, f = _gqa_common(k_cache, v_cache, k_scale, v_scale, block_table, q_start, kv_len, max_q_len)
+    act, heads, dim = (torch.bfloat16,), f["kv_heads"], f["head_dim"]
+    _need_tensor(k_new, "k_new", act, (None, heads, dim), dev)
+    T = k_new.shape[0]
+    _need_tensor(v_new, "v_new", act, (T, heads, dim), dev)
+    _need((q is None) == (q_out is None), "q and q_out go together")
+    p = _abi.make(_abi.GqaAppendParams, T=T, k_new=_ptr(k_new), v_new=_ptr(v_new), k_token_stride=k_new.stride(0),
+                  k_head_stride=k_new.stride(1), v_token_stride=v_new.stride(0), v_head_stride=v_new.stride(1),
+                  q_heads=1, **f)
+    if q is not None:
+        _need_tensor(q, "q", act, (T, None, dim), dev)
+        _need_tensor(q_out, "q_out", act, (T, q.shape[1], dim), dev)
+        p.q, p.q_out, p.q_heads = _ptr(q), _ptr(q_out), q.shape[1]
+        p.q_token_stride, p.q_head_stride = q.stride(0), q.stride(1)
+        p.q_out_token_stride, p.q_out_head_stride = q_out.stride(0), q_out.stride(1)
+    if cos_sin is not None:
+        _need_flat(cos_sin, "cos_sin", torch.float32, (None, None), dev)
+        p.cos_sin, p.max_pos, p.rope_dim = _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1]
+        p.rope_first, p.rope_halves = rope_first, int(rope_halves)
+    p.device = dev
+    p.tensors = (k_new, v_new, k_cache, v_cache, block_table, q_start, kv_len, k_scale, v_scale, cos_sin, q, q_out)
+    return p
+
+
+def gqa_attention_params(q, k_cache, v_cache, block_table, q_start, kv_len, max_q_len, max_kv_len, softmax_scale, out,
+                         lse=None, k_scale=None, v_scale=None, causal=True, prefix_len=None, kv_start=None, window=0,
+                         softcap=0.0, slopes=None, sink=None, workspace=None):
+    """Parameter struct of dsv4_gqa_attention (caches and batch as in gqa_append_params).  q [T, q_heads, dim]
+    bf16 of any strides; out [T, q_heads, dim] bf16 or fp32 and lse [T, q_heads] fp32, contiguous; prefix_len [B]
+    and kv_start [T] int32; slopes and sink [q_heads] fp32."""
+    dev, f = _gqa_common(k_cache, v_cache, k_scale, v_scale, block_table, q_start, kv_len, max_q_len)
+    dim = f["head_dim"]
+    _need_tensor(q, "q", (torch.bfloat16,), (None, None, dim), dev)
+    T, H, _ = q.shape
+    _need(out.dtype in (torch.bfloat16, torch.float32), f"out: dtype {out.dtype}")
+    _need_flat(out, "out", out.dtype, (T, H, dim), dev)
+    for t, name, dt, shape in ((lse, "lse", torch.float32, (T, H)), (prefix_len, "prefix_len", torch.int32, (f["B"],)),
+                               (kv_start, "kv_start", torch.int32, (T,)), (slopes, "slopes", torch.float32, (H,)),
+                               (sink, "sink", torch.float32, (H,))):
+        if t is not None:
+            _need_flat(t, name, dt, shape, dev)
+    p = _abi.make(_abi.GqaAttentionParams, q=_ptr(q), q_token_stride=q.stride(0), q_head_stride=q.stride(1), T=T,
+                  q_heads=H, max_kv_len=max_kv_len, softmax_scale=softmax_scale, causal=int(causal),
+                  prefix_len=_ptr(prefix_len), kv_start=_ptr(kv_start), window=window, softcap=softcap,
+                  slopes=_ptr(slopes), sink=_ptr(sink), out=_ptr(out),
+                  out_dtype=BF16 if out.dtype == torch.bfloat16 else F32, lse=_ptr(lse), **f)
+    p.device = dev
+    p.tensors = (q, k_cache, v_cache, block_table, q_start, kv_len, out, lse, k_scale, v_scale, prefix_len, kv_start,
+                 slopes, sink)
+    if workspace is not None:
+        gqa_set_workspace(p, workspace)
+    return p
+
+
+def dsv4_gqa_attention_workspace_bytes(params) -> int:
+    with torch.cuda.device(params.device):
+        n = int(_lib.dsv4_gqa_attention_workspace_bytes(params))
+    if n == 0:  # refused: the call itself says why
+        _abi.check("dsv4_gqa_attention_workspace_bytes", _abi.ERR_INVALID)
+    return n
+
+
+def gqa_set_workspace(params, workspace):
+    """Gives the params a workspace (a tensor of at least dsv4_gqa_attention_workspace_bytes(params) bytes).  Calls
+    that may overlap on the GPU need one each."""
+    _need(workspace.device == params.device and workspace.is_contiguous(), "workspace: wrong device, or not contiguous")
+    params.workspace, params.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    params.workspace_tensor = workspace
+
+
+def _gqa_call(name, fn, params, stream):
+    dev = params.device
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            status = fn(params, _stream(stream))
+    else:
+        status = fn(params, _stream(stream))
+    _abi.check(name, status)
+
+
+def dsv4_gqa_append(params, stream=None):
+    """Rotates and stores the new tokens' keys and values, and rotates their queries (see include/dsv4_gqa.h)."""
+    _gqa_call("dsv4_gqa_append", _lib.dsv4_gqa_append, params, stream)
+
+
+def dsv4_gqa_attention(params, stream=None):
+    """Attention of the new tokens over the paged per-head caches into params' out and lse (see include/dsv4_gqa.h)."""
+    _gqa_call("dsv4_gqa_attention", _lib.dsv4_gqa_attention, params, stream)
 
 
 def dsv4_kernel_launches() -> int:

@@ -12,6 +12,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libdsv4.so")
 
 F32, BF16, FP8_DS_MLA, I8_ROWSCALE, MXFP4 = 0, 1, 2, 3, 4
+E4M3_PAGE = 5  # per-head caches: e4m3 codes with one UE8M0 exponent per page and head
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_BOUNDS, ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
 LATENT_DIM, VALUE_DIM, ROPE_DIM, FP8_DS_MLA_BYTES = 576, 512, 64, 656
 ABI_VERSION = 3
@@ -63,10 +64,37 @@ class SparseMlaDecodeParams(C.Structure):
                 ("workspace_bytes", C.c_size_t)]
 
 
+class GqaAppendParams(C.Structure):
+    _fields_ = [("struct_size", u32), ("k_new", vp), ("v_new", vp), ("k_token_stride", i64), ("k_head_stride", i64),
+                ("v_token_stride", i64), ("v_head_stride", i64), ("q", vp), ("q_out", vp), ("q_token_stride", i64),
+                ("q_head_stride", i64), ("q_out_token_stride", i64), ("q_out_head_stride", i64), ("k_cache", vp),
+                ("v_cache", vp), ("k_page_stride", i64), ("k_cache_head_stride", i64), ("k_row_stride", i64),
+                ("v_page_stride", i64), ("v_cache_head_stride", i64), ("v_row_stride", i64), ("k_exp", vp),
+                ("v_exp", vp), ("cache_dtype", i32), ("T", i32), ("B", i32), ("q_heads", i32), ("kv_heads", i32),
+                ("head_dim", i32), ("page_size", i32), ("num_pages", i64), ("block_table", vp),
+                ("max_pages_per_seq", i32), ("q_start", vp), ("kv_len", vp), ("max_q_len", i32), ("cos_sin", vp),
+                ("max_pos", i32), ("rope_first", i32), ("rope_dim", i32), ("rope_halves", i32)]
+
+
+class GqaAttentionParams(C.Structure):
+    _fields_ = [("struct_size", u32), ("q", vp), ("q_token_stride", i64), ("q_head_stride", i64), ("k_cache", vp),
+                ("v_cache", vp), ("k_page_stride", i64), ("k_cache_head_stride", i64), ("k_row_stride", i64),
+                ("v_page_stride", i64), ("v_cache_head_stride", i64), ("v_row_stride", i64), ("k_exp", vp),
+                ("v_exp", vp), ("cache_dtype", i32), ("T", i32), ("B", i32), ("q_heads", i32), ("kv_heads", i32),
+                ("head_dim", i32), ("page_size", i32), ("num_pages", i64), ("block_table", vp),
+                ("max_pages_per_seq", i32), ("q_start", vp), ("kv_len", vp), ("max_q_len", i32),
+                ("max_kv_len", i32), ("softmax_scale", f32), ("causal", i32), ("prefix_len", vp), ("kv_start", vp),
+                ("window", i32), ("softcap", f32), ("slopes", vp), ("sink", vp), ("out", vp), ("out_dtype", i32),
+                ("lse", vp), ("workspace", vp), ("workspace_bytes", C.c_size_t)]
+
+
 EXPORTS = ["dsv4_kv_insert", "dsv4_compress_update", "dsv4_indexer_topk_workspace_bytes", "dsv4_indexer_topk",
            "dsv4_sparse_mla_decode_workspace_bytes", "dsv4_sparse_mla_decode", "dsv4_abi_version",
            "dsv4_status_string", "dsv4_last_cuda_error", "dsv4_read_device_flags", "dsv4_indexer_topk_noalloc",
            "dsv4_qnorm_rope_kv_insert", "dsv4_padded_num_q_heads", "dsv4_kernel_launches"]
+
+# the grouped-query calls (include/dsv4_gqa.h)
+GQA_EXPORTS = ["dsv4_gqa_append", "dsv4_gqa_attention_workspace_bytes", "dsv4_gqa_attention"]
 
 # bytes of the scratch array built into the library for dsv4_indexer_topk_noalloc
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -86,12 +114,14 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     for name, st in (("dsv4_kv_insert", KvInsertParams), ("dsv4_compress_update", CompressUpdateParams),
                      ("dsv4_qnorm_rope_kv_insert", QnormRopeKvInsertParams),
                      ("dsv4_indexer_topk", IndexerTopkParams), ("dsv4_sparse_mla_decode", SparseMlaDecodeParams),
-                     ("dsv4_indexer_topk_noalloc", IndexerTopkParams)):
+                     ("dsv4_indexer_topk_noalloc", IndexerTopkParams), ("dsv4_gqa_append", GqaAppendParams),
+                     ("dsv4_gqa_attention", GqaAttentionParams)):
         fn = getattr(lib, name)
         fn.argtypes = [C.POINTER(st), vp]
         fn.restype = C.c_int
     for name, st in (("dsv4_indexer_topk_workspace_bytes", IndexerTopkParams),
-                     ("dsv4_sparse_mla_decode_workspace_bytes", SparseMlaDecodeParams)):
+                     ("dsv4_sparse_mla_decode_workspace_bytes", SparseMlaDecodeParams),
+                     ("dsv4_gqa_attention_workspace_bytes", GqaAttentionParams)):
         fn = getattr(lib, name)
         fn.argtypes = [C.POINTER(st)]
         fn.restype = C.c_size_t

@@ -1,11 +1,13 @@
 // C ABI entry points: host-side argument validation, then the kernel launches.
 // The declarations, argument meanings and error behaviour are documented in include/dsv4.h.
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
 #include "dsv4_common.cuh"
 #include "dsv4_launch.h"
+#include "gqa_common.cuh"
 
 using namespace dsv4;
 
@@ -29,6 +31,32 @@ bool act_dtype(int d) { return d == DSV4_F32 || d == DSV4_BF16; }
   do {                    \
     if (!(cond)) return (code); \
   } while (0)
+
+// What the two grouped-query calls share: the ragged batch, the caches and their exponents.
+template <typename P>
+int check_gqa(const P& p) {
+  CHECK(p.T >= 0 && p.B >= 0 && p.B <= 65535 && p.max_q_len >= 1, DSV4_ERR_INVALID);
+  CHECK(p.num_pages >= 0 && p.num_pages <= 0x7FFFFFFF && p.max_pages_per_seq > 0, DSV4_ERR_INVALID);
+  CHECK(p.q_heads >= 1 && p.q_heads <= 1024 && p.kv_heads >= 1 && p.kv_heads <= 1024, DSV4_ERR_INVALID);
+  CHECK(p.head_dim == 64 || p.head_dim == 128, DSV4_ERR_UNSUPPORTED);
+  CHECK(p.page_size == 16 || p.page_size == 32 || p.page_size == 64 || p.page_size == 128 || p.page_size == 256,
+        DSV4_ERR_UNSUPPORTED);
+  CHECK(p.cache_dtype == DSV4_BF16 || p.cache_dtype == DSV4_E4M3_PAGE, DSV4_ERR_UNSUPPORTED);
+  if (p.T == 0 || p.B == 0) return DSV4_OK;
+  CHECK(p.k_cache && p.v_cache && p.block_table && p.q_start && p.kv_len, DSV4_ERR_INVALID);
+  CHECK(aligned(p.k_cache, 16) && aligned(p.v_cache, 16) && aligned(p.block_table, 4) && aligned(p.q_start, 4) &&
+            aligned(p.kv_len, 4),
+        DSV4_ERR_INVALID);
+  const int64_t unit = p.cache_dtype == DSV4_BF16 ? 8 : 16;  // elements of 16 bytes
+  const int64_t strides[] = {p.k_page_stride, p.k_cache_head_stride, p.k_row_stride,
+                             p.v_page_stride, p.v_cache_head_stride, p.v_row_stride};
+  for (int64_t x : strides) CHECK(x > 0 && x % unit == 0, DSV4_ERR_INVALID);
+  CHECK(p.k_row_stride >= p.head_dim && p.v_row_stride >= p.head_dim, DSV4_ERR_INVALID);
+  CHECK(p.cache_dtype == DSV4_BF16 || (p.k_exp && p.v_exp), DSV4_ERR_INVALID);
+  return DSV4_OK;
+}
+
+bool token_strides(int64_t token, int64_t head) { return token >= 0 && head >= 0 && token % 8 == 0 && head % 8 == 0; }
 
 }  // namespace
 
@@ -69,6 +97,10 @@ int dsv4_read_device_flags(uint32_t* flags) {
   st = cuda_status(read_flags_indexer(flags));
   if (st != DSV4_OK) return st;
   st = cuda_status(read_flags_attention(flags));
+  if (st != DSV4_OK) return st;
+  st = cuda_status(read_flags_gqa_append(flags));
+  if (st != DSV4_OK) return st;
+  st = cuda_status(read_flags_gqa_attention(flags));
   if (st != DSV4_OK) return st;
   if (*flags & 4u) return DSV4_ERR_TIMEOUT;
   return *flags ? DSV4_ERR_BOUNDS : DSV4_OK;
@@ -201,6 +233,63 @@ int dsv4_sparse_mla_decode(const dsv4_sparse_mla_decode_params* p, dsv4_stream_t
   CHECK(p->workspace != nullptr && aligned(p->workspace, 256), DSV4_ERR_INVALID);
   CHECK(p->workspace_bytes >= sparse_mla_workspace(*p), DSV4_ERR_INVALID);
   return cuda_status(launch_sparse_mla_decode(*p, (cudaStream_t)stream));
+}
+
+int dsv4_gqa_append(const dsv4_gqa_append_params* p, dsv4_stream_t stream) {
+  CHECK(p != nullptr && p->struct_size == sizeof(dsv4_gqa_append_params), DSV4_ERR_INVALID);
+  const int st = check_gqa(*p);
+  CHECK(st == DSV4_OK, st);
+  if (p->cos_sin != nullptr) {
+    CHECK(p->max_pos > 0 && p->rope_first >= 0 && p->rope_first % 8 == 0 && p->rope_dim >= 16 &&
+              p->rope_dim % 16 == 0 && p->rope_first + p->rope_dim <= p->head_dim && aligned(p->cos_sin, 4),
+          DSV4_ERR_INVALID);
+  }
+  if (p->T == 0 || p->B == 0) return DSV4_OK;
+  CHECK(p->k_new && p->v_new && aligned(p->k_new, 16) && aligned(p->v_new, 16), DSV4_ERR_INVALID);
+  CHECK(token_strides(p->k_token_stride, p->k_head_stride) && token_strides(p->v_token_stride, p->v_head_stride),
+        DSV4_ERR_INVALID);
+  if (p->q != nullptr) {
+    CHECK(p->q_out && aligned(p->q, 16) && aligned(p->q_out, 16), DSV4_ERR_INVALID);
+    CHECK(token_strides(p->q_token_stride, p->q_head_stride) &&
+              token_strides(p->q_out_token_stride, p->q_out_head_stride),
+          DSV4_ERR_INVALID);
+    CHECK(p->q != p->q_out || (p->q_token_stride == p->q_out_token_stride && p->q_head_stride == p->q_out_head_stride),
+          DSV4_ERR_INVALID);
+  }
+  return cuda_status(launch_gqa_append(*p, (cudaStream_t)stream));
+}
+
+namespace {
+int check_gqa_attention(const dsv4_gqa_attention_params& p) {
+  const int st = check_gqa(p);
+  CHECK(st == DSV4_OK, st);
+  CHECK(p.q_heads % p.kv_heads == 0, DSV4_ERR_INVALID);
+  CHECK(p.max_kv_len >= 0 && p.max_kv_len <= (1 << 30) && p.window >= 0, DSV4_ERR_INVALID);
+  CHECK(p.causal == 0 || p.causal == 1, DSV4_ERR_INVALID);
+  CHECK(std::isfinite(p.softmax_scale) && std::isfinite(p.softcap) && p.softcap >= 0.f, DSV4_ERR_INVALID);
+  CHECK(act_dtype(p.out_dtype), DSV4_ERR_UNSUPPORTED);
+  return DSV4_OK;
+}
+}  // namespace
+
+size_t dsv4_gqa_attention_workspace_bytes(const dsv4_gqa_attention_params* p) {
+  if (p == nullptr || p->struct_size != sizeof(dsv4_gqa_attention_params) || check_gqa_attention(*p) != DSV4_OK)
+    return 0;
+  return gqa_attention_workspace(*p);
+}
+
+int dsv4_gqa_attention(const dsv4_gqa_attention_params* p, dsv4_stream_t stream) {
+  CHECK(p != nullptr && p->struct_size == sizeof(dsv4_gqa_attention_params), DSV4_ERR_INVALID);
+  const int st = check_gqa_attention(*p);
+  CHECK(st == DSV4_OK, st);
+  if (p->T == 0 || p->B == 0) return DSV4_OK;
+  CHECK(p->q && p->out && aligned(p->q, 16) && aligned(p->out, 16) && aligned(p->lse, 4), DSV4_ERR_INVALID);
+  CHECK(token_strides(p->q_token_stride, p->q_head_stride), DSV4_ERR_INVALID);
+  CHECK(aligned(p->prefix_len, 4) && aligned(p->kv_start, 4) && aligned(p->slopes, 4) && aligned(p->sink, 4),
+        DSV4_ERR_INVALID);
+  CHECK(p->workspace != nullptr && aligned(p->workspace, 256), DSV4_ERR_INVALID);
+  CHECK(p->workspace_bytes >= gqa_attention_workspace(*p), DSV4_ERR_INVALID);
+  return cuda_status(launch_gqa_attention(*p, (cudaStream_t)stream));
 }
 
 }  // extern "C"
