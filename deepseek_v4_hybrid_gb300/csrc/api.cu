@@ -102,6 +102,8 @@ int dsv4_read_device_flags(uint32_t* flags) {
   if (st != DSV4_OK) return st;
   st = cuda_status(read_flags_gqa_attention(flags));
   if (st != DSV4_OK) return st;
+  st = cuda_status(read_flags_gqa_decode(flags));
+  if (st != DSV4_OK) return st;
   if (*flags & 4u) return DSV4_ERR_TIMEOUT;
   return *flags ? DSV4_ERR_BOUNDS : DSV4_OK;
 }

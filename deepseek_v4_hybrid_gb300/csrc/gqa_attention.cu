@@ -2,26 +2,13 @@
 //
 // Simple form: one warp per (token, query head), the row's dims spread over the lanes, fp32 online
 // softmax over the visible rows.
-#include "gqa_common.cuh"
+#include "gqa_attention.cuh"
 
 namespace dsv4 {
 
 static __device__ unsigned int g_flags_gq = 0;
 
 namespace gqa {
-
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994531f;
-
-// First and one-past-last visible row of a token at position pos (the visible rows are contiguous).
-__device__ __forceinline__ int2 visible_rows(const dsv4_gqa_attention_params& p, int b, int t, int pos, int kv) {
-  int lo = p.kv_start ? max(0, p.kv_start[t]) : 0, hi = kv;
-  if (p.causal) {
-    hi = pos + 1;
-    if (p.prefix_len) hi = max(hi, min(kv, p.prefix_len[b]));
-  }
-  if (p.window > 0) lo = max(lo, pos - p.window + 1);
-  return make_int2(lo, hi);
-}
 
 template <int D>
 __global__ void __launch_bounds__(128) attention_simple(dsv4_gqa_attention_params p) {
@@ -102,10 +89,20 @@ __global__ void __launch_bounds__(128) attention_simple(dsv4_gqa_attention_param
 
 }  // namespace gqa
 
-size_t gqa_attention_workspace(const dsv4_gqa_attention_params&) { return 256; }
+// Up to 32 rows of (token, head) a kv head and sequence: the streaming kernel.
+static bool use_decode(const dsv4_gqa_attention_params& p) {
+  const int64_t max_n = p.max_q_len < p.T ? p.max_q_len : p.T;
+  return max_n * (p.q_heads / p.kv_heads) <= 32;
+}
+
+size_t gqa_attention_workspace(const dsv4_gqa_attention_params& p) {
+  if (p.T == 0 || p.B == 0) return 256;
+  return use_decode(p) ? gqa::decode_workspace(p) : 256;
+}
 
 cudaError_t launch_gqa_attention(const dsv4_gqa_attention_params& p, cudaStream_t s) {
   if (p.T == 0 || p.B == 0) return cudaSuccess;
+  if (use_decode(p)) return gqa::launch_decode(p, s);
   const int64_t units = (int64_t)p.T * p.q_heads;
   const dim3 grid((unsigned)((units + 3) / 4));
   return p.head_dim == 128 ? launch_pdl(gqa::attention_simple<128>, grid, dim3(128), 0, s, true, p)

@@ -1,0 +1,748 @@
+// Grouped-query attention of few new tokens a sequence (at most 32 rows of (token, head) per kv head).
+//
+// Bound by HBM: every visible row of the cache is read once for all rows of its kv head, and the rows of
+// a kv head together are far below the tensor cores' rate, so the products run on warp-level MMAs from
+// registers (tcgen05 would spend 128 rows on at most 32) and the design is about the stream of rows:
+//  - The visible rows of all (sequence, kv head) units form one list of 16-row stages that is cut into
+//    equal pieces, one per CTA, whatever the lengths; a unit cut by a piece's border leaves partial
+//    results that a second kernel merges.
+//  - Each warp streams its own stages (every fourth of its CTA's) through its own ring of cp.async
+//    copies, and keeps its own running maximum, sum and output: no barrier between warps until a unit ends.
+//  - S = Q K^T has the rows of a kv head as its M (16) and 8 cache rows as its N; its result is, register
+//    for register, the A operand of O += P V.  The order of a contraction's terms is free, so a lane
+//    reads 16 contiguous bytes of a row and Q's fragments are laid out to match; for P V a lane holds 16
+//    contiguous dims of the four rows it needs, and one byte permute a register pairs two rows' codes.
+//  - e4m3 codes become fp16 by masks and a shift (value x 2^-8, exact, subnormals included).  K's scale and
+//    the query row's own power of two (which brings bf16 queries into fp16's range) multiply the logit; V's
+//    exponent is added to the logit's, so that P V is taken against a running maximum of its own and pages
+//    of very different scales lose nothing.  P is rounded to fp16 (bf16 caches: bf16), sums are fp32.
+#include "gqa_attention.cuh"
+#include "tmap.h"
+
+namespace dsv4 {
+
+static __device__ unsigned int g_flags_gd = 0;
+
+namespace gqa {
+
+namespace dec {
+
+constexpr int NW = 4, THREADS = 32 * NW;
+constexpr int SR = 16;             // rows of a stage
+constexpr int MAX_SCAN = 1024;     // sequences whose stages are cut evenly; above, a CTA takes a whole unit
+constexpr int MIN_STAGES = 8;      // stages of a piece, at least: two a warp
+constexpr float LAZY = 8.f;        // a running maximum moves when it is exceeded by more than 2^8
+
+struct Args {
+  dsv4_gqa_attention_params p;
+  float* o_part;    // [2 G][rows][D]
+  float4* ml_part;  // [2 G][rows]: maximum of the logits, sum, maximum that O is taken against (log2 units)
+  int4* unit;       // [B * kv_heads]: first and last CTA of the unit, slot in the first, 0 / 1 = merge
+  int G, rows;      // CTAs, rows of a partial
+};
+
+// Shared memory and CTAs per SM: 12 to 16 warps an SM, each with at least 8 KB of copies in flight
+// (about 46 KB an SM cover the latency at the full rate), as registers allow.
+__host__ __device__ constexpr int ctas_per_sm(int D, int HB) { return HB == 4 ? 2 : (D == 64 && HB == 1) ? 4 : 3; }
+
+template <int D, bool E4M3, int HB>
+struct Cfg {
+  static constexpr int ROWB = E4M3 ? D : 2 * D;
+  static constexpr int STAGE = 2 * SR * ROWB;  // K then V
+  static constexpr int CTAS = ctas_per_sm(D, HB);
+  static constexpr int RING = CTAS == 4 ? 12288 : 16384;
+  static constexpr int NST = RING / STAGE;
+  static constexpr int QMEM = HB == 4 ? 2 * (D / 16) * 512 : 0;  // 32 rows: Q's fragments live in shared memory
+  static constexpr int SMEM = NW * RING + QMEM;
+  static_assert(NST >= 2, "at least one stage ahead");
+  static_assert(8 * HB * D * 4 <= RING, "a warp's output fits its ring");
+};
+
+struct Shared {
+  float m[NW][32], l[NW][32], mo[NW][32];
+  int2 meta[NW][16];  // [ring slot]: page usable, (k exponent byte | v exponent byte << 8)
+  int64_t total;
+  int64_t at;
+  int b;
+};
+
+// c += a b (m16n8k16), fp16 (e4m3 caches) or bf16; with UPPER only rows 0-7 of the tile are kept, and the
+// registers of rows 8-15 (of a zero A) are not carried along.
+template <bool E4M3, bool UPPER>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (UPPER) {
+    float x, y;
+    if (E4M3)
+      asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%10,%10};"
+          : "+f"(c[0]), "+f"(c[1]), "=f"(x), "=f"(y)
+          : "r"(a[0]), "r"(0u), "r"(a[2]), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
+    else
+      asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%10,%10};"
+          : "+f"(c[0]), "+f"(c[1]), "=f"(x), "=f"(y)
+          : "r"(a[0]), "r"(0u), "r"(a[2]), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
+  } else if (E4M3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
+// Two e4m3 codes, in the top byte of each half of m (the bottom bytes hold anything), as fp16 x 2^-8.
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t m) {
+  return ((m >> 1) & 0x3F803F80u) | (m & 0x80008000u);
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+// Byte offset of 16-byte chunk ch of row r in a stage's K or V half: the chunks of a 128-byte line (one
+// row, half of one, or two) are exchanged so that the quarter-warps of both read patterns (rows 2k, 2k + 1
+// with chunks c; rows 2c with the chunks of two lane groups) meet eight different ones.
+template <int ROWB>
+__device__ __forceinline__ int chunk_at(int r, int ch) {
+  if (ROWB == 64) {
+    const int line = r >> 1;
+    return line * 128 + (((((r & 1) << 2) | ch) ^ (((line & 1) << 2) | (line & 2))) << 4);
+  }
+  return r * ROWB + ((ch ^ (((r & 1) << 2) | ((r >> 1) & 3))) << 4);
+}
+
+struct Unit {
+  Seq s;
+  int lo, stages;  // first row read (a multiple of SR), stages (0: nothing to do)
+  int vlo;         // first row any token sees
+};
+
+__device__ __forceinline__ Unit unit_of(const dsv4_gqa_attention_params& p, int b) {
+  Unit u;
+  u.s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.max_kv_len);
+  u.stages = 0;
+  u.lo = u.vlo = 0;
+  if (!u.s.ok || u.s.n == 0) return u;
+  int lo = 0;
+  if (p.window > 0) lo = max(0, u.s.kv - u.s.n - p.window + 1);
+  if (p.kv_start) {
+    int first = 0x7FFFFFFF;
+    for (int i = 0; i < u.s.n; ++i) first = min(first, p.kv_start[u.s.t0 + i]);
+    lo = max(lo, first);
+  }
+  u.vlo = min(lo, u.s.kv);
+  u.lo = u.vlo & ~(SR - 1);
+  u.stages = max(1, (u.s.kv - u.lo + SR - 1) / SR);  // (one empty stage where nothing is visible)
+  return u;
+}
+
+template <int D, bool E4M3, int HB>
+__global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel(Args a) {
+  using C = Cfg<D, E4M3, HB>;
+  constexpr int MT = HB == 4 ? 2 : 1, KS = D / 16, NT = D / 8;
+  extern __shared__ __align__(1024) uint8_t ring_all[];
+  __shared__ Shared sm;
+  const dsv4_gqa_attention_params& p = a.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  uint8_t* ring = ring_all + warp * C::RING;
+  uint32_t* qmem = reinterpret_cast<uint32_t*>(ring_all + NW * C::RING);
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---------------- this CTA's piece of the list of stages
+  int64_t first, last;  // [first, last) in the list
+  int b, h;
+  int64_t per;
+  int64_t base;  // list position of unit (b, 0)
+  if (p.B <= MAX_SCAN) {
+    int64_t* pre = reinterpret_cast<int64_t*>(ring_all);  // [B + 1] stages of the sequences before
+    int64_t* wsum = pre + MAX_SCAN + 1;
+    int64_t run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+      const int bb = b0 + tid;
+      int st = 0;
+      if (bb < p.B) {
+        const Unit u = unit_of(p, bb);
+        st = u.stages;
+        if (blockIdx.x == 0 && st == 0) {
+          if (!u.s.ok) atomicOr(&g_flags_gd, FLAG_PAGE);
+          for (int k = 0; k < p.kv_heads; ++k) a.unit[(int64_t)bb * p.kv_heads + k] = make_int4(0, 0, 0, 0);
+        }
+      }
+      int64_t x = st;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) wsum[warp] = x;
+      __syncthreads();
+      int64_t off = run;
+      for (int w = 0; w < warp; ++w) off += wsum[w];
+      if (bb < p.B) pre[bb] = off + x - st;
+      for (int w = 0; w < NW; ++w) run += wsum[w];
+      __syncthreads();
+    }
+    const int64_t total = run * p.kv_heads;
+    per = (total + a.G - 1) / a.G;
+    if (per < MIN_STAGES) per = MIN_STAGES;
+    first = (int64_t)blockIdx.x * per;
+    last = min(total, first + per);
+    if (first >= last) return;
+    int lo = 0, hi = p.B;  // the last b whose list position is <= first (empty sequences share one: the last)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] * p.kv_heads <= first) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    base = pre[b] * p.kv_heads;
+    __syncthreads();
+  } else {
+    b = blockIdx.x / p.kv_heads;
+    const Unit u = unit_of(p, b);
+    if (u.stages == 0) {
+      if (tid == 0) {
+        if (!u.s.ok) atomicOr(&g_flags_gd, FLAG_PAGE);
+        a.unit[blockIdx.x] = make_int4(0, 0, 0, 0);
+      }
+      return;
+    }
+    base = 0;
+    per = u.stages;
+    first = (int64_t)(blockIdx.x % p.kv_heads) * per;
+    last = first + per;
+  }
+
+  const int group = p.q_heads / p.kv_heads;
+  const bool plain = p.softcap == 0.f && p.slopes == nullptr;
+  const float rcap2 = p.softcap > 0.f ? 2.f * LOG2E / p.softcap : 0.f;
+
+  // ---------------- the units that the piece meets
+  for (int64_t at = first; at < last; ++b) {
+    const Unit u = unit_of(p, b);
+    if (u.stages == 0) continue;
+    for (h = (int)((at - base) / u.stages); h < p.kv_heads && at < last; ++h) {
+      const int64_t u0 = base + (int64_t)h * u.stages;  // the unit's list positions [u0, u0 + stages)
+      const int s0 = (int)(at - u0), s1 = (int)(min(last, u0 + u.stages) - u0);
+      const bool whole = s0 == 0 && s1 == u.stages;
+      const int rows = u.s.n * group;
+      const int pos0 = u.s.kv - u.s.n;
+
+      // rows g + 8 k of this lane
+      int rlo[HB], rhi[HB];
+      float rmul[HB], slope[HB], rpos[HB];
+      float m[HB], mo[HB], l[HB];
+      int all_lo = 0, all_hi = 0x7FFFFFFF;  // rows that every token sees
+      uint32_t q[HB == 4 ? 1 : KS][4];
+#pragma unroll
+      for (int k = 0; k < HB; ++k) {
+        const int r = g + 8 * k, i = r / group;
+        const bool live = r < rows;
+        const int pos = pos0 + i, t = u.s.t0 + i;
+        rlo[k] = 0;
+        rhi[k] = 0;
+        slope[k] = 0.f;
+        rpos[k] = (float)pos;
+        rmul[k] = 0.f;
+        m[k] = mo[k] = -INFINITY;
+        l[k] = 0.f;
+        const int head = h * group + r % group;
+        if (live) {
+          const int2 v = visible_rows(p, b, t, pos, u.s.kv);
+          rlo[k] = v.x;
+          rhi[k] = v.y;
+          if (p.slopes) slope[k] = p.slopes[head] * LOG2E;
+          all_lo = max(all_lo, v.x);
+          all_hi = min(all_hi, v.y);
+        }
+        // Q fragments: the 4 dims of K step s that this lane's K registers hold
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q) +
+                             2 * ((int64_t)t * p.q_token_stride + (int64_t)head * p.q_head_stride);
+        uint2 w[KS];
+        float big = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const int d = E4M3 ? 64 * (s / 4) + 16 * c + 4 * (s % 4) : 32 * (s / 2) + 8 * c + 4 * (s % 2);
+          w[s] = live ? *reinterpret_cast<const uint2*>(src + 2 * d) : make_uint2(0u, 0u);
+          if (E4M3) {
+            big = fmaxf(big, fmaxf(fmaxf(fabsf(__uint_as_float(w[s].x << 16)), fabsf(__uint_as_float(w[s].x & 0xFFFF0000u))),
+                                   fmaxf(fabsf(__uint_as_float(w[s].y << 16)), fabsf(__uint_as_float(w[s].y & 0xFFFF0000u)))));
+          }
+        }
+        float mul = p.softmax_scale;
+        if (E4M3) {
+          // the row's largest magnitude is brought into [2^14, 2^15): elements down to 2^-39 of it keep
+          // all bits that matter next to fp32 sums
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          int e = big > 0.f && big < INFINITY ? (int)(__float_as_uint(big) >> 23) - 127 - 14 : 0;
+          e = max(-126, min(112, e));
+          const float f = exp2_neg_int(e);
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            const __half2 h0 = __floats2half2_rn(__uint_as_float(w[s].x << 16) * f, __uint_as_float(w[s].x & 0xFFFF0000u) * f);
+            const __half2 h1 = __floats2half2_rn(__uint_as_float(w[s].y << 16) * f, __uint_as_float(w[s].y & 0xFFFF0000u) * f);
+            w[s] = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+          }
+          mul *= exp2_neg_int(-e) * 256.f;  // (codes_to_f16's 2^-8)
+        }
+        rmul[k] = plain ? mul * LOG2E : mul;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          if (HB == 4) {  // [MMA tile][K step][lane][4 registers]
+            if (warp == 0) {
+              uint32_t* dst = qmem + (((k / 2) * KS + s) * 32 + lane) * 4;
+              dst[k & 1] = w[s].x;
+              dst[2 + (k & 1)] = w[s].y;
+            }
+          } else {
+            q[s][k & 1] = w[s].x;
+            q[s][2 + (k & 1)] = w[s].y;
+            if (HB == 1) q[s][1] = q[s][3] = 0u;
+          }
+        }
+      }
+      if (HB == 4) __syncthreads();
+      all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+      all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+
+      float o[MT][NT][4];
+#pragma unroll
+      for (int x = 0; x < MT; ++x)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
+
+      auto score = [&](float (&s)[MT][2][4], int nt, int ks, uint32_t b0, uint32_t b1) {
+        if (HB == 4) {
+#pragma unroll
+          for (int x = 0; x < MT; ++x) {
+            const uint4 w = *reinterpret_cast<const uint4*>(qmem + ((x * KS + ks) * 32 + lane) * 4);
+            const uint32_t f[4] = {w.x, w.y, w.z, w.w};
+            mma<E4M3, HB == 1>(s[x][nt], f, b0, b1);
+          }
+        } else {
+          mma<E4M3, HB == 1>(s[0][nt], q[ks], b0, b1);
+        }
+      };
+      // this warp's stages: s0 + warp, s0 + warp + NW, ...
+      const int count = s1 - s0 > warp ? (s1 - s0 - warp + NW - 1) / NW : 0;
+      int pid = -1, pexp = 0;
+      auto fill = [&](int k) {
+        if (k < count) {
+          if ((k & 31) == 0) {  // pages and exponents of the next 32 stages, one a lane
+            const int j = u.lo + (s0 + warp + (k + lane) * NW) * SR;
+            pid = -1;
+            pexp = 0;
+            if (k + lane < count && j < u.s.kv) {
+              const int lp = j / p.page_size;
+              pid = lp < p.max_pages_per_seq ? p.block_table[(int64_t)b * p.max_pages_per_seq + lp] : -1;
+              if (pid < 0 || pid >= p.num_pages) {
+                atomicOr(&g_flags_gd, FLAG_PAGE);
+                pid = -1;
+              } else if (E4M3) {
+                const int64_t e = (int64_t)pid * p.kv_heads + h;
+                pexp = (int)p.k_exp[e] | ((int)p.v_exp[e] << 8);
+              }
+            }
+          }
+          const int page = __shfl_sync(0xffffffffu, pid, k & 31), ex = __shfl_sync(0xffffffffu, pexp, k & 31);
+          const int slot = k % C::NST, j0 = u.lo + (s0 + warp + k * NW) * SR;
+          if (lane == 0) sm.meta[warp][slot] = make_int2(page >= 0, ex);
+          uint8_t* dst = ring + slot * C::STAGE;
+          constexpr int CPR = C::ROWB / 16, RPI = 32 / CPR;
+          const int ch = lane % CPR;
+          const int off = j0 & (p.page_size - 1);
+          const int64_t es = E4M3 ? 1 : 2;
+          const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k_cache) +
+                              es * ((int64_t)max(page, 0) * p.k_page_stride + (int64_t)h * p.k_cache_head_stride) + 16 * ch;
+          const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v_cache) +
+                              es * ((int64_t)max(page, 0) * p.v_page_stride + (int64_t)h * p.v_cache_head_stride) + 16 * ch;
+#pragma unroll
+          for (int i = 0; i < SR / RPI; ++i) {
+            const int r = i * RPI + lane / CPR;
+            // rows that no token sees read nothing and become zeros, whatever the cache holds there
+            const uint32_t n = page >= 0 && j0 + r >= u.vlo && j0 + r < u.s.kv ? 16u : 0u;
+            const int64_t row = n ? off + r : 0;
+            tc::cp_async16(dst + chunk_at<C::ROWB>(r, ch), kb + es * row * p.k_row_stride, n);
+            tc::cp_async16(dst + SR * C::ROWB + chunk_at<C::ROWB>(r, ch), vb + es * row * p.v_row_stride, n);
+          }
+        }
+        tc::cp_async_commit();
+      };
+#pragma unroll
+      for (int k = 0; k < C::NST - 1; ++k) fill(k);
+
+      for (int k = 0; k < count; ++k) {
+        tc::cp_async_wait<C::NST - 2>();
+        __syncwarp();
+        fill(k + C::NST - 1);
+        const int slot = k % C::NST, j0 = u.lo + (s0 + warp + k * NW) * SR;
+        const uint8_t* kt = ring + slot * C::STAGE;
+        const uint8_t* vt = kt + SR * C::ROWB;
+        const int2 meta = sm.meta[warp][slot];
+
+        // ---- S = Q K^T
+        float s[MT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+          for (int x = 0; x < MT; ++x) s[x][nt][0] = s[x][nt][1] = s[x][nt][2] = s[x][nt][3] = 0.f;
+          constexpr int KCH = C::ROWB / 64;  // 16-byte chunks a lane holds of a row
+#pragma unroll
+          for (int x = 0; x < KCH; ++x) {
+            const uint4 w = *reinterpret_cast<const uint4*>(kt + chunk_at<C::ROWB>(8 * nt + g, c + 4 * x));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            if (E4M3) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t b0 = codes_to_f16(__byte_perm(ww[y], 0u, 0x1404u));
+                const uint32_t b1 = codes_to_f16(__byte_perm(ww[y], 0u, 0x3424u));
+                score(s, nt, 4 * x + y, b0, b1);
+              }
+            } else {
+#pragma unroll
+              for (int y = 0; y < 2; ++y) score(s, nt, 2 * x + y, ww[2 * y], ww[2 * y + 1]);
+            }
+          }
+        }
+
+        // ---- logits in log2 units, masks
+        const float kmul = E4M3 ? ue8m0_scale((uint8_t)(meta.y & 255)) : 1.f;
+        const float vexp = E4M3 ? (float)((meta.y >> 8) - 127 + 8) : 0.f;  // (8: codes_to_f16)
+        const bool inside = meta.x != 0 && j0 >= all_lo && j0 + SR <= all_hi;
+        float top[HB];
+#pragma unroll
+        for (int k2 = 0; k2 < HB; ++k2) {
+          float (&x0)[4] = s[k2 / 2][0];
+          float (&x1)[4] = s[k2 / 2][1];
+          const int e = 2 * (k2 & 1);
+          float z[4] = {x0[e], x0[e + 1], x1[e], x1[e + 1]};
+          const float f = rmul[k2];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) z[y] = z[y] * kmul * f;
+          if (!plain) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              if (p.softcap > 0.f) z[y] = cap_logit(z[y], p.softcap, rcap2);
+              const int j = j0 + 2 * c + (y & 1) + 8 * (y >> 1);
+              z[y] = z[y] * LOG2E - slope[k2] * fabsf(rpos[k2] - (float)j);
+            }
+          }
+          if (!inside) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int j = j0 + 2 * c + (y & 1) + 8 * (y >> 1);
+              if (meta.x == 0 || j < rlo[k2] || j >= rhi[k2]) z[y] = -INFINITY;
+            }
+          }
+          top[k2] = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+          x0[e] = z[0];
+          x0[e + 1] = z[1];
+          x1[e] = z[2];
+          x1[e + 1] = z[3];
+        }
+        // ---- running maxima: moved (by the whole quad) only when some logit exceeds one by more than LAZY
+        bool move = false;
+#pragma unroll
+        for (int k2 = 0; k2 < HB; ++k2) move |= top[k2] > m[k2] + LAZY || (E4M3 && top[k2] + vexp > mo[k2] + LAZY);
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int k2 = 0; k2 < HB; ++k2) {
+            float t = top[k2];
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+            const float mn = fmaxf(m[k2], t), on = E4M3 ? fmaxf(mo[k2], t + vexp) : mn;
+            const float fl = m[k2] == -INFINITY ? 0.f : tc::ex2_approx(m[k2] - mn);
+            const float fo = E4M3 ? (mo[k2] == -INFINITY ? 0.f : tc::ex2_approx(mo[k2] - on)) : fl;
+            l[k2] *= fl;
+            m[k2] = mn;
+            mo[k2] = on;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              o[k2 / 2][j][2 * (k2 & 1)] *= fo;
+              o[k2 / 2][j][2 * (k2 & 1) + 1] *= fo;
+            }
+          }
+        }
+        // ---- P: weights for the sum, and (scaled by V's exponent) for the product
+        uint32_t pa[MT][4];
+        if (HB == 1) pa[0][1] = pa[0][3] = 0u;
+#pragma unroll
+        for (int k2 = 0; k2 < HB; ++k2) {
+          const int e = 2 * (k2 & 1);
+          const float z[4] = {s[k2 / 2][0][e], s[k2 / 2][0][e + 1], s[k2 / 2][1][e], s[k2 / 2][1][e + 1]};
+          const float mm = m[k2] == -INFINITY ? 0.f : m[k2];
+          float w[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) w[y] = tc::ex2_approx(z[y] - mm);
+          l[k2] += (w[0] + w[1]) + (w[2] + w[3]);
+          if (E4M3) {
+            const float om = mo[k2] == -INFINITY ? 0.f : mo[k2] - vexp;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[y] = tc::ex2_approx(z[y] - om);
+            const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
+            pa[k2 / 2][k2 & 1] = *reinterpret_cast<const uint32_t*>(&h0);
+            pa[k2 / 2][2 + (k2 & 1)] = *reinterpret_cast<const uint32_t*>(&h1);
+          } else {
+            pa[k2 / 2][k2 & 1] = float2_to_bf16x2_bits(w[0], w[1]);
+            pa[k2 / 2][2 + (k2 & 1)] = float2_to_bf16x2_bits(w[2], w[3]);
+          }
+        }
+        // ---- O += P V
+        if (E4M3) {
+          constexpr int WD = D / 32;  // words (of 4 dims) a lane holds of a row
+          uint32_t v[4][WD];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int r = 2 * c + (y & 1) + 8 * (y >> 1);
+            if (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(vt + chunk_at<C::ROWB>(r, (g >> 1) | ((g & 1) << 2)));
+              v[y][0] = w.x;
+              v[y][1] = w.y;
+              v[y][WD - 2] = w.z;
+              v[y][WD - 1] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(vt + chunk_at<C::ROWB>(r, g >> 1) + 8 * (g & 1));
+              v[y][0] = w.x;
+              v[y][1] = w.y;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint32_t sel = ((4u + (j & 3)) << 12) | ((uint32_t)(j & 3) << 4);
+            const uint32_t b0 = codes_to_f16(__byte_perm(v[0][j >> 2], v[1][j >> 2], sel));
+            const uint32_t b1 = codes_to_f16(__byte_perm(v[2][j >> 2], v[3][j >> 2], sel));
+#pragma unroll
+            for (int x = 0; x < MT; ++x) mma<E4M3, HB == 1>(o[x][j], pa[x], b0, b1);
+          }
+        } else {
+          // matrices of an x4 load: rows 0-7 and 8-15 of dims 8 (2 jj), then of dims 8 (2 jj + 1)
+          const int r = (lane & 7) + (lane & 8);
+#pragma unroll
+          for (int jj = 0; jj < NT / 2; ++jj) {
+            uint32_t w[4];
+            ldmatrix_x4_trans(w, tc::smem_addr(vt + chunk_at<C::ROWB>(r, 2 * jj + (lane >> 4))));
+#pragma unroll
+            for (int x = 0; x < MT; ++x) {
+              mma<E4M3, HB == 1>(o[x][2 * jj], pa[x], w[0], w[1]);
+              mma<E4M3, HB == 1>(o[x][2 * jj + 1], pa[x], w[2], w[3]);
+            }
+          }
+        }
+      }
+      tc::cp_async_wait<0>();
+
+      // ---------------- the four warps' results of the unit
+#pragma unroll
+      for (int k = 0; k < HB; ++k) {
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+        if (c == 0) {
+          sm.m[warp][g + 8 * k] = m[k];
+          sm.l[warp][g + 8 * k] = l[k];
+          sm.mo[warp][g + 8 * k] = mo[k];
+        }
+      }
+      __syncthreads();
+      float* part = reinterpret_cast<float*>(ring);  // [rows][D]: the ring is drained
+#pragma unroll
+      for (int k = 0; k < HB; ++k) {
+        const int r = g + 8 * k;
+        float on = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) on = fmaxf(on, sm.mo[w][r]);
+        const float f = mo[k] == -INFINITY ? 0.f : tc::ex2_approx(mo[k] - on);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          // column n of tile j is dim 16 f(n) + j, f(n) the chunk of lane group n (e4m3, D = 128), 8 n + j (D = 64)
+          // or 8 j + n (bf16); this lane has columns 2 c and 2 c + 1
+          const int d0 = !E4M3 ? 8 * j + 2 * c : D == 128 ? 16 * c + j : 16 * c + j;
+          const int d1 = !E4M3 ? d0 + 1 : D == 128 ? d0 + 64 : d0 + 8;
+          part[r * D + d0] = o[k / 2][j][2 * (k & 1)] * f;
+          part[r * D + d1] = o[k / 2][j][2 * (k & 1) + 1] * f;
+        }
+      }
+      __syncthreads();
+      const int slot = 2 * blockIdx.x + (at == first ? 0 : 1);
+      for (int x = tid; x < rows * (D / 4); x += THREADS) {
+        const int r = x / (D / 4), d4 = x % (D / 4);
+        float mn = -INFINITY, on = -INFINITY, ls = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          mn = fmaxf(mn, sm.m[w][r]);
+          on = fmaxf(on, sm.mo[w][r]);
+          const float4 v = reinterpret_cast<const float4*>(ring_all + w * C::RING)[r * (D / 4) + d4];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+        }
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+          if (sm.m[w][r] > -INFINITY) ls += sm.l[w][r] * tc::ex2_approx(sm.m[w][r] - mn);
+        if (whole) {
+          const int head = h * group + r % group;
+          const int64_t row = (int64_t)(u.s.t0 + r / group) * p.q_heads + head;
+          const float f = finish_scale(p, row, head, mn, ls, on, d4 == 0);
+          store4<D>(p, row, d4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+        } else {
+          reinterpret_cast<float4*>(a.o_part)[((int64_t)slot * a.rows + r) * (D / 4) + d4] = acc;
+          if (d4 == 0) a.ml_part[(int64_t)slot * a.rows + r] = make_float4(mn, ls, on, 0.f);
+        }
+      }
+      if (tid == 0 && s0 == 0)
+        a.unit[(int64_t)b * p.kv_heads + h] =
+            whole ? make_int4(0, 0, 0, 0)
+                  : make_int4((int)blockIdx.x, (int)((u0 + u.stages - 1) / per), at == first ? 0 : 1, 1);
+      __syncthreads();
+      at = u0 + s1;
+    }
+    base += (int64_t)p.kv_heads * u.stages;
+  }
+}
+
+// Units cut by a border between CTAs: a warp joins the partial results of one row.
+template <int D>
+__global__ void __launch_bounds__(THREADS) merge_kernel(Args a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const dsv4_gqa_attention_params& p = a.p;
+  const int4 info = a.unit[blockIdx.x];
+  if (info.w == 0) return;
+  const int b = blockIdx.x / p.kv_heads, h = blockIdx.x % p.kv_heads, lane = threadIdx.x & 31;
+  const Seq s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.max_kv_len);
+  const int group = p.q_heads / p.kv_heads, rows = s.n * group, n = info.y - info.x + 1;
+  auto slot = [&](int i) { return 2 * (info.x + i) + (i == 0 ? info.z : 0); };
+  for (int r = blockIdx.y * NW + (threadIdx.x >> 5); r < rows; r += gridDim.y * NW) {
+    float mn = -INFINITY, on = -INFINITY;
+    for (int i = lane; i < n; i += 32) {
+      const float4 x = a.ml_part[(int64_t)slot(i) * a.rows + r];
+      mn = fmaxf(mn, x.x);
+      on = fmaxf(on, x.z);
+    }
+    mn = warp_max(mn);
+    on = warp_max(on);
+    float ls = 0.f;
+    constexpr int E = D / 32;  // dims of a lane, from lane * E on
+    float acc[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) acc[k] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float f = 0.f;
+      if (i0 + lane < n) {
+        const float4 x = a.ml_part[(int64_t)slot(i0 + lane) * a.rows + r];
+        if (x.x > -INFINITY) {
+          ls += x.y * tc::ex2_approx(x.x - mn);
+          f = tc::ex2_approx(x.z - on);
+        }
+      }
+      const int m = min(32, n - i0);
+#pragma unroll 4
+      for (int i = 0; i < m; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float2* src = reinterpret_cast<const float2*>(a.o_part + ((int64_t)slot(i0 + i) * a.rows + r) * D + lane * E);
+#pragma unroll
+        for (int k = 0; k < E; k += 2) {
+          const float2 v = src[k / 2];
+          acc[k] = fmaf(v.x, fi, acc[k]);
+          acc[k + 1] = fmaf(v.y, fi, acc[k + 1]);
+        }
+      }
+    }
+    ls = warp_sum(ls);
+    const int head = h * group + r % group;
+    const int64_t row = (int64_t)(s.t0 + r / group) * p.q_heads + head;
+    const float f = finish_scale(p, row, head, mn, ls, on, lane == 0);
+    if (p.out_dtype == DSV4_F32) {
+#pragma unroll
+      for (int k = 0; k < E; k += 2)
+        reinterpret_cast<float2*>(p.out)[(row * D + lane * E + k) / 2] = make_float2(acc[k] * f, acc[k + 1] * f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; k += 2)
+        reinterpret_cast<uint32_t*>(p.out)[(row * D + lane * E + k) / 2] = float2_to_bf16x2_bits(acc[k] * f, acc[k + 1] * f);
+    }
+  }
+}
+
+struct Plan {
+  int hb, rows, G;
+  size_t ml_off, unit_off, total;
+};
+
+// Row halves of 8 that hold the rows of a kv head, and the CTAs: what the device holds at once, or fewer
+// where even the largest batch within the call's bounds has fewer pieces of MIN_STAGES.
+static Plan plan(const dsv4_gqa_attention_params& p) {
+  Plan L;
+  const int max_n = p.max_q_len < p.T ? p.max_q_len : p.T;
+  L.rows = max_n * (p.q_heads / p.kv_heads);
+  L.hb = L.rows <= 8 ? 1 : L.rows <= 16 ? 2 : 4;
+  L.rows = 8 * L.hb;
+  const int ctas = ctas_per_sm(p.head_dim, L.hb);
+  const int64_t stages = (int64_t)p.B * p.kv_heads * (p.max_kv_len / SR + 2);
+  const int64_t pieces = (stages + MIN_STAGES - 1) / MIN_STAGES;
+  L.G = num_sms() * ctas;
+  if (pieces < L.G) L.G = (int)pieces;
+  const int64_t slots = p.B <= MAX_SCAN ? 2LL * L.G : 0;
+  L.ml_off = align_up((size_t)slots * L.rows * p.head_dim * 4, 256);
+  L.unit_off = align_up(L.ml_off + (size_t)slots * L.rows * 16, 256);
+  L.total = align_up(L.unit_off + (size_t)p.B * p.kv_heads * 16, 256);
+  return L;
+}
+
+template <int D, bool E4M3, int HB>
+static cudaError_t launch(const Args& a, cudaStream_t s) {
+  using C = Cfg<D, E4M3, HB>;
+  const void* fn = reinterpret_cast<const void*>(decode_kernel<D, E4M3, HB>);
+  cudaError_t e = ensure_max_dynamic_smem(fn, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const dsv4_gqa_attention_params& p = a.p;
+  const int64_t units = (int64_t)p.B * p.kv_heads;
+  if (units > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const bool scan = p.B <= MAX_SCAN;
+  e = launch_pdl(decode_kernel<D, E4M3, HB>, dim3(scan ? a.G : (unsigned)units), dim3(THREADS), C::SMEM, s, true, a);
+  if (e != cudaSuccess || !scan) return e;
+  return launch_pdl(merge_kernel<D>, dim3((unsigned)units, 2 * HB), dim3(THREADS), 0, s, true, a);
+}
+
+template <int D, bool E4M3>
+static cudaError_t launch_hb(const Args& a, int hb, cudaStream_t s) {
+  return hb == 1 ? launch<D, E4M3, 1>(a, s) : hb == 2 ? launch<D, E4M3, 2>(a, s) : launch<D, E4M3, 4>(a, s);
+}
+
+}  // namespace dec
+
+size_t decode_workspace(const dsv4_gqa_attention_params& p) { return dec::plan(p).total; }
+
+cudaError_t launch_decode(const dsv4_gqa_attention_params& p, cudaStream_t s) {
+  const dec::Plan L = dec::plan(p);
+  dec::Args a;
+  a.p = p;
+  uint8_t* ws = reinterpret_cast<uint8_t*>(p.workspace);
+  a.o_part = reinterpret_cast<float*>(ws);
+  a.ml_part = reinterpret_cast<float4*>(ws + L.ml_off);
+  a.unit = reinterpret_cast<int4*>(ws + L.unit_off);
+  a.G = L.G;
+  a.rows = L.rows;
+  const bool e4m3 = p.cache_dtype == DSV4_E4M3_PAGE;
+  if (p.head_dim == 128)
+    return e4m3 ? dec::launch_hb<128, true>(a, L.hb, s) : dec::launch_hb<128, false>(a, L.hb, s);
+  return e4m3 ? dec::launch_hb<64, true>(a, L.hb, s) : dec::launch_hb<64, false>(a, L.hb, s);
+}
+
+}  // namespace gqa
+
+cudaError_t read_flags_gqa_decode(uint32_t* f) {
+  unsigned int v = 0, z = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_flags_gd, sizeof(v));
+  if (e != cudaSuccess) return e;
+  *f |= v;
+  return cudaMemcpyToSymbol(g_flags_gd, &z, sizeof(z));
+}
+
+}  // namespace dsv4

@@ -51,7 +51,7 @@ cudaError_t make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* b
 
 namespace {
 constexpr int kMaxDevices = 64;
-constexpr int kMaxKernels = 16;
+constexpr int kMaxKernels = 64;
 std::mutex g_dev_mutex;
 int g_sms[kMaxDevices] = {0};
 struct SmemAttr {

@@ -339,6 +339,14 @@ def test_attention_flags_bad_pages_and_sequences(M):
         for cache in ("bf16", "e4m3"):
             bt = Batch(n, kv, 4, 2, 128, 64, cache, seed=4)
             good = check_attention(M, bt)[1]
+            want, wlse, mag, size = G.attention(bt.q64(), bt.caches, bt.exps, bt.table, bt.q_start, bt.kv, bt.D ** -0.5)
+            # (where the rows are cut depends on the whole batch, so another batch gives other roundings: both
+            # results are within tol of the exact ones)
+            tol = torch.from_numpy(bounds(mag, size, want, wlse, False)[0]).cuda()
+
+            def same(out, t0, t1):
+                return bool(((out[t0:t1] - good[t0:t1]).abs().double() <= 2 * tol[t0:t1]).all())
+
             for entry in (-1, bt.caches[0].shape[0], 2 ** 31 - 1):
                 b2 = Batch(n, kv, 4, 2, 128, 64, cache, seed=4)
                 b2.table[0, 1] = entry
@@ -346,7 +354,7 @@ def test_attention_flags_bad_pages_and_sequences(M):
                 assert M.dsv4_read_device_flags() == 1
                 assert torch.isfinite(out).all()
                 t1 = int(bt.q_start[1])
-                assert torch.equal(out[t1:], good[t1:])
+                assert same(out, t1, bt.T)
                 assert not torch.equal(out[:t1], good[:t1])
             for what in ("kv", "max_kv", "max_q"):
                 b2 = Batch(n, kv, 4, 2, 128, 64, cache, seed=4)
@@ -362,7 +370,7 @@ def test_attention_flags_bad_pages_and_sequences(M):
                 bad = int(np.argmax(n)) if what == "max_q" else 0
                 for b in range(3):
                     t0, t1 = int(bt.q_start[b]), int(bt.q_start[b + 1])
-                    assert ((out[t0:t1] == -3).all() if b == bad else torch.equal(out[t0:t1], good[t0:t1])), what
+                    assert ((out[t0:t1] == -3).all() if b == bad else same(out, t0, t1)), what
 
 
 def test_attention_is_repeatable_and_replays(M):
