@@ -100,7 +100,7 @@ int dsv4_read_device_flags(uint32_t* flags) {
   if (st != DSV4_OK) return st;
   st = cuda_status(read_flags_gqa_append(flags));
   if (st != DSV4_OK) return st;
-  st = cuda_status(read_flags_gqa_attention(flags));
+  st = cuda_status(read_flags_gqa_prefill(flags));
   if (st != DSV4_OK) return st;
   st = cuda_status(read_flags_gqa_decode(flags));
   if (st != DSV4_OK) return st;

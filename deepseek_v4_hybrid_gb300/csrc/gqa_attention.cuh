@@ -21,9 +21,15 @@ __device__ __forceinline__ int2 visible_rows(const dsv4_gqa_attention_params& p,
   return make_int2(lo, hi);
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // cap * tanh(z / cap) with rcap2 = 2 log2(e) / cap: tanh x = 1 - 2 / (1 + e^2x), off by some 2^-23 cap.
 __device__ __forceinline__ float cap_logit(float z, float cap, float rcap2) {
-  return cap - 2.f * cap * __frcp_rn(1.f + tc::ex2_approx(z * rcap2));
+  return cap - 2.f * cap * rcp_approx(1.f + tc::ex2_approx(z * rcap2));
 }
 
 // A row's sums: m the logits' reference (log2 units), l their sum against it, mo the reference that the
@@ -50,6 +56,8 @@ __device__ __forceinline__ void store4(const dsv4_gqa_attention_params& p, int64
 }
 
 size_t decode_workspace(const dsv4_gqa_attention_params& p);
+size_t prefill_workspace(const dsv4_gqa_attention_params& p);
+cudaError_t launch_prefill(const dsv4_gqa_attention_params& p, cudaStream_t s);
 cudaError_t launch_decode(const dsv4_gqa_attention_params& p, cudaStream_t s);
 
 }  // namespace gqa

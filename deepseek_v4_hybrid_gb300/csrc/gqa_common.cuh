@@ -11,8 +11,8 @@ cudaError_t launch_gqa_append(const dsv4_gqa_append_params& p, cudaStream_t s);
 cudaError_t read_flags_gqa_append(uint32_t* f);
 size_t gqa_attention_workspace(const dsv4_gqa_attention_params& p);
 cudaError_t launch_gqa_attention(const dsv4_gqa_attention_params& p, cudaStream_t s);
-cudaError_t read_flags_gqa_attention(uint32_t* f);
 cudaError_t read_flags_gqa_decode(uint32_t* f);
+cudaError_t read_flags_gqa_prefill(uint32_t* f);
 
 namespace gqa {
 

@@ -1,0 +1,810 @@
+// Grouped-query attention of many new tokens a sequence: tcgen05 products with TMEM accumulators.
+//
+// The rows (token, head of the group) of one kv head, token by token, are cut into units of 256: two MMA
+// tiles of 128 rows that share every key and value tile of 128 cache rows.
+//   S_i = Q_i K^T          M = 128 rows, N = 128 cache rows, K = head_dim     (shared memory x shared memory)
+//   O_i += P_i V           M = 128 rows, N = head_dim, K = 128 cache rows     (tensor memory x shared memory)
+// TMEM: S_0, S_1 (128 columns each; P_i as bf16 over the first half of S_i), O_0, O_1.
+//   Warps 0-3 and 4-7 (a warpgroup a tile): a thread owns a row: reads S from TMEM, masks, caps, takes the online
+//   softmax in log2 units (O is rescaled only when a row's maximum grows by more than 2^8) and writes P back;
+//   loads its tile's queries at a unit's start and writes the output at its end.
+//   Warp 8 loads key and value tiles by TMA (one box a page) into a ring of four tiles.
+//   Lane 0 of warp 9 issues the MMAs: P_0 V, S_0 of the next tile, P_1 V, S_1 of the next tile, so that the
+//   tensor cores work on one tile while the other's softmax runs.
+// Bound by the tensor cores and, at head_dim 64 or with capped scores, by the exponentials.
+//
+// The work of a batch is one list of key tiles, ordered (sequence, kv head, unit), a unit weighing its tiles
+// plus UNIT_COST (its queries' load and output), cut evenly over one persistent CTA per SM: ragged batches,
+// causal triangles and few long prompts all end together.  A unit cut by a border leaves partial results
+// that a small kernel joins.
+//
+// e4m3 caches are expanded once into a bf16 copy of the sequences' rows in the workspace (exact: a code times
+// a power of two): 256 rows share a tile, so the copy's extra bytes cost less than expanding each tile in
+// every unit that reads it would.
+#include "gqa_attention.cuh"
+#include "tmap.h"
+
+namespace dsv4 {
+
+static __device__ unsigned int g_flags_gp = 0;
+
+namespace gqa {
+namespace pre {
+
+constexpr int TILE = 128, UROWS = 256;
+constexpr int SOFTMAX_WARPS = 8, W_LOAD = 8, W_MMA = 9, THREADS = 384;
+// Registers a thread: 384 x 168 at launch = 256 x 216 for the softmax + 128 x 72 for the other warpgroup.
+constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;
+constexpr int NSLOT = 4;
+constexpr int UNIT_COST = 3;
+constexpr int MAX_UNITS = 8192;   // units of the evenly cut list; above, a CTA takes a whole unit
+constexpr float LAZY = 8.f;
+constexpr uint32_t FLAG_TIMEOUT = 4u;
+
+struct Args {
+  dsv4_gqa_attention_params p;
+  int4* unit;        // [B * tps]: first row seen, end of the rows seen, key tiles of tile 0 and 1 (bit 30 of the
+                     // latter: some page is out of range)
+  float* o_part;     // [2 G][256][D]
+  float2* ml_part;   // [2 G][256]
+  int4* cut;         // [G]: unit, kv head, last CTA (-1: no unit that begins here goes on), slot here
+  uint16_t* bf_k;    // e4m3: the expanded rows [B][kv_heads][kv_pad][D]
+  uint16_t* bf_v;
+  int kv_pad;
+  int tps;           // units a sequence can have
+  int G;
+  int even;          // 1: the list is cut evenly, 0: a CTA takes a whole unit
+  int box;           // cache rows of a TMA box
+};
+
+// ------------------------------------------------------------------------------------------------
+// The units' rows (one warp each), and the expansion of e4m3 rows (a CTA per 64 rows and kv head).
+// ------------------------------------------------------------------------------------------------
+constexpr int PREP_THREADS = 256, EXPAND_ROWS = 64;
+
+__device__ __forceinline__ void plan_unit(const Args& a, int u) {
+  const dsv4_gqa_attention_params& p = a.p;
+  const int lane = threadIdx.x & 31;
+  const int b = u / a.tps, tile = u % a.tps, group = p.q_heads / p.kv_heads;
+  const Seq s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.max_kv_len);
+  int4 e = make_int4(0, 0, 0, 0);
+  if (!s.ok) {
+    if (tile == 0 && lane == 0) atomicOr(&g_flags_gp, FLAG_PAGE);
+  } else if ((int64_t)tile * UROWS < (int64_t)s.n * group) {
+    int lo = 0x7FFFFFFF, hi[2] = {0, 0};
+    bool live[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t r0 = (int64_t)tile * UROWS + i * TILE, r1 = min(r0 + TILE, (int64_t)s.n * group);
+      live[i] = r0 < r1;
+      if (!live[i]) continue;
+      const int t0 = (int)(r0 / group), t1 = (int)((r1 - 1) / group);
+      for (int t = t0 + lane; t <= t1; t += 32) {
+        const int2 v = visible_rows(p, b, s.t0 + t, s.kv - s.n + t, s.kv);
+        if (v.x < v.y) {
+          lo = min(lo, v.x);
+          hi[i] = max(hi[i], v.y);
+        }
+      }
+      hi[i] = __reduce_max_sync(0xffffffffu, hi[i]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    if (lo == 0x7FFFFFFF) lo = 0;
+    const int start = lo & ~(a.box - 1);
+    int n[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) n[i] = hi[i] > start ? (hi[i] - start + TILE - 1) / TILE : 0;
+    if (live[0]) n[0] = max(n[0], 1);  // (a unit that sees nothing still writes its output)
+    const int end = max(hi[0], hi[1]);
+    bool bad = false;
+    for (int lp = start / p.page_size + lane; (int64_t)lp * p.page_size < end; lp += 32) {
+      const int page = lp < p.max_pages_per_seq ? p.block_table[(int64_t)b * p.max_pages_per_seq + lp] : -1;
+      bad |= page < 0 || page >= p.num_pages;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad && lane == 0) atomicOr(&g_flags_gp, FLAG_PAGE);
+    e = make_int4(lo, end, n[0], n[1] | (bad ? 1 << 30 : 0));
+  }
+  if (lane == 0) a.unit[u] = e;
+}
+
+template <int D>
+__device__ __forceinline__ void expand_rows(const Args& a, int item) {
+  const dsv4_gqa_attention_params& p = a.p;
+  const int blocks = a.kv_pad / EXPAND_ROWS;
+  const int blk = item % blocks, u = item / blocks, h = u % p.kv_heads, b = u / p.kv_heads;
+  const Seq s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.max_kv_len);
+  const int r0 = blk * EXPAND_ROWS;
+  if (!s.ok || s.n == 0 || r0 >= ((s.kv + TILE - 1) & ~(TILE - 1))) return;
+  if (p.window > 0 && r0 + EXPAND_ROWS + TILE <= s.kv - s.n - p.window) return;  // before every token's window
+  constexpr int CPR = D / 16;  // 16-byte pieces of a row of codes
+  for (int x = threadIdx.x; x < EXPAND_ROWS * CPR; x += PREP_THREADS) {
+    const int r = r0 + x / CPR, ch = x % CPR;
+    const int lp = r / p.page_size;
+    int page = -1;
+    if (r < s.kv && lp < p.max_pages_per_seq) page = p.block_table[(int64_t)b * p.max_pages_per_seq + lp];
+    const bool in = page >= 0 && page < p.num_pages;
+    const int64_t o = (((int64_t)b * p.kv_heads + h) * a.kv_pad + r) * D + ch * 16;
+    const int row = r & (p.page_size - 1);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      float f = 0.f;
+      if (in) {
+        const uint8_t* src = kv ? reinterpret_cast<const uint8_t*>(p.v_cache) + (int64_t)page * p.v_page_stride +
+                                      (int64_t)h * p.v_cache_head_stride + (int64_t)row * p.v_row_stride
+                                : reinterpret_cast<const uint8_t*>(p.k_cache) + (int64_t)page * p.k_page_stride +
+                                      (int64_t)h * p.k_cache_head_stride + (int64_t)row * p.k_row_stride;
+        w = __ldg(reinterpret_cast<const uint4*>(src + ch * 16));
+        f = ue8m0_scale((kv ? p.v_exp : p.k_exp)[(int64_t)page * p.kv_heads + h]);
+      }
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      uint32_t out[8];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float2 c0 = e4m3x2_to_float2((uint16_t)(ww[y] & 0xFFFFu)), c1 = e4m3x2_to_float2((uint16_t)(ww[y] >> 16));
+        out[2 * y] = in ? float2_to_bf16x2_bits(c0.x * f, c0.y * f) : 0u;
+        out[2 * y + 1] = in ? float2_to_bf16x2_bits(c1.x * f, c1.y * f) : 0u;
+      }
+      uint4* dst = reinterpret_cast<uint4*>((kv ? a.bf_v : a.bf_k) + o);
+      dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+      dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(PREP_THREADS) prepare_kernel(Args a, int plan_ctas) {
+  pdl_wait();
+  pdl_launch_dependents();
+  if ((int)blockIdx.x < plan_ctas) {
+    const int u = blockIdx.x * (PREP_THREADS / 32) + (threadIdx.x >> 5);
+    if (u < a.p.B * a.tps) plan_unit(a, u);
+  } else {
+    expand_rows<D>(a, blockIdx.x - plan_ctas);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// The attention kernel.
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(tc::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w),
+      "r"(tc::smem_addr(bar))
+      : "memory");
+}
+
+struct Smem {
+  uint64_t full[NSLOT], empty[NSLOT], vraw, qfull[2], sfull[2], pfull[2], odone[2];
+  int64_t first, last, u0;
+  int64_t wsum[THREADS / 32];
+  int64_t per;
+  int b, h, tile;
+  uint32_t tmem_base;
+  int abort;
+};
+
+struct Segment {
+  int b, h, tile;      // unit `tile` of sequence b, kv head h
+  int lo, end;         // rows seen by the unit: lo .. end - 1
+  int start;           // cache row of key tile 0
+  int k0, k1, n[2];    // this CTA's key tiles k0 .. k1 - 1; tiles of the two row tiles
+  bool bad, whole;
+  int64_t u0, w;       // the unit's place and weight in the list
+  __device__ int count(int i) const { return max(0, min(k1, n[i]) - k0); }
+};
+
+// The CTA's segments in order; every role walks them by itself.
+struct Walk {
+  int b, h, tile;
+  int64_t u0;
+  __device__ __forceinline__ bool next(const Args& a, int64_t first, int64_t last, Segment& g) {
+    while (u0 < last && b < a.p.B) {
+      const int4 e = a.unit[(int64_t)b * a.tps + tile];
+      g.n[0] = e.z;
+      g.n[1] = e.w & 0x3FFFFFFF;
+      g.bad = (e.w >> 30) & 1;
+      g.b = b;
+      g.h = h;
+      g.tile = tile;
+      g.lo = e.x;
+      g.end = e.y;
+      g.start = e.x & ~(a.box - 1);
+      g.u0 = u0;
+      const int n = max(g.n[0], g.n[1]);
+      g.w = n ? n + UNIT_COST : 0;
+      if (++tile == a.tps || n == 0) {  // (a sequence's units with work come first)
+        tile = 0;
+        if (++h == a.p.kv_heads) {
+          h = 0;
+          ++b;
+        }
+      }
+      if (n == 0) continue;
+      u0 += g.w;
+      if (u0 <= first) continue;
+      const int64_t x0 = max(first, g.u0) - g.u0, x1 = min(last, u0) - g.u0;
+      g.k0 = (int)max((int64_t)0, x0 - UNIT_COST);
+      g.k1 = (int)max((int64_t)0, x1 - UNIT_COST);
+      if (g.k0 >= g.k1) continue;
+      g.whole = g.k0 == 0 && g.k1 == n;
+      return true;
+    }
+    return false;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, Args a) {
+  constexpr int QT = TILE * D * 2;     // bytes of a query tile, and of a key or value tile
+  constexpr int HB = TILE * 128;       // one 64-dim half of it (or all, D = 64)
+  constexpr uint32_t COL_O = 256;
+  const dsv4_gqa_attention_params& p = a.p;
+  extern __shared__ uint8_t raw_mem[];
+  uint8_t* mem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_mem) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_mem = mem;
+  uint8_t* kv_mem = mem + 2 * QT;
+  Smem* sm = reinterpret_cast<Smem*>(mem + 2 * QT + NSLOT * QT);
+  volatile int* abort = &sm->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    sm->abort = 0;
+    for (int i = 0; i < NSLOT; ++i) {
+      tc::mbar_init(&sm->full[i], 1);
+      tc::mbar_init(&sm->empty[i], 1);
+    }
+    tc::mbar_init(&sm->vraw, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm->qfull[i], 4);
+      tc::mbar_init(&sm->sfull[i], 1);
+      tc::mbar_init(&sm->pfull[i], 4);
+      tc::mbar_init(&sm->odone[i], 1);
+    }
+    tc::fence_barrier_init();
+  }
+  if (warp == W_MMA) {
+    tc::tmem_alloc(&sm->tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---------------- this CTA's piece of the list
+  if (a.even) {
+    int64_t* pre = reinterpret_cast<int64_t*>(kv_mem);  // inclusive sums of the units' weights
+    const int U = p.B * a.tps, per_thread = (U + THREADS - 1) / THREADS;
+    const int i0 = min(U, tid * per_thread), i1 = min(U, i0 + per_thread);
+    int64_t sum = 0;
+    for (int i = i0; i < i1; ++i) {
+      const int4 e = a.unit[i];
+      const int n = max(e.z, e.w & 0x3FFFFFFF);
+      sum += n ? n + UNIT_COST : 0;
+      pre[i] = sum;
+    }
+    int64_t x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sm->wsum[warp] = x;
+    __syncthreads();
+    int64_t off = x - sum, total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) off += sm->wsum[w];
+      total += sm->wsum[w];
+    }
+    for (int i = i0; i < i1; ++i) pre[i] += off;
+    __syncthreads();
+    if (tid == 0) {
+      const int64_t all = total * p.kv_heads;
+      const int64_t per = max((all + a.G - 1) / a.G, (int64_t)(UNIT_COST + 4));
+      const int64_t first = (int64_t)blockIdx.x * per;
+      sm->per = per;
+      sm->first = first;
+      sm->last = min(all, first + per);
+      sm->b = p.B;
+      if (first < sm->last) {
+        int lo = 0, hi = p.B - 1;  // the first b whose units end behind `first`
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (pre[(int64_t)(mid + 1) * a.tps - 1] * p.kv_heads > first) hi = mid;
+          else lo = mid + 1;
+        }
+        const int64_t before = lo ? pre[(int64_t)lo * a.tps - 1] : 0;
+        const int64_t W = pre[(int64_t)(lo + 1) * a.tps - 1] - before;
+        const int h = (int)((first - before * p.kv_heads) / W);
+        const int64_t base = before * p.kv_heads + h * W, x0 = first - base;
+        int tl = 0, th = a.tps - 1;  // the first unit that ends behind x0
+        while (tl < th) {
+          const int mid = (tl + th) >> 1;
+          if (pre[(int64_t)lo * a.tps + mid] - before > x0) th = mid;
+          else tl = mid + 1;
+        }
+        sm->b = lo;
+        sm->h = h;
+        sm->tile = tl;
+        sm->u0 = base + (tl ? pre[(int64_t)lo * a.tps + tl - 1] - before : 0);
+      }
+      a.cut[blockIdx.x] = make_int4(0, 0, -1, 0);
+    }
+  } else if (tid == 0) {
+    // a whole unit a CTA: units fastest and the last ones (which see most) first, then heads, then sequences
+    const int64_t x = blockIdx.x;
+    sm->tile = a.tps - 1 - (int)(x % a.tps);
+    sm->h = (int)(x / a.tps % p.kv_heads);
+    sm->b = (int)(x / a.tps / p.kv_heads);
+    const int4 e = a.unit[(int64_t)sm->b * a.tps + sm->tile];
+    const int n = max(e.z, e.w & 0x3FFFFFFF);
+    sm->u0 = sm->first = 0;
+    sm->last = n ? n + UNIT_COST : 0;
+    sm->per = 1;
+  }
+  tc::fence_proxy_async_smem();  // (the sums lie where key and value tiles will land)
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = sm->tmem_base;
+  const int64_t first = sm->first, last = sm->last;
+  Walk walk{sm->b, sm->h, sm->tile, sm->u0};
+  Segment g;
+
+  if (warp >= SOFTMAX_WARPS) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+  if (warp == W_LOAD) {
+    // ---------------- TMA loads
+    int it = 0, armed = 0;  // tiles handed out, tiles armed on their own barrier
+    bool raw = false;       // a tile is on its way to vraw
+    bool ok = true;
+    uint32_t raw_phase = 0;
+    if (lane == 0) {
+      tc::tma_prefetch_desc(&kmap);
+      tc::tma_prefetch_desc(&vmap);
+    }
+    const int nbox = TILE / a.box;
+    const bool expanded = a.bf_k != nullptr;
+    while (ok && walk.next(a, first, last, g)) {
+      for (int k = g.k0; k < g.k1 && ok; ++k) {
+        const int t0 = g.start + k * TILE;
+        // box `lane` of the tile: its page (out of range, so that zeros come, where it has none) and row
+        int page = expanded ? g.b : (int)max(p.num_pages, (int64_t)1), y = expanded ? t0 : 0;
+        if (!expanded && lane < nbox) {
+          const int r = t0 + lane * a.box, lp = r / p.page_size;
+          if (r < g.end && lp < p.max_pages_per_seq) {
+            const int x = p.block_table[(int64_t)g.b * p.max_pages_per_seq + lp];
+            if (x >= 0 && x < p.num_pages) page = x;
+          }
+          y = r & (p.page_size - 1);
+        }
+        for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
+          const int slot = it % NSLOT;
+          if (it >= NSLOT) ok = tc::mbar_wait_bounded(&sm->empty[slot], ((it / NSLOT) & 1) ^ 1, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          uint8_t* dst = kv_mem + slot * QT;
+          // value rows that no row of the unit sees may hold anything, and 0 x NaN would reach the output:
+          // such a tile lands on a barrier of this warp's, which clears the rows before handing it over
+          // (expanded rows from kv_len on are zeros already)
+          const bool clear = kv == 1 && (t0 < g.lo || (!expanded && t0 + TILE > g.end));
+          uint64_t* bar = clear ? &sm->vraw : &sm->full[slot];
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar, QT);
+          raw = clear;
+          if (!clear) armed = it + 1;
+          __syncwarp();
+          if (lane < nbox) {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d(dst + c * HB + lane * a.box * 128, kv ? &vmap : &kmap, c * 64, y, g.h, page, bar);
+          }
+          if (clear) {
+            ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->vraw, raw_phase, abort));
+            if (!ok) break;
+            raw_phase ^= 1u;
+            raw = false;
+            armed = it + 1;
+            for (int r = lane; r < TILE; r += 32) {
+              if (t0 + r >= g.lo && t0 + r < g.end) continue;
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  *reinterpret_cast<uint4*>(dst + c * HB + r * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm->full[slot]);
+          }
+        }
+      }
+    }
+    if (!ok) {  // gave up: no copy may still be on its way when the CTA ends
+      volatile int none = 0;
+      for (int x = max(0, armed - NSLOT); x < armed; ++x)
+        tc::mbar_wait_bounded(&sm->full[x % NSLOT], (x / NSLOT) & 1, &none, 50000000ull);
+      if (raw) tc::mbar_wait_bounded(&sm->vraw, raw_phase, &none, 50000000ull);
+    }
+  } else if (warp == W_MMA) {
+    if (lane == 0) {
+      // ---------------- MMAs
+      const uint32_t idesc_s = tc::idesc_bf16_f32(TILE, TILE), idesc_o = tc::idesc_bf16_f32_bmn(TILE, D);
+      const uint64_t qd = tc::sdesc_k_sw128(tc::smem_addr(q_mem)), kd = tc::sdesc_k_sw128(tc::smem_addr(kv_mem));
+      const uint64_t vd = tc::sdesc_mn_sw128(tc::smem_addr(kv_mem), HB, 1024);
+      int it = 0;
+      uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
+      bool ok = true;
+      auto wait_full = [&](int x) {
+        ok = ok && tc::mbar_wait_bounded(&sm->full[x % NSLOT], (x / NSLOT) & 1, abort);
+        tc::tc_fence_after();
+      };
+      auto scores = [&](int i, int x) {
+        const uint64_t kb = kd + (uint64_t)((x % NSLOT) * QT >> 4), qb = qd + (uint64_t)(i * QT >> 4);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            tc::mma_bf16(tmem + 128 * i, qb + (uint64_t)((c * HB + s * 32) >> 4), kb + (uint64_t)((c * HB + s * 32) >> 4),
+                         idesc_s, (c | s) != 0);
+        tc::mma_commit(&sm->sfull[i]);
+      };
+      auto values = [&](int i, int x, bool more) {
+        const uint64_t vb = vd + (uint64_t)((x % NSLOT) * QT >> 4);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          tc::mma_bf16_ts(tmem + COL_O + D * i, tmem + 128 * i + 8 * s, vb + (uint64_t)(s * 2048 >> 4), idesc_o,
+                          (more || s) ? 1u : 0u);
+      };
+      while (ok && walk.next(a, first, last, g)) {
+        const int cnt[2] = {g.count(0), g.count(1)}, n = g.k1 - g.k0;
+        for (int i = 0; i < 2; ++i)
+          if (cnt[i] && ok) {
+            ok = tc::mbar_wait_bounded(&sm->qfull[i], qph[i], abort);
+            qph[i] ^= 1u;
+          }
+        wait_full(it);
+        if (!ok) break;
+        for (int i = 0; i < 2; ++i)
+          if (cnt[i]) scores(i, it);
+        tc::mma_commit(&sm->empty[it % NSLOT]);
+        for (int k = 0; k < n && ok; ++k, it += 2) {
+          wait_full(it + 1);
+          bool next_k = false;
+          for (int i = 0; i < 2 && ok; ++i) {
+            if (k < cnt[i]) {
+              ok = tc::mbar_wait_bounded(&sm->pfull[i], pph[i], abort);
+              pph[i] ^= 1u;
+              if (!ok) break;
+              tc::tc_fence_after();
+              values(i, it + 1, k > 0);
+              if (k == cnt[i] - 1) tc::mma_commit(&sm->odone[i]);
+            }
+            if (k + 1 < n) {
+              if (!next_k) wait_full(it + 2);
+              next_k = true;
+              if (ok && k + 1 < cnt[i]) scores(i, it + 2);
+            }
+          }
+          if (!ok) break;
+          tc::mma_commit(&sm->empty[(it + 1) % NSLOT]);
+          if (next_k) tc::mma_commit(&sm->empty[(it + 2) % NSLOT]);
+        }
+      }
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    // ---------------- softmax: warpgroup i owns row tile i, a thread a row
+    const int i = warp >> 2, R = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t t_s = lanes + 128 * i, t_o = lanes + COL_O + D * i;
+    const int group = p.q_heads / p.kv_heads;
+    const bool plain = p.softcap == 0.f && p.slopes == nullptr && p.softmax_scale > 0.f;
+    const float cl = p.softmax_scale * LOG2E;
+    const float rcap2 = p.softcap > 0.f ? 2.f * LOG2E / p.softcap : 0.f;
+    uint32_t sph = 0, oph = 0;
+    bool ok = true;
+    while (ok && walk.next(a, first, last, g)) {
+      const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
+      const int64_t r = (int64_t)g.tile * UROWS + i * TILE + R;
+      const bool live = r < (int64_t)s.n * group;
+      const int tok = (int)(r / group), head = g.h * group + (int)(r % group), pos = s.kv - s.n + tok;
+      int2 vis = make_int2(0, 0);
+      float slope = 0.f;
+      if (live) {
+        vis = visible_rows(p, g.b, s.t0 + tok, pos, s.kv);
+        if (p.slopes) slope = p.slopes[head] * LOG2E;
+      }
+      const int cnt = g.count(i);
+      float m = -INFINITY, l = 0.f;
+      if (cnt) {
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                          (int64_t)(s.t0 + tok) * p.q_token_stride +
+                                                          (int64_t)head * p.q_head_stride);
+        uint8_t* dst = q_mem + i * QT + R * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * HB + (((c & 7) ^ (R & 7)) << 4)) = live ? src[c] : make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm->qfull[i]);
+      }
+      for (int k = 0; k < cnt; ++k) {
+        ok = tc::mbar_wait_bounded(&sm->sfull[i], sph, abort);
+        sph ^= 1u;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc::tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::tmem_ld32_nowait(t_s + 32 * c, x + 32 * c);
+        tc::tmem_wait_ld_regs<128>(x);
+        const int t0 = g.start + (g.k0 + k) * TILE;
+        float mul = cl;
+        if (!plain) {  // logits in log2 units
+          mul = 1.f;
+          const float far = (float)(pos - t0);
+#pragma unroll
+          for (int c = 0; c < 128; ++c) {
+            float z = __uint_as_float(x[c]) * p.softmax_scale;
+            if (p.softcap > 0.f) z = cap_logit(z, p.softcap, rcap2);
+            z = z * LOG2E - slope * fabsf(far - (float)c);
+            x[c] = __float_as_uint(z);
+          }
+        }
+        const bool inside = !live || (t0 >= vis.x && t0 + TILE <= vis.y);
+        if (!__all_sync(0xffffffffu, inside && !g.bad)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (t0 + c < vis.x || t0 + c >= vis.y) x[c] = __float_as_uint(-INFINITY);
+          if (g.bad) {
+            for (int c0 = 0; c0 < 128; c0 += 16) {
+              const int lp = (t0 + c0) / p.page_size;
+              const int page = t0 + c0 < g.end && lp < p.max_pages_per_seq
+                                   ? p.block_table[(int64_t)g.b * p.max_pages_per_seq + lp] : -1;
+              const bool gone = page < 0 || page >= p.num_pages;
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                if (gone && (c & ~15) == c0) x[c] = __float_as_uint(-INFINITY);
+            }
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; ++c) top = fmaxf(top, __uint_as_float(x[c]));
+        top *= mul;
+        const bool move = top > m + LAZY;
+        if (__any_sync(0xffffffffu, move)) {
+          const float mn = move ? top : m;
+          const float f = m == -INFINITY ? 0.f : tc::ex2_approx(m - mn);
+          m = mn;
+          l *= f;
+          if (k > 0) {  // (the scores' commit also covers the product of the tile before)
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tc::tmem_ld32_nowait(t_o + c, o);
+              tc::tmem_wait_ld_regs<32>(o);
+#pragma unroll
+              for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(__uint_as_float(o[d]) * f);
+              tc::tmem_st32(t_o + c, o);
+            }
+          }
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int d = 0; d < 64; d += 2) {
+            const float e0 = tc::ex2_approx(fmaf(__uint_as_float(x[c + d]), mul, -mm));
+            const float e1 = tc::ex2_approx(fmaf(__uint_as_float(x[c + d + 1]), mul, -mm));
+            l0 += e0;
+            l1 += e1;
+            pk[d / 2] = float2_to_bf16x2_bits(e0, e1);
+          }
+          tc::tmem_st32(t_s + c / 2, pk);
+        }
+        l += l0 + l1;
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm->pfull[i]);
+      }
+      if (!ok) break;
+      if (cnt) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->odone[i], oph, abort));
+        oph ^= 1u;
+        if (!ok) break;
+        tc::tc_fence_after();
+      }
+      const int64_t row = (int64_t)(s.t0 + tok) * p.q_heads + head;
+      const int slot = 2 * blockIdx.x + (g.u0 <= first ? 0 : 1);
+      const int64_t prow = (int64_t)slot * UROWS + i * TILE + R;
+      float f = 1.f;
+      if (g.whole) {
+        if (live) f = finish_scale(p, row, head, m, l, m, true);
+      } else {
+        a.ml_part[prow] = make_float2(m, l);
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (cnt) {
+          tc::tmem_ld32_nowait(t_o + c, o);
+          tc::tmem_wait_ld_regs<32>(o);
+        }
+#pragma unroll
+        for (int d = 0; d < 32; d += 4) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (cnt && m > -INFINITY)  // (a row that saw nothing: what O holds does not matter)
+            v = make_float4(__uint_as_float(o[d]) * f, __uint_as_float(o[d + 1]) * f, __uint_as_float(o[d + 2]) * f,
+                            __uint_as_float(o[d + 3]) * f);
+          if (!g.whole) reinterpret_cast<float4*>(a.o_part)[prow * (D / 4) + (c + d) / 4] = v;
+          else if (live) store4<D>(p, row, (c + d) / 4, v);
+        }
+      }
+      tc::tc_fence_before();
+      if (tid == 0 && !g.whole && g.k0 == 0)  // the unit's first piece: it goes on up to the CTA of its last tile
+        a.cut[blockIdx.x] = make_int4(g.b * a.tps + g.tile, g.h, (int)((g.u0 + g.w - 1) / sm->per), g.u0 <= first ? 0 : 1);
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && sm->abort) atomicOr(&g_flags_gp, FLAG_TIMEOUT);
+  if (warp == W_MMA) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// The units that a border between CTAs cuts: CTA (c, y) joins rows 32 y .. 32 y + 31 of the one that begins in
+// CTA c, a warp a row.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(Args a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const dsv4_gqa_attention_params& p = a.p;
+  const int4 cut = a.cut[blockIdx.x];
+  if (cut.z < 0) return;
+  const int b = cut.x / a.tps, tile = cut.x % a.tps, group = p.q_heads / p.kv_heads, lane = threadIdx.x & 31;
+  const Seq s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.max_kv_len);
+  const int parts = cut.z - (int)blockIdx.x + 1;
+  constexpr int E = D / 32;
+  for (int x = threadIdx.x >> 5; x < 32; x += 8) {
+    const int rr = blockIdx.y * 32 + x;
+    const int64_t r = (int64_t)tile * UROWS + rr;
+    if (r >= (int64_t)s.n * group) return;
+    auto place = [&](int i) { return ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? cut.w : 0)) * UROWS + rr; };
+    float m = -INFINITY, l = 0.f, acc[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) acc[k] = 0.f;
+    for (int i = 0; i < parts; ++i) m = fmaxf(m, a.ml_part[place(i)].x);
+    for (int i = 0; i < parts; ++i) {
+      const int64_t at = place(i);
+      const float2 ml = a.ml_part[at];
+      if (ml.x == -INFINITY) continue;
+      const float f = tc::ex2_approx(ml.x - m);
+      l += ml.y * f;
+      const float2* src = reinterpret_cast<const float2*>(a.o_part + at * D + lane * E);
+#pragma unroll
+      for (int k = 0; k < E; k += 2) {
+        const float2 v = src[k / 2];
+        acc[k] = fmaf(v.x, f, acc[k]);
+        acc[k + 1] = fmaf(v.y, f, acc[k + 1]);
+      }
+    }
+    const int head = cut.y * group + (int)(r % group);
+    const int64_t row = (int64_t)(s.t0 + (int)(r / group)) * p.q_heads + head;
+    const float f = finish_scale(p, row, head, m, l, m, lane == 0);
+#pragma unroll
+    for (int k = 0; k < E; k += 2) {
+      if (p.out_dtype == DSV4_F32)
+        reinterpret_cast<float2*>(p.out)[(row * D + lane * E + k) / 2] = make_float2(acc[k] * f, acc[k + 1] * f);
+      else
+        reinterpret_cast<uint32_t*>(p.out)[(row * D + lane * E + k) / 2] = float2_to_bf16x2_bits(acc[k] * f, acc[k + 1] * f);
+    }
+  }
+}
+
+struct Plan {
+  int tps, G, even, kv_pad;
+  size_t unit, part, ml, cut, k, v, total;
+};
+
+static Plan plan(const dsv4_gqa_attention_params& p) {
+  Plan L;
+  const int64_t max_n = p.max_q_len < p.T ? p.max_q_len : p.T;
+  L.tps = (int)((max_n * (p.q_heads / p.kv_heads) + UROWS - 1) / UROWS);
+  const int64_t units = (int64_t)p.B * L.tps;
+  L.even = units <= MAX_UNITS;
+  L.G = num_sms();
+  const size_t slots = L.even ? 2 * (size_t)L.G : 0;
+  L.kv_pad = p.cache_dtype == DSV4_E4M3_PAGE ? (p.max_kv_len + TILE - 1) / TILE * TILE : 0;
+  const size_t rows = (size_t)p.B * p.kv_heads * L.kv_pad * p.head_dim * 2;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at = align_up(at + bytes, 256);
+    return x;
+  };
+  L.unit = take((size_t)units * 16);
+  L.part = take(slots * UROWS * p.head_dim * 4);
+  L.ml = take(slots * UROWS * 8);
+  L.cut = take((size_t)L.G * 16);
+  L.k = take(rows);
+  L.v = take(rows);
+  L.total = at;
+  return L;
+}
+
+template <int D>
+static cudaError_t launch(const dsv4_gqa_attention_params& p, cudaStream_t s) {
+  const Plan L = plan(p);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(p.workspace);
+  Args a;
+  a.p = p;
+  a.unit = reinterpret_cast<int4*>(ws + L.unit);
+  a.o_part = reinterpret_cast<float*>(ws + L.part);
+  a.ml_part = reinterpret_cast<float2*>(ws + L.ml);
+  a.cut = reinterpret_cast<int4*>(ws + L.cut);
+  const bool e4m3 = p.cache_dtype == DSV4_E4M3_PAGE && L.kv_pad > 0;
+  a.bf_k = e4m3 ? reinterpret_cast<uint16_t*>(ws + L.k) : nullptr;
+  a.bf_v = e4m3 ? reinterpret_cast<uint16_t*>(ws + L.v) : nullptr;
+  a.kv_pad = L.kv_pad;
+  a.tps = L.tps;
+  a.G = L.G;
+  a.even = L.even;
+  a.box = e4m3 || p.page_size > TILE ? TILE : p.page_size;
+  const int64_t units = (int64_t)p.B * L.tps;
+  const int64_t plan_ctas = (units + PREP_THREADS / 32 - 1) / (PREP_THREADS / 32);
+  const int64_t expand = e4m3 ? (int64_t)p.B * p.kv_heads * (L.kv_pad / EXPAND_ROWS) : 0;
+  const int64_t ctas = L.even ? L.G : units * p.kv_heads;
+  if (plan_ctas + expand > 0x7FFFFFFF || ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  CUtensorMap kmap, vmap;
+  cudaError_t e;
+  if (e4m3) {
+    const int64_t row = D * 2, head = row * L.kv_pad, seq = head * p.kv_heads;
+    e = make_tmap_4d_bf16(&kmap, a.bf_k, D, L.kv_pad, p.kv_heads, p.B, row, head, seq, 64, TILE);
+    if (e == cudaSuccess) e = make_tmap_4d_bf16(&vmap, a.bf_v, D, L.kv_pad, p.kv_heads, p.B, row, head, seq, 64, TILE);
+  } else {
+    const uint64_t pages = p.num_pages > 0 ? p.num_pages : 1;
+    e = make_tmap_4d_bf16(&kmap, p.k_cache, D, p.page_size, p.kv_heads, pages, 2 * p.k_row_stride, 2 * p.k_cache_head_stride,
+                          2 * p.k_page_stride, 64, a.box);
+    if (e == cudaSuccess)
+      e = make_tmap_4d_bf16(&vmap, p.v_cache, D, p.page_size, p.kv_heads, pages, 2 * p.v_row_stride,
+                            2 * p.v_cache_head_stride, 2 * p.v_page_stride, 64, a.box);
+  }
+  if (e != cudaSuccess) return e;
+  const int smem = (2 + NSLOT) * TILE * D * 2 + (int)sizeof(Smem) + 1024;
+  e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(prefill_kernel<D>), smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(prepare_kernel<D>, dim3((unsigned)(plan_ctas + expand)), dim3(PREP_THREADS), 0, s, true, a, (int)plan_ctas);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(prefill_kernel<D>, dim3((unsigned)ctas), dim3(THREADS), smem, s, true, kmap, vmap, a);
+  if (e != cudaSuccess || !L.even) return e;
+  return launch_pdl(join_kernel<D>, dim3(L.G, UROWS / 32), dim3(256), 0, s, true, a);
+}
+
+}  // namespace pre
+
+size_t prefill_workspace(const dsv4_gqa_attention_params& p) { return pre::plan(p).total; }
+
+cudaError_t launch_prefill(const dsv4_gqa_attention_params& p, cudaStream_t s) {
+  return p.head_dim == 128 ? pre::launch<128>(p, s) : pre::launch<64>(p, s);
+}
+
+}  // namespace gqa
+
+cudaError_t read_flags_gqa_prefill(uint32_t* f) {
+  unsigned int v = 0, z = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_flags_gp, sizeof(v));
+  if (e != cudaSuccess) return e;
+  *f |= v;
+  return cudaMemcpyToSymbol(g_flags_gp, &z, sizeof(z));
+}
+
+}  // namespace dsv4
