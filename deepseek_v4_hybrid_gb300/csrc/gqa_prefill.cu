@@ -32,9 +32,7 @@ namespace gqa {
 namespace pre {
 
 constexpr int TILE = 128, UROWS = 256;
-constexpr int SOFTMAX_WARPS = 8, W_LOAD = 8, W_MMA = 9, THREADS = 384;
-// Registers a thread: 384 x 168 at launch = 256 x 216 for the softmax + 128 x 72 for the other warpgroup.
-constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;
+constexpr int SOFTMAX_WARPS = 8, W_LOAD = 8, W_MMA = 9, THREADS = 320;
 constexpr int NSLOT = 4;
 constexpr int UNIT_COST = 3;
 constexpr int MAX_UNITS = 8192;   // units of the evenly cut list; above, a CTA takes a whole unit
@@ -176,8 +174,31 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Two fp32 values in one register pair: one instruction does both lanes.
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) { return pack2u(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 struct Smem {
-  uint64_t full[NSLOT], empty[NSLOT], vraw, qfull[2], sfull[2], pfull[2], odone[2];
+  uint64_t full[NSLOT], empty[NSLOT], vraw, qfull[2], sfull[2], phalf[2], pfull[2], odone[2];
   int64_t first, last, u0;
   int64_t wsum[THREADS / 32];
   int64_t per;
@@ -261,6 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm->qfull[i], 4);
       tc::mbar_init(&sm->sfull[i], 1);
+      tc::mbar_init(&sm->phalf[i], 4);
       tc::mbar_init(&sm->pfull[i], 4);
       tc::mbar_init(&sm->odone[i], 1);
     }
@@ -353,8 +375,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   Walk walk{sm->b, sm->h, sm->tile, sm->u0};
   Segment g;
 
-  if (warp >= SOFTMAX_WARPS) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
   if (warp == W_LOAD) {
     // ---------------- TMA loads
     int it = 0, armed = 0;  // tiles handed out, tiles armed on their own barrier
@@ -450,12 +470,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                          idesc_s, (c | s) != 0);
         tc::mma_commit(&sm->sfull[i]);
       };
-      auto values = [&](int i, int x, bool more) {
+      auto values = [&](int i, int x, int half, bool more) {
         const uint64_t vb = vd + (uint64_t)((x % NSLOT) * QT >> 4);
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
+        for (int y = 0; y < 4; ++y) {
+          const int s = 4 * half + y;
           tc::mma_bf16_ts(tmem + COL_O + D * i, tmem + 128 * i + 8 * s, vb + (uint64_t)(s * 2048 >> 4), idesc_o,
                           (more || s) ? 1u : 0u);
+        }
       };
       while (ok && walk.next(a, first, last, g)) {
         const int cnt[2] = {g.count(0), g.count(1)}, n = g.k1 - g.k0;
@@ -474,11 +496,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           bool next_k = false;
           for (int i = 0; i < 2 && ok; ++i) {
             if (k < cnt[i]) {
+              ok = tc::mbar_wait_bounded(&sm->phalf[i], pph[i], abort);
+              if (!ok) break;
+              tc::tc_fence_after();
+              values(i, it + 1, 0, k > 0);
               ok = tc::mbar_wait_bounded(&sm->pfull[i], pph[i], abort);
               pph[i] ^= 1u;
               if (!ok) break;
               tc::tc_fence_after();
-              values(i, it + 1, k > 0);
+              values(i, it + 1, 1, true);
               if (k == cnt[i] - 1) tc::mma_commit(&sm->odone[i]);
             }
             if (k + 1 < n) {
@@ -493,9 +519,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     // ---------------- softmax: warpgroup i owns row tile i, a thread a row
     const int i = warp >> 2, R = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -537,44 +561,57 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc::tc_fence_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_ld32_nowait(t_s + 32 * c, x + 32 * c);
-        tc::tmem_wait_ld_regs<128>(x);
         const int t0 = g.start + (g.k0 + k) * TILE;
-        float mul = cl;
-        if (!plain) {  // logits in log2 units
-          mul = 1.f;
-          const float far = (float)(pos - t0);
-#pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            float z = __uint_as_float(x[c]) * p.softmax_scale;
-            if (p.softcap > 0.f) z = cap_logit(z, p.softcap, rcap2);
-            z = z * LOG2E - slope * fabsf(far - (float)c);
-            x[c] = __float_as_uint(z);
-          }
-        }
         const bool inside = !live || (t0 >= vis.x && t0 + TILE <= vis.y);
-        if (!__all_sync(0xffffffffu, inside && !g.bad)) {
+        // The row's maximum: S is read from tensor memory a first time, 32 columns ahead of the work on 32.
+        // Where something has to be done to the logits, they go back in log2 units and the maximum is theirs.
+        uint32_t xa[32], xb[32];
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mul = cl;
+        if (plain && __all_sync(0xffffffffu, inside && !g.bad)) {
+          tc::tmem_ld32_nowait(t_s, xa);
+          tc::tmem_wait_ld_regs<32>(xa);
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (t0 + c < vis.x || t0 + c >= vis.y) x[c] = __float_as_uint(-INFINITY);
-          if (g.bad) {
-            for (int c0 = 0; c0 < 128; c0 += 16) {
-              const int lp = (t0 + c0) / p.page_size;
-              const int page = t0 + c0 < g.end && lp < p.max_pages_per_seq
-                                   ? p.block_table[(int64_t)g.b * p.max_pages_per_seq + lp] : -1;
-              const bool gone = page < 0 || page >= p.num_pages;
+          for (int c = 0; c < 4; ++c) {
+            uint32_t* cur = c & 1 ? xb : xa;
+            uint32_t* nxt = c & 1 ? xa : xb;
+            if (c < 3) tc::tmem_ld32_nowait(t_s + 32 * (c + 1), nxt);
 #pragma unroll
-              for (int c = 0; c < 128; ++c)
-                if (gone && (c & ~15) == c0) x[c] = __float_as_uint(-INFINITY);
-            }
+            for (int d = 0; d < 32; ++d) tops[d & 3] = fmaxf(tops[d & 3], __uint_as_float(cur[d]));
+            if (c < 3) tc::tmem_wait_ld_regs<32>(nxt);
           }
-        }
-        float top = -INFINITY;
+        } else {
+          mul = 1.f;
+#pragma unroll 1
+          for (int c = 0; c < TILE; c += 32) {
+            tc::tmem_ld32_nowait(t_s + c, xa);
+            uint32_t gone = 0;  // bit y: the 16 rows from t0 + c + 16 y on lie in no page
+            if (g.bad) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c) top = fmaxf(top, __uint_as_float(x[c]));
-        top *= mul;
+              for (int y = 0; y < 2; ++y) {
+                const int j = t0 + c + 16 * y, lp = j / p.page_size;
+                const int page = j < g.end && lp < p.max_pages_per_seq
+                                     ? p.block_table[(int64_t)g.b * p.max_pages_per_seq + lp] : -1;
+                if (page < 0 || page >= p.num_pages) gone |= 1u << y;
+              }
+            }
+            const float far = (float)(pos - t0 - c);
+            const int lo = vis.x - t0 - c, hi = vis.y - t0 - c;
+            tc::tmem_wait_ld_regs<32>(xa);
+#pragma unroll
+            for (int d = 0; d < 32; ++d) {
+              float z = __uint_as_float(xa[d]) * p.softmax_scale;
+              if (p.softcap > 0.f) z = cap_logit(z, p.softcap, rcap2);
+              z = z * LOG2E - slope * fabsf(far - (float)d);
+              if (d < lo || d >= hi || ((gone >> (d >> 4)) & 1u)) z = -INFINITY;
+              tops[d & 3] = fmaxf(tops[d & 3], z);
+              xa[d] = __float_as_uint(z);
+            }
+            tc::tmem_st32(t_s + c, xa);
+          }
+          tc::tmem_wait_st();
+        }
+        const float top = mul * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         const bool move = top > m + LAZY;
         if (__any_sync(0xffffffffu, move)) {
           const float mn = move ? top : m;
@@ -593,22 +630,35 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         }
+        tc::tmem_ld32_nowait(t_s, xa);
         const float mm = m == -INFINITY ? 0.f : m;
-        float l0 = 0.f, l1 = 0.f;
+        const uint64_t mul2 = pack2(mul, mul), ref2 = pack2(-mm, -mm);
+        uint64_t sum2[2] = {0, 0};
+        tc::tmem_wait_ld_regs<32>(xa);
 #pragma unroll
-        for (int c = 0; c < 128; c += 64) {
-          uint32_t pk[32];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t* cur = c & 1 ? xb : xa;
+          uint32_t* nxt = c & 1 ? xa : xb;
+          if (c < 3) tc::tmem_ld32_nowait(t_s + 32 * (c + 1), nxt);
+          uint32_t pk[16];
 #pragma unroll
-          for (int d = 0; d < 64; d += 2) {
-            const float e0 = tc::ex2_approx(fmaf(__uint_as_float(x[c + d]), mul, -mm));
-            const float e1 = tc::ex2_approx(fmaf(__uint_as_float(x[c + d + 1]), mul, -mm));
-            l0 += e0;
-            l1 += e1;
+          for (int d = 0; d < 32; d += 2) {
+            const float2 z = unpack2(fma2(pack2u(cur[d], cur[d + 1]), mul2, ref2));
+            const float e0 = tc::ex2_approx(z.x), e1 = tc::ex2_approx(z.y);
+            sum2[(d >> 1) & 1] = add2(sum2[(d >> 1) & 1], pack2(e0, e1));
             pk[d / 2] = float2_to_bf16x2_bits(e0, e1);
           }
-          tc::tmem_st32(t_s + c / 2, pk);
+          if (c < 3) tc::tmem_wait_ld_regs<32>(nxt);  // (P lies over columns that have been read)
+          tc::tmem_st16(t_s + 16 * c, pk);
+          if (c == 1) {  // the product can start on the first half
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm->phalf[i]);
+          }
         }
-        l += l0 + l1;
+        const float2 sums = unpack2(add2(sum2[0], sum2[1]));
+        l += sums.x + sums.y;
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
