@@ -207,6 +207,16 @@ struct Smem {
   int abort;
 };
 
+// One lane of a converged warp.  The MMA warp runs its loop with all lanes and issues under this, so that
+// descriptors and barrier addresses stay in uniform registers: issued from a lane == 0 branch, every MMA
+// first moved its operands there and 32 of them took 3740 cycles instead of 2048.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 struct Segment {
   int b, h, tile;      // unit `tile` of sequence b, kv head h
   int lo, end;         // rows seen by the unit: lo .. end - 1
@@ -448,75 +458,83 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (raw) tc::mbar_wait_bounded(&sm->vraw, raw_phase, &none, 50000000ull);
     }
   } else if (warp == W_MMA) {
-    if (lane == 0) {
-      // ---------------- MMAs
-      const uint32_t idesc_s = tc::idesc_bf16_f32(TILE, TILE), idesc_o = tc::idesc_bf16_f32_bmn(TILE, D);
-      const uint64_t qd = tc::sdesc_k_sw128(tc::smem_addr(q_mem)), kd = tc::sdesc_k_sw128(tc::smem_addr(kv_mem));
-      const uint64_t vd = tc::sdesc_mn_sw128(tc::smem_addr(kv_mem), HB, 1024);
-      int it = 0;
-      uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
-      bool ok = true;
-      auto wait_full = [&](int x) {
-        ok = ok && tc::mbar_wait_bounded(&sm->full[x % NSLOT], (x / NSLOT) & 1, abort);
-        tc::tc_fence_after();
-      };
-      auto scores = [&](int i, int x) {
-        const uint64_t kb = kd + (uint64_t)((x % NSLOT) * QT >> 4), qb = qd + (uint64_t)(i * QT >> 4);
+    // ---------------- MMAs
+    const uint32_t idesc_s = tc::idesc_bf16_f32(TILE, TILE), idesc_o = tc::idesc_bf16_f32_bmn(TILE, D);
+    const uint32_t tm = (uint32_t)uniform((int)tmem);
+    const uint64_t qd = tc::sdesc_k_sw128(tc::smem_addr(q_mem)), kd = tc::sdesc_k_sw128(tc::smem_addr(kv_mem));
+    const uint64_t vd = tc::sdesc_mn_sw128(tc::smem_addr(kv_mem), HB, 1024);
+    int it = 0;
+    uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_bounded(bar, phase, abort));
+      tc::tc_fence_after();
+    };
+    auto wait_full = [&](int x) { wait(&sm->full[x % NSLOT], (x / NSLOT) & 1); };
+    auto scores = [&](int i, int x) {
+      const uint64_t kb = kd + (uint64_t)((x % NSLOT) * QT >> 4), qb = qd + (uint64_t)(i * QT >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            tc::mma_bf16(tmem + 128 * i, qb + (uint64_t)((c * HB + s * 32) >> 4), kb + (uint64_t)((c * HB + s * 32) >> 4),
+            tc::mma_bf16(tm + 128 * i, qb + (uint64_t)((c * HB + s * 32) >> 4), kb + (uint64_t)((c * HB + s * 32) >> 4),
                          idesc_s, (c | s) != 0);
         tc::mma_commit(&sm->sfull[i]);
-      };
-      auto values = [&](int i, int x, int half, bool more) {
-        const uint64_t vb = vd + (uint64_t)((x % NSLOT) * QT >> 4);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int i, int x, int half, bool more, bool done) {
+      const uint64_t vb = vd + (uint64_t)((x % NSLOT) * QT >> 4);
+      if (elect_one()) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int s = 4 * half + y;
-          tc::mma_bf16_ts(tmem + COL_O + D * i, tmem + 128 * i + 8 * s, vb + (uint64_t)(s * 2048 >> 4), idesc_o,
-                          (more || s) ? 1u : 0u);
+        for (int y = 0; y < 4; ++y)
+          tc::mma_bf16_ts(tm + COL_O + D * i, tm + 128 * i + 8 * (4 * half + y),
+                          vb + (uint64_t)((4 * half + y) * 2048 >> 4), idesc_o, (more || y) ? 1u : 0u);
+        if (done) tc::mma_commit(&sm->odone[i]);
+      }
+      __syncwarp();
+    };
+    auto release = [&](int x) {
+      if (elect_one()) tc::mma_commit(&sm->empty[x % NSLOT]);
+      __syncwarp();
+    };
+    while (ok && walk.next(a, first, last, g)) {
+      const int cnt[2] = {uniform(g.count(0)), uniform(g.count(1))}, n = uniform(g.k1 - g.k0);
+      it = uniform(it);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (cnt[i] && ok) {
+          wait(&sm->qfull[i], qph[i]);
+          qph[i] ^= 1u;
         }
-      };
-      while (ok && walk.next(a, first, last, g)) {
-        const int cnt[2] = {g.count(0), g.count(1)}, n = g.k1 - g.k0;
-        for (int i = 0; i < 2; ++i)
-          if (cnt[i] && ok) {
-            ok = tc::mbar_wait_bounded(&sm->qfull[i], qph[i], abort);
-            qph[i] ^= 1u;
+      wait_full(it);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (cnt[i]) scores(i, it);
+      release(it);
+      for (int k = 0; k < n && ok; ++k, it += 2) {
+        wait_full(it + 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (ok && k < cnt[i]) {
+            wait(&sm->phalf[i], pph[i]);
+            if (!ok) break;
+            values(i, it + 1, 0, k > 0, false);
+            wait(&sm->pfull[i], pph[i]);
+            if (!ok) break;
+            values(i, it + 1, 1, true, k == cnt[i] - 1);
+            pph[i] ^= 1u;
           }
-        wait_full(it);
+          if (ok && k + 1 < n) {
+            if (i == 0) wait_full(it + 2);
+            if (ok && k + 1 < cnt[i]) scores(i, it + 2);
+          }
+        }
         if (!ok) break;
-        for (int i = 0; i < 2; ++i)
-          if (cnt[i]) scores(i, it);
-        tc::mma_commit(&sm->empty[it % NSLOT]);
-        for (int k = 0; k < n && ok; ++k, it += 2) {
-          wait_full(it + 1);
-          bool next_k = false;
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (k < cnt[i]) {
-              ok = tc::mbar_wait_bounded(&sm->phalf[i], pph[i], abort);
-              if (!ok) break;
-              tc::tc_fence_after();
-              values(i, it + 1, 0, k > 0);
-              ok = tc::mbar_wait_bounded(&sm->pfull[i], pph[i], abort);
-              pph[i] ^= 1u;
-              if (!ok) break;
-              tc::tc_fence_after();
-              values(i, it + 1, 1, true);
-              if (k == cnt[i] - 1) tc::mma_commit(&sm->odone[i]);
-            }
-            if (k + 1 < n) {
-              if (!next_k) wait_full(it + 2);
-              next_k = true;
-              if (ok && k + 1 < cnt[i]) scores(i, it + 2);
-            }
-          }
-          if (!ok) break;
-          tc::mma_commit(&sm->empty[(it + 1) % NSLOT]);
-          if (next_k) tc::mma_commit(&sm->empty[(it + 2) % NSLOT]);
-        }
+        release(it + 1);
+        if (k + 1 < n) release(it + 2);
       }
     }
   } else {
