@@ -8,7 +8,7 @@
 //   Warps 0-3 and 4-7 (a warpgroup a tile): a thread owns a row: reads S from TMEM, masks, caps, takes the online
 //   softmax in log2 units (O is rescaled only when a row's maximum grows by more than 2^8) and writes P back;
 //   loads its tile's queries at a unit's start and writes the output at its end.
-//   Warp 8 loads key and value tiles by TMA (one box a page) into a ring of four tiles.
+//   Warp 8 loads key and value tiles by TMA (one box a page) into a ring of five tiles.
 //   Lane 0 of warp 9 issues the MMAs: P_0 V, S_0 of the next tile, P_1 V, S_1 of the next tile, so that the
 //   tensor cores work on one tile while the other's softmax runs.
 // Bound by the tensor cores and, at head_dim 64 or with capped scores, by the exponentials.
@@ -33,7 +33,7 @@ namespace pre {
 
 constexpr int TILE = 128, UROWS = 256;
 constexpr int SOFTMAX_WARPS = 8, W_LOAD = 8, W_MMA = 9, THREADS = 320;
-constexpr int NSLOT = 4;
+constexpr int NSLOT = 5;
 constexpr int UNIT_COST = 3;
 constexpr int MAX_UNITS = 8192;   // units of the evenly cut list; above, a CTA takes a whole unit
 constexpr float LAZY = 8.f;
@@ -502,17 +502,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     while (ok && walk.next(a, first, last, g)) {
       const int cnt[2] = {uniform(g.count(0)), uniform(g.count(1))}, n = uniform(g.k1 - g.k0);
       it = uniform(it);
+      wait_full(it);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (cnt[i] && ok) {
           wait(&sm->qfull[i], qph[i]);
           qph[i] ^= 1u;
+          if (ok) scores(i, it);
         }
-      wait_full(it);
       if (!ok) break;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (cnt[i]) scores(i, it);
       release(it);
       for (int k = 0; k < n && ok; ++k, it += 2) {
         wait_full(it + 1);
@@ -547,12 +545,37 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float cl = p.softmax_scale * LOG2E;
     const float rcap2 = p.softcap > 0.f ? 2.f * LOG2E / p.softcap : 0.f;
     uint32_t sph = 0, oph = 0;
-    bool ok = true;
-    while (ok && walk.next(a, first, last, g)) {
+    // Queries of a segment's row tile into shared memory, each warp its own 32 rows (whole rows by consecutive
+    // lanes), then handed to the MMA warp.  The tile's scores before must have been read.
+    auto load_queries = [&](const Segment& g) {
+      constexpr int CPR = D / 8, RPI = 32 / CPR;
       const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
-      const int64_t r = (int64_t)g.tile * UROWS + i * TILE + R;
-      const bool live = r < (int64_t)s.n * group;
-      const int tok = (int)(r / group), head = g.h * group + (int)(r % group), pos = s.kv - s.n + tok;
+      const int64_t base = (int64_t)g.tile * UROWS, rows = (int64_t)s.n * group - base;
+      const int tok0 = (int)(base / group), rem = (int)(base % group), ch = lane % CPR;
+      uint8_t* dst = q_mem + i * QT + (ch >> 3) * HB;
+#pragma unroll 4
+      for (int x = 0; x < 32 / RPI; ++x) {
+        const int Rr = (warp & 3) * 32 + x * RPI + lane / CPR, r = i * TILE + Rr;
+        const int tok = tok0 + (rem + r) / group, head = g.h * group + (rem + r) % group;
+        const bool in = r < rows;
+        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q);
+        if (in) src += (int64_t)(s.t0 + tok) * p.q_token_stride + (int64_t)head * p.q_head_stride + 8 * ch;
+        tc::cp_async16(dst + Rr * 128 + (((ch & 7) ^ (Rr & 7)) << 4), src, in ? 16u : 0u);
+      }
+      tc::cp_async_commit();
+      tc::cp_async_wait<0>();
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm->qfull[i]);
+    };
+    bool ok = true, have = walk.next(a, first, last, g);
+    if (have && g.count(i)) load_queries(g);
+    while (ok && have) {
+      const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
+      const int64_t base = (int64_t)g.tile * UROWS;
+      const int tok0 = (int)(base / group), rem = (int)(base % group), r = i * TILE + R;
+      const bool live = r < (int64_t)s.n * group - base;
+      const int tok = tok0 + (rem + r) / group, head = g.h * group + (rem + r) % group, pos = s.kv - s.n + tok;
       int2 vis = make_int2(0, 0);
       float slope = 0.f;
       if (live) {
@@ -561,18 +584,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       const int cnt = g.count(i);
       float m = -INFINITY, l = 0.f;
-      if (cnt) {
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                                          (int64_t)(s.t0 + tok) * p.q_token_stride +
-                                                          (int64_t)head * p.q_head_stride);
-        uint8_t* dst = q_mem + i * QT + R * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * HB + (((c & 7) ^ (R & 7)) << 4)) = live ? src[c] : make_uint4(0, 0, 0, 0);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm->qfull[i]);
-      }
       for (int k = 0; k < cnt; ++k) {
         ok = tc::mbar_wait_bounded(&sm->sfull[i], sph, abort);
         sph ^= 1u;
@@ -586,7 +597,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t xa[32], xb[32];
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         float mul = cl;
-        if (plain && __all_sync(0xffffffffu, inside && !g.bad)) {
+        const bool all = __all_sync(0xffffffffu, inside && !g.bad);
+        if (plain && all) {
           tc::tmem_ld32_nowait(t_s, xa);
           tc::tmem_wait_ld_regs<32>(xa);
 #pragma unroll
@@ -599,32 +611,44 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (c < 3) tc::tmem_wait_ld_regs<32>(nxt);
           }
         } else {
-          mul = 1.f;
+          if (!plain) mul = 1.f;
 #pragma unroll 1
           for (int c = 0; c < TILE; c += 32) {
             tc::tmem_ld32_nowait(t_s + c, xa);
-            uint32_t gone = 0;  // bit y: the 16 rows from t0 + c + 16 y on lie in no page
+            int lo = max(0, vis.x - t0 - c), hi = min(32, vis.y - t0 - c);
+            uint32_t see = 0;  // bit d: the row sees column c + d
+            if (hi > lo) see = (0xFFFFFFFFu >> (32 - (hi - lo))) << lo;
             if (g.bad) {
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const int j = t0 + c + 16 * y, lp = j / p.page_size;
                 const int page = j < g.end && lp < p.max_pages_per_seq
                                      ? p.block_table[(int64_t)g.b * p.max_pages_per_seq + lp] : -1;
-                if (page < 0 || page >= p.num_pages) gone |= 1u << y;
+                if (page < 0 || page >= p.num_pages) see &= ~(0xFFFFu << (16 * y));
               }
             }
-            const float far = (float)(pos - t0 - c);
-            const int lo = vis.x - t0 - c, hi = vis.y - t0 - c;
             tc::tmem_wait_ld_regs<32>(xa);
+            if (p.softcap > 0.f) {
 #pragma unroll
-            for (int d = 0; d < 32; ++d) {
-              float z = __uint_as_float(xa[d]) * p.softmax_scale;
-              if (p.softcap > 0.f) z = cap_logit(z, p.softcap, rcap2);
-              z = z * LOG2E - slope * fabsf(far - (float)d);
-              if (d < lo || d >= hi || ((gone >> (d >> 4)) & 1u)) z = -INFINITY;
-              tops[d & 3] = fmaxf(tops[d & 3], z);
-              xa[d] = __float_as_uint(z);
+              for (int d = 0; d < 32; ++d)
+                xa[d] = __float_as_uint(cap_logit(__uint_as_float(xa[d]) * p.softmax_scale, p.softcap, rcap2) * LOG2E);
+            } else if (!plain) {
+#pragma unroll
+              for (int d = 0; d < 32; ++d) xa[d] = __float_as_uint(__uint_as_float(xa[d]) * cl);
             }
+            if (p.slopes) {
+              const float far = (float)(pos - t0 - c);
+#pragma unroll
+              for (int d = 0; d < 32; ++d)
+                xa[d] = __float_as_uint(fmaf(-slope, fabsf(far - (float)d), __uint_as_float(xa[d])));
+            }
+            if (!all) {
+#pragma unroll
+              for (int d = 0; d < 32; ++d)
+                if (!((see >> d) & 1u)) xa[d] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int d = 0; d < 32; ++d) tops[d & 3] = fmaxf(tops[d & 3], __uint_as_float(xa[d]));
             tc::tmem_st32(t_s + c, xa);
           }
           tc::tmem_wait_st();
@@ -683,6 +707,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) tc::mbar_arrive(&sm->pfull[i]);
       }
       if (!ok) break;
+      Segment gn;
+      have = walk.next(a, first, last, gn);
+      if (have && gn.count(i)) load_queries(gn);  // its first scores run beside this segment's end
       if (cnt) {
         ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->odone[i], oph, abort));
         oph ^= 1u;
@@ -691,7 +718,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       const int64_t row = (int64_t)(s.t0 + tok) * p.q_heads + head;
       const int slot = 2 * blockIdx.x + (g.u0 <= first ? 0 : 1);
-      const int64_t prow = (int64_t)slot * UROWS + i * TILE + R;
+      const int64_t prow = (int64_t)slot * UROWS + r;
+      const bool some = cnt && m > -INFINITY;  // (a row that saw nothing: what O holds does not matter)
       float f = 1.f;
       if (g.whole) {
         if (live) f = finish_scale(p, row, head, m, l, m, true);
@@ -706,18 +734,29 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc::tmem_wait_ld_regs<32>(o);
         }
 #pragma unroll
-        for (int d = 0; d < 32; d += 4) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (cnt && m > -INFINITY)  // (a row that saw nothing: what O holds does not matter)
-            v = make_float4(__uint_as_float(o[d]) * f, __uint_as_float(o[d + 1]) * f, __uint_as_float(o[d + 2]) * f,
-                            __uint_as_float(o[d + 3]) * f);
-          if (!g.whole) reinterpret_cast<float4*>(a.o_part)[prow * (D / 4) + (c + d) / 4] = v;
-          else if (live) store4<D>(p, row, (c + d) / 4, v);
+        for (int d = 0; d < 32; ++d) o[d] = some ? __float_as_uint(__uint_as_float(o[d]) * f) : 0u;
+        if (!g.whole || p.out_dtype == DSV4_F32) {
+          float* dst = g.whole ? reinterpret_cast<float*>(p.out) + row * D : a.o_part + prow * D;
+          if (!g.whole || live) {
+#pragma unroll
+            for (int d = 0; d < 32; d += 4) *reinterpret_cast<uint4*>(dst + c + d) = make_uint4(o[d], o[d + 1], o[d + 2], o[d + 3]);
+          }
+        } else if (live) {
+          uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + row * D;
+#pragma unroll
+          for (int d = 0; d < 32; d += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              w[y] = float2_to_bf16x2_bits(__uint_as_float(o[d + 2 * y]), __uint_as_float(o[d + 2 * y + 1]));
+            *reinterpret_cast<uint4*>(dst + c + d) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
       }
       tc::tc_fence_before();
       if (tid == 0 && !g.whole && g.k0 == 0)  // the unit's first piece: it goes on up to the CTA of its last tile
         a.cut[blockIdx.x] = make_int4(g.b * a.tps + g.tile, g.h, (int)((g.u0 + g.w - 1) / sm->per), g.u0 <= first ? 0 : 1);
+      g = gn;
     }
   }
   tc::tc_fence_before();
