@@ -267,6 +267,7 @@ int check_gqa_attention(const dsv4_gqa_attention_params& p) {
   CHECK(st == DSV4_OK, st);
   CHECK(p.q_heads % p.kv_heads == 0, DSV4_ERR_INVALID);
   CHECK(p.max_kv_len >= 0 && p.max_kv_len <= (1 << 30) && p.window >= 0, DSV4_ERR_INVALID);
+  CHECK((int64_t)(p.max_q_len < p.T ? p.max_q_len : p.T) * (p.q_heads / p.kv_heads) <= (1 << 30), DSV4_ERR_UNSUPPORTED);
   CHECK(p.causal == 0 || p.causal == 1, DSV4_ERR_INVALID);
   CHECK(std::isfinite(p.softmax_scale) && std::isfinite(p.softcap) && p.softcap >= 0.f, DSV4_ERR_INVALID);
   CHECK(act_dtype(p.out_dtype), DSV4_ERR_UNSUPPORTED);

@@ -8,7 +8,7 @@
 //   Warps 0-3 and 4-7 (a warpgroup a tile): a thread owns a row: reads S from TMEM, masks, caps, takes the online
 //   softmax in log2 units (O is rescaled only when a row's maximum grows by more than 2^8) and writes P back;
 //   loads its tile's queries at a unit's start and writes the output at its end.
-//   Warp 8 loads key and value tiles by TMA (one box a page) into a ring of five tiles.
+//   Warp 8 loads key and value tiles by TMA (one box a page) into a ring of four tiles.
 //   Lane 0 of warp 9 issues the MMAs: P_0 V, S_0 of the next tile, P_1 V, S_1 of the next tile, so that the
 //   tensor cores work on one tile while the other's softmax runs.
 // Bound by the tensor cores and, at head_dim 64 or with capped scores, by the exponentials.
@@ -33,7 +33,7 @@ namespace pre {
 
 constexpr int TILE = 128, UROWS = 256;
 constexpr int SOFTMAX_WARPS = 8, W_LOAD = 8, W_MMA = 9, THREADS = 320;
-constexpr int NSLOT = 5;
+constexpr int NSLOT = 4;
 constexpr int UNIT_COST = 3;
 constexpr int MAX_UNITS = 8192;   // units of the evenly cut list; above, a CTA takes a whole unit
 constexpr float LAZY = 8.f;
@@ -43,7 +43,7 @@ struct Args {
   dsv4_gqa_attention_params p;
   int4* unit;        // [B * tps]: first row seen, end of the rows seen, key tiles of tile 0 and 1 (bit 30 of the
                      // latter: some page is out of range)
-  float* o_part;     // [2 G][256][D]
+  float4* o_part;    // [2 G][8 groups of 32 rows][D / 4][32 rows]: a warp stores and loads whole lines
   float2* ml_part;   // [2 G][256]
   int4* cut;         // [G]: unit, kv head, last CTA (-1: no unit that begins here goes on), slot here
   uint16_t* bf_k;    // e4m3: the expanded rows [B][kv_heads][kv_pad][D]
@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* mem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_mem) + 1023) & ~uintptr_t(1023));
   uint8_t* q_mem = mem;
   uint8_t* kv_mem = mem + 2 * QT;
-  Smem* sm = reinterpret_cast<Smem*>(mem + 2 * QT + NSLOT * QT);
+  uint8_t* stage_mem = mem + 2 * QT + NSLOT * QT;  // 2 KB a softmax warp
+  Smem* sm = reinterpret_cast<Smem*>(stage_mem + SOFTMAX_WARPS * 2048);
   volatile int* abort = &sm->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -540,7 +541,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int i = warp >> 2, R = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + 128 * i, t_o = lanes + COL_O + D * i;
-    const int group = p.q_heads / p.kv_heads;
+    const uint32_t group = p.q_heads / p.kv_heads;
+    const uint32_t rpi_q = (256u / D) / group, rpi_r = (256u / D) % group;  // rows a warp loads at once
     const bool plain = p.softcap == 0.f && p.slopes == nullptr && p.softmax_scale > 0.f;
     const float cl = p.softmax_scale * LOG2E;
     const float rcap2 = p.softcap > 0.f ? 2.f * LOG2E / p.softcap : 0.f;
@@ -550,17 +552,26 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto load_queries = [&](const Segment& g) {
       constexpr int CPR = D / 8, RPI = 32 / CPR;
       const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
-      const int64_t base = (int64_t)g.tile * UROWS, rows = (int64_t)s.n * group - base;
-      const int tok0 = (int)(base / group), rem = (int)(base % group), ch = lane % CPR;
+      const uint32_t r0 = (uint32_t)g.tile * UROWS + i * TILE + (warp & 3) * 32 + lane / CPR, rows = (uint32_t)s.n * group;
+      uint32_t tok = r0 / group, head = r0 % group;  // of this lane's first row; then RPI rows on each time
+      const int ch = lane % CPR;
       uint8_t* dst = q_mem + i * QT + (ch >> 3) * HB;
+      const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)s.t0 * p.q_token_stride +
+                                 (int64_t)g.h * group * p.q_head_stride + 8 * ch;
 #pragma unroll 4
       for (int x = 0; x < 32 / RPI; ++x) {
-        const int Rr = (warp & 3) * 32 + x * RPI + lane / CPR, r = i * TILE + Rr;
-        const int tok = tok0 + (rem + r) / group, head = g.h * group + (rem + r) % group;
-        const bool in = r < rows;
-        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q);
-        if (in) src += (int64_t)(s.t0 + tok) * p.q_token_stride + (int64_t)head * p.q_head_stride + 8 * ch;
-        tc::cp_async16(dst + Rr * 128 + (((ch & 7) ^ (Rr & 7)) << 4), src, in ? 16u : 0u);
+        const int Rr = (warp & 3) * 32 + x * RPI + lane / CPR;
+        const bool in = r0 + x * RPI < rows;
+        tc::cp_async16(dst + Rr * 128 + (((ch & 7) ^ (Rr & 7)) << 4),
+                       in ? src + (int64_t)tok * p.q_token_stride + (int64_t)head * p.q_head_stride
+                          : reinterpret_cast<const __nv_bfloat16*>(p.q),
+                       in ? 16u : 0u);
+        head += rpi_r;
+        tok += rpi_q;
+        if (head >= group) {
+          head -= group;
+          ++tok;
+        }
       }
       tc::cp_async_commit();
       tc::cp_async_wait<0>();
@@ -572,10 +583,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (have && g.count(i)) load_queries(g);
     while (ok && have) {
       const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
-      const int64_t base = (int64_t)g.tile * UROWS;
-      const int tok0 = (int)(base / group), rem = (int)(base % group), r = i * TILE + R;
-      const bool live = r < (int64_t)s.n * group - base;
-      const int tok = tok0 + (rem + r) / group, head = g.h * group + (rem + r) % group, pos = s.kv - s.n + tok;
+      const int r = i * TILE + R;
+      const uint32_t ru = (uint32_t)g.tile * UROWS + r;
+      const bool live = ru < (uint32_t)s.n * group;
+      const int tok = (int)(ru / group), head = g.h * (int)group + (int)(ru % group), pos = s.kv - s.n + tok;
+      Segment gn;
+      have = walk.next(a, first, last, gn);
       int2 vis = make_int2(0, 0);
       float slope = 0.f;
       if (live) {
@@ -707,8 +720,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) tc::mbar_arrive(&sm->pfull[i]);
       }
       if (!ok) break;
-      Segment gn;
-      have = walk.next(a, first, last, gn);
       if (have && gn.count(i)) load_queries(gn);  // its first scores run beside this segment's end
       if (cnt) {
         ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->odone[i], oph, abort));
@@ -718,14 +729,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       const int64_t row = (int64_t)(s.t0 + tok) * p.q_heads + head;
       const int slot = 2 * blockIdx.x + (g.u0 <= first ? 0 : 1);
-      const int64_t prow = (int64_t)slot * UROWS + r;
       const bool some = cnt && m > -INFINITY;  // (a row that saw nothing: what O holds does not matter)
       float f = 1.f;
       if (g.whole) {
         if (live) f = finish_scale(p, row, head, m, l, m, true);
       } else {
-        a.ml_part[prow] = make_float2(m, l);
+        a.ml_part[(int64_t)slot * UROWS + r] = make_float2(m, l);
       }
+      const uint32_t n_rows = (uint32_t)s.n * group;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -735,21 +746,40 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
 #pragma unroll
         for (int d = 0; d < 32; ++d) o[d] = some ? __float_as_uint(__uint_as_float(o[d]) * f) : 0u;
-        if (!g.whole || p.out_dtype == DSV4_F32) {
-          float* dst = g.whole ? reinterpret_cast<float*>(p.out) + row * D : a.o_part + prow * D;
-          if (!g.whole || live) {
+        if (!g.whole) {
+          float4* dst = a.o_part + (((int64_t)slot * 8 + warp) * (D / 4) + c / 4) * 32 + lane;
 #pragma unroll
-            for (int d = 0; d < 32; d += 4) *reinterpret_cast<uint4*>(dst + c + d) = make_uint4(o[d], o[d + 1], o[d + 2], o[d + 3]);
+          for (int d = 0; d < 32; d += 4)
+            dst[d * 8] = make_float4(__uint_as_float(o[d]), __uint_as_float(o[d + 1]), __uint_as_float(o[d + 2]),
+                                     __uint_as_float(o[d + 3]));
+        } else if (p.out_dtype == DSV4_F32) {
+          if (live) {
+#pragma unroll
+            for (int d = 0; d < 32; d += 4)
+              *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.out) + row * D + c + d) =
+                  make_uint4(o[d], o[d + 1], o[d + 2], o[d + 3]);
           }
-        } else if (live) {
-          uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + row * D;
+        } else {
+          // 32 dims of the warp's 32 rows turn in shared memory (16-byte pieces, exchanged by row), so that a store
+          // writes whole sectors of 8 rows
+          uint4* stage = reinterpret_cast<uint4*>(stage_mem) + warp * 128;
+          __syncwarp();
 #pragma unroll
-          for (int d = 0; d < 32; d += 8) {
+          for (int d = 0; d < 4; ++d) {
             uint32_t w[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              w[y] = float2_to_bf16x2_bits(__uint_as_float(o[d + 2 * y]), __uint_as_float(o[d + 2 * y + 1]));
-            *reinterpret_cast<uint4*>(dst + c + d) = make_uint4(w[0], w[1], w[2], w[3]);
+              w[y] = float2_to_bf16x2_bits(__uint_as_float(o[8 * d + 2 * y]), __uint_as_float(o[8 * d + 2 * y + 1]));
+            stage[lane * 4 + (d ^ ((lane >> 1) & 3))] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int rr = x * 8 + (lane >> 2), d = lane & 3;
+            const uint4 w = stage[rr * 4 + (d ^ ((rr >> 1) & 3))];
+            const int64_t ro = __shfl_sync(0xffffffffu, row, rr);
+            if ((uint32_t)g.tile * UROWS + i * TILE + (warp & 3) * 32 + rr < n_rows)
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + ro * D + c + 8 * d) = w;
           }
         }
       }
@@ -769,7 +799,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // The units that a border between CTAs cuts: CTA (c, y) joins rows 32 y .. 32 y + 31 of the one that begins in
-// CTA c, a warp a row.
+// CTA c; a lane has a row, a warp D / 8 of its dims.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(Args a) {
   pdl_wait();
@@ -777,44 +807,41 @@ __global__ void __launch_bounds__(256) join_kernel(Args a) {
   const dsv4_gqa_attention_params& p = a.p;
   const int4 cut = a.cut[blockIdx.x];
   if (cut.z < 0) return;
-  const int b = cut.x / a.tps, tile = cut.x % a.tps, group = p.q_heads / p.kv_heads, lane = threadIdx.x & 31;
+  const int b = cut.x / a.tps, tile = cut.x % a.tps, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t group = p.q_heads / p.kv_heads;
   const Seq s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.max_kv_len);
-  const int parts = cut.z - (int)blockIdx.x + 1;
-  constexpr int E = D / 32;
-  for (int x = threadIdx.x >> 5; x < 32; x += 8) {
-    const int rr = blockIdx.y * 32 + x;
-    const int64_t r = (int64_t)tile * UROWS + rr;
-    if (r >= (int64_t)s.n * group) return;
-    auto place = [&](int i) { return ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? cut.w : 0)) * UROWS + rr; };
-    float m = -INFINITY, l = 0.f, acc[E];
+  const int parts = cut.z - (int)blockIdx.x + 1, rr = blockIdx.y * 32 + lane;
+  const uint32_t r = (uint32_t)tile * UROWS + rr;
+  if (r >= (uint32_t)s.n * group) return;
+  constexpr int E = D / 32;  // float4s of a warp's dims
+  auto place = [&](int i) { return (int64_t)2 * (blockIdx.x + i) + (i == 0 ? cut.w : 0); };
+  float m = -INFINITY, l = 0.f;
+  float4 acc[E];
 #pragma unroll
-    for (int k = 0; k < E; ++k) acc[k] = 0.f;
-    for (int i = 0; i < parts; ++i) m = fmaxf(m, a.ml_part[place(i)].x);
-    for (int i = 0; i < parts; ++i) {
-      const int64_t at = place(i);
-      const float2 ml = a.ml_part[at];
-      if (ml.x == -INFINITY) continue;
-      const float f = tc::ex2_approx(ml.x - m);
-      l += ml.y * f;
-      const float2* src = reinterpret_cast<const float2*>(a.o_part + at * D + lane * E);
+  for (int k = 0; k < E; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, a.ml_part[place(i) * UROWS + rr].x);
+#pragma unroll 2
+  for (int i = 0; i < parts; ++i) {
+    const float2 ml = a.ml_part[place(i) * UROWS + rr];
+    const float f = ml.x > -INFINITY ? tc::ex2_approx(ml.x - m) : 0.f;  // (its sums are zeros then)
+    l += ml.y * f;
+    const float4* src = a.o_part + ((place(i) * 8 + blockIdx.y) * (D / 4) + warp * E) * 32 + lane;
 #pragma unroll
-      for (int k = 0; k < E; k += 2) {
-        const float2 v = src[k / 2];
-        acc[k] = fmaf(v.x, f, acc[k]);
-        acc[k + 1] = fmaf(v.y, f, acc[k + 1]);
-      }
-    }
-    const int head = cut.y * group + (int)(r % group);
-    const int64_t row = (int64_t)(s.t0 + (int)(r / group)) * p.q_heads + head;
-    const float f = finish_scale(p, row, head, m, l, m, lane == 0);
-#pragma unroll
-    for (int k = 0; k < E; k += 2) {
-      if (p.out_dtype == DSV4_F32)
-        reinterpret_cast<float2*>(p.out)[(row * D + lane * E + k) / 2] = make_float2(acc[k] * f, acc[k + 1] * f);
-      else
-        reinterpret_cast<uint32_t*>(p.out)[(row * D + lane * E + k) / 2] = float2_to_bf16x2_bits(acc[k] * f, acc[k + 1] * f);
+    for (int k = 0; k < E; ++k) {
+      const float4 v = src[k * 32];
+      acc[k].x = fmaf(v.x, f, acc[k].x);
+      acc[k].y = fmaf(v.y, f, acc[k].y);
+      acc[k].z = fmaf(v.z, f, acc[k].z);
+      acc[k].w = fmaf(v.w, f, acc[k].w);
     }
   }
+  const int head = cut.y * (int)group + (int)(r % group);
+  const int64_t row = (int64_t)(s.t0 + (int)(r / group)) * p.q_heads + head;
+  const float f = finish_scale(p, row, head, m, l, m, warp == 0);
+#pragma unroll
+  for (int k = 0; k < E; ++k)
+    store4<D>(p, row, warp * E + k, make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f));
 }
 
 struct Plan {
@@ -855,7 +882,7 @@ static cudaError_t launch(const dsv4_gqa_attention_params& p, cudaStream_t s) {
   Args a;
   a.p = p;
   a.unit = reinterpret_cast<int4*>(ws + L.unit);
-  a.o_part = reinterpret_cast<float*>(ws + L.part);
+  a.o_part = reinterpret_cast<float4*>(ws + L.part);
   a.ml_part = reinterpret_cast<float2*>(ws + L.ml);
   a.cut = reinterpret_cast<int4*>(ws + L.cut);
   const bool e4m3 = p.cache_dtype == DSV4_E4M3_PAGE && L.kv_pad > 0;
@@ -886,7 +913,7 @@ static cudaError_t launch(const dsv4_gqa_attention_params& p, cudaStream_t s) {
                             2 * p.v_cache_head_stride, 2 * p.v_page_stride, 64, a.box);
   }
   if (e != cudaSuccess) return e;
-  const int smem = (2 + NSLOT) * TILE * D * 2 + (int)sizeof(Smem) + 1024;
+  const int smem = (2 + NSLOT) * TILE * D * 2 + SOFTMAX_WARPS * 2048 + (int)sizeof(Smem) + 1024;
   e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(prefill_kernel<D>), smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(prepare_kernel<D>, dim3((unsigned)(plan_ctas + expand)), dim3(PREP_THREADS), 0, s, true, a, (int)plan_ctas);
