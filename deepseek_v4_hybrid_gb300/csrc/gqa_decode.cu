@@ -12,10 +12,17 @@
 //    for register, the A operand of O += P V.  The order of a contraction's terms is free, so a lane
 //    reads 16 contiguous bytes of a row and Q's fragments are laid out to match; for P V a lane holds 16
 //    contiguous dims of the four rows it needs, and one byte permute a register pairs two rows' codes.
-//  - e4m3 codes become fp16 by masks and a shift (value x 2^-8, exact, subnormals included).  K's scale and
-//    the query row's own power of two (which brings bf16 queries into fp16's range) multiply the logit; V's
-//    exponent is added to the logit's, so that P V is taken against a running maximum of its own and pages
-//    of very different scales lose nothing.  P is rounded to fp16 (bf16 caches: bf16), sums are fp32.
+//  - e4m3 caches are never expanded: keys and values enter the MMAs (k32, four times the fp16 rate of these
+//    MMAs) as they are, and what meets them is split into two e4m3 terms, x = hi + lo / 2^s, with a sum each.  With at
+//    most 8 rows the two terms are the two halves of the MMA's 16 rows, and the second one costs nothing.
+//      Queries, brought to at most 448 by a power of two a row, s = 4: a bf16 query's 8 bits are hi's 4 and lo's
+//      4, exact down to 2^-15 of the row's largest element, off by 2^-23 of it at most below that.
+//      Weights, taken against the stage's own maximum (and its larger V exponent) and scaled to at most 256, s =
+//      5: off by 2^-8 of themselves or 2^-23 of the stage's largest; the stage's product is added to the running
+//      fp32 output with its factor, so a flat tail behind one large weight keeps its precision.
+//    V's exponent is part of the reference that the output is taken against, so pages of very different scales lose
+//    nothing.  The values' bytes are transposed in registers, 4 rows by 4 dims with 8 byte permutes.
+//  - bf16 caches: P is rounded to bf16, against a maximum that moves when it is exceeded by more than 2^8.
 #include "gqa_attention.cuh"
 #include "tmap.h"
 
@@ -28,9 +35,9 @@ namespace gqa {
 namespace dec {
 
 constexpr int NW = 4, THREADS = 32 * NW;
-constexpr int SR = 16;             // rows of a stage
+constexpr int BLK = 16;            // rows that lie in one page
 constexpr int MAX_SCAN = 1024;     // sequences whose stages are cut evenly; above, a CTA takes a whole unit
-constexpr int MIN_STAGES = 8;      // stages of a piece, at least: two a warp
+constexpr int MIN_ROWS = 128;      // rows of a piece, at least
 constexpr float LAZY = 8.f;        // a running maximum moves when it is exceeded by more than 2^8
 
 struct Args {
@@ -43,14 +50,18 @@ struct Args {
 
 // Shared memory and CTAs per SM: 12 to 16 warps an SM, each with at least 8 KB of copies in flight
 // (about 46 KB an SM cover the latency at the full rate), as registers allow.
-__host__ __device__ constexpr int ctas_per_sm(int D, int HB) { return HB == 4 ? 2 : (D == 64 && HB == 1) ? 4 : 3; }
+__host__ __device__ constexpr int ctas_per_sm(int D, bool e4m3, int HB) {
+  return HB == 4 || (D == 128 && e4m3 && HB == 2) ? 2 : (D == 64 && HB == 1) ? 4 : 3;
+}
 
 template <int D, bool E4M3, int HB>
 struct Cfg {
   static constexpr int ROWB = E4M3 ? D : 2 * D;
+  static constexpr int SUB = E4M3 ? 2 : 1;     // blocks of a stage: an MMA's K, 32 or 16 rows
+  static constexpr int SR = BLK * SUB;
   static constexpr int STAGE = 2 * SR * ROWB;  // K then V
-  static constexpr int CTAS = ctas_per_sm(D, HB);
-  static constexpr int RING = CTAS == 4 ? 12288 : 16384;
+  static constexpr int CTAS = ctas_per_sm(D, E4M3, HB);
+  static constexpr int RING = CTAS == 4 ? 12288 : CTAS == 3 ? 16384 : 24576;
   static constexpr int NST = RING / STAGE;
   static constexpr int QMEM = HB == 4 ? 2 * (D / 16) * 512 : 0;  // 32 rows: Q's fragments live in shared memory
   static constexpr int SMEM = NW * RING + QMEM;
@@ -60,41 +71,39 @@ struct Cfg {
 
 struct Shared {
   float m[NW][32], l[NW][32], mo[NW][32];
-  int2 meta[NW][16];  // [ring slot]: page usable, (k exponent byte | v exponent byte << 8)
+  int2 meta[NW][16];  // [block of the ring]: page usable, (k exponent byte | v exponent byte << 8)
   int64_t total;
   int64_t at;
   int b;
 };
 
-// c += a b (m16n8k16), fp16 (e4m3 caches) or bf16; with UPPER only rows 0-7 of the tile are kept, and the
-// registers of rows 8-15 (of a zero A) are not carried along.
-template <bool E4M3, bool UPPER>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (UPPER) {
-    float x, y;
-    if (E4M3)
-      asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%10,%10};"
-          : "+f"(c[0]), "+f"(c[1]), "=f"(x), "=f"(y)
-          : "r"(a[0]), "r"(0u), "r"(a[2]), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
-    else
-      asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%10,%10};"
-          : "+f"(c[0]), "+f"(c[1]), "=f"(x), "=f"(y)
-          : "r"(a[0]), "r"(0u), "r"(a[2]), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
-  } else if (E4M3) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  } else {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
+// c += a b (m16n8k16), bf16.
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c += a b (m16n8k32), e4m3; and c = a b.
+__device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Two e4m3 codes, in the top byte of each half of m (the bottom bytes hold anything), as fp16 x 2^-8.
-__device__ __forceinline__ uint32_t codes_to_f16(uint32_t m) {
-  return ((m >> 1) & 0x3F803F80u) | (m & 0x80008000u);
+// Two terms of four values |x| <= 448: x = hi + lo / f, f a power of two.
+__device__ __forceinline__ uint2 split_e4m3(float x0, float x1, float x2, float x3, float f) {
+  const uint32_t h0 = float2_to_e4m3x2(x0, x1), h1 = float2_to_e4m3x2(x2, x3);
+  const float2 f0 = e4m3x2_to_float2((uint16_t)h0), f1 = e4m3x2_to_float2((uint16_t)h1);
+  const uint32_t l0 = float2_to_e4m3x2((x0 - f0.x) * f, (x1 - f0.y) * f);
+  const uint32_t l1 = float2_to_e4m3x2((x2 - f1.x) * f, (x3 - f1.y) * f);
+  return make_uint2(h0 | (h1 << 16), l0 | (l1 << 16));
 }
+constexpr float QF = 16.f, PF = 32.f;  // 2^s of queries and weights
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -120,6 +129,7 @@ struct Unit {
   int vlo;         // first row any token sees
 };
 
+template <int SR>
 __device__ __forceinline__ Unit unit_of(const dsv4_gqa_attention_params& p, int b) {
   Unit u;
   u.s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.max_kv_len);
@@ -142,7 +152,9 @@ __device__ __forceinline__ Unit unit_of(const dsv4_gqa_attention_params& p, int 
 template <int D, bool E4M3, int HB>
 __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel(Args a) {
   using C = Cfg<D, E4M3, HB>;
-  constexpr int MT = HB == 4 ? 2 : 1, KS = D / 16, NT = D / 8;
+  constexpr int MT = HB == 4 ? 2 : 1, NT = D / 8, SR = C::SR, SUB = C::SUB;
+  constexpr int KS = E4M3 ? D / 32 : D / 16;             // K steps of Q K^T
+  constexpr int NQ = E4M3 && HB > 1 ? 2 * KS : KS;       // A fragments of an MMA tile of Q (two terms apart)
   extern __shared__ __align__(1024) uint8_t ring_all[];
   __shared__ Shared sm;
   const dsv4_gqa_attention_params& p = a.p;
@@ -165,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
       const int bb = b0 + tid;
       int st = 0;
       if (bb < p.B) {
-        const Unit u = unit_of(p, bb);
+        const Unit u = unit_of<SR>(p, bb);
         st = u.stages;
         if (blockIdx.x == 0 && st == 0) {
           if (!u.s.ok) atomicOr(&g_flags_gd, FLAG_PAGE);
@@ -188,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
     }
     const int64_t total = run * p.kv_heads;
     per = (total + a.G - 1) / a.G;
-    if (per < MIN_STAGES) per = MIN_STAGES;
+    if (per < MIN_ROWS / SR) per = MIN_ROWS / SR;
     first = (int64_t)blockIdx.x * per;
     last = min(total, first + per);
     if (first >= last) return;
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
     __syncthreads();
   } else {
     b = blockIdx.x / p.kv_heads;
-    const Unit u = unit_of(p, b);
+    const Unit u = unit_of<SR>(p, b);
     if (u.stages == 0) {
       if (tid == 0) {
         if (!u.s.ok) atomicOr(&g_flags_gd, FLAG_PAGE);
@@ -223,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
 
   // ---------------- the units that the piece meets
   for (int64_t at = first; at < last; ++b) {
-    const Unit u = unit_of(p, b);
+    const Unit u = unit_of<SR>(p, b);
     if (u.stages == 0) continue;
     for (h = (int)((at - base) / u.stages); h < p.kv_heads && at < last; ++h) {
       const int64_t u0 = base + (int64_t)h * u.stages;  // the unit's list positions [u0, u0 + stages)
@@ -237,7 +249,21 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
       float rmul[HB], slope[HB], rpos[HB];
       float m[HB], mo[HB], l[HB];
       int all_lo = 0, all_hi = 0x7FFFFFFF;  // rows that every token sees
-      uint32_t q[HB == 4 ? 1 : KS][4];
+      // Q's A fragments; e4m3: [K step][hi, lo], or both terms in one for 8 rows.  32 rows: in shared memory,
+      // [MMA tile][fragment][lane][4 registers].
+      uint32_t q[HB == 4 ? 1 : NQ][4];
+      auto keep_q = [&](int x, int k, uint32_t lo, uint32_t hi) {  // fragment x, row half k of its tile
+        if (HB == 4) {
+          if (warp == 0) {
+            uint32_t* dst = qmem + (((k / 2) * NQ + x) * 32 + lane) * 4;
+            dst[k & 1] = lo;
+            dst[2 + (k & 1)] = hi;
+          }
+        } else {
+          q[x][k & 1] = lo;
+          q[x][2 + (k & 1)] = hi;
+        }
+      };
 #pragma unroll
       for (int k = 0; k < HB; ++k) {
         const int r = g + 8 * k, i = r / group;
@@ -259,85 +285,95 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
           all_lo = max(all_lo, v.x);
           all_hi = min(all_hi, v.y);
         }
-        // Q fragments: the 4 dims of K step s that this lane's K registers hold
         const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q) +
                              2 * ((int64_t)t * p.q_token_stride + (int64_t)head * p.q_head_stride);
-        uint2 w[KS];
-        float big = 0.f;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const int d = E4M3 ? 64 * (s / 4) + 16 * c + 4 * (s % 4) : 32 * (s / 2) + 8 * c + 4 * (s % 2);
-          w[s] = live ? *reinterpret_cast<const uint2*>(src + 2 * d) : make_uint2(0u, 0u);
-          if (E4M3) {
-            big = fmaxf(big, fmaxf(fmaxf(fabsf(__uint_as_float(w[s].x << 16)), fabsf(__uint_as_float(w[s].x & 0xFFFF0000u))),
-                                   fmaxf(fabsf(__uint_as_float(w[s].y << 16)), fabsf(__uint_as_float(w[s].y & 0xFFFF0000u)))));
-          }
-        }
         float mul = p.softmax_scale;
         if (E4M3) {
-          // the row's largest magnitude is brought into [2^14, 2^15): elements down to 2^-39 of it keep
-          // all bits that matter next to fp32 sums
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          int e = big > 0.f && big < INFINITY ? (int)(__float_as_uint(big) >> 23) - 127 - 14 : 0;
-          e = max(-126, min(112, e));
-          const float f = exp2_neg_int(e);
+          // the 8 dims of K step s (of 32) that this lane's K registers hold, split in two terms
+          uint4 w[KS];
+          float big = 0.f;
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
-            const __half2 h0 = __floats2half2_rn(__uint_as_float(w[s].x << 16) * f, __uint_as_float(w[s].x & 0xFFFF0000u) * f);
-            const __half2 h1 = __floats2half2_rn(__uint_as_float(w[s].y << 16) * f, __uint_as_float(w[s].y & 0xFFFF0000u) * f);
-            w[s] = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+            w[s] = live ? *reinterpret_cast<const uint4*>(src + 2 * (64 * (s / 2) + 16 * c + 8 * (s % 2))) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t ww[4] = {w[s].x, w[s].y, w[s].z, w[s].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              big = fmaxf(big, fmaxf(fabsf(__uint_as_float(ww[y] << 16)), fabsf(__uint_as_float(ww[y] & 0xFFFF0000u))));
           }
-          mul *= exp2_neg_int(-e) * 256.f;  // (codes_to_f16's 2^-8)
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          const int e = ue8m0_exponent(big);
+          const float f = exp2_neg_int(e);
+          mul *= exp2_neg_int(-e);
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            const uint32_t ww[4] = {w[s].x, w[s].y, w[s].z, w[s].w};
+            float v[8];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              v[2 * y] = __uint_as_float(ww[y] << 16) * f;
+              v[2 * y + 1] = __uint_as_float(ww[y] & 0xFFFF0000u) * f;
+            }
+            const uint2 u0 = split_e4m3(v[0], v[1], v[2], v[3], QF), u1 = split_e4m3(v[4], v[5], v[6], v[7], QF);
+            if (HB == 1) {  // (rows 0-7: hi, rows 8-15: lo)
+              keep_q(s, 0, u0.x, u1.x);
+              keep_q(s, 1, u0.y, u1.y);
+            } else {
+              keep_q(2 * s, k, u0.x, u1.x);
+              keep_q(2 * s + 1, k, u0.y, u1.y);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {  // the 4 dims of K step s (of 16)
+            const uint2 w = live ? *reinterpret_cast<const uint2*>(src + 2 * (32 * (s / 2) + 8 * c + 4 * (s % 2))) : make_uint2(0u, 0u);
+            keep_q(s, k, w.x, w.y);
+            if (HB == 1) keep_q(s, 1, 0u, 0u);
+          }
         }
         rmul[k] = plain ? mul * LOG2E : mul;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          if (HB == 4) {  // [MMA tile][K step][lane][4 registers]
-            if (warp == 0) {
-              uint32_t* dst = qmem + (((k / 2) * KS + s) * 32 + lane) * 4;
-              dst[k & 1] = w[s].x;
-              dst[2 + (k & 1)] = w[s].y;
-            }
-          } else {
-            q[s][k & 1] = w[s].x;
-            q[s][2 + (k & 1)] = w[s].y;
-            if (HB == 1) q[s][1] = q[s][3] = 0u;
-          }
-        }
       }
       if (HB == 4) __syncthreads();
       all_lo = __reduce_max_sync(0xffffffffu, all_lo);
       all_hi = __reduce_min_sync(0xffffffffu, all_hi);
 
-      float o[MT][NT][4];
+      // the running output: row half k, column tile j, columns 2c and 2c + 1.  bf16: the MMAs' accumulators
+      float o[E4M3 ? HB : (HB + 1) / 2][NT][E4M3 ? 2 : 4];
 #pragma unroll
-      for (int x = 0; x < MT; ++x)
+      for (auto& x : o)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
+        for (auto& y : x)
+#pragma unroll
+          for (float& v : y) v = 0.f;
+      auto out = [&](int k, int j, int y) -> float& { return E4M3 ? o[k][j][y] : o[k / 2][j][2 * (k & 1) + y]; };
 
-      auto score = [&](float (&s)[MT][2][4], int nt, int ks, uint32_t b0, uint32_t b1) {
+      auto q_frag = [&](int z, int x, uint32_t (&f)[4]) {
         if (HB == 4) {
-#pragma unroll
-          for (int x = 0; x < MT; ++x) {
-            const uint4 w = *reinterpret_cast<const uint4*>(qmem + ((x * KS + ks) * 32 + lane) * 4);
-            const uint32_t f[4] = {w.x, w.y, w.z, w.w};
-            mma<E4M3, HB == 1>(s[x][nt], f, b0, b1);
-          }
+          const uint4 w = *reinterpret_cast<const uint4*>(qmem + ((z * NQ + x) * 32 + lane) * 4);
+          f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
         } else {
-          mma<E4M3, HB == 1>(s[0][nt], q[ks], b0, b1);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) f[y] = q[x][y];
         }
       };
       // this warp's stages: s0 + warp, s0 + warp + NW, ...
       const int count = s1 - s0 > warp ? (s1 - s0 - warp + NW - 1) / NW : 0;
       int pid = -1, pexp = 0;
+      constexpr int CPR = C::ROWB / 16, RPI = 32 / CPR;  // lanes of a row, rows a warp copies at once
+      constexpr int64_t ES = E4M3 ? 1 : 2;
+      const uint8_t* k_base = reinterpret_cast<const uint8_t*>(p.k_cache) + ES * ((int64_t)h * p.k_cache_head_stride) + 16 * (lane % CPR);
+      const uint8_t* v_base = reinterpret_cast<const uint8_t*>(p.v_cache) + ES * ((int64_t)h * p.v_cache_head_stride) + 16 * (lane % CPR);
+      const int64_t k_step = ES * RPI * p.k_row_stride, v_step = ES * RPI * p.v_row_stride;
+      int doff[BLK / RPI];
+#pragma unroll
+      for (int i = 0; i < BLK / RPI; ++i) doff[i] = chunk_at<C::ROWB>(i * RPI + lane / CPR, lane % CPR);
       auto fill = [&](int k) {
         if (k < count) {
-          if ((k & 31) == 0) {  // pages and exponents of the next 32 stages, one a lane
-            const int j = u.lo + (s0 + warp + (k + lane) * NW) * SR;
+          if ((k * SUB & 31) == 0) {  // pages and exponents of the next 32 blocks, one a lane
+            const int ks = k + lane / SUB, j = u.lo + (s0 + warp + ks * NW) * SR + lane % SUB * BLK;
             pid = -1;
             pexp = 0;
-            if (k + lane < count && j < u.s.kv) {
+            if (ks < count && j < u.s.kv) {
               const int lp = j / p.page_size;
               pid = lp < p.max_pages_per_seq ? p.block_table[(int64_t)b * p.max_pages_per_seq + lp] : -1;
               if (pid < 0 || pid >= p.num_pages) {
@@ -349,33 +385,42 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
               }
             }
           }
-          const int page = __shfl_sync(0xffffffffu, pid, k & 31), ex = __shfl_sync(0xffffffffu, pexp, k & 31);
-          const int slot = k % C::NST, j0 = u.lo + (s0 + warp + k * NW) * SR;
-          if (lane == 0) sm.meta[warp][slot] = make_int2(page >= 0, ex);
-          uint8_t* dst = ring + slot * C::STAGE;
-          constexpr int CPR = C::ROWB / 16, RPI = 32 / CPR;
-          const int ch = lane % CPR;
-          const int off = j0 & (p.page_size - 1);
-          const int64_t es = E4M3 ? 1 : 2;
-          const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k_cache) +
-                              es * ((int64_t)max(page, 0) * p.k_page_stride + (int64_t)h * p.k_cache_head_stride) + 16 * ch;
-          const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v_cache) +
-                              es * ((int64_t)max(page, 0) * p.v_page_stride + (int64_t)h * p.v_cache_head_stride) + 16 * ch;
+          const int slot = k % C::NST;
 #pragma unroll
-          for (int i = 0; i < SR / RPI; ++i) {
-            const int r = i * RPI + lane / CPR;
-            // rows that no token sees read nothing and become zeros, whatever the cache holds there
-            const uint32_t n = page >= 0 && j0 + r >= u.vlo && j0 + r < u.s.kv ? 16u : 0u;
-            const int64_t row = n ? off + r : 0;
-            tc::cp_async16(dst + chunk_at<C::ROWB>(r, ch), kb + es * row * p.k_row_stride, n);
-            tc::cp_async16(dst + SR * C::ROWB + chunk_at<C::ROWB>(r, ch), vb + es * row * p.v_row_stride, n);
+          for (int sub = 0; sub < SUB; ++sub) {
+            const int page = __shfl_sync(0xffffffffu, pid, (k * SUB + sub) & 31);
+            const int ex = __shfl_sync(0xffffffffu, pexp, (k * SUB + sub) & 31);
+            const int j0 = u.lo + (s0 + warp + k * NW) * SR + sub * BLK;
+            if (lane == 0) sm.meta[warp][slot * SUB + sub] = make_int2(page >= 0, ex);
+            uint8_t* dst = ring + slot * C::STAGE + sub * BLK * C::ROWB;
+            const int row = (j0 & (p.page_size - 1)) + lane / CPR;
+            const uint8_t* kr = k_base + ES * ((int64_t)max(page, 0) * p.k_page_stride + (int64_t)row * p.k_row_stride);
+            const uint8_t* vr = v_base + ES * ((int64_t)max(page, 0) * p.v_page_stride + (int64_t)row * p.v_row_stride);
+            if (page >= 0 && j0 >= u.vlo && j0 + BLK <= u.s.kv) {
+#pragma unroll
+              for (int i = 0; i < BLK / RPI; ++i) {
+                tc::cp_async16(dst + doff[i], kr + i * k_step, 16u);
+                tc::cp_async16(dst + SR * C::ROWB + doff[i], vr + i * v_step, 16u);
+              }
+            } else {
+              // rows that no token sees read nothing and become zeros, whatever the cache holds there
+#pragma unroll
+              for (int i = 0; i < BLK / RPI; ++i) {
+                const int j = j0 + i * RPI + lane / CPR;
+                const bool in = page >= 0 && j >= u.vlo && j < u.s.kv;
+                tc::cp_async16(dst + doff[i], in ? kr + i * k_step : reinterpret_cast<const uint8_t*>(p.k_cache), in ? 16u : 0u);
+                tc::cp_async16(dst + SR * C::ROWB + doff[i], in ? vr + i * v_step : reinterpret_cast<const uint8_t*>(p.v_cache),
+                               in ? 16u : 0u);
+              }
+            }
           }
         }
         tc::cp_async_commit();
       };
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < C::NST - 1; ++k) fill(k);
 
+#pragma unroll 1
       for (int k = 0; k < count; ++k) {
         tc::cp_async_wait<C::NST - 2>();
         __syncwarp();
@@ -383,153 +428,242 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
         const int slot = k % C::NST, j0 = u.lo + (s0 + warp + k * NW) * SR;
         const uint8_t* kt = ring + slot * C::STAGE;
         const uint8_t* vt = kt + SR * C::ROWB;
-        const int2 meta = sm.meta[warp][slot];
 
-        // ---- S = Q K^T
-        float s[MT][2][4];
+        // ---- S = Q K^T: z[row half][tile of 8 rows][row 2c, 2c + 1 of it]
+        float z[HB][2 * SUB][2];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-#pragma unroll
-          for (int x = 0; x < MT; ++x) s[x][nt][0] = s[x][nt][1] = s[x][nt][2] = s[x][nt][3] = 0.f;
+        for (int nt = 0; nt < 2 * SUB; ++nt) {
           constexpr int KCH = C::ROWB / 64;  // 16-byte chunks a lane holds of a row
+          float s[MT][4], s_lo[MT][4];
 #pragma unroll
           for (int x = 0; x < KCH; ++x) {
             const uint4 w = *reinterpret_cast<const uint4*>(kt + chunk_at<C::ROWB>(8 * nt + g, c + 4 * x));
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            if (E4M3) {
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const uint32_t b0 = codes_to_f16(__byte_perm(ww[y], 0u, 0x1404u));
-                const uint32_t b1 = codes_to_f16(__byte_perm(ww[y], 0u, 0x3424u));
-                score(s, nt, 4 * x + y, b0, b1);
+            for (int y = 0; y < 2; ++y) {
+              const int ks = 2 * x + y;
+#pragma unroll
+              for (int m2 = 0; m2 < MT; ++m2) {
+                uint32_t f[4];
+                if (E4M3) {
+                  q_frag(m2, HB == 1 ? ks : 2 * ks, f);
+                  if (ks == 0) mma8_first(s[m2], f, ww[2 * y], ww[2 * y + 1]);
+                  else mma8(s[m2], f, ww[2 * y], ww[2 * y + 1]);
+                  if (HB > 1) {
+                    q_frag(m2, 2 * ks + 1, f);
+                    if (ks == 0) mma8_first(s_lo[m2], f, ww[2 * y], ww[2 * y + 1]);
+                    else mma8(s_lo[m2], f, ww[2 * y], ww[2 * y + 1]);
+                  }
+                } else {
+                  q_frag(m2, ks, f);
+                  if (ks == 0) s[m2][0] = s[m2][1] = s[m2][2] = s[m2][3] = 0.f;
+                  mma16(s[m2], f, ww[2 * y], ww[2 * y + 1]);
+                }
               }
-            } else {
-#pragma unroll
-              for (int y = 0; y < 2; ++y) score(s, nt, 2 * x + y, ww[2 * y], ww[2 * y + 1]);
             }
           }
+#pragma unroll
+          for (int k2 = 0; k2 < HB; ++k2)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int e = 2 * (k2 & 1) + y;
+              z[k2][nt][y] = !E4M3 ? s[k2 / 2][e] : HB == 1 ? fmaf(s[0][2 + y], 1.f / QF, s[0][y])
+                                                            : fmaf(s_lo[k2 / 2][e], 1.f / QF, s[k2 / 2][e]);
+            }
         }
 
-        // ---- logits in log2 units, masks
-        const float kmul = E4M3 ? ue8m0_scale((uint8_t)(meta.y & 255)) : 1.f;
-        const float vexp = E4M3 ? (float)((meta.y >> 8) - 127 + 8) : 0.f;  // (8: codes_to_f16)
-        const bool inside = meta.x != 0 && j0 >= all_lo && j0 + SR <= all_hi;
-        float top[HB];
+        // ---- logits in log2 units, masks, the stage's maximum of each row (this lane's part)
+        float top[HB], vexp[SUB];
+        bool inside = j0 >= all_lo && j0 + SR <= all_hi;
+        float kmul[SUB];
+        bool page_ok[SUB];
+#pragma unroll
+        for (int sub = 0; sub < SUB; ++sub) {
+          const int2 meta = sm.meta[warp][slot * SUB + sub];
+          page_ok[sub] = meta.x != 0;
+          inside = inside && page_ok[sub];
+          kmul[sub] = E4M3 ? ue8m0_scale((uint8_t)(meta.y & 255)) : 1.f;
+          vexp[sub] = (float)((meta.y >> 8) - 127);
+        }
 #pragma unroll
         for (int k2 = 0; k2 < HB; ++k2) {
-          float (&x0)[4] = s[k2 / 2][0];
-          float (&x1)[4] = s[k2 / 2][1];
-          const int e = 2 * (k2 & 1);
-          float z[4] = {x0[e], x0[e + 1], x1[e], x1[e + 1]};
-          const float f = rmul[k2];
+          top[k2] = -INFINITY;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) z[y] = z[y] * kmul * f;
-          if (!plain) {
+          for (int nt = 0; nt < 2 * SUB; ++nt)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              if (p.softcap > 0.f) z[y] = cap_logit(z[y], p.softcap, rcap2);
-              const int j = j0 + 2 * c + (y & 1) + 8 * (y >> 1);
-              z[y] = z[y] * LOG2E - slope[k2] * fabsf(rpos[k2] - (float)j);
+            for (int y = 0; y < 2; ++y) {
+              float& v = z[k2][nt][y];
+              v = E4M3 ? v * kmul[nt / 2] * rmul[k2] : v * rmul[k2];
+              const int j = j0 + 8 * nt + 2 * c + y;
+              if (!plain) {
+                if (p.softcap > 0.f) v = cap_logit(v, p.softcap, rcap2);
+                v = v * LOG2E - slope[k2] * fabsf(rpos[k2] - (float)j);
+              }
+              if (!inside && (!page_ok[nt / 2] || j < rlo[k2] || j >= rhi[k2])) v = -INFINITY;
+              top[k2] = fmaxf(top[k2], v);
             }
-          }
-          if (!inside) {
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int j = j0 + 2 * c + (y & 1) + 8 * (y >> 1);
-              if (meta.x == 0 || j < rlo[k2] || j >= rhi[k2]) z[y] = -INFINITY;
-            }
-          }
-          top[k2] = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-          x0[e] = z[0];
-          x0[e + 1] = z[1];
-          x1[e] = z[2];
-          x1[e + 1] = z[3];
         }
-        // ---- running maxima: moved (by the whole quad) only when some logit exceeds one by more than LAZY
-        bool move = false;
+
+        if (E4M3) {
+          // ---- weights against the stage's maximum, in two e4m3 terms
+          const float vtop = fmaxf(page_ok[0] ? vexp[0] : -127.f, page_ok[SUB - 1] ? vexp[SUB - 1] : -127.f);
+          float vf[SUB];
 #pragma unroll
-        for (int k2 = 0; k2 < HB; ++k2) move |= top[k2] > m[k2] + LAZY || (E4M3 && top[k2] + vexp > mo[k2] + LAZY);
-        if (__any_sync(0xffffffffu, move)) {
+          for (int sub = 0; sub < SUB; ++sub) vf[sub] = page_ok[sub] ? tc::ex2_approx(vexp[sub] - vtop + 8.f) : 0.f;
+          uint32_t hi[HB][2], lo[HB][2];
+          float fs[HB];
+          bool move = false;
+          float fo[HB];
 #pragma unroll
           for (int k2 = 0; k2 < HB; ++k2) {
             float t = top[k2];
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-            const float mn = fmaxf(m[k2], t), on = E4M3 ? fmaxf(mo[k2], t + vexp) : mn;
-            const float fl = m[k2] == -INFINITY ? 0.f : tc::ex2_approx(m[k2] - mn);
-            const float fo = E4M3 ? (mo[k2] == -INFINITY ? 0.f : tc::ex2_approx(mo[k2] - on)) : fl;
-            l[k2] *= fl;
+            const float ref = t == -INFINITY ? 0.f : t;
+            float sum = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < 2 * SUB; ++nt)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                float& v = z[k2][nt][y];
+                v = tc::ex2_approx(v - ref);
+                sum += v;
+                v *= vf[nt / 2];
+              }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint2 w = split_e4m3(z[k2][2 * x][0], z[k2][2 * x][1], z[k2][2 * x + 1][0], z[k2][2 * x + 1][1], PF);
+              hi[k2][x] = w.x;
+              lo[k2][x] = w.y;
+            }
+            const float mn = fmaxf(m[k2], t), on = fmaxf(mo[k2], t + vtop);
+            const float mr = mn == -INFINITY ? 0.f : mn, orf = on == -INFINITY ? 0.f : on;
+            l[k2] = fmaf(l[k2], tc::ex2_approx(m[k2] - mr), sum * tc::ex2_approx(t - mr));
+            fo[k2] = tc::ex2_approx(mo[k2] - orf);
+            fs[k2] = tc::ex2_approx(t + vtop - 8.f - orf);
+            move |= on > mo[k2];
             m[k2] = mn;
             mo[k2] = on;
+          }
+          if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              o[k2 / 2][j][2 * (k2 & 1)] *= fo;
-              o[k2 / 2][j][2 * (k2 & 1) + 1] *= fo;
+            for (int k2 = 0; k2 < HB; ++k2)
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                out(k2, j, 0) *= fo[k2];
+                out(k2, j, 1) *= fo[k2];
+              }
+          }
+          // ---- O += P V: 4 dims (a word of the lane's) at a time; 32 rows hold half the lane's words at once
+          constexpr int WD = D / 32, WH = HB == 4 && D == 128 ? 2 : WD;
+          uint32_t v[8][WH];
+#pragma unroll
+          for (int wd = 0; wd < WD; ++wd) {
+            if (wd % WH == 0) {
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const int r = 2 * c + (y & 1) + 8 * (y >> 1);
+                const uint8_t* src = D == 128 ? vt + chunk_at<C::ROWB>(r, (g >> 1) | ((g & 1) << 2)) + 4 * wd
+                                              : vt + chunk_at<C::ROWB>(r, g >> 1) + 8 * (g & 1);
+                if (WH == 4) {
+                  const uint4 w = *reinterpret_cast<const uint4*>(src);
+                  v[y][0] = w.x;
+                  v[y][1] = w.y;
+                  v[y][WH - 2] = w.z;
+                  v[y][WH - 1] = w.w;
+                } else {
+                  const uint2 w = *reinterpret_cast<const uint2*>(src);
+                  v[y][0] = w.x;
+                  v[y][1] = w.y;
+                }
+              }
+            }
+            uint32_t bt[2][4];  // [rows 0-15, 16-31 of the stage][dim]: four rows' codes of one dim
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t t0 = __byte_perm(v[4 * x][wd % WH], v[4 * x + 1][wd % WH], 0x5140u);
+              const uint32_t t1 = __byte_perm(v[4 * x][wd % WH], v[4 * x + 1][wd % WH], 0x7362u);
+              const uint32_t u0 = __byte_perm(v[4 * x + 2][wd % WH], v[4 * x + 3][wd % WH], 0x5140u);
+              const uint32_t u1 = __byte_perm(v[4 * x + 2][wd % WH], v[4 * x + 3][wd % WH], 0x7362u);
+              bt[x][0] = __byte_perm(t0, u0, 0x5410u);
+              bt[x][1] = __byte_perm(t0, u0, 0x7632u);
+              bt[x][2] = __byte_perm(t1, u1, 0x5410u);
+              bt[x][3] = __byte_perm(t1, u1, 0x7632u);
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              const int j = 4 * wd + d;
+              if (HB == 1) {
+                const uint32_t f[4] = {hi[0][0], lo[0][0], hi[0][1], lo[0][1]};
+                float x[4];
+                mma8_first(x, f, bt[0][d], bt[1][d]);
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  out(0, j, y) = fmaf(fmaf(x[2 + y], 1.f / PF, x[y]), fs[0], out(0, j, y));
+              } else {
+#pragma unroll
+                for (int m2 = 0; m2 < MT; ++m2) {
+                  const int k0 = 2 * m2, k1 = 2 * m2 + (HB > 1 ? 1 : 0);
+                  const uint32_t f[4] = {hi[k0][0], hi[k1][0], hi[k0][1], hi[k1][1]};
+                  const uint32_t f2[4] = {lo[k0][0], lo[k1][0], lo[k0][1], lo[k1][1]};
+                  float x[4], x2[4];
+                  mma8_first(x, f, bt[0][d], bt[1][d]);
+                  mma8_first(x2, f2, bt[0][d], bt[1][d]);
+#pragma unroll
+                  for (int y = 0; y < 2; ++y) {
+                    out(k0, j, y) = fmaf(fmaf(x2[y], 1.f / PF, x[y]), fs[k0], out(k0, j, y));
+                    out(k1, j, y) = fmaf(fmaf(x2[2 + y], 1.f / PF, x[2 + y]), fs[k1], out(k1, j, y));
+                  }
+                }
+              }
             }
           }
-        }
-        // ---- P: weights for the sum, and (scaled by V's exponent) for the product
-        uint32_t pa[MT][4];
-        if (HB == 1) pa[0][1] = pa[0][3] = 0u;
+        } else {
+          // ---- running maxima: moved (by the whole quad) only when some logit exceeds one by more than LAZY
+          bool move = false;
 #pragma unroll
-        for (int k2 = 0; k2 < HB; ++k2) {
-          const int e = 2 * (k2 & 1);
-          const float z[4] = {s[k2 / 2][0][e], s[k2 / 2][0][e + 1], s[k2 / 2][1][e], s[k2 / 2][1][e + 1]};
-          const float mm = m[k2] == -INFINITY ? 0.f : m[k2];
-          float w[4];
+          for (int k2 = 0; k2 < HB; ++k2) move |= top[k2] > m[k2] + LAZY;
+          if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) w[y] = tc::ex2_approx(z[y] - mm);
-          l[k2] += (w[0] + w[1]) + (w[2] + w[3]);
-          if (E4M3) {
-            const float om = mo[k2] == -INFINITY ? 0.f : mo[k2] - vexp;
+            for (int k2 = 0; k2 < HB; ++k2) {
+              float t = top[k2];
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+              const float mn = fmaxf(m[k2], t);
+              const float f = m[k2] == -INFINITY ? 0.f : tc::ex2_approx(m[k2] - mn);
+              l[k2] *= f;
+              m[k2] = mo[k2] = mn;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) w[y] = tc::ex2_approx(z[y] - om);
-            const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
-            pa[k2 / 2][k2 & 1] = *reinterpret_cast<const uint32_t*>(&h0);
-            pa[k2 / 2][2 + (k2 & 1)] = *reinterpret_cast<const uint32_t*>(&h1);
-          } else {
+              for (int j = 0; j < NT; ++j) {
+                out(k2, j, 0) *= f;
+                out(k2, j, 1) *= f;
+              }
+            }
+          }
+          uint32_t pa[MT][4];
+          if (HB == 1) pa[0][1] = pa[0][3] = 0u;
+#pragma unroll
+          for (int k2 = 0; k2 < HB; ++k2) {
+            const float mm = m[k2] == -INFINITY ? 0.f : m[k2];
+            float w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[y] = tc::ex2_approx(z[k2][y >> 1][y & 1] - mm);
+            l[k2] += (w[0] + w[1]) + (w[2] + w[3]);
             pa[k2 / 2][k2 & 1] = float2_to_bf16x2_bits(w[0], w[1]);
             pa[k2 / 2][2 + (k2 & 1)] = float2_to_bf16x2_bits(w[2], w[3]);
           }
-        }
-        // ---- O += P V
-        if (E4M3) {
-          constexpr int WD = D / 32;  // words (of 4 dims) a lane holds of a row
-          uint32_t v[4][WD];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int r = 2 * c + (y & 1) + 8 * (y >> 1);
-            if (D == 128) {
-              const uint4 w = *reinterpret_cast<const uint4*>(vt + chunk_at<C::ROWB>(r, (g >> 1) | ((g & 1) << 2)));
-              v[y][0] = w.x;
-              v[y][1] = w.y;
-              v[y][WD - 2] = w.z;
-              v[y][WD - 1] = w.w;
-            } else {
-              const uint2 w = *reinterpret_cast<const uint2*>(vt + chunk_at<C::ROWB>(r, g >> 1) + 8 * (g & 1));
-              v[y][0] = w.x;
-              v[y][1] = w.y;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const uint32_t sel = ((4u + (j & 3)) << 12) | ((uint32_t)(j & 3) << 4);
-            const uint32_t b0 = codes_to_f16(__byte_perm(v[0][j >> 2], v[1][j >> 2], sel));
-            const uint32_t b1 = codes_to_f16(__byte_perm(v[2][j >> 2], v[3][j >> 2], sel));
-#pragma unroll
-            for (int x = 0; x < MT; ++x) mma<E4M3, HB == 1>(o[x][j], pa[x], b0, b1);
-          }
-        } else {
-          // matrices of an x4 load: rows 0-7 and 8-15 of dims 8 (2 jj), then of dims 8 (2 jj + 1)
+          // ---- O += P V; the matrices of an x4 load: rows 0-7 and 8-15 of dims 16 jj .. + 7, then of the next 8
           const int r = (lane & 7) + (lane & 8);
 #pragma unroll
           for (int jj = 0; jj < NT / 2; ++jj) {
             uint32_t w[4];
             ldmatrix_x4_trans(w, tc::smem_addr(vt + chunk_at<C::ROWB>(r, 2 * jj + (lane >> 4))));
+            if constexpr (!E4M3) {
 #pragma unroll
-            for (int x = 0; x < MT; ++x) {
-              mma<E4M3, HB == 1>(o[x][2 * jj], pa[x], w[0], w[1]);
-              mma<E4M3, HB == 1>(o[x][2 * jj + 1], pa[x], w[2], w[3]);
+              for (int x = 0; x < MT; ++x) {
+                mma16(o[x][2 * jj], pa[x], w[0], w[1]);
+                mma16(o[x][2 * jj + 1], pa[x], w[2], w[3]);
+              }
             }
           }
         }
@@ -562,8 +696,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
           // or 8 j + n (bf16); this lane has columns 2 c and 2 c + 1
           const int d0 = !E4M3 ? 8 * j + 2 * c : D == 128 ? 16 * c + j : 16 * c + j;
           const int d1 = !E4M3 ? d0 + 1 : D == 128 ? d0 + 64 : d0 + 8;
-          part[r * D + d0] = o[k / 2][j][2 * (k & 1)] * f;
-          part[r * D + d1] = o[k / 2][j][2 * (k & 1) + 1] * f;
+          part[r * D + d0] = out(k, j, 0) * f;
+          part[r * D + d1] = out(k, j, 1) * f;
         }
       }
       __syncthreads();
@@ -676,16 +810,15 @@ struct Plan {
 };
 
 // Row halves of 8 that hold the rows of a kv head, and the CTAs: what the device holds at once, or fewer
-// where even the largest batch within the call's bounds has fewer pieces of MIN_STAGES.
+// where even the largest batch within the call's bounds has fewer pieces of MIN_ROWS.
 static Plan plan(const dsv4_gqa_attention_params& p) {
   Plan L;
   const int max_n = p.max_q_len < p.T ? p.max_q_len : p.T;
   L.rows = max_n * (p.q_heads / p.kv_heads);
   L.hb = L.rows <= 8 ? 1 : L.rows <= 16 ? 2 : 4;
   L.rows = 8 * L.hb;
-  const int ctas = ctas_per_sm(p.head_dim, L.hb);
-  const int64_t stages = (int64_t)p.B * p.kv_heads * (p.max_kv_len / SR + 2);
-  const int64_t pieces = (stages + MIN_STAGES - 1) / MIN_STAGES;
+  const int ctas = ctas_per_sm(p.head_dim, p.cache_dtype == DSV4_E4M3_PAGE, L.hb);
+  const int64_t pieces = ((int64_t)p.B * p.kv_heads * (p.max_kv_len + 2 * 32) + MIN_ROWS - 1) / MIN_ROWS;
   L.G = num_sms() * ctas;
   if (pieces < L.G) L.G = (int)pieces;
   const int64_t slots = p.B <= MAX_SCAN ? 2LL * L.G : 0;
