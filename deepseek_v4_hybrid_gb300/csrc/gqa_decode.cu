@@ -23,8 +23,12 @@
 //    V's exponent is part of the reference that the output is taken against, so pages of very different scales lose
 //    nothing.  The values' bytes are transposed in registers, 4 rows by 4 dims with 8 byte permutes.
 //  - bf16 caches: P is rounded to bf16, against a maximum that moves when it is exceeded by more than 2^8.
+#include <cooperative_groups.h>
+
 #include "gqa_attention.cuh"
 #include "tmap.h"
+
+namespace cg = cooperative_groups;
 
 namespace dsv4 {
 
@@ -37,7 +41,9 @@ namespace dec {
 constexpr int NW = 4, THREADS = 32 * NW;
 constexpr int BLK = 16;            // rows that lie in one page
 constexpr int MAX_SCAN = 1024;     // sequences whose stages are cut evenly; above, a CTA takes a whole unit
+constexpr int MAX_CLUSTER = 8;     // CTAs of a unit (portable cluster size)
 constexpr int MIN_ROWS = 128;      // rows of a piece, at least
+constexpr int CLUSTER_ROWS = 1024; // rows of a cluster's CTA, at most
 constexpr float LAZY = 8.f;        // a running maximum moves when it is exceeded by more than 2^8
 
 struct Args {
@@ -46,6 +52,7 @@ struct Args {
   float4* ml_part;  // [2 G][rows]: maximum of the logits, sum, maximum that O is taken against (log2 units)
   int4* unit;       // [B * kv_heads]: first and last CTA of the unit, slot in the first, 0 / 1 = merge
   int G, rows;      // CTAs, rows of a partial
+  int cs;           // 0: equal pieces of the list; else CTAs (a cluster) of each unit
 };
 
 // Shared memory and CTAs per SM: 12 to 16 warps an SM, each with at least 8 KB of copies in flight
@@ -71,6 +78,7 @@ struct Cfg {
 
 struct Shared {
   float m[NW][32], l[NW][32], mo[NW][32];
+  float4 cml[32];     // cluster: this CTA's (maximum, sum, reference) of each row
   int2 meta[NW][16];  // [block of the ring]: page usable, (k exponent byte | v exponent byte << 8)
   int64_t total;
   int64_t at;
@@ -169,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
   int b, h;
   int64_t per;
   int64_t base;  // list position of unit (b, 0)
-  if (p.B <= MAX_SCAN) {
+  if (a.cs == 0) {
     int64_t* pre = reinterpret_cast<int64_t*>(ring_all);  // [B + 1] stages of the sequences before
     int64_t* wsum = pre + MAX_SCAN + 1;
     int64_t run = 0;
@@ -214,19 +222,21 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
     base = pre[b] * p.kv_heads;
     __syncthreads();
   } else {
-    b = blockIdx.x / p.kv_heads;
+    // a unit's stages in even pieces over the CTAs of a cluster
+    const int unit = blockIdx.x / a.cs, rank = blockIdx.x % a.cs;
+    b = unit / p.kv_heads;
     const Unit u = unit_of<SR>(p, b);
     if (u.stages == 0) {
-      if (tid == 0) {
-        if (!u.s.ok) atomicOr(&g_flags_gd, FLAG_PAGE);
-        a.unit[blockIdx.x] = make_int4(0, 0, 0, 0);
-      }
+      if (tid == 0 && rank == 0 && !u.s.ok) atomicOr(&g_flags_gd, FLAG_PAGE);
       return;
     }
     base = 0;
-    per = u.stages;
-    first = (int64_t)(blockIdx.x % p.kv_heads) * per;
-    last = first + per;
+    per = (u.stages + a.cs - 1) / a.cs;
+    first = (int64_t)(unit % p.kv_heads) * u.stages;
+    last = first + min((int64_t)u.stages, (rank + 1) * per);
+    first += min((int64_t)u.stages, rank * per);
+    if (tid < 32) sm.cml[tid] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    __syncthreads();
   }
 
   const int group = p.q_heads / p.kv_heads;
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
     for (h = (int)((at - base) / u.stages); h < p.kv_heads && at < last; ++h) {
       const int64_t u0 = base + (int64_t)h * u.stages;  // the unit's list positions [u0, u0 + stages)
       const int s0 = (int)(at - u0), s1 = (int)(min(last, u0 + u.stages) - u0);
-      const bool whole = s0 == 0 && s1 == u.stages;
+      const bool whole = a.cs == 1 || (a.cs == 0 && s0 == 0 && s1 == u.stages);
       const int rows = u.s.n * group;
       const int pos0 = u.s.kv - u.s.n;
 
@@ -724,12 +734,15 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
           const int64_t row = (int64_t)(u.s.t0 + r / group) * p.q_heads + head;
           const float f = finish_scale(p, row, head, mn, ls, on, d4 == 0);
           store4<D>(p, row, d4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+        } else if (a.cs) {
+          reinterpret_cast<float4*>(ring_all)[x] = acc;  // (over warp 0's, which this thread has read here)
+          if (d4 == 0) sm.cml[r] = make_float4(mn, ls, on, 0.f);
         } else {
           reinterpret_cast<float4*>(a.o_part)[((int64_t)slot * a.rows + r) * (D / 4) + d4] = acc;
           if (d4 == 0) a.ml_part[(int64_t)slot * a.rows + r] = make_float4(mn, ls, on, 0.f);
         }
       }
-      if (tid == 0 && s0 == 0)
+      if (tid == 0 && s0 == 0 && a.cs == 0)
         a.unit[(int64_t)b * p.kv_heads + h] =
             whole ? make_int4(0, 0, 0, 0)
                   : make_int4((int)blockIdx.x, (int)((u0 + u.stages - 1) / per), at == first ? 0 : 1, 1);
@@ -737,6 +750,51 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
       at = u0 + s1;
     }
     base += (int64_t)p.kv_heads * u.stages;
+  }
+
+  if (a.cs > 1) {
+    // ---------------- the cluster's pieces of the unit, joined through distributed shared memory: every CTA finishes
+    // its share of the output
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    const int unit = blockIdx.x / a.cs, rank = blockIdx.x % a.cs;
+    const Unit u = unit_of<SR>(p, unit / p.kv_heads);
+    const int rows = u.s.n * group;
+    for (int x = rank * THREADS + tid; x < rows * (D / 4); x += a.cs * THREADS) {
+      const int r = x / (D / 4), d4 = x % (D / 4);
+      float4 ml[MAX_CLUSTER], v[MAX_CLUSTER];
+      float mn = -INFINITY, on = -INFINITY, ls = 0.f;
+#pragma unroll
+      for (int i = 0; i < MAX_CLUSTER; ++i) {  // (all at once: one latency)
+        ml[i] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < a.cs) {
+          ml[i] = cl.map_shared_rank(sm.cml, i)[r];
+          v[i] = cl.map_shared_rank(reinterpret_cast<float4*>(ring_all), i)[x];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MAX_CLUSTER; ++i) {
+        mn = fmaxf(mn, ml[i].x);
+        on = fmaxf(on, ml[i].z);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < MAX_CLUSTER; ++i) {
+        if (ml[i].x == -INFINITY) continue;  // (a piece without visible rows: its sums may not have been written)
+        ls += ml[i].y * tc::ex2_approx(ml[i].x - mn);
+        const float f = tc::ex2_approx(ml[i].z - on);
+        acc.x = fmaf(v[i].x, f, acc.x);
+        acc.y = fmaf(v[i].y, f, acc.y);
+        acc.z = fmaf(v[i].z, f, acc.z);
+        acc.w = fmaf(v[i].w, f, acc.w);
+      }
+      const int head = unit % p.kv_heads * group + r % group;
+      const int64_t row = (int64_t)(u.s.t0 + r / group) * p.q_heads + head;
+      const float f = finish_scale(p, row, head, mn, ls, on, d4 == 0);
+      store4<D>(p, row, d4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+    }
+    cl.sync();  // no CTA leaves while its shared memory is read
   }
 }
 
@@ -805,7 +863,7 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(Args a) {
 }
 
 struct Plan {
-  int hb, rows, G;
+  int hb, rows, G, cs;
   size_t ml_off, unit_off, total;
 };
 
@@ -821,7 +879,15 @@ static Plan plan(const dsv4_gqa_attention_params& p) {
   const int64_t pieces = ((int64_t)p.B * p.kv_heads * (p.max_kv_len + 2 * 32) + MIN_ROWS - 1) / MIN_ROWS;
   L.G = num_sms() * ctas;
   if (pieces < L.G) L.G = (int)pieces;
-  const int64_t slots = p.B <= MAX_SCAN ? 2LL * L.G : 0;
+  // A cluster a unit where the batch is small enough for all units' clusters to be resident and a warp to have
+  // few stages: its join costs less than a second kernel.  (Else, evenly cut pieces; beyond MAX_SCAN, a CTA a unit.)
+  const int64_t units = (int64_t)p.B * p.kv_heads;
+  int64_t seen = p.max_kv_len;
+  if (p.window > 0 && (int64_t)p.window + max_n < seen) seen = (int64_t)p.window + max_n;
+  L.cs = p.B > MAX_SCAN ? 1 : 0;
+  for (int cs = MAX_CLUSTER; cs >= 2 && L.cs == 0; cs /= 2)
+    if (units * cs <= (int64_t)num_sms() * ctas && seen <= (int64_t)CLUSTER_ROWS * cs) L.cs = cs;
+  const int64_t slots = L.cs == 0 ? 2LL * L.G : 0;
   L.ml_off = align_up((size_t)slots * L.rows * p.head_dim * 4, 256);
   L.unit_off = align_up(L.ml_off + (size_t)slots * L.rows * 16, 256);
   L.total = align_up(L.unit_off + (size_t)p.B * p.kv_heads * 16, 256);
@@ -837,9 +903,22 @@ static cudaError_t launch(const Args& a, cudaStream_t s) {
   const dsv4_gqa_attention_params& p = a.p;
   const int64_t units = (int64_t)p.B * p.kv_heads;
   if (units > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const bool scan = p.B <= MAX_SCAN;
-  e = launch_pdl(decode_kernel<D, E4M3, HB>, dim3(scan ? a.G : (unsigned)units), dim3(THREADS), C::SMEM, s, true, a);
-  if (e != cudaSuccess || !scan) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.cs ? (unsigned)(units * a.cs) : a.G);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cs ? a.cs : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = count_launch(cudaLaunchKernelEx(&cfg, decode_kernel<D, E4M3, HB>, a));
+  if (e != cudaSuccess || a.cs) return e;
   return launch_pdl(merge_kernel<D>, dim3((unsigned)units, 2 * HB), dim3(THREADS), 0, s, true, a);
 }
 
@@ -862,6 +941,7 @@ cudaError_t launch_decode(const dsv4_gqa_attention_params& p, cudaStream_t s) {
   a.unit = reinterpret_cast<int4*>(ws + L.unit_off);
   a.G = L.G;
   a.rows = L.rows;
+  a.cs = L.cs;
   const bool e4m3 = p.cache_dtype == DSV4_E4M3_PAGE;
   if (p.head_dim == 128)
     return e4m3 ? dec::launch_hb<128, true>(a, L.hb, s) : dec::launch_hb<128, false>(a, L.hb, s);
