@@ -1,10 +1,11 @@
 // Append of new keys and values to paged per-head caches, keys and queries rotated on the way.
 //
-// One launch, two kinds of CTA.  A cache CTA takes the rows that one sequence stores into one page for
-// one kv head, keys and values both: a thread holds up to NR 16-byte chunks of each in registers, so the
-// rows are read once although the e4m3 exponent of a (page, head) needs the maximum over all of them
-// before the first code is written.  A query CTA takes one token: a thread keeps the cos and sin of its
-// chunk in registers and turns that chunk of head after head.
+// One launch, two kinds of CTA.  A cache CTA takes the rows of K or of V that one sequence stores into one
+// page for one kv head.  A thread holds up to 4 of their 16-byte chunks in registers, so rows are read once
+// although the e4m3 exponent of a (page, head) needs the maximum over all of them before the first code is
+// written (more rows than that are read again, from the caches of the first reading).  A query CTA takes one
+// token: a thread keeps the cos and sin of its chunk and turns that chunk of head after head, four in flight,
+// whose loads go out before the token's position is known.
 // The rotation is fp32 with every product and sum rounded (no contraction), so codes and exponents
 // are the same whatever kernel or library computes them from the formula.
 // Bound by HBM: every row is read once and written once.
@@ -16,19 +17,46 @@ static __device__ unsigned int g_flags_ga = 0;
 
 namespace gqa {
 
-constexpr int Q_THREADS = 256;
-
 struct Rope {
   const float* cos_sin;
   int first, half, halves;
 };
 
-// Chunk c (dims 8c .. 8c + 7) of a row at position pos, whose bf16 values are `raw`, rotated.  With
-// halves, the partner dims are in chunk c +- half / 8 of the same row, which another lane of the warp
-// holds (`cpr` lanes hold one row); every lane of the warp calls this.
+// cos and sin of chunk c (dims 8c .. 8c + 7) of a row at position pos: 4 pairs (GPT-J), or with halves the 8 dims'
+// own, both in registers; kind: 0 the chunk is not turned, 1 GPT-J pairs, 2 / 3 the lower / upper half.
+struct Turn {
+  float co[8], si[8];
+  int kind;
+};
+
+template <int N>
+__device__ __forceinline__ void load_turn(Turn& tr, const float* cs, int half) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {  // (16-byte aligned: rope_dim is a multiple of 16, dims come by 8)
+    const float4 a = __ldg(reinterpret_cast<const float4*>(cs + i)), b = __ldg(reinterpret_cast<const float4*>(cs + half + i));
+    tr.co[i] = a.x, tr.co[i + 1] = a.y, tr.co[i + 2] = a.z, tr.co[i + 3] = a.w;
+    tr.si[i] = b.x, tr.si[i + 1] = b.y, tr.si[i + 2] = b.z, tr.si[i + 3] = b.w;
+  }
+}
+
+__device__ __forceinline__ void turn_of(const Rope& r, int c, int64_t pos, bool live, Turn& tr) {
+  const int d0 = 8 * c - r.first;  // the chunk's first dim inside the rotated range
+  tr.kind = 0;
+  if (r.cos_sin == nullptr || !live || d0 < 0 || d0 >= 2 * r.half) return;
+  const float* row = r.cos_sin + pos * (2 * r.half);
+  if (!r.halves) {
+    tr.kind = 1;
+    load_turn<4>(tr, row + d0 / 2, r.half);
+  } else {
+    tr.kind = d0 < r.half ? 2 : 3;
+    load_turn<8>(tr, row + (d0 < r.half ? d0 : d0 - r.half), r.half);
+  }
+}
+
+// The chunk's bf16 values `raw`, turned.  With halves, the partner dims are in chunk c +- half / 8 of the same
+// row, which another lane of the warp holds (CPR lanes hold one row); every lane of the warp calls this.
 template <int CPR>
-__device__ __forceinline__ void rotate_chunk(const Rope& r, const uint4& raw, int c, int64_t pos, bool live,
-                                             float (&x)[8]) {
+__device__ __forceinline__ void rotate_chunk(const Rope& r, const Turn& tr, const uint4& raw, int c, float (&x)[8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -36,32 +64,27 @@ __device__ __forceinline__ void rotate_chunk(const Rope& r, const uint4& raw, in
     x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
   if (r.cos_sin == nullptr) return;
-  const int d0 = 8 * c - r.first;  // the chunk's first dim inside the rotated range
-  const bool in = live && d0 >= 0 && d0 < 2 * r.half;
   if (!r.halves) {
-    if (!in) return;
-    const float* cs = r.cos_sin + pos * (2 * r.half) + d0 / 2;
+    if (tr.kind == 0) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float co = __ldg(cs + i), si = __ldg(cs + r.half + i), a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = __fsub_rn(__fmul_rn(a, co), __fmul_rn(b, si));
-      x[2 * i + 1] = __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, si));
+      const float a = x[2 * i], b = x[2 * i + 1];
+      x[2 * i] = __fsub_rn(__fmul_rn(a, tr.co[i]), __fmul_rn(b, tr.si[i]));
+      x[2 * i + 1] = __fadd_rn(__fmul_rn(b, tr.co[i]), __fmul_rn(a, tr.si[i]));
     }
     return;
   }
-  const bool low = d0 < r.half;
   const int lane = threadIdx.x & 31, row0 = lane & ~(CPR - 1);
-  const int src = in ? row0 + c + (low ? r.half / 8 : -(r.half / 8)) : lane;
+  const int src = tr.kind ? row0 + c + (tr.kind == 2 ? r.half / 8 : -(r.half / 8)) : lane;
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(0xffffffffu, w[i], src);
-  if (!in) return;
-  const float* cs = r.cos_sin + pos * (2 * r.half) + (low ? d0 : d0 - r.half);
+  if (tr.kind == 0) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float co = __ldg(cs + i), si = __ldg(cs + r.half + i);
     const float y = __uint_as_float(i & 1 ? o[i >> 1] & 0xFFFF0000u : o[i >> 1] << 16);
-    x[i] = low ? __fsub_rn(__fmul_rn(x[i], co), __fmul_rn(y, si)) : __fadd_rn(__fmul_rn(x[i], co), __fmul_rn(y, si));
+    x[i] = tr.kind == 2 ? __fsub_rn(__fmul_rn(x[i], tr.co[i]), __fmul_rn(y, tr.si[i]))
+                        : __fadd_rn(__fmul_rn(x[i], tr.co[i]), __fmul_rn(y, tr.si[i]));
   }
 }
 
@@ -75,11 +98,23 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&x)[8]) {
 __device__ __forceinline__ int page_exponent(float amax) { return amax == 0.f ? -127 : ue8m0_exponent(amax); }
 
 // Queries: one token a CTA.
-template <int D>
+template <int D, int THREADS>
 __device__ __forceinline__ void rotate_queries(const dsv4_gqa_append_params& p, const Rope& rope, int t) {
-  constexpr int CPR = D / 8;
+  constexpr int CPR = D / 8, HPI = THREADS / CPR;  // heads the CTA turns at once
+  const int lane = threadIdx.x & 31, c = threadIdx.x % CPR, hl = threadIdx.x / CPR;
+  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)t * p.q_token_stride + 8 * c;
+  __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.q_out) + (int64_t)t * p.q_out_token_stride + 8 * c;
+  uint4 raw[4];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = h0 + i * HPI + hl;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (h < p.q_heads) raw[i] = *reinterpret_cast<const uint4*>(q + (int64_t)h * p.q_head_stride);
+    }
+  };
+  load(0);
   // the token's sequence: the last b with q_start[b] <= t (32 probes a step)
-  const int lane = threadIdx.x & 31;
   int lo = 0, hi = p.B;  // the answer is in [lo, hi)
   if (p.q_start[0] > t) return;
   while (hi - lo > 1) {
@@ -93,24 +128,25 @@ __device__ __forceinline__ void rotate_queries(const dsv4_gqa_append_params& p, 
   }
   const Seq s = sequence(p.q_start, p.kv_len, lo, p.T, p.max_q_len, p.cos_sin ? p.max_pos : -1);
   if (!s.ok || t >= s.t0 + s.n) return;  // padding behind the last sequence, or a skipped sequence
-  const int64_t pos = s.kv - s.n + (t - s.t0);
-  const int c = threadIdx.x % CPR;
-  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)t * p.q_token_stride + 8 * c;
-  __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.q_out) + (int64_t)t * p.q_out_token_stride + 8 * c;
-  for (int h0 = 0; h0 < p.q_heads; h0 += Q_THREADS / CPR) {
-    const int h = h0 + threadIdx.x / CPR;
-    const bool live = h < p.q_heads;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) raw = *reinterpret_cast<const uint4*>(q + (int64_t)h * p.q_head_stride);
-    float x[8];
-    rotate_chunk<CPR>(rope, raw, c, pos, live, x);
-    if (live) *reinterpret_cast<uint4*>(o + (int64_t)h * p.q_out_head_stride) = pack_bf16(x);
+  Turn tr;
+  turn_of(rope, c, s.kv - s.n + (t - s.t0), true, tr);
+  for (int h0 = 0; h0 < p.q_heads; h0 += 4 * HPI) {
+    if (h0 > 0) load(h0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = h0 + i * HPI + hl;
+      float x[8];
+      rotate_chunk<CPR>(rope, tr, raw[i], c, x);
+      if (h < p.q_heads) *reinterpret_cast<uint4*>(o + (int64_t)h * p.q_out_head_stride) = pack_bf16(x);
+    }
   }
 }
 
-template <int D, int NR, bool E4M3>
-__global__ void __launch_bounds__(1024) append_kernel(dsv4_gqa_append_params p, int q_ctas, int pages_per_seq) {
-  constexpr int CPR = D / 8;  // 16-byte chunks of a bf16 row
+template <int D, bool E4M3, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 64 ? 8 : E4M3 ? 2 : 3)
+    append_kernel(dsv4_gqa_append_params p, int q_ctas, int pages_per_seq) {
+  constexpr int CPR = D / 8;       // 16-byte chunks of a bf16 row
+  constexpr int RPI = THREADS / CPR, NR = 4;
   pdl_wait();
   pdl_launch_dependents();
   Rope rope;
@@ -120,11 +156,12 @@ __global__ void __launch_bounds__(1024) append_kernel(dsv4_gqa_append_params p, 
   rope.halves = p.rope_halves;
   const int tid = threadIdx.x;
   if ((int)blockIdx.x < q_ctas) {
-    if (tid < Q_THREADS) rotate_queries<D>(p, rope, blockIdx.x);
+    rotate_queries<D, THREADS>(p, rope, blockIdx.x);
     return;
   }
   const int item = blockIdx.x - q_ctas;
-  const int h = item % p.kv_heads, u = item / p.kv_heads;
+  const bool is_v = item & 1;
+  const int h = (item >> 1) % p.kv_heads, u = (item >> 1) / p.kv_heads;
   const int b = u / pages_per_seq, slot = u % pages_per_seq;
   const Seq s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.cos_sin ? p.max_pos : -1);
   if (!s.ok) {
@@ -135,125 +172,106 @@ __global__ void __launch_bounds__(1024) append_kernel(dsv4_gqa_append_params p, 
   const int lo = max(first, p0), hi = min(first + p.page_size, s.kv);
   if (lo >= hi) return;
   const int page = lp < p.max_pages_per_seq ? p.block_table[(int64_t)b * p.max_pages_per_seq + lp] : -1;
-  if (page < 0 || page >= p.num_pages) {
-    if (h == 0 && tid == 0) atomicOr(&g_flags_ga, FLAG_PAGE);
-    return;
-  }
-  const int64_t eslot = (int64_t)page * p.kv_heads + h;
-  int old_k = 0, old_v = 0;
-  if (E4M3 && lo > first) {
-    old_k = (int)p.k_exp[eslot] - 127;
-    old_v = (int)p.v_exp[eslot] - 127;
-  }
-  const int c = tid % CPR, r0 = tid / CPR, rstep = blockDim.x / CPR;
-  const __nv_bfloat16* kn = reinterpret_cast<const __nv_bfloat16*>(p.k_new) + (int64_t)h * p.k_head_stride + 8 * c;
-  const __nv_bfloat16* vn = reinterpret_cast<const __nv_bfloat16*>(p.v_new) + (int64_t)h * p.v_head_stride + 8 * c;
-  uint4 kraw[NR], vraw[NR];
-#pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int row = lo + r0 + i * rstep;
-    kraw[i] = vraw[i] = make_uint4(0, 0, 0, 0);
-    if (row < hi) {
-      const int64_t t = s.t0 + (row - p0);
-      kraw[i] = *reinterpret_cast<const uint4*>(kn + t * p.k_token_stride);
-      vraw[i] = *reinterpret_cast<const uint4*>(vn + t * p.v_token_stride);
-    }
-  }
-  if (!E4M3) {
-    __nv_bfloat16* kc = reinterpret_cast<__nv_bfloat16*>(p.k_cache) + (int64_t)page * p.k_page_stride +
-                        (int64_t)h * p.k_cache_head_stride + 8 * c;
-    __nv_bfloat16* vc = reinterpret_cast<__nv_bfloat16*>(p.v_cache) + (int64_t)page * p.v_page_stride +
-                        (int64_t)h * p.v_cache_head_stride + 8 * c;
+  if (is_v) rope.cos_sin = nullptr;
+  const int c = tid % CPR, r0 = tid / CPR;
+  const int64_t tstride = is_v ? p.v_token_stride : p.k_token_stride;
+  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(is_v ? p.v_new : p.k_new) +
+                             (int64_t)h * (is_v ? p.v_head_stride : p.k_head_stride) + 8 * c;
+  uint4 raw[NR];
+  auto load = [&](int from) {  // NR chunks of this thread, from row `from` on
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const int row = lo + r0 + i * rstep;
-      float x[8];
-      rotate_chunk<CPR>(rope, kraw[i], c, row, row < hi, x);
-      if (row < hi) {
-        *reinterpret_cast<uint4*>(kc + (int64_t)(row - first) * p.k_row_stride) = pack_bf16(x);
-        *reinterpret_cast<uint4*>(vc + (int64_t)(row - first) * p.v_row_stride) = vraw[i];
+      const int row = from + r0 + i * RPI;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (row < hi) raw[i] = *reinterpret_cast<const uint4*>(src + (int64_t)(s.t0 + (row - p0)) * tstride);
+    }
+  };
+  auto turned = [&](int from, int i, float (&x)[8]) {
+    const int row = from + r0 + i * RPI;
+    Turn tr;
+    turn_of(rope, c, row, row < hi, tr);
+    rotate_chunk<CPR>(rope, tr, raw[i], c, x);
+  };
+  load(lo);
+  if (page < 0 || page >= p.num_pages) {
+    if (h == 0 && tid == 0 && !is_v) atomicOr(&g_flags_ga, FLAG_PAGE);
+    return;
+  }
+  const int64_t rstride = is_v ? p.v_row_stride : p.k_row_stride;
+  const int64_t base = (int64_t)page * (is_v ? p.v_page_stride : p.k_page_stride) +
+                       (int64_t)h * (is_v ? p.v_cache_head_stride : p.k_cache_head_stride);
+  if (!E4M3) {
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_v ? p.v_cache : p.k_cache) + base + 8 * c;
+    for (int from = lo; from < hi; from += NR * RPI) {
+      if (from > lo) load(from);
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const int row = from + r0 + i * RPI;
+        float x[8];
+        turned(from, i, x);
+        if (row < hi) *reinterpret_cast<uint4*>(dst + (int64_t)(row - first) * rstride) = pack_bf16(x);
       }
     }
     return;
   }
-  float kx[NR][8], kmax = 0.f, vmax = 0.f;
+  uint8_t* ex = (is_v ? p.v_exp : p.k_exp) + (int64_t)page * p.kv_heads + h;
+  const int old = lo > first ? (int)*ex - 127 : 0;
+  float x[NR][8], amax = 0.f;
+  const bool once = hi - lo <= NR * RPI;  // everything stays in registers
+  for (int from = lo; from < hi; from += NR * RPI) {
+    if (from > lo) load(from);
 #pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int row = lo + r0 + i * rstep;
-    rotate_chunk<CPR>(rope, kraw[i], c, row, row < hi, kx[i]);
+    for (int i = 0; i < NR; ++i) {
+      turned(from, i, x[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) kmax = fmaxf(kmax, fabsf(kx[i][j]));
-    const uint32_t w[4] = {vraw[i].x, vraw[i].y, vraw[i].z, vraw[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      vmax = fmaxf(vmax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[i][j]));
+    }
   }
-  __shared__ float red[2][32];
-  kmax = warp_max(kmax);
-  vmax = warp_max(vmax);
-  if ((tid & 31) == 0) {
-    red[0][tid >> 5] = kmax;
-    red[1][tid >> 5] = vmax;
-  }
+  __shared__ float red[32];
+  amax = warp_max(amax);
+  if ((tid & 31) == 0) red[tid >> 5] = amax;
   __syncthreads();
-  const int nw = blockDim.x / 32, lane = tid & 31;
-  kmax = warp_max(lane < nw ? red[0][lane] : 0.f);
-  vmax = warp_max(lane < nw ? red[1][lane] : 0.f);
-  int ek = page_exponent(kmax), ev = page_exponent(vmax);
-  uint8_t* kc = reinterpret_cast<uint8_t*>(p.k_cache) + (int64_t)page * p.k_page_stride +
-                (int64_t)h * p.k_cache_head_stride;
-  uint8_t* vc = reinterpret_cast<uint8_t*>(p.v_cache) + (int64_t)page * p.v_page_stride +
-                (int64_t)h * p.v_cache_head_stride;
+  amax = red[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 32; ++w) amax = fmaxf(amax, red[w]);
+  int e = page_exponent(amax);
+  uint8_t* dst = reinterpret_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + base;
   if (lo > first) {
-    ek = max(ek, old_k);
-    ev = max(ev, old_v);
-#pragma unroll 1
-    for (int kv = 0; kv < 2; ++kv) {  // rows stored earlier, re-encoded where the exponent grew
-      const int d = kv ? ev - old_v : ek - old_k;
-      if (d == 0) continue;
+    e = max(e, old);
+    const int d = e - old;
+    if (d > 0) {  // rows stored earlier, re-encoded for the larger exponent
       const float f = d < 64 ? exp2_neg_int(d) : 0.f;  // (code magnitudes lie in [2^-9, 448]: 0 from 2^-64 on)
-      uint8_t* base = kv ? vc : kc;
-      const int64_t rs = kv ? p.v_row_stride : p.k_row_stride;
-      for (int x = tid; x < (lo - first) * (D / 4); x += blockDim.x) {
-        uint32_t* a = reinterpret_cast<uint32_t*>(base + (int64_t)(x / (D / 4)) * rs) + x % (D / 4);
+      for (int y = tid; y < (lo - first) * (D / 4); y += THREADS) {
+        uint32_t* a = reinterpret_cast<uint32_t*>(dst + (int64_t)(y / (D / 4)) * rstride) + y % (D / 4);
         const uint32_t w = *a;
         const float2 g0 = e4m3x2_to_float2((uint16_t)(w & 0xFFFFu)), g1 = e4m3x2_to_float2((uint16_t)(w >> 16));
         *a = (uint32_t)float2_to_e4m3x2(g0.x * f, g0.y * f) | ((uint32_t)float2_to_e4m3x2(g1.x * f, g1.y * f) << 16);
       }
     }
   }
-  if (tid == 0) {
-    p.k_exp[eslot] = (uint8_t)(ek + 127);
-    p.v_exp[eslot] = (uint8_t)(ev + 127);
-  }
-  const float fk = exp2_neg_int(ek), fv = exp2_neg_int(ev);
+  if (tid == 0) *ex = (uint8_t)(e + 127);  // (every thread has read the old one: the barrier above)
+  const float f = exp2_neg_int(e);
+  for (int from = lo; from < hi; from += NR * RPI) {
+    if (!once) load(from);
 #pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    const int row = lo + r0 + i * rstep;
-    if (row >= hi) continue;
-    uint32_t ko[2], vo[2];
-    const uint32_t w[4] = {vraw[i].x, vraw[i].y, vraw[i].z, vraw[i].w};
+    for (int i = 0; i < NR; ++i) {
+      if (!once) turned(from, i, x[i]);
+      const int row = from + r0 + i * RPI;
+      uint32_t o[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      ko[j] = (uint32_t)float2_to_e4m3x2(kx[i][4 * j] * fk, kx[i][4 * j + 1] * fk) |
-              ((uint32_t)float2_to_e4m3x2(kx[i][4 * j + 2] * fk, kx[i][4 * j + 3] * fk) << 16);
-      vo[j] = (uint32_t)float2_to_e4m3x2(__uint_as_float(w[2 * j] << 16) * fv,
-                                         __uint_as_float(w[2 * j] & 0xFFFF0000u) * fv) |
-              ((uint32_t)float2_to_e4m3x2(__uint_as_float(w[2 * j + 1] << 16) * fv,
-                                          __uint_as_float(w[2 * j + 1] & 0xFFFF0000u) * fv)
-               << 16);
+      for (int j = 0; j < 2; ++j)
+        o[j] = (uint32_t)float2_to_e4m3x2(x[i][4 * j] * f, x[i][4 * j + 1] * f) |
+               ((uint32_t)float2_to_e4m3x2(x[i][4 * j + 2] * f, x[i][4 * j + 3] * f) << 16);
+      if (row < hi) *reinterpret_cast<uint2*>(dst + (int64_t)(row - first) * rstride + 8 * c) = make_uint2(o[0], o[1]);
     }
-    *reinterpret_cast<uint2*>(kc + (int64_t)(row - first) * p.k_row_stride + 8 * c) = make_uint2(ko[0], ko[1]);
-    *reinterpret_cast<uint2*>(vc + (int64_t)(row - first) * p.v_row_stride + 8 * c) = make_uint2(vo[0], vo[1]);
   }
 }
 
-template <int D, int NR>
-cudaError_t launch_append(const dsv4_gqa_append_params& p, dim3 grid, int threads, int q_ctas, int pages,
-                          cudaStream_t s) {
+template <int D, int THREADS>
+cudaError_t launch_append(const dsv4_gqa_append_params& p, dim3 grid, int q_ctas, int pages, cudaStream_t s) {
   return p.cache_dtype == DSV4_E4M3_PAGE
-             ? launch_pdl(append_kernel<D, NR, true>, grid, dim3(threads), 0, s, true, p, q_ctas, pages)
-             : launch_pdl(append_kernel<D, NR, false>, grid, dim3(threads), 0, s, true, p, q_ctas, pages);
+             ? launch_pdl(append_kernel<D, true, THREADS>, grid, dim3(THREADS), 0, s, true, p, q_ctas, pages)
+             : launch_pdl(append_kernel<D, false, THREADS>, grid, dim3(THREADS), 0, s, true, p, q_ctas, pages);
 }
 
 }  // namespace gqa
@@ -263,20 +281,15 @@ cudaError_t launch_gqa_append(const dsv4_gqa_append_params& p, cudaStream_t s) {
   const int max_n = p.max_q_len < p.T ? p.max_q_len : p.T;
   const int pages = (max_n + p.page_size - 2) / p.page_size + 1;  // pages a sequence's new rows can touch
   const int q_ctas = p.q != nullptr ? p.T : 0;
-  const int64_t grid = (int64_t)q_ctas + (int64_t)p.B * pages * p.kv_heads;
+  const int64_t grid = (int64_t)q_ctas + 2 * (int64_t)p.B * pages * p.kv_heads;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const int chunks = p.page_size * p.head_dim / 8;  // of a whole page: NR a thread
-  const int nr = chunks <= 256 ? 1 : chunks <= 512 ? 2 : 4;
-  const int threads = chunks / nr < 256 ? 256 : chunks / nr;
   const dim3 g((unsigned)grid);
-  if (p.head_dim == 128) {
-    if (nr == 1) return gqa::launch_append<128, 1>(p, g, threads, q_ctas, pages, s);
-    if (nr == 2) return gqa::launch_append<128, 2>(p, g, threads, q_ctas, pages, s);
-    return gqa::launch_append<128, 4>(p, g, threads, q_ctas, pages, s);
-  }
-  if (nr == 1) return gqa::launch_append<64, 1>(p, g, threads, q_ctas, pages, s);
-  if (nr == 2) return gqa::launch_append<64, 2>(p, g, threads, q_ctas, pages, s);
-  return gqa::launch_append<64, 4>(p, g, threads, q_ctas, pages, s);
+  // Few rows a page (decode steps): two warps hold them, and their barrier and idle lanes cost less than eight's.
+  const int rows = max_n < p.page_size ? max_n : p.page_size;
+  const bool small = rows * p.head_dim / 8 <= 64 * 4;
+  if (p.head_dim == 128)
+    return small ? gqa::launch_append<128, 64>(p, g, q_ctas, pages, s) : gqa::launch_append<128, 256>(p, g, q_ctas, pages, s);
+  return small ? gqa::launch_append<64, 64>(p, g, q_ctas, pages, s) : gqa::launch_append<64, 256>(p, g, q_ctas, pages, s);
 }
 
 cudaError_t read_flags_gqa_append(uint32_t* f) {

@@ -77,7 +77,7 @@ typedef struct dsv4_gqa_append_params {
   const int32_t* q_start;      /* [B + 1] */
   const int32_t* kv_len;       /* [B] */
   int32_t max_q_len;           /* host bound on n_b, >= 1 */
-  const float* cos_sin;        /* [max_pos, rope_dim] or NULL: nothing is rotated */
+  const float* cos_sin;        /* [max_pos, rope_dim], 16-byte aligned, or NULL: nothing is rotated */
   int32_t max_pos;             /* bound on kv_len when cos_sin is given */
   int32_t rope_first, rope_dim;  /* rope_first a multiple of 8, rope_dim of 16, within head_dim */
   int32_t rope_halves;

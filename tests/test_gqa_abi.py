@@ -75,7 +75,7 @@ def append_params(abi, **kw):
     (dict(v_cache_head_stride=-8192), -1),
     (dict(q=0x20000), -1), (dict(q=0x20000, q_out=0x30004), -1), (dict(q=0x20000, q_out=0x20000, q_out_token_stride=2048), -1),
     (dict(cos_sin=0x20000, rope_dim=24), -1), (dict(cos_sin=0x20000, rope_first=4), -1),
-    (dict(cos_sin=0x20000, rope_first=72), -1), (dict(cos_sin=0x20000, max_pos=0), -1), (dict(cos_sin=0x20002), -1),
+    (dict(cos_sin=0x20000, rope_first=72), -1), (dict(cos_sin=0x20000, max_pos=0), -1), (dict(cos_sin=0x20008), -1),
     (dict(struct_size=8), -1),
 ])
 def test_append_refusals(abi, kw, status):
