@@ -142,6 +142,20 @@ __device__ __forceinline__ void rotate_queries(const dsv4_gqa_append_params& p, 
   }
 }
 
+// The queries of a long append, after append_kernel on the stream: starts once that one's CTAs have all started
+// (which were let go when the kernels before had finished), and ends after it.
+template <int D>
+__global__ void __launch_bounds__(256, 4) append_queries_kernel(dsv4_gqa_append_params p) {
+  pdl_start(true);
+  Rope rope;
+  rope.cos_sin = p.cos_sin;
+  rope.first = p.rope_first;
+  rope.half = p.rope_dim / 2;
+  rope.halves = p.rope_halves;
+  rotate_queries<D, 256>(p, rope, blockIdx.x);
+  pdl_wait();
+}
+
 template <int D, bool E4M3, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 64 ? 8 : E4M3 ? 2 : 3)
     append_kernel(dsv4_gqa_append_params p, int q_ctas, int pages_per_seq) {
@@ -281,15 +295,21 @@ cudaError_t launch_gqa_append(const dsv4_gqa_append_params& p, cudaStream_t s) {
   const int max_n = p.max_q_len < p.T ? p.max_q_len : p.T;
   const int pages = (max_n + p.page_size - 2) / p.page_size + 1;  // pages a sequence's new rows can touch
   const int q_ctas = p.q != nullptr ? p.T : 0;
-  const int64_t grid = (int64_t)q_ctas + 2 * (int64_t)p.B * pages * p.kv_heads;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const dim3 g((unsigned)grid);
   // Few rows a page (decode steps): two warps hold them, and their barrier and idle lanes cost less than eight's.
   const int rows = max_n < p.page_size ? max_n : p.page_size;
+  // There the queries ride along; else they are a second kernel, whose CTAs need half the registers.
   const bool small = rows * p.head_dim / 8 <= 64 * 4;
-  if (p.head_dim == 128)
-    return small ? gqa::launch_append<128, 64>(p, g, q_ctas, pages, s) : gqa::launch_append<128, 256>(p, g, q_ctas, pages, s);
-  return small ? gqa::launch_append<64, 64>(p, g, q_ctas, pages, s) : gqa::launch_append<64, 256>(p, g, q_ctas, pages, s);
+  const int64_t grid = 2 * (int64_t)p.B * pages * p.kv_heads + (small ? q_ctas : 0);
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const dim3 g((unsigned)grid);
+  if (small)
+    return p.head_dim == 128 ? gqa::launch_append<128, 64>(p, g, q_ctas, pages, s)
+                             : gqa::launch_append<64, 64>(p, g, q_ctas, pages, s);
+  const cudaError_t e = p.head_dim == 128 ? gqa::launch_append<128, 256>(p, g, 0, pages, s)
+                                          : gqa::launch_append<64, 256>(p, g, 0, pages, s);
+  if (e != cudaSuccess || q_ctas == 0) return e;
+  return p.head_dim == 128 ? launch_pdl(gqa::append_queries_kernel<128>, dim3(q_ctas), dim3(256), 0, s, true, p)
+                           : launch_pdl(gqa::append_queries_kernel<64>, dim3(q_ctas), dim3(256), 0, s, true, p);
 }
 
 cudaError_t read_flags_gqa_append(uint32_t* f) {
