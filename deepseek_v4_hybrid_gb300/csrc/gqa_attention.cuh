@@ -41,8 +41,8 @@ __device__ __forceinline__ float finish_scale(const dsv4_gqa_attention_params& p
   float L = 0.f;
   if (m > -INFINITY) L = l * tc::ex2_approx(m - mf);
   if (sink > -INFINITY) L += tc::ex2_approx(sink - mf);
-  if (write && p.lse) p.lse[row] = mf > -INFINITY ? (mf + log2f(L)) * LN2 : -INFINITY;
-  return mo > -INFINITY ? tc::ex2_approx(mo - mf) / L : 0.f;
+  if (write && p.lse) p.lse[row] = mf > -INFINITY ? (mf + __log2f(L)) * LN2 : -INFINITY;
+  return mo > -INFINITY ? tc::ex2_approx(mo - mf) * rcp_approx(L) : 0.f;
 }
 
 // Stores 4 consecutive dims of an output row.

@@ -6,11 +6,13 @@
 //   O_i += P_i V           M = 128 rows, N = head_dim, K = 128 cache rows     (tensor memory x shared memory)
 // TMEM: S_0, S_1 (128 columns each; P_i as bf16 over the first half of S_i), O_0, O_1.
 //   Warps 0-3 and 4-7 (a warpgroup a tile): a thread owns a row: reads S from TMEM, masks, caps, takes the online
-//   softmax in log2 units (O is rescaled only when a row's maximum grows by more than 2^8) and writes P back;
-//   loads its tile's queries at a unit's start and writes the output at its end.
-//   Warp 8 loads key and value tiles by TMA (one box a page) into a ring of four tiles.
-//   Lane 0 of warp 9 issues the MMAs: P_0 V, S_0 of the next tile, P_1 V, S_1 of the next tile, so that the
-//   tensor cores work on one tile while the other's softmax runs.
+//   softmax in log2 units (O is rescaled only when a row's maximum grows by more than 2^8) and writes P back.
+//   Warps 8-11 write the output of a finished unit while the softmax is at the next one.
+//   Warp 12 loads key and value tiles by TMA (one box a page) into a ring of four tiles.
+//   Warp 13 issues the MMAs: P_0 V, S_0 of the next tile, P_1 V, S_1 of the next tile, so that the tensor cores
+//   work on one tile while the other's softmax runs.  (Two warps, one a tile, mix the tiles' MMAs and lost 12 %.)
+//   Warps 14 and 15 load the tiles' queries: by TMA where the group divides 128 (a box of tokens x heads is
+//   128 rows), else by cp.async.
 // Bound by the tensor cores and, at head_dim 64 or with capped scores, by the exponentials.
 //
 // The work of a batch is one list of key tiles, ordered (sequence, kv head, unit), a unit weighing its tiles
@@ -32,9 +34,12 @@ namespace gqa {
 namespace pre {
 
 constexpr int TILE = 128, UROWS = 256;
-constexpr int SOFTMAX_WARPS = 8, W_LOAD = 8, W_MMA = 9, THREADS = 320;
+constexpr int SOFTMAX_WARPS = 8, W_OUT = 8, W_LOAD = 12, W_MMA = 13, W_QUERY = 14, THREADS = 512;
+// Registers a thread: 512 x 128 at launch = 256 x 168 (softmax) + 128 x 96 (output) + 128 x 80 (the rest).
+constexpr int REGS_SOFTMAX = 168, REGS_OUT = 96, REGS_REST = 80;
 constexpr int NSLOT = 4;
 constexpr int UNIT_COST = 3;
+constexpr int FEW_ROWS = 1024;
 constexpr int MAX_UNITS = 8192;   // units of the evenly cut list; above, a CTA takes a whole unit
 constexpr float LAZY = 8.f;
 constexpr uint32_t FLAG_TIMEOUT = 4u;
@@ -53,6 +58,7 @@ struct Args {
   int G;
   int even;          // 1: the list is cut evenly, 0: a CTA takes a whole unit
   int box;           // cache rows of a TMA box
+  int q_tma;         // 1: queries by TMA
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -60,7 +66,8 @@ struct Args {
 // ------------------------------------------------------------------------------------------------
 constexpr int PREP_THREADS = 256, EXPAND_ROWS = 64;
 
-__device__ __forceinline__ void plan_unit(const Args& a, int u) {
+// Unit u's rows and tiles (a warp).
+__device__ __forceinline__ int4 plan_unit(const Args& a, int u) {
   const dsv4_gqa_attention_params& p = a.p;
   const int lane = threadIdx.x & 31;
   const int b = u / a.tps, tile = u % a.tps, group = p.q_heads / p.kv_heads;
@@ -103,7 +110,7 @@ __device__ __forceinline__ void plan_unit(const Args& a, int u) {
     if (bad && lane == 0) atomicOr(&g_flags_gp, FLAG_PAGE);
     e = make_int4(lo, end, n[0], n[1] | (bad ? 1 << 30 : 0));
   }
-  if (lane == 0) a.unit[u] = e;
+  return e;
 }
 
 template <int D>
@@ -157,7 +164,10 @@ __global__ void __launch_bounds__(PREP_THREADS) prepare_kernel(Args a, int plan_
   pdl_launch_dependents();
   if ((int)blockIdx.x < plan_ctas) {
     const int u = blockIdx.x * (PREP_THREADS / 32) + (threadIdx.x >> 5);
-    if (u < a.p.B * a.tps) plan_unit(a, u);
+    if (u < a.p.B * a.tps) {
+      const int4 e = plan_unit(a, u);
+      if ((threadIdx.x & 31) == 0) a.unit[u] = e;
+    }
   } else {
     expand_rows<D>(a, blockIdx.x - plan_ctas);
   }
@@ -198,7 +208,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 struct Smem {
-  uint64_t full[NSLOT], empty[NSLOT], vraw, qfull[2], sfull[2], phalf[2], pfull[2], odone[2];
+  uint64_t full[NSLOT], empty[NSLOT], vraw, qfull[2], qfree[2], sfull[2], phalf[2], pfull[2], odone[2], ofree[2], stats[2], drain;
+  float2 stat[2][TILE];  // a finished tile's (maximum, sum) of each row
+  int4 one;              // whole units: the CTA's
   int64_t first, last, u0;
   int64_t wsum[THREADS / 32];
   int64_t per;
@@ -231,9 +243,10 @@ struct Segment {
 struct Walk {
   int b, h, tile;
   int64_t u0;
+  const int4* one;  // whole units: the CTA's only entry
   __device__ __forceinline__ bool next(const Args& a, int64_t first, int64_t last, Segment& g) {
     while (u0 < last && b < a.p.B) {
-      const int4 e = a.unit[(int64_t)b * a.tps + tile];
+      const int4 e = one ? *one : a.unit[(int64_t)b * a.tps + tile];
       g.n[0] = e.z;
       g.n[1] = e.w & 0x3FFFFFFF;
       g.bad = (e.w >> 30) & 1;
@@ -269,7 +282,8 @@ struct Walk {
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
-    prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, Args a) {
+    prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap qmap, Args a) {
   constexpr int QT = TILE * D * 2;     // bytes of a query tile, and of a key or value tile
   constexpr int HB = TILE * 128;       // one 64-dim half of it (or all, D = 64)
   constexpr uint32_t COL_O = 256;
@@ -278,8 +292,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* mem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_mem) + 1023) & ~uintptr_t(1023));
   uint8_t* q_mem = mem;
   uint8_t* kv_mem = mem + 2 * QT;
-  uint8_t* stage_mem = mem + 2 * QT + NSLOT * QT;  // 2 KB a softmax warp
-  Smem* sm = reinterpret_cast<Smem*>(stage_mem + SOFTMAX_WARPS * 2048);
+  uint8_t* stage_mem = mem + 2 * QT + NSLOT * QT;  // 2 KB an output warp
+  Smem* sm = reinterpret_cast<Smem*>(stage_mem + 4 * 2048);
   volatile int* abort = &sm->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -290,8 +304,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::mbar_init(&sm->empty[i], 1);
     }
     tc::mbar_init(&sm->vraw, 1);
+    tc::mbar_init(&sm->drain, 1);
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sm->qfull[i], 4);
+      tc::mbar_init(&sm->qfull[i], 1);
+      tc::mbar_init(&sm->qfree[i], 1);
+      tc::mbar_init(&sm->ofree[i], 4);
+      tc::mbar_init(&sm->stats[i], 4);
       tc::mbar_init(&sm->sfull[i], 1);
       tc::mbar_init(&sm->phalf[i], 4);
       tc::mbar_init(&sm->pfull[i], 4);
@@ -363,19 +381,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         sm->tile = tl;
         sm->u0 = base + (tl ? pre[(int64_t)lo * a.tps + tl - 1] - before : 0);
       }
-      a.cut[blockIdx.x] = make_int4(0, 0, -1, 0);
     }
-  } else if (tid == 0) {
+    if (tid == W_OUT * 32) a.cut[blockIdx.x] = make_int4(0, 0, -1, 0);  // (its writer later)
+  } else if (warp == 0) {
     // a whole unit a CTA: units fastest and the last ones (which see most) first, then heads, then sequences
     const int64_t x = blockIdx.x;
-    sm->tile = a.tps - 1 - (int)(x % a.tps);
-    sm->h = (int)(x / a.tps % p.kv_heads);
-    sm->b = (int)(x / a.tps / p.kv_heads);
-    const int4 e = a.unit[(int64_t)sm->b * a.tps + sm->tile];
-    const int n = max(e.z, e.w & 0x3FFFFFFF);
-    sm->u0 = sm->first = 0;
-    sm->last = n ? n + UNIT_COST : 0;
-    sm->per = 1;
+    const int tile = a.tps - 1 - (int)(x % a.tps), b = (int)(x / a.tps / p.kv_heads);
+    const int4 e = plan_unit(a, b * a.tps + tile);
+    if (lane == 0) {
+      const int n = max(e.z, e.w & 0x3FFFFFFF);
+      sm->tile = tile;
+      sm->h = (int)(x / a.tps % p.kv_heads);
+      sm->b = b;
+      sm->one = e;
+      sm->u0 = sm->first = 0;
+      sm->last = n ? n + UNIT_COST : 0;
+      sm->per = 1;
+    }
   }
   tc::fence_proxy_async_smem();  // (the sums lie where key and value tiles will land)
   tc::tc_fence_before();
@@ -383,9 +405,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc::tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
   const int64_t first = sm->first, last = sm->last;
-  Walk walk{sm->b, sm->h, sm->tile, sm->u0};
+  Walk walk{sm->b, sm->h, sm->tile, sm->u0, a.even ? nullptr : &sm->one};
   Segment g;
 
+  if (warp >= W_LOAD) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
   if (warp == W_LOAD) {
     // ---------------- TMA loads
     int it = 0, armed = 0;  // tiles handed out, tiles armed on their own barrier
@@ -465,14 +489,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint64_t qd = tc::sdesc_k_sw128(tc::smem_addr(q_mem)), kd = tc::sdesc_k_sw128(tc::smem_addr(kv_mem));
     const uint64_t vd = tc::sdesc_mn_sw128(tc::smem_addr(kv_mem), HB, 1024);
     int it = 0;
-    uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
+    uint32_t qph[2] = {0, 0}, pph[2] = {0, 0}, oph[2] = {1, 1};  // (ofree: nothing to wait for the first time)
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_bounded(bar, phase, abort));
       tc::tc_fence_after();
     };
     auto wait_full = [&](int x) { wait(&sm->full[x % NSLOT], (x / NSLOT) & 1); };
-    auto scores = [&](int i, int x) {
+    auto scores = [&](int i, int x, bool last_one) {
       const uint64_t kb = kd + (uint64_t)((x % NSLOT) * QT >> 4), qb = qd + (uint64_t)(i * QT >> 4);
       if (elect_one()) {
 #pragma unroll
@@ -482,6 +506,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::mma_bf16(tm + 128 * i, qb + (uint64_t)((c * HB + s * 32) >> 4), kb + (uint64_t)((c * HB + s * 32) >> 4),
                          idesc_s, (c | s) != 0);
         tc::mma_commit(&sm->sfull[i]);
+        if (last_one) tc::mma_commit(&sm->qfree[i]);
       }
       __syncwarp();
     };
@@ -509,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (cnt[i] && ok) {
           wait(&sm->qfull[i], qph[i]);
           qph[i] ^= 1u;
-          if (ok) scores(i, it);
+          if (ok) scores(i, it, cnt[i] == 1);
         }
       if (!ok) break;
       release(it);
@@ -518,6 +543,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (ok && k < cnt[i]) {
+            if (k == 0) {
+              wait(&sm->ofree[i], oph[i]);  // the output of the unit before has been read
+              oph[i] ^= 1u;
+            }
             wait(&sm->phalf[i], pph[i]);
             if (!ok) break;
             values(i, it + 1, 0, k > 0, false);
@@ -528,7 +557,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           if (ok && k + 1 < n) {
             if (i == 0) wait_full(it + 2);
-            if (ok && k + 1 < cnt[i]) scores(i, it + 2);
+            if (ok && k + 1 < cnt[i]) scores(i, it + 2, k + 2 == cnt[i]);
           }
         }
         if (!ok) break;
@@ -536,33 +565,49 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (k + 1 < n) release(it + 2);
       }
     }
-  } else {
-    // ---------------- softmax: warpgroup i owns row tile i, a thread a row
-    const int i = warp >> 2, R = (warp & 3) * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = lanes + 128 * i, t_o = lanes + COL_O + D * i;
-    const uint32_t group = p.q_heads / p.kv_heads;
-    const uint32_t rpi_q = (256u / D) / group, rpi_r = (256u / D) % group;  // rows a warp loads at once
-    const bool plain = p.softcap == 0.f && p.slopes == nullptr && p.softmax_scale > 0.f;
-    const float cl = p.softmax_scale * LOG2E;
-    const float rcap2 = p.softcap > 0.f ? 2.f * LOG2E / p.softcap : 0.f;
-    uint32_t sph = 0, oph = 0;
-    // Queries of a segment's row tile into shared memory, each warp its own 32 rows (whole rows by consecutive
-    // lanes), then handed to the MMA warp.  The tile's scores before must have been read.
-    auto load_queries = [&](const Segment& g) {
-      constexpr int CPR = D / 8, RPI = 32 / CPR;
+    if (!ok) {  // gave up: no MMA may still run when tensor memory is returned
+      volatile int none = 0;
+      if (elect_one()) tc::mma_commit(&sm->drain);
+      __syncwarp();
+      tc::mbar_wait_bounded(&sm->drain, 0, &none, 50000000ull);
+    }
+  } else if (warp >= W_QUERY) {
+    // ---------------- queries of row tile i
+    const int i = warp - W_QUERY;
+    constexpr int CPR = D / 8, RPI = 32 / CPR;
+    const uint32_t group = p.q_heads / p.kv_heads, rpi_q = RPI / group, rpi_r = RPI % group;
+    uint32_t fph = 1, armed = 0;  // (qfree: nothing to wait for the first time)
+    bool ok = true;
+    while (ok && walk.next(a, first, last, g)) {
+      if (!g.count(i)) continue;
       const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
-      const uint32_t r0 = (uint32_t)g.tile * UROWS + i * TILE + (warp & 3) * 32 + lane / CPR, rows = (uint32_t)s.n * group;
-      uint32_t tok = r0 / group, head = r0 % group;  // of this lane's first row; then RPI rows on each time
+      const uint32_t r0 = (uint32_t)g.tile * UROWS + i * TILE;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->qfree[i], fph, abort));
+      fph ^= 1u;
+      if (!ok) break;
+      if (a.q_tma) {
+        // (rows of tokens behind the sequence's: another's, or zeros; their output is not written)
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(&sm->qfull[i], QT);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(q_mem + i * QT + c * HB, &qmap, c * 64, g.h * (int)group, s.t0 + (int)(r0 / group), 0, &sm->qfull[i]);
+        }
+        ++armed;
+        __syncwarp();
+        continue;
+      }
+      const uint32_t r = r0 + lane / CPR, rows = (uint32_t)s.n * group;
+      uint32_t tok = r / group, head = r % group;  // of this lane's first row; then RPI rows on each time
       const int ch = lane % CPR;
       uint8_t* dst = q_mem + i * QT + (ch >> 3) * HB;
       const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)s.t0 * p.q_token_stride +
                                  (int64_t)g.h * group * p.q_head_stride + 8 * ch;
 #pragma unroll 4
-      for (int x = 0; x < 32 / RPI; ++x) {
-        const int Rr = (warp & 3) * 32 + x * RPI + lane / CPR;
-        const bool in = r0 + x * RPI < rows;
-        tc::cp_async16(dst + Rr * 128 + (((ch & 7) ^ (Rr & 7)) << 4),
+      for (int x = 0; x < TILE / RPI; ++x) {
+        const int R = x * RPI + lane / CPR;
+        const bool in = r + x * RPI < rows;
+        tc::cp_async16(dst + R * 128 + (((ch & 7) ^ (R & 7)) << 4),
                        in ? src + (int64_t)tok * p.q_token_stride + (int64_t)head * p.q_head_stride
                           : reinterpret_cast<const __nv_bfloat16*>(p.q),
                        in ? 16u : 0u);
@@ -578,24 +623,128 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm->qfull[i]);
-    };
-    bool ok = true, have = walk.next(a, first, last, g);
-    if (have && g.count(i)) load_queries(g);
-    while (ok && have) {
+    }
+    if (!ok && armed) {  // gave up: no copy may still be on its way when the CTA ends
+      volatile int none = 0;
+      tc::mbar_wait_bounded(&sm->qfull[i], (armed - 1) & 1, &none, 50000000ull);
+    }
+  }
+  } else if (warp >= W_OUT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OUT));
+    // ---------------- output: warp W_OUT + y writes rows 32 y .. 32 y + 31 of both tiles
+    const uint32_t group = p.q_heads / p.kv_heads;
+    uint32_t oph[2] = {0, 0};
+    bool ok = true;
+    while (ok && walk.next(a, first, last, g)) {
       const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
-      const int r = i * TILE + R;
-      const uint32_t ru = (uint32_t)g.tile * UROWS + r;
+      const int slot = 2 * blockIdx.x + (g.u0 <= first ? 0 : 1);
+      const uint32_t n_rows = (uint32_t)s.n * group;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const int R = (warp & 3) * 32 + lane, r = i * TILE + R;
+        const uint32_t t_o = tmem + ((uint32_t)((warp & 3) * 32) << 16) + COL_O + D * i;
+        const uint32_t ru = (uint32_t)g.tile * UROWS + r;
+        const bool live = ru < n_rows;
+        const int head = g.h * (int)group + (int)(ru % group);
+        const int64_t row = (int64_t)(s.t0 + (int)(ru / group)) * p.q_heads + head;
+        const int cnt = g.count(i);
+        float m = -INFINITY, l = 0.f;
+        if (cnt) {
+          ok = tc::mbar_wait_bounded(&sm->stats[i], oph[i], abort) && tc::mbar_wait_bounded(&sm->odone[i], oph[i], abort);
+          ok = __all_sync(0xffffffffu, ok);
+          oph[i] ^= 1u;
+          if (!ok) break;
+          tc::tc_fence_after();
+          const float2 ml = sm->stat[i][R];
+          m = ml.x;
+          l = ml.y;
+        }
+        const bool some = m > -INFINITY;  // (a row that saw nothing: what O holds does not matter)
+        float f = 1.f;
+        if (g.whole) {
+          if (live) f = finish_scale(p, row, head, m, l, m, true);
+        } else {
+          a.ml_part[(int64_t)slot * UROWS + r] = make_float2(m, l);
+        }
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (cnt) {
+            tc::tmem_ld32_nowait(t_o + c, o);
+            tc::tmem_wait_ld_regs<32>(o);
+          }
+#pragma unroll
+          for (int d = 0; d < 32; ++d) o[d] = some ? __float_as_uint(__uint_as_float(o[d]) * f) : 0u;
+          if (!g.whole) {
+            float4* dst = a.o_part + (((int64_t)slot * 8 + i * 4 + (warp & 3)) * (D / 4) + c / 4) * 32 + lane;
+#pragma unroll
+            for (int d = 0; d < 32; d += 4)
+              dst[d * 8] = make_float4(__uint_as_float(o[d]), __uint_as_float(o[d + 1]), __uint_as_float(o[d + 2]),
+                                       __uint_as_float(o[d + 3]));
+          } else if (p.out_dtype == DSV4_F32) {
+            if (live) {
+#pragma unroll
+              for (int d = 0; d < 32; d += 4)
+                *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.out) + row * D + c + d) =
+                    make_uint4(o[d], o[d + 1], o[d + 2], o[d + 3]);
+            }
+          } else {
+            // 32 dims of the warp's 32 rows turn in shared memory (16-byte pieces, exchanged by row), so that a store
+            // writes whole sectors of 8 rows
+            uint4* stage = reinterpret_cast<uint4*>(stage_mem) + (warp & 3) * 128;
+            __syncwarp();
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[y] = float2_to_bf16x2_bits(__uint_as_float(o[8 * d + 2 * y]), __uint_as_float(o[8 * d + 2 * y + 1]));
+              stage[lane * 4 + (d ^ ((lane >> 1) & 3))] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int rr = x * 8 + (lane >> 2), d = lane & 3;
+              const uint4 w = stage[rr * 4 + (d ^ ((rr >> 1) & 3))];
+              const int64_t ro = __shfl_sync(0xffffffffu, row, rr);
+              if ((uint32_t)g.tile * UROWS + i * TILE + (warp & 3) * 32 + rr < n_rows)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + ro * D + c + 8 * d) = w;
+            }
+          }
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (cnt && lane == 0) tc::mbar_arrive(&sm->ofree[i]);
+      }
+      if (warp == W_OUT && lane == 0 && !g.whole && g.k0 == 0)
+        // the unit's first piece: it goes on up to the CTA of its last tile
+        a.cut[blockIdx.x] = make_int4(g.b * a.tps + g.tile, g.h, (int)((g.u0 + g.w - 1) / sm->per), g.u0 <= first ? 0 : 1);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    // ---------------- softmax: warpgroup i owns row tile i, a thread a row
+    const int i = warp >> 2, R = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t t_s = lanes + 128 * i, t_o = lanes + COL_O + D * i;
+    const uint32_t group = p.q_heads / p.kv_heads;
+    const bool plain = p.softcap == 0.f && p.slopes == nullptr && p.softmax_scale > 0.f;
+    const float cl = p.softmax_scale * LOG2E;
+    const float rcap2 = p.softcap > 0.f ? 2.f * LOG2E / p.softcap : 0.f;
+    uint32_t sph = 0, fph = 1;  // (ofree: nothing to wait for the first time)
+    bool ok = true;
+    while (ok && walk.next(a, first, last, g)) {
+      const int cnt = g.count(i);
+      if (!cnt) continue;
+      const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
+      const uint32_t ru = (uint32_t)g.tile * UROWS + i * TILE + R;
       const bool live = ru < (uint32_t)s.n * group;
       const int tok = (int)(ru / group), head = g.h * (int)group + (int)(ru % group), pos = s.kv - s.n + tok;
-      Segment gn;
-      have = walk.next(a, first, last, gn);
       int2 vis = make_int2(0, 0);
       float slope = 0.f;
       if (live) {
         vis = visible_rows(p, g.b, s.t0 + tok, pos, s.kv);
         if (p.slopes) slope = p.slopes[head] * LOG2E;
       }
-      const int cnt = g.count(i);
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < cnt; ++k) {
         ok = tc::mbar_wait_bounded(&sm->sfull[i], sph, abort);
@@ -720,73 +869,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) tc::mbar_arrive(&sm->pfull[i]);
       }
       if (!ok) break;
-      if (have && gn.count(i)) load_queries(gn);  // its first scores run beside this segment's end
-      if (cnt) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->odone[i], oph, abort));
-        oph ^= 1u;
-        if (!ok) break;
-        tc::tc_fence_after();
-      }
-      const int64_t row = (int64_t)(s.t0 + tok) * p.q_heads + head;
-      const int slot = 2 * blockIdx.x + (g.u0 <= first ? 0 : 1);
-      const bool some = cnt && m > -INFINITY;  // (a row that saw nothing: what O holds does not matter)
-      float f = 1.f;
-      if (g.whole) {
-        if (live) f = finish_scale(p, row, head, m, l, m, true);
-      } else {
-        a.ml_part[(int64_t)slot * UROWS + r] = make_float2(m, l);
-      }
-      const uint32_t n_rows = (uint32_t)s.n * group;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (cnt) {
-          tc::tmem_ld32_nowait(t_o + c, o);
-          tc::tmem_wait_ld_regs<32>(o);
-        }
-#pragma unroll
-        for (int d = 0; d < 32; ++d) o[d] = some ? __float_as_uint(__uint_as_float(o[d]) * f) : 0u;
-        if (!g.whole) {
-          float4* dst = a.o_part + (((int64_t)slot * 8 + warp) * (D / 4) + c / 4) * 32 + lane;
-#pragma unroll
-          for (int d = 0; d < 32; d += 4)
-            dst[d * 8] = make_float4(__uint_as_float(o[d]), __uint_as_float(o[d + 1]), __uint_as_float(o[d + 2]),
-                                     __uint_as_float(o[d + 3]));
-        } else if (p.out_dtype == DSV4_F32) {
-          if (live) {
-#pragma unroll
-            for (int d = 0; d < 32; d += 4)
-              *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.out) + row * D + c + d) =
-                  make_uint4(o[d], o[d + 1], o[d + 2], o[d + 3]);
-          }
-        } else {
-          // 32 dims of the warp's 32 rows turn in shared memory (16-byte pieces, exchanged by row), so that a store
-          // writes whole sectors of 8 rows
-          uint4* stage = reinterpret_cast<uint4*>(stage_mem) + warp * 128;
-          __syncwarp();
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            uint32_t w[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              w[y] = float2_to_bf16x2_bits(__uint_as_float(o[8 * d + 2 * y]), __uint_as_float(o[8 * d + 2 * y + 1]));
-            stage[lane * 4 + (d ^ ((lane >> 1) & 3))] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int rr = x * 8 + (lane >> 2), d = lane & 3;
-            const uint4 w = stage[rr * 4 + (d ^ ((rr >> 1) & 3))];
-            const int64_t ro = __shfl_sync(0xffffffffu, row, rr);
-            if ((uint32_t)g.tile * UROWS + i * TILE + (warp & 3) * 32 + rr < n_rows)
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + ro * D + c + 8 * d) = w;
-          }
-        }
-      }
-      tc::tc_fence_before();
-      if (tid == 0 && !g.whole && g.k0 == 0)  // the unit's first piece: it goes on up to the CTA of its last tile
-        a.cut[blockIdx.x] = make_int4(g.b * a.tps + g.tile, g.h, (int)((g.u0 + g.w - 1) / sm->per), g.u0 <= first ? 0 : 1);
-      g = gn;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->ofree[i], fph, abort));  // the stats before have been read
+      fph ^= 1u;
+      if (!ok) break;
+      sm->stat[i][R] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm->stats[i]);
     }
   }
   tc::tc_fence_before();
@@ -854,8 +942,11 @@ static Plan plan(const dsv4_gqa_attention_params& p) {
   const int64_t max_n = p.max_q_len < p.T ? p.max_q_len : p.T;
   L.tps = (int)((max_n * (p.q_heads / p.kv_heads) + UROWS - 1) / UROWS);
   const int64_t units = (int64_t)p.B * L.tps;
-  L.even = units <= MAX_UNITS;
   L.G = num_sms();
+  // A CTA a unit where that fills the device at most twice with few key tiles each: it needs no list, no join and, for
+  // bf16 caches, no kernel before it.  (And beyond MAX_UNITS.)
+  const bool few = units * p.kv_heads <= 2 * L.G && p.max_kv_len <= FEW_ROWS;
+  L.even = units <= MAX_UNITS && !few;
   const size_t slots = L.even ? 2 * (size_t)L.G : 0;
   L.kv_pad = p.cache_dtype == DSV4_E4M3_PAGE ? (p.max_kv_len + TILE - 1) / TILE * TILE : 0;
   const size_t rows = (size_t)p.B * p.kv_heads * L.kv_pad * p.head_dim * 2;
@@ -894,7 +985,7 @@ static cudaError_t launch(const dsv4_gqa_attention_params& p, cudaStream_t s) {
   a.even = L.even;
   a.box = e4m3 || p.page_size > TILE ? TILE : p.page_size;
   const int64_t units = (int64_t)p.B * L.tps;
-  const int64_t plan_ctas = (units + PREP_THREADS / 32 - 1) / (PREP_THREADS / 32);
+  const int64_t plan_ctas = L.even ? (units + PREP_THREADS / 32 - 1) / (PREP_THREADS / 32) : 0;
   const int64_t expand = e4m3 ? (int64_t)p.B * p.kv_heads * (L.kv_pad / EXPAND_ROWS) : 0;
   const int64_t ctas = L.even ? L.G : units * p.kv_heads;
   if (plan_ctas + expand > 0x7FFFFFFF || ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
@@ -902,23 +993,34 @@ static cudaError_t launch(const dsv4_gqa_attention_params& p, cudaStream_t s) {
   cudaError_t e;
   if (e4m3) {
     const int64_t row = D * 2, head = row * L.kv_pad, seq = head * p.kv_heads;
-    e = make_tmap_4d_bf16(&kmap, a.bf_k, D, L.kv_pad, p.kv_heads, p.B, row, head, seq, 64, TILE);
-    if (e == cudaSuccess) e = make_tmap_4d_bf16(&vmap, a.bf_v, D, L.kv_pad, p.kv_heads, p.B, row, head, seq, 64, TILE);
+    e = make_tmap_4d_bf16(&kmap, a.bf_k, D, L.kv_pad, p.kv_heads, p.B, row, head, seq, 64, TILE, 1);
+    if (e == cudaSuccess) e = make_tmap_4d_bf16(&vmap, a.bf_v, D, L.kv_pad, p.kv_heads, p.B, row, head, seq, 64, TILE, 1);
   } else {
     const uint64_t pages = p.num_pages > 0 ? p.num_pages : 1;
     e = make_tmap_4d_bf16(&kmap, p.k_cache, D, p.page_size, p.kv_heads, pages, 2 * p.k_row_stride, 2 * p.k_cache_head_stride,
-                          2 * p.k_page_stride, 64, a.box);
+                          2 * p.k_page_stride, 64, a.box, 1);
     if (e == cudaSuccess)
       e = make_tmap_4d_bf16(&vmap, p.v_cache, D, p.page_size, p.kv_heads, pages, 2 * p.v_row_stride,
-                            2 * p.v_cache_head_stride, 2 * p.v_page_stride, 64, a.box);
+                            2 * p.v_cache_head_stride, 2 * p.v_page_stride, 64, a.box, 1);
   }
   if (e != cudaSuccess) return e;
-  const int smem = (2 + NSLOT) * TILE * D * 2 + SOFTMAX_WARPS * 2048 + (int)sizeof(Smem) + 1024;
+  // queries: a box of TILE / group tokens x the group's heads; strides TMA can take
+  const int group = p.q_heads / p.kv_heads;
+  CUtensorMap qmap = kmap;
+  const int64_t ts = 2 * p.q_token_stride, hs = 2 * p.q_head_stride;
+  a.q_tma = TILE % group == 0 && ts > 0 && hs > 0 && ts < (1LL << 40) && hs < (1LL << 40);
+  if (a.q_tma) {
+    e = make_tmap_4d_bf16(&qmap, p.q, D, p.q_heads, p.T, 1, hs, ts, ts * p.T, 64, group, TILE / group);
+    if (e != cudaSuccess) a.q_tma = 0;
+  }
+  const int smem = (2 + NSLOT) * TILE * D * 2 + 4 * 2048 + (int)sizeof(Smem) + 1024;
   e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(prefill_kernel<D>), smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(prepare_kernel<D>, dim3((unsigned)(plan_ctas + expand)), dim3(PREP_THREADS), 0, s, true, a, (int)plan_ctas);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(prefill_kernel<D>, dim3((unsigned)ctas), dim3(THREADS), smem, s, true, kmap, vmap, a);
+  if (plan_ctas + expand > 0) {
+    e = launch_pdl(prepare_kernel<D>, dim3((unsigned)(plan_ctas + expand)), dim3(PREP_THREADS), 0, s, true, a, (int)plan_ctas);
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_pdl(prefill_kernel<D>, dim3((unsigned)ctas), dim3(THREADS), smem, s, true, kmap, vmap, qmap, a);
   if (e != cudaSuccess || !L.even) return e;
   return launch_pdl(join_kernel<D>, dim3(L.G, UROWS / 32), dim3(256), 0, s, true, a);
 }

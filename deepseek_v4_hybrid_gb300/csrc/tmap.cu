@@ -50,12 +50,12 @@ cudaError_t make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* b
 }
 
 cudaError_t make_tmap_4d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
-                              uint64_t s1, uint64_t s2, uint64_t s3, uint32_t b0, uint32_t b1) {
+                              uint64_t s1, uint64_t s2, uint64_t s3, uint32_t b0, uint32_t b1, uint32_t b2) {
   std::call_once(g_once, load_encode);
   if (g_encode_err != cudaSuccess) return g_encode_err;
   const cuuint64_t dims[4] = {d0, d1, d2, d3};
   const cuuint64_t strides[3] = {s1, s2, s3};
-  const cuuint32_t box[4] = {b0, b1, 1, 1};
+  const cuuint32_t box[4] = {b0, b1, b2, 1};
   const cuuint32_t elem[4] = {1, 1, 1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, elem,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

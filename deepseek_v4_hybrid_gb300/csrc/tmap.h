@@ -20,9 +20,9 @@ cudaError_t make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* b
                          uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw);
 
 // 4-D bf16 tensor [d3, d2, d1, d0] (d0 innermost and contiguous; the others `s1`, `s2`, `s3` bytes apart), box of
-// [1, 1, b1, b0] elements with 128-byte swizzle (b0 * 2 must be 128).  Elements out of range read as zeros.
+// [1, b2, b1, b0] elements with 128-byte swizzle (b0 * 2 must be 128).  Elements out of range read as zeros.
 cudaError_t make_tmap_4d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
-                              uint64_t s1, uint64_t s2, uint64_t s3, uint32_t b0, uint32_t b1);
+                              uint64_t s1, uint64_t s2, uint64_t s3, uint32_t b0, uint32_t b1, uint32_t b2);
 
 // Multiprocessor count of the current device.
 int num_sms();

@@ -14,7 +14,7 @@
  *  - Batches are ragged: q_start[B + 1] holds the first flat token of each sequence; sequence b has
  *    n_b = q_start[b+1] - q_start[b] new tokens, and kv_len[b] rows INCLUDING them, so its token i is
  *    at position kv_len[b] - n_b + i.  n_b = 0 and kv_len[b] = 0 are allowed.  Tokens from q_start[B] on
- *    (the padding of a fixed-size batch) are neither read nor written.
+ *    (the padding of a fixed-size batch) are not written, and what they hold does not matter.
  *  - A sequence with q_start not in 0 <= q_start[b] <= q_start[b+1] <= T, n_b > max_q_len,
  *    kv_len[b] < n_b or kv_len[b] over the call's bound is skipped (its outputs stay as they were) and
  *    flagged (bit 0).
