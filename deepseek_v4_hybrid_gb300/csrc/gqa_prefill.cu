@@ -34,9 +34,9 @@ namespace gqa {
 namespace pre {
 
 constexpr int TILE = 128, UROWS = 256;
-constexpr int SOFTMAX_WARPS = 8, W_OUT = 8, W_LOAD = 12, W_MMA = 13, W_QUERY = 14, THREADS = 512;
-// Registers a thread: 512 x 128 at launch = 256 x 168 (softmax) + 128 x 96 (output) + 128 x 80 (the rest).
-constexpr int REGS_SOFTMAX = 168, REGS_OUT = 96, REGS_REST = 80;
+constexpr int W_OUT = 8, W_LOAD = 12, W_MMA = 13, W_QUERY = 14, THREADS = 512;
+// Registers a thread: 512 x 128 at launch = 256 x 136 (softmax) + 128 x 120 (output) + 128 x 120 (the rest).
+constexpr int REGS_SOFTMAX = 136, REGS_OUT = 120, REGS_REST = 120;
 constexpr int NSLOT = 4;
 constexpr int UNIT_COST = 3;
 constexpr int FEW_ROWS = 1024;
@@ -207,10 +207,79 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+struct Segment {
+  int b, h, tile;      // unit `tile` of sequence b, kv head h
+  int lo, end;         // rows seen by the unit: lo .. end - 1
+  int start;           // cache row of key tile 0
+  int k0, k1, n[2];    // this CTA's key tiles k0 .. k1 - 1; tiles of the two row tiles
+  bool bad, whole;
+  int slot;            // of a cut unit's partial results in this CTA
+  int64_t u0, w;       // the unit's place and weight in the list
+  __device__ int count(int i) const { return max(0, min(k1, n[i]) - k0); }
+};
+
+// The CTA's segments in order; every warp walks them by itself.
+struct Walk {
+  const int4* unit;
+  const int4* one;  // whole units: the CTA's only entry
+  int tps, heads, B, box;
+  int b, h, tile;
+  int64_t u0, first, last;
+  __device__ __forceinline__ bool next(Segment& g) {
+    while (u0 < last && b < B) {
+      const int4 e = one ? *one : unit[(int64_t)b * tps + tile];
+      g.n[0] = e.z;
+      g.n[1] = e.w & 0x3FFFFFFF;
+      g.bad = (e.w >> 30) & 1;
+      g.b = b;
+      g.h = h;
+      g.tile = tile;
+      g.lo = e.x;
+      g.end = e.y;
+      g.start = e.x & ~(box - 1);
+      g.u0 = u0;
+      const int n = max(g.n[0], g.n[1]);
+      g.w = n ? n + UNIT_COST : 0;
+      if (++tile == tps || n == 0) {  // (a sequence's units with work come first)
+        tile = 0;
+        if (++h == heads) {
+          h = 0;
+          ++b;
+        }
+      }
+      if (n == 0) continue;
+      u0 += g.w;
+      if (u0 <= first) continue;
+      const int64_t x0 = max(first, g.u0) - g.u0, x1 = min(last, u0) - g.u0;
+      g.k0 = (int)max((int64_t)0, x0 - UNIT_COST);
+      g.k1 = (int)max((int64_t)0, x1 - UNIT_COST);
+      if (g.k0 >= g.k1) continue;
+      g.whole = g.k0 == 0 && g.k1 == n;
+      g.slot = g.u0 <= first ? 0 : 1;
+      return true;
+    }
+    return false;
+  }
+};
+
+// A warp's walk, in shared memory: lane 0 takes the step, and the state takes no registers from the loops between.
+struct WarpWalk {
+  Walk w;
+  Segment g;
+  int have;
+  __device__ __forceinline__ bool next(int lane) {
+    __syncwarp();
+    if (lane == 0) have = w.next(g);
+    __syncwarp();
+    return have;
+  }
+};
+
 struct Smem {
   uint64_t full[NSLOT], empty[NSLOT], vraw, qfull[2], qfree[2], sfull[2], phalf[2], pfull[2], odone[2], ofree[2], stats[2], drain;
   float2 stat[2][TILE];  // a finished tile's (maximum, sum) of each row
   int4 one;              // whole units: the CTA's
+  WarpWalk walk[THREADS / 32];
   int64_t first, last, u0;
   int64_t wsum[THREADS / 32];
   int64_t per;
@@ -228,57 +297,6 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
-struct Segment {
-  int b, h, tile;      // unit `tile` of sequence b, kv head h
-  int lo, end;         // rows seen by the unit: lo .. end - 1
-  int start;           // cache row of key tile 0
-  int k0, k1, n[2];    // this CTA's key tiles k0 .. k1 - 1; tiles of the two row tiles
-  bool bad, whole;
-  int64_t u0, w;       // the unit's place and weight in the list
-  __device__ int count(int i) const { return max(0, min(k1, n[i]) - k0); }
-};
-
-// The CTA's segments in order; every role walks them by itself.
-struct Walk {
-  int b, h, tile;
-  int64_t u0;
-  const int4* one;  // whole units: the CTA's only entry
-  __device__ __forceinline__ bool next(const Args& a, int64_t first, int64_t last, Segment& g) {
-    while (u0 < last && b < a.p.B) {
-      const int4 e = one ? *one : a.unit[(int64_t)b * a.tps + tile];
-      g.n[0] = e.z;
-      g.n[1] = e.w & 0x3FFFFFFF;
-      g.bad = (e.w >> 30) & 1;
-      g.b = b;
-      g.h = h;
-      g.tile = tile;
-      g.lo = e.x;
-      g.end = e.y;
-      g.start = e.x & ~(a.box - 1);
-      g.u0 = u0;
-      const int n = max(g.n[0], g.n[1]);
-      g.w = n ? n + UNIT_COST : 0;
-      if (++tile == a.tps || n == 0) {  // (a sequence's units with work come first)
-        tile = 0;
-        if (++h == a.p.kv_heads) {
-          h = 0;
-          ++b;
-        }
-      }
-      if (n == 0) continue;
-      u0 += g.w;
-      if (u0 <= first) continue;
-      const int64_t x0 = max(first, g.u0) - g.u0, x1 = min(last, u0) - g.u0;
-      g.k0 = (int)max((int64_t)0, x0 - UNIT_COST);
-      g.k1 = (int)max((int64_t)0, x1 - UNIT_COST);
-      if (g.k0 >= g.k1) continue;
-      g.whole = g.k0 == 0 && g.k1 == n;
-      return true;
-    }
-    return false;
-  }
-};
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -404,9 +422,23 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  const int64_t first = sm->first, last = sm->last;
-  Walk walk{sm->b, sm->h, sm->tile, sm->u0, a.even ? nullptr : &sm->one};
-  Segment g;
+  WarpWalk& ww = sm->walk[warp];
+  const Segment& g = ww.g;
+  if (lane == 0) {
+  Walk& walk = ww.w;
+  walk.unit = a.unit;
+  walk.one = a.even ? nullptr : &sm->one;
+  walk.tps = a.tps;
+  walk.heads = p.kv_heads;
+  walk.B = p.B;
+  walk.box = a.box;
+  walk.b = sm->b;
+  walk.h = sm->h;
+  walk.tile = sm->tile;
+  walk.u0 = sm->u0;
+  walk.first = sm->first;
+  walk.last = sm->last;
+  }
 
   if (warp >= W_LOAD) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
@@ -422,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     const int nbox = TILE / a.box;
     const bool expanded = a.bf_k != nullptr;
-    while (ok && walk.next(a, first, last, g)) {
+    while (ok && ww.next(lane)) {
       for (int k = g.k0; k < g.k1 && ok; ++k) {
         const int t0 = g.start + k * TILE;
         // box `lane` of the tile: its page (out of range, so that zeros come, where it has none) and row
@@ -525,7 +557,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (elect_one()) tc::mma_commit(&sm->empty[x % NSLOT]);
       __syncwarp();
     };
-    while (ok && walk.next(a, first, last, g)) {
+    while (ok && ww.next(lane)) {
       const int cnt[2] = {uniform(g.count(0)), uniform(g.count(1))}, n = uniform(g.k1 - g.k0);
       it = uniform(it);
       wait_full(it);
@@ -578,7 +610,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t group = p.q_heads / p.kv_heads, rpi_q = RPI / group, rpi_r = RPI % group;
     uint32_t fph = 1, armed = 0;  // (qfree: nothing to wait for the first time)
     bool ok = true;
-    while (ok && walk.next(a, first, last, g)) {
+    while (ok && ww.next(lane)) {
       if (!g.count(i)) continue;
       const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
       const uint32_t r0 = (uint32_t)g.tile * UROWS + i * TILE;
@@ -635,9 +667,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t group = p.q_heads / p.kv_heads;
     uint32_t oph[2] = {0, 0};
     bool ok = true;
-    while (ok && walk.next(a, first, last, g)) {
+    while (ok && ww.next(lane)) {
       const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
-      const int slot = 2 * blockIdx.x + (g.u0 <= first ? 0 : 1);
+      const int slot = 2 * blockIdx.x + g.slot;
       const uint32_t n_rows = (uint32_t)s.n * group;
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
@@ -718,7 +750,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (warp == W_OUT && lane == 0 && !g.whole && g.k0 == 0)
         // the unit's first piece: it goes on up to the CTA of its last tile
-        a.cut[blockIdx.x] = make_int4(g.b * a.tps + g.tile, g.h, (int)((g.u0 + g.w - 1) / sm->per), g.u0 <= first ? 0 : 1);
+        a.cut[blockIdx.x] = make_int4(g.b * a.tps + g.tile, g.h, (int)((g.u0 + g.w - 1) / sm->per), g.slot);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
@@ -732,7 +764,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float rcap2 = p.softcap > 0.f ? 2.f * LOG2E / p.softcap : 0.f;
     uint32_t sph = 0, fph = 1;  // (ofree: nothing to wait for the first time)
     bool ok = true;
-    while (ok && walk.next(a, first, last, g)) {
+    while (ok && ww.next(lane)) {
       const int cnt = g.count(i);
       if (!cnt) continue;
       const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
