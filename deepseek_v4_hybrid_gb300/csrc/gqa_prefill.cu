@@ -201,6 +201,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -274,6 +279,36 @@ struct WarpWalk {
     return have;
   }
 };
+
+// x = cap tanh(x scale / cap) log2(e) for 32 columns.  While every |x scale| of the warp is at most cap, tanh t =
+// t P(t^2) with P of degree 6 (minimax on t^2 in [0, 1], relative error 5e-8 before rounding): packed fp32, where
+// the exponential form needs two special-function results an element.
+__device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float scale, float cap) {
+  float top = 0.f;
+#pragma unroll
+  for (int d = 0; d < 32; ++d) top = fmaxf(top, fabsf(__uint_as_float(x[d])));
+  const float r = 1.f / cap;
+  if (__all_sync(0xffffffffu, top * fabsf(scale) <= cap)) {
+    const uint64_t t2 = pack2(scale * r, scale * r), z2 = pack2(scale * LOG2E, scale * LOG2E);
+    uint64_t c[7];
+#pragma unroll
+    for (int k = 0; k < 7; ++k) c[k] = pack2(tanh_p(k), tanh_p(k));
+#pragma unroll
+    for (int d = 0; d < 32; d += 2) {
+      const uint64_t v = pack2u(x[d], x[d + 1]), t = mul2(v, t2), u = mul2(t, t);
+      uint64_t y = c[6];
+#pragma unroll
+      for (int k = 5; k >= 0; --k) y = fma2(y, u, c[k]);
+      const float2 z = unpack2(mul2(mul2(v, z2), y));
+      x[d] = __float_as_uint(z.x);
+      x[d + 1] = __float_as_uint(z.y);
+    }
+  } else {
+    const float rcap2 = 2.f * LOG2E * r;
+#pragma unroll
+    for (int d = 0; d < 32; ++d) x[d] = __float_as_uint(cap_logit(__uint_as_float(x[d]) * scale, cap, rcap2) * LOG2E);
+  }
+}
 
 struct Smem {
   uint64_t full[NSLOT], empty[NSLOT], vraw, qfull[2], qfree[2], sfull[2], phalf[2], pfull[2], odone[2], ofree[2], stats[2], drain;
@@ -761,7 +796,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t group = p.q_heads / p.kv_heads;
     const bool plain = p.softcap == 0.f && p.slopes == nullptr && p.softmax_scale > 0.f;
     const float cl = p.softmax_scale * LOG2E;
-    const float rcap2 = p.softcap > 0.f ? 2.f * LOG2E / p.softcap : 0.f;
     uint32_t sph = 0, fph = 1;  // (ofree: nothing to wait for the first time)
     bool ok = true;
     while (ok && ww.next(lane)) {
@@ -823,9 +857,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             tc::tmem_wait_ld_regs<32>(xa);
             if (p.softcap > 0.f) {
-#pragma unroll
-              for (int d = 0; d < 32; ++d)
-                xa[d] = __float_as_uint(cap_logit(__uint_as_float(xa[d]) * p.softmax_scale, p.softcap, rcap2) * LOG2E);
+              cap_logits(xa, p.softmax_scale, p.softcap);
             } else if (!plain) {
 #pragma unroll
               for (int d = 0; d < 32; ++d) xa[d] = __float_as_uint(__uint_as_float(xa[d]) * cl);

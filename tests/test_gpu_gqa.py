@@ -328,6 +328,33 @@ def test_attention_large_logits(M):
         check_attention(M, Batch(n, kv, 8, 2, 128, 64, "e4m3", seed=3, qscale=60.0))
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("at", [{70: 12.0}, {200: 14.0, 230: 20.0, 310: 60.0}, {250: 75.0, 400: 160.0}, {215: 300.0}, {0: 90.0},
+                                {500: -200.0, 330: 90.0, 459: 91.0, 460: 170.0}], ids=lambda a: "_".join(map(str, a)))
+def test_attention_logits_that_jump(M, at, cache):
+    """Flat logits but for a few rows far above (or below) them: the reference of the running softmax moves late, by
+    little, by much and in the second half of a tile."""
+    for n, kv in (([1], [600]), ([60, 3], [600, 599])):
+        bt = Batch(n, kv, 4, 2, 128, 64, cache, seed=3)
+        bt.q[:] = O.bf16_encode(np.ones(bt.q.shape))
+        bt.q[:, 1] = O.bf16_encode(-np.ones(bt.q.shape[2]))
+        if cache == "e4m3":
+            bt.exps[0][:] = 127
+        for b in range(len(n)):
+            for j in range(kv[b]):
+                v = at.get(j, 0.01 * (j % 7)) * 128 ** 0.5 / 128
+                bt.caches[0][bt.table[b, j // 64], :, j % 64] = O.bf16_encode(v) if cache == "bf16" else O.e4m3_encode(v)
+        check_attention(M, bt)
+
+
+@pytest.mark.parametrize("cap", [0.5, 30.0])
+def test_attention_capped_within_and_beyond(M, cap):
+    """Logits well inside the cap, around it and far beyond it (the two forms of the tanh)."""
+    for n, kv in (([1, 4], [300, 129]), ([90, 20], [310, 20])):
+        for gain in (0.02, 1.0, 40.0):
+            check_attention(M, Batch(n, kv, 8, 2, 128, 64, "bf16", seed=5, qscale=gain * cap), softcap=cap)
+
+
 def test_attention_bounds_larger_than_the_batch(M):
     bt = Batch([1, 3], [300, 65], 8, 2, 128, 64, "e4m3", seed=1)
     check_attention(M, bt, max_q=4, max_kv=100000)
