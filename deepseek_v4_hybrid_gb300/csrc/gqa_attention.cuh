@@ -21,13 +21,6 @@ __device__ __forceinline__ int2 visible_rows(const dsv4_gqa_attention_params& p,
   return make_int2(lo, hi);
 }
 
-// tanh t / t as a polynomial in t^2 for |t| <= 1: minimax in the relative error (5e-8; 1.7e-7 in fp32 arithmetic).
-__host__ __device__ constexpr float tanh_p(int k) {
-  const float c[7] = {0.9999999403953552f,   -0.33332839608192444f,  0.13325203955173492f, -0.053457021713256836f,
-                      0.020289966836571693f, -0.006203366909176111f, 0.0010410185204818845f};
-  return c[k];
-}
-
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -42,6 +42,7 @@ constexpr int UNIT_COST = 3;
 constexpr int FEW_ROWS = 1024;
 constexpr int MAX_UNITS = 8192;   // units of the evenly cut list; above, a CTA takes a whole unit
 constexpr float LAZY = 8.f;
+constexpr float CAP_ROOM = 80.f;  // (2^80 x 2^20 rows x values up to 2^20 stay in fp32)
 constexpr uint32_t FLAG_TIMEOUT = 4u;
 
 struct Args {
@@ -201,11 +202,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -280,33 +276,28 @@ struct WarpWalk {
   }
 };
 
-// x = cap tanh(x scale / cap) log2(e) for 32 columns.  While every |x scale| of the warp is at most cap, tanh t =
-// t P(t^2) with P of degree 6 (minimax on t^2 in [0, 1], relative error 5e-8 before rounding): packed fp32, where
-// the exponential form needs two special-function results an element.
-__device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float scale, float cap) {
-  float top = 0.f;
+// x = cap2 tanh(x to_exp / (2 log2 e)) - m for 32 columns, cap2 = cap log2(e), to_exp = 2 log2(e) scale / cap: tanh t = 1 - 2 / (1 +
+// e^2t), one reciprocal for two columns.  Bound by the special-function unit: 10 cycles an element with the weight's
+// exponential.  (A degree-13 polynomial in packed fp32 was no faster: fp32 pairs issue at half rate.)
+__device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float to_exp, float cap2, float m) {
+  const float c0 = cap2 - m, c1 = -2.f * cap2;
 #pragma unroll
-  for (int d = 0; d < 32; ++d) top = fmaxf(top, fabsf(__uint_as_float(x[d])));
-  const float r = 1.f / cap;
-  if (__all_sync(0xffffffffu, top * fabsf(scale) <= cap)) {
-    const uint64_t t2 = pack2(scale * r, scale * r), z2 = pack2(scale * LOG2E, scale * LOG2E);
-    uint64_t c[7];
+  for (int d = 0; d < 32; d += 2) {
+    const float a = 1.f + tc::ex2_approx(fminf(__uint_as_float(x[d]) * to_exp, 60.f));
+    const float b = 1.f + tc::ex2_approx(fminf(__uint_as_float(x[d + 1]) * to_exp, 60.f));
+    const float r = rcp_approx(a * b);
+    x[d] = __float_as_uint(fmaf(r * b, c1, c0));
+    x[d + 1] = __float_as_uint(fmaf(r * a, c1, c0));
+  }
+}
+
+// Weights 2^x of 32 columns: their sums (two chains) and bf16 pairs.
+__device__ __forceinline__ void plain_weights(const uint32_t (&x)[32], uint64_t (&sum2)[2], uint32_t (&pk)[16]) {
 #pragma unroll
-    for (int k = 0; k < 7; ++k) c[k] = pack2(tanh_p(k), tanh_p(k));
-#pragma unroll
-    for (int d = 0; d < 32; d += 2) {
-      const uint64_t v = pack2u(x[d], x[d + 1]), t = mul2(v, t2), u = mul2(t, t);
-      uint64_t y = c[6];
-#pragma unroll
-      for (int k = 5; k >= 0; --k) y = fma2(y, u, c[k]);
-      const float2 z = unpack2(mul2(mul2(v, z2), y));
-      x[d] = __float_as_uint(z.x);
-      x[d + 1] = __float_as_uint(z.y);
-    }
-  } else {
-    const float rcap2 = 2.f * LOG2E * r;
-#pragma unroll
-    for (int d = 0; d < 32; ++d) x[d] = __float_as_uint(cap_logit(__uint_as_float(x[d]) * scale, cap, rcap2) * LOG2E);
+  for (int d = 0; d < 32; d += 2) {
+    const float e0 = tc::ex2_approx(__uint_as_float(x[d])), e1 = tc::ex2_approx(__uint_as_float(x[d + 1]));
+    sum2[(d >> 1) & 1] = add2(sum2[(d >> 1) & 1], pack2(e0, e1));
+    pk[d / 2] = float2_to_bf16x2_bits(e0, e1);
   }
 }
 
@@ -333,7 +324,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-template <int D>
+// PLAIN: the logits are the scaled scores, the scale positive (its code is half as long, and its loops fetch faster).
+template <int D, bool PLAIN>
 __global__ void __launch_bounds__(THREADS, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap qmap, Args a) {
@@ -794,8 +786,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + 128 * i, t_o = lanes + COL_O + D * i;
     const uint32_t group = p.q_heads / p.kv_heads;
-    const bool plain = p.softcap == 0.f && p.slopes == nullptr && p.softmax_scale > 0.f;
-    const float cl = p.softmax_scale * LOG2E;
+    constexpr bool plain = PLAIN;
+    const bool capped = !PLAIN && p.softcap > 0.f && p.slopes == nullptr;
+    const float cl = p.softmax_scale * LOG2E, cap2 = p.softcap * LOG2E;
+    const float to_exp = p.softcap > 0.f ? 2.f * LOG2E * p.softmax_scale / p.softcap : 0.f;
     uint32_t sph = 0, fph = 1;  // (ofree: nothing to wait for the first time)
     bool ok = true;
     while (ok && ww.next(lane)) {
@@ -809,7 +803,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float slope = 0.f;
       if (live) {
         vis = visible_rows(p, g.b, s.t0 + tok, pos, s.kv);
-        if (p.slopes) slope = p.slopes[head] * LOG2E;
+        if (!PLAIN && p.slopes) slope = p.slopes[head] * LOG2E;
       }
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < cnt; ++k) {
@@ -826,6 +820,33 @@ __global__ void __launch_bounds__(THREADS, 1)
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         float mul = cl;
         const bool all = __all_sync(0xffffffffu, inside && !g.bad);
+        if (capped && all && __all_sync(0xffffffffu, cap2 - m <= CAP_ROOM)) {
+          // Capped logits lie at most at cap2 (log2 units), here at most CAP_ROOM above every row's reference: no maximum
+          // is needed, and the tile is read once.  (Rolled: this code is long, and instruction fetch counts.)
+          uint64_t sum2[2] = {0, 0};
+          tc::tmem_ld32_nowait(t_s, xa);
+          tc::tmem_wait_ld_regs<32>(xa);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            if (c < 3) tc::tmem_ld32_nowait(t_s + 32 * (c + 1), xb);
+            uint32_t pk[16];
+            cap_logits(xa, to_exp, cap2, m);
+            plain_weights(xa, sum2, pk);
+            if (c < 3) tc::tmem_wait_ld_regs<32>(xb);  // (P lies over columns that have been read)
+            tc::tmem_st16(t_s + 16 * c, pk);
+#pragma unroll
+            for (int d = 0; d < 32; ++d) xa[d] = xb[d];
+            if (c & 1) {
+              tc::tmem_wait_st();
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(c == 1 ? &sm->phalf[i] : &sm->pfull[i]);
+            }
+          }
+          const float2 sums = unpack2(add2(sum2[0], sum2[1]));
+          l += sums.x + sums.y;
+          continue;
+        }
         if (plain && all) {
           tc::tmem_ld32_nowait(t_s, xa);
           tc::tmem_wait_ld_regs<32>(xa);
@@ -856,13 +877,13 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
             }
             tc::tmem_wait_ld_regs<32>(xa);
-            if (p.softcap > 0.f) {
-              cap_logits(xa, p.softmax_scale, p.softcap);
+            if (!PLAIN && p.softcap > 0.f) {
+              cap_logits(xa, to_exp, cap2, 0.f);
             } else if (!plain) {
 #pragma unroll
               for (int d = 0; d < 32; ++d) xa[d] = __float_as_uint(__uint_as_float(xa[d]) * cl);
             }
-            if (p.slopes) {
+            if (!PLAIN && p.slopes) {
               const float far = (float)(pos - t0 - c);
 #pragma unroll
               for (int d = 0; d < 32; ++d)
@@ -880,7 +901,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc::tmem_wait_st();
         }
         const float top = mul * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        const bool move = top > m + LAZY;
+        const bool move = top > m + (capped && cap2 - m > CAP_ROOM ? 0.f : LAZY);
         if (__any_sync(0xffffffffu, move)) {
           const float mn = move ? top : m;
           const float f = m == -INFINITY ? 0.f : tc::ex2_approx(m - mn);
@@ -1078,13 +1099,15 @@ static cudaError_t launch(const dsv4_gqa_attention_params& p, cudaStream_t s) {
     if (e != cudaSuccess) a.q_tma = 0;
   }
   const int smem = (2 + NSLOT) * TILE * D * 2 + 4 * 2048 + (int)sizeof(Smem) + 1024;
-  e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(prefill_kernel<D>), smem);
+  const bool plain = p.softcap == 0.f && p.slopes == nullptr && p.softmax_scale > 0.f;
+  const auto kernel = plain ? prefill_kernel<D, true> : prefill_kernel<D, false>;
+  e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   if (plan_ctas + expand > 0) {
     e = launch_pdl(prepare_kernel<D>, dim3((unsigned)(plan_ctas + expand)), dim3(PREP_THREADS), 0, s, true, a, (int)plan_ctas);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(prefill_kernel<D>, dim3((unsigned)ctas), dim3(THREADS), smem, s, true, kmap, vmap, qmap, a);
+  e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(THREADS), smem, s, true, kmap, vmap, qmap, a);
   if (e != cudaSuccess || !L.even) return e;
   return launch_pdl(join_kernel<D>, dim3(L.G, UROWS / 32), dim3(256), 0, s, true, a);
 }
