@@ -3,11 +3,15 @@
 // Bound by HBM: every visible row of the cache is read once for all rows of its kv head, and the rows of
 // a kv head together are far below the tensor cores' rate, so the products run on warp-level MMAs from
 // registers (tcgen05 would spend 128 rows on at most 32) and the design is about the stream of rows:
-//  - The visible rows of all (sequence, kv head) units form one list of 16-row stages that is cut into
+//  - The visible rows of all (sequence, kv head) units form one list of stages (16 rows, e4m3 32) that is cut into
 //    equal pieces, one per CTA, whatever the lengths; a unit cut by a piece's border leaves partial
 //    results that a second kernel merges.
-//  - Each warp streams its own stages (every fourth of its CTA's) through its own ring of cp.async
-//    copies, and keeps its own running maximum, sum and output: no barrier between warps until a unit ends.
+//  - A warp takes up to 16 rows of (token, head).  The one or two warps that hold a unit's rows share their stages in a
+//    ring of cp.async copies, with one barrier of theirs a stage; these groups stream their own stages and keep their
+//    own running maximum, sum and output: no barrier between them until a unit ends.  (All 32 rows in one warp took
+//    two CTAs' registers of three, each warp waiting on its own chain of MMAs: at 32 rows a kv head, 48 sequences of
+//    up to 4000 rows, 4 kv heads of 128, e4m3 142 us and 98 so, capped bf16 in a window of 1024 41.7 and 39.2; plain
+//    bf16 67 and 75.  8 rows a warp, four warps a group: e4m3 111 us, and 16 rows of 64-wide heads 28 for 21 us.)
 //  - S = Q K^T has the rows of a kv head as its M (16) and 8 cache rows as its N; its result is, register
 //    for register, the A operand of O += P V.  The order of a contraction's terms is free, so a lane
 //    reads 16 contiguous bytes of a row and Q's fragments are laid out to match; for P V a lane holds 16
@@ -43,46 +47,43 @@ constexpr int BLK = 16;            // rows that lie in one page
 constexpr int MAX_SCAN = 1024;     // sequences whose stages are cut evenly; above, a CTA takes a whole unit
 constexpr int MAX_CLUSTER = 8;     // CTAs of a unit (portable cluster size)
 constexpr int MIN_ROWS = 128;      // rows of a piece, at least
-constexpr int CLUSTER_ROWS = 1024; // rows of a cluster's CTA, at most
+constexpr int CLUSTER_ROWS = 1024; // rows of a cluster's CTA, at most (512: 1 x 6000 rows 21 us for 15; 2048: 16 x 4000 43 for 35)
 constexpr float LAZY = 8.f;        // a running maximum moves when it is exceeded by more than 2^8
 
 struct Args {
   dsv4_gqa_attention_params p;
   float* o_part;    // [2 G][rows][D]
   float4* ml_part;  // [2 G][rows]: maximum of the logits, sum, maximum that O is taken against (log2 units)
-  int4* unit;       // [B * kv_heads]: first and last CTA of the unit, slot in the first, 0 / 1 = merge
+  int4* unit;       // [B * heads]: first and last CTA of the unit, slot in the first, 0 / 1 = merge
   int G, rows;      // CTAs, rows of a partial
   int cs;           // 0: equal pieces of the list; else CTAs (a cluster) of each unit
 };
 
-// Shared memory and CTAs per SM: 12 to 16 warps an SM, each with at least 8 KB of copies in flight
-// (about 46 KB an SM cover the latency at the full rate), as registers allow.
+// Shared memory and CTAs per SM: 8 to 16 warps an SM, each with at least 8 KB of copies in flight
+// (about 46 KB an SM cover the latency at the full rate), as registers allow (16 rows of e4m3, 128 wide, on three
+// CTAs' registers: 75 us where two take 61, at 48 x 4000 rows, 4 kv heads, 16 rows a kv head).
 __host__ __device__ constexpr int ctas_per_sm(int D, bool e4m3, int HB) {
-  return HB == 4 || (D == 128 && e4m3 && HB == 2) ? 2 : (D == 64 && HB == 1) ? 4 : 3;
+  return D == 128 && e4m3 && HB == 2 ? 2 : D == 64 && HB == 1 ? 4 : 3;
 }
 
-template <int D, bool E4M3, int HB>
+template <int D, bool E4M3, int HB, int PW>
 struct Cfg {
   static constexpr int ROWB = E4M3 ? D : 2 * D;
   static constexpr int SUB = E4M3 ? 2 : 1;     // blocks of a stage: an MMA's K, 32 or 16 rows
   static constexpr int SR = BLK * SUB;
   static constexpr int STAGE = 2 * SR * ROWB;  // K then V
   static constexpr int CTAS = ctas_per_sm(D, E4M3, HB);
-  static constexpr int RING = CTAS == 4 ? 12288 : CTAS == 3 ? 16384 : 24576;
-  static constexpr int NST = RING / STAGE;
-  static constexpr int QMEM = HB == 4 ? 2 * (D / 16) * 512 : 0;  // 32 rows: Q's fragments live in shared memory
-  static constexpr int SMEM = NW * RING + QMEM;
+  static constexpr int RING = CTAS == 4 ? 12288 : CTAS == 3 ? 16384 : 24576;  // of a warp; a group's are one
+  static constexpr int NST = PW * RING / STAGE;
+  static constexpr int SMEM = NW * RING;
   static_assert(NST >= 2, "at least one stage ahead");
   static_assert(8 * HB * D * 4 <= RING, "a warp's output fits its ring");
 };
 
 struct Shared {
-  float m[NW][32], l[NW][32], mo[NW][32];
+  float m[NW][16], l[NW][16], mo[NW][16];
   float4 cml[32];     // cluster: this CTA's (maximum, sum, reference) of each row
-  int2 meta[NW][16];  // [block of the ring]: page usable, (k exponent byte | v exponent byte << 8)
-  int64_t total;
-  int64_t at;
-  int b;
+  int2 meta[NW][32];  // [group][block of the ring]: page usable, (k exponent byte | v exponent byte << 8)
 };
 
 // c += a b (m16n8k16), bf16.
@@ -157,24 +158,25 @@ __device__ __forceinline__ Unit unit_of(const dsv4_gqa_attention_params& p, int 
   return u;
 }
 
-template <int D, bool E4M3, int HB>
-__global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel(Args a) {
-  using C = Cfg<D, E4M3, HB>;
-  constexpr int MT = HB == 4 ? 2 : 1, NT = D / 8, SR = C::SR, SUB = C::SUB;
+template <int D, bool E4M3, int HB, int PW>
+__global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB, PW>::CTAS) decode_kernel(Args a) {
+  using C = Cfg<D, E4M3, HB, PW>;
+  constexpr int RW = 8 * HB, NG = NW / PW;               // rows of a warp; groups of warps with stages of their own
+  constexpr int NT = D / 8, SR = C::SR, SUB = C::SUB;
   constexpr int KS = E4M3 ? D / 32 : D / 16;             // K steps of Q K^T
   constexpr int NQ = E4M3 && HB > 1 ? 2 * KS : KS;       // A fragments of an MMA tile of Q (two terms apart)
   extern __shared__ __align__(1024) uint8_t ring_all[];
   __shared__ Shared sm;
   const dsv4_gqa_attention_params& p = a.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  uint8_t* ring = ring_all + warp * C::RING;
-  uint32_t* qmem = reinterpret_cast<uint32_t*>(ring_all + NW * C::RING);
+  const int gw = warp / PW, mw = warp % PW;  // group, member
+  uint8_t* ring = ring_all + gw * PW * C::RING;
   pdl_wait();
   pdl_launch_dependents();
 
   // ---------------- this CTA's piece of the list of stages
   int64_t first, last;  // [first, last) in the list
-  int b, h;
+  int b;
   int64_t per;
   int64_t base;  // list position of unit (b, 0)
   if (a.cs == 0) {
@@ -247,11 +249,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
   for (int64_t at = first; at < last; ++b) {
     const Unit u = unit_of<SR>(p, b);
     if (u.stages == 0) continue;
-    for (h = (int)((at - base) / u.stages); h < p.kv_heads && at < last; ++h) {
+    for (int h = (int)((at - base) / u.stages); h < p.kv_heads && at < last; ++h) {
       const int64_t u0 = base + (int64_t)h * u.stages;  // the unit's list positions [u0, u0 + stages)
       const int s0 = (int)(at - u0), s1 = (int)(min(last, u0 + u.stages) - u0);
       const bool whole = a.cs == 1 || (a.cs == 0 && s0 == 0 && s1 == u.stages);
-      const int rows = u.s.n * group;
+      const int rows = u.s.n * group, row0 = RW * mw;  // the unit's, this warp's first
       const int pos0 = u.s.kv - u.s.n;
 
       // rows g + 8 k of this lane
@@ -259,24 +261,15 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
       float rmul[HB], slope[HB], rpos[HB];
       float m[HB], mo[HB], l[HB];
       int all_lo = 0, all_hi = 0x7FFFFFFF;  // rows that every token sees
-      // Q's A fragments; e4m3: [K step][hi, lo], or both terms in one for 8 rows.  32 rows: in shared memory,
-      // [MMA tile][fragment][lane][4 registers].
-      uint32_t q[HB == 4 ? 1 : NQ][4];
-      auto keep_q = [&](int x, int k, uint32_t lo, uint32_t hi) {  // fragment x, row half k of its tile
-        if (HB == 4) {
-          if (warp == 0) {
-            uint32_t* dst = qmem + (((k / 2) * NQ + x) * 32 + lane) * 4;
-            dst[k & 1] = lo;
-            dst[2 + (k & 1)] = hi;
-          }
-        } else {
-          q[x][k & 1] = lo;
-          q[x][2 + (k & 1)] = hi;
-        }
+      // Q's A fragments; e4m3: [K step][hi, lo], or both terms in one for 8 rows.
+      uint32_t q[NQ][4];
+      auto keep_q = [&](int x, int k, uint32_t lo, uint32_t hi) {  // fragment x, row half k
+        q[x][k] = lo;
+        q[x][2 + k] = hi;
       };
 #pragma unroll
       for (int k = 0; k < HB; ++k) {
-        const int r = g + 8 * k, i = r / group;
+        const int r = row0 + g + 8 * k, i = r / group;
         const bool live = r < rows;
         const int pos = pos0 + i, t = u.s.t0 + i;
         rlo[k] = 0;
@@ -343,44 +336,37 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
         }
         rmul[k] = plain ? mul * LOG2E : mul;
       }
-      if (HB == 4) __syncthreads();
       all_lo = __reduce_max_sync(0xffffffffu, all_lo);
       all_hi = __reduce_min_sync(0xffffffffu, all_hi);
 
       // the running output: row half k, column tile j, columns 2c and 2c + 1.  bf16: the MMAs' accumulators
-      float o[E4M3 ? HB : (HB + 1) / 2][NT][E4M3 ? 2 : 4];
+      float o[E4M3 ? HB : 1][NT][E4M3 ? 2 : 4];
 #pragma unroll
       for (auto& x : o)
 #pragma unroll
         for (auto& y : x)
 #pragma unroll
           for (float& v : y) v = 0.f;
-      auto out = [&](int k, int j, int y) -> float& { return E4M3 ? o[k][j][y] : o[k / 2][j][2 * (k & 1) + y]; };
+      auto out = [&](int k, int j, int y) -> float& { return E4M3 ? o[k][j][y] : o[0][j][2 * k + y]; };
 
-      auto q_frag = [&](int z, int x, uint32_t (&f)[4]) {
-        if (HB == 4) {
-          const uint4 w = *reinterpret_cast<const uint4*>(qmem + ((z * NQ + x) * 32 + lane) * 4);
-          f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
-        } else {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) f[y] = q[x][y];
-        }
-      };
-      // this warp's stages: s0 + warp, s0 + warp + NW, ...
-      const int count = s1 - s0 > warp ? (s1 - s0 - warp + NW - 1) / NW : 0;
+      // this group's stages: s0 + gw, s0 + gw + NG, ...
+      const int count = s1 - s0 > gw ? (s1 - s0 - gw + NG - 1) / NG : 0;
       int pid = -1, pexp = 0;
-      constexpr int CPR = C::ROWB / 16, RPI = 32 / CPR;  // lanes of a row, rows a warp copies at once
+      constexpr int CPR = C::ROWB / 16, RPI = 32 * PW / CPR;  // lanes of a row, rows the group copies at once
+      constexpr int NU = SR / RPI;                            // 16-byte pieces of K (and V) that a thread copies
       constexpr int64_t ES = E4M3 ? 1 : 2;
-      const uint8_t* k_base = reinterpret_cast<const uint8_t*>(p.k_cache) + ES * ((int64_t)h * p.k_cache_head_stride) + 16 * (lane % CPR);
-      const uint8_t* v_base = reinterpret_cast<const uint8_t*>(p.v_cache) + ES * ((int64_t)h * p.v_cache_head_stride) + 16 * (lane % CPR);
+      static_assert(NU * RPI == SR, "whole rounds");
+      const int gl = mw * 32 + lane, r_in = gl / CPR;
+      const uint8_t* k_base = reinterpret_cast<const uint8_t*>(p.k_cache) + ES * ((int64_t)h * p.k_cache_head_stride) + 16 * (gl % CPR);
+      const uint8_t* v_base = reinterpret_cast<const uint8_t*>(p.v_cache) + ES * ((int64_t)h * p.v_cache_head_stride) + 16 * (gl % CPR);
       const int64_t k_step = ES * RPI * p.k_row_stride, v_step = ES * RPI * p.v_row_stride;
-      int doff[BLK / RPI];
+      int doff[NU];
 #pragma unroll
-      for (int i = 0; i < BLK / RPI; ++i) doff[i] = chunk_at<C::ROWB>(i * RPI + lane / CPR, lane % CPR);
+      for (int i = 0; i < NU; ++i) doff[i] = chunk_at<C::ROWB>(i * RPI + r_in, gl % CPR);
       auto fill = [&](int k) {
         if (k < count) {
           if ((k * SUB & 31) == 0) {  // pages and exponents of the next 32 blocks, one a lane
-            const int ks = k + lane / SUB, j = u.lo + (s0 + warp + ks * NW) * SR + lane % SUB * BLK;
+            const int ks = k + lane / SUB, j = u.lo + (s0 + gw + ks * NG) * SR + lane % SUB * BLK;
             pid = -1;
             pexp = 0;
             if (ks < count && j < u.s.kv) {
@@ -395,31 +381,39 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
               }
             }
           }
-          const int slot = k % C::NST;
+          const int slot = k % C::NST, js = u.lo + (s0 + gw + k * NG) * SR;
+          uint8_t* dst = ring + slot * C::STAGE;
+          constexpr int PER = RPI < BLK ? BLK / RPI : 1;  // pieces that a thread copies of a block
+          static_assert(NU % PER == 0 && C::NST * SUB <= 32, "whole blocks; the ring's lie in sm.meta");
 #pragma unroll
           for (int sub = 0; sub < SUB; ++sub) {
             const int page = __shfl_sync(0xffffffffu, pid, (k * SUB + sub) & 31);
             const int ex = __shfl_sync(0xffffffffu, pexp, (k * SUB + sub) & 31);
-            const int j0 = u.lo + (s0 + warp + k * NW) * SR + sub * BLK;
-            if (lane == 0) sm.meta[warp][slot * SUB + sub] = make_int2(page >= 0, ex);
-            uint8_t* dst = ring + slot * C::STAGE + sub * BLK * C::ROWB;
-            const int row = (j0 & (p.page_size - 1)) + lane / CPR;
+            if (mw == 0 && lane == 0) sm.meta[gw][slot * SUB + sub] = make_int2(page >= 0, ex);
+          }
+#pragma unroll
+          for (int nb = 0; nb < NU; nb += PER) {
+            const int rb = nb * RPI + r_in;  // the first of PER rows in one block
+            const int page = __shfl_sync(0xffffffffu, pid, (k * SUB + rb / BLK) & 31);
+            const int j0 = js + rb;
+            const int row = j0 & (p.page_size - 1);
             const uint8_t* kr = k_base + ES * ((int64_t)max(page, 0) * p.k_page_stride + (int64_t)row * p.k_row_stride);
             const uint8_t* vr = v_base + ES * ((int64_t)max(page, 0) * p.v_page_stride + (int64_t)row * p.v_row_stride);
-            if (page >= 0 && j0 >= u.vlo && j0 + BLK <= u.s.kv) {
+            const int jb = j0 & ~(BLK - 1);
+            if (page >= 0 && jb >= u.vlo && jb + BLK <= u.s.kv) {
 #pragma unroll
-              for (int i = 0; i < BLK / RPI; ++i) {
-                tc::cp_async16(dst + doff[i], kr + i * k_step, 16u);
-                tc::cp_async16(dst + SR * C::ROWB + doff[i], vr + i * v_step, 16u);
+              for (int i = 0; i < PER; ++i) {
+                tc::cp_async16(dst + doff[nb + i], kr + i * k_step, 16u);
+                tc::cp_async16(dst + SR * C::ROWB + doff[nb + i], vr + i * v_step, 16u);
               }
             } else {
               // rows that no token sees read nothing and become zeros, whatever the cache holds there
 #pragma unroll
-              for (int i = 0; i < BLK / RPI; ++i) {
-                const int j = j0 + i * RPI + lane / CPR;
+              for (int i = 0; i < PER; ++i) {
+                const int j = j0 + i * RPI;
                 const bool in = page >= 0 && j >= u.vlo && j < u.s.kv;
-                tc::cp_async16(dst + doff[i], in ? kr + i * k_step : reinterpret_cast<const uint8_t*>(p.k_cache), in ? 16u : 0u);
-                tc::cp_async16(dst + SR * C::ROWB + doff[i], in ? vr + i * v_step : reinterpret_cast<const uint8_t*>(p.v_cache),
+                tc::cp_async16(dst + doff[nb + i], in ? kr + i * k_step : reinterpret_cast<const uint8_t*>(p.k_cache), in ? 16u : 0u);
+                tc::cp_async16(dst + SR * C::ROWB + doff[nb + i], in ? vr + i * v_step : reinterpret_cast<const uint8_t*>(p.v_cache),
                                in ? 16u : 0u);
               }
             }
@@ -427,15 +421,20 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
         }
         tc::cp_async_commit();
       };
+      auto group_sync = [&]() {
+        if (PW == 1) __syncwarp();
+        else tc::named_bar_sync(1 + gw, 32 * PW);
+      };
 #pragma unroll 1
       for (int k = 0; k < C::NST - 1; ++k) fill(k);
 
 #pragma unroll 1
       for (int k = 0; k < count; ++k) {
         tc::cp_async_wait<C::NST - 2>();
-        __syncwarp();
+        group_sync();  // the stage is there for all, and the one before is read
         fill(k + C::NST - 1);
-        const int slot = k % C::NST, j0 = u.lo + (s0 + warp + k * NW) * SR;
+        if (row0 >= rows) continue;  // (a warp with no rows only copies)
+        const int slot = k % C::NST, j0 = u.lo + (s0 + gw + k * NG) * SR;
         const uint8_t* kt = ring + slot * C::STAGE;
         const uint8_t* vt = kt + SR * C::ROWB;
 
@@ -444,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
 #pragma unroll
         for (int nt = 0; nt < 2 * SUB; ++nt) {
           constexpr int KCH = C::ROWB / 64;  // 16-byte chunks a lane holds of a row
-          float s[MT][4], s_lo[MT][4];
+          float s[4], s_lo[4];
 #pragma unroll
           for (int x = 0; x < KCH; ++x) {
             const uint4 w = *reinterpret_cast<const uint4*>(kt + chunk_at<C::ROWB>(8 * nt + g, c + 4 * x));
@@ -452,23 +451,17 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const int ks = 2 * x + y;
-#pragma unroll
-              for (int m2 = 0; m2 < MT; ++m2) {
-                uint32_t f[4];
-                if (E4M3) {
-                  q_frag(m2, HB == 1 ? ks : 2 * ks, f);
-                  if (ks == 0) mma8_first(s[m2], f, ww[2 * y], ww[2 * y + 1]);
-                  else mma8(s[m2], f, ww[2 * y], ww[2 * y + 1]);
-                  if (HB > 1) {
-                    q_frag(m2, 2 * ks + 1, f);
-                    if (ks == 0) mma8_first(s_lo[m2], f, ww[2 * y], ww[2 * y + 1]);
-                    else mma8(s_lo[m2], f, ww[2 * y], ww[2 * y + 1]);
-                  }
-                } else {
-                  q_frag(m2, ks, f);
-                  if (ks == 0) s[m2][0] = s[m2][1] = s[m2][2] = s[m2][3] = 0.f;
-                  mma16(s[m2], f, ww[2 * y], ww[2 * y + 1]);
+              if (E4M3) {
+                const int f = HB == 1 ? ks : 2 * ks;
+                if (ks == 0) mma8_first(s, q[f], ww[2 * y], ww[2 * y + 1]);
+                else mma8(s, q[f], ww[2 * y], ww[2 * y + 1]);
+                if (HB > 1) {
+                  if (ks == 0) mma8_first(s_lo, q[f + 1], ww[2 * y], ww[2 * y + 1]);
+                  else mma8(s_lo, q[f + 1], ww[2 * y], ww[2 * y + 1]);
                 }
+              } else {
+                if (ks == 0) s[0] = s[1] = s[2] = s[3] = 0.f;
+                mma16(s, q[ks], ww[2 * y], ww[2 * y + 1]);
               }
             }
           }
@@ -476,9 +469,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
           for (int k2 = 0; k2 < HB; ++k2)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const int e = 2 * (k2 & 1) + y;
-              z[k2][nt][y] = !E4M3 ? s[k2 / 2][e] : HB == 1 ? fmaf(s[0][2 + y], 1.f / QF, s[0][y])
-                                                            : fmaf(s_lo[k2 / 2][e], 1.f / QF, s[k2 / 2][e]);
+              const int e = 2 * k2 + y;
+              z[k2][nt][y] = !E4M3 ? s[e] : HB == 1 ? fmaf(s[2 + y], 1.f / QF, s[y]) : fmaf(s_lo[e], 1.f / QF, s[e]);
             }
         }
 
@@ -489,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
         bool page_ok[SUB];
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub) {
-          const int2 meta = sm.meta[warp][slot * SUB + sub];
+          const int2 meta = sm.meta[gw][slot * SUB + sub];
           page_ok[sub] = meta.x != 0;
           inside = inside && page_ok[sub];
           kmul[sub] = E4M3 ? ue8m0_scale((uint8_t)(meta.y & 255)) : 1.f;
@@ -564,37 +556,33 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
                 out(k2, j, 1) *= fo[k2];
               }
           }
-          // ---- O += P V: 4 dims (a word of the lane's) at a time; 32 rows hold half the lane's words at once
-          constexpr int WD = D / 32, WH = HB == 4 && D == 128 ? 2 : WD;
-          uint32_t v[8][WH];
+          // ---- O += P V: 4 dims (a word of the lane's) at a time
+          constexpr int WD = D / 32;
+          uint32_t v[8][WD];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int r = 2 * c + (y & 1) + 8 * (y >> 1);
+            if (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(vt + chunk_at<C::ROWB>(r, (g >> 1) | ((g & 1) << 2)));
+              v[y][0] = w.x;
+              v[y][1] = w.y;
+              v[y][WD - 2] = w.z;
+              v[y][WD - 1] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(vt + chunk_at<C::ROWB>(r, g >> 1) + 8 * (g & 1));
+              v[y][0] = w.x;
+              v[y][1] = w.y;
+            }
+          }
 #pragma unroll
           for (int wd = 0; wd < WD; ++wd) {
-            if (wd % WH == 0) {
-#pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                const int r = 2 * c + (y & 1) + 8 * (y >> 1);
-                const uint8_t* src = D == 128 ? vt + chunk_at<C::ROWB>(r, (g >> 1) | ((g & 1) << 2)) + 4 * wd
-                                              : vt + chunk_at<C::ROWB>(r, g >> 1) + 8 * (g & 1);
-                if (WH == 4) {
-                  const uint4 w = *reinterpret_cast<const uint4*>(src);
-                  v[y][0] = w.x;
-                  v[y][1] = w.y;
-                  v[y][WH - 2] = w.z;
-                  v[y][WH - 1] = w.w;
-                } else {
-                  const uint2 w = *reinterpret_cast<const uint2*>(src);
-                  v[y][0] = w.x;
-                  v[y][1] = w.y;
-                }
-              }
-            }
             uint32_t bt[2][4];  // [rows 0-15, 16-31 of the stage][dim]: four rows' codes of one dim
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint32_t t0 = __byte_perm(v[4 * x][wd % WH], v[4 * x + 1][wd % WH], 0x5140u);
-              const uint32_t t1 = __byte_perm(v[4 * x][wd % WH], v[4 * x + 1][wd % WH], 0x7362u);
-              const uint32_t u0 = __byte_perm(v[4 * x + 2][wd % WH], v[4 * x + 3][wd % WH], 0x5140u);
-              const uint32_t u1 = __byte_perm(v[4 * x + 2][wd % WH], v[4 * x + 3][wd % WH], 0x7362u);
+              const uint32_t t0 = __byte_perm(v[4 * x][wd], v[4 * x + 1][wd], 0x5140u);
+              const uint32_t t1 = __byte_perm(v[4 * x][wd], v[4 * x + 1][wd], 0x7362u);
+              const uint32_t u0 = __byte_perm(v[4 * x + 2][wd], v[4 * x + 3][wd], 0x5140u);
+              const uint32_t u1 = __byte_perm(v[4 * x + 2][wd], v[4 * x + 3][wd], 0x7362u);
               bt[x][0] = __byte_perm(t0, u0, 0x5410u);
               bt[x][1] = __byte_perm(t0, u0, 0x7632u);
               bt[x][2] = __byte_perm(t1, u1, 0x5410u);
@@ -611,19 +599,16 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
                 for (int y = 0; y < 2; ++y)
                   out(0, j, y) = fmaf(fmaf(x[2 + y], 1.f / PF, x[y]), fs[0], out(0, j, y));
               } else {
+                constexpr int k1 = HB - 1;
+                const uint32_t f[4] = {hi[0][0], hi[k1][0], hi[0][1], hi[k1][1]};
+                const uint32_t f2[4] = {lo[0][0], lo[k1][0], lo[0][1], lo[k1][1]};
+                float x[4], x2[4];
+                mma8_first(x, f, bt[0][d], bt[1][d]);
+                mma8_first(x2, f2, bt[0][d], bt[1][d]);
 #pragma unroll
-                for (int m2 = 0; m2 < MT; ++m2) {
-                  const int k0 = 2 * m2, k1 = 2 * m2 + (HB > 1 ? 1 : 0);
-                  const uint32_t f[4] = {hi[k0][0], hi[k1][0], hi[k0][1], hi[k1][1]};
-                  const uint32_t f2[4] = {lo[k0][0], lo[k1][0], lo[k0][1], lo[k1][1]};
-                  float x[4], x2[4];
-                  mma8_first(x, f, bt[0][d], bt[1][d]);
-                  mma8_first(x2, f2, bt[0][d], bt[1][d]);
-#pragma unroll
-                  for (int y = 0; y < 2; ++y) {
-                    out(k0, j, y) = fmaf(fmaf(x2[y], 1.f / PF, x[y]), fs[k0], out(k0, j, y));
-                    out(k1, j, y) = fmaf(fmaf(x2[2 + y], 1.f / PF, x[2 + y]), fs[k1], out(k1, j, y));
-                  }
+                for (int y = 0; y < 2; ++y) {
+                  out(0, j, y) = fmaf(fmaf(x2[y], 1.f / PF, x[y]), fs[0], out(0, j, y));
+                  out(k1, j, y) = fmaf(fmaf(x2[2 + y], 1.f / PF, x[2 + y]), fs[k1], out(k1, j, y));
                 }
               }
             }
@@ -650,8 +635,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
               }
             }
           }
-          uint32_t pa[MT][4];
-          if (HB == 1) pa[0][1] = pa[0][3] = 0u;
+          uint32_t pa[4];
+          if (HB == 1) pa[1] = pa[3] = 0u;
 #pragma unroll
           for (int k2 = 0; k2 < HB; ++k2) {
             const float mm = m[k2] == -INFINITY ? 0.f : m[k2];
@@ -659,8 +644,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
 #pragma unroll
             for (int y = 0; y < 4; ++y) w[y] = tc::ex2_approx(z[k2][y >> 1][y & 1] - mm);
             l[k2] += (w[0] + w[1]) + (w[2] + w[3]);
-            pa[k2 / 2][k2 & 1] = float2_to_bf16x2_bits(w[0], w[1]);
-            pa[k2 / 2][2 + (k2 & 1)] = float2_to_bf16x2_bits(w[2], w[3]);
+            pa[k2] = float2_to_bf16x2_bits(w[0], w[1]);
+            pa[2 + k2] = float2_to_bf16x2_bits(w[2], w[3]);
           }
           // ---- O += P V; the matrices of an x4 load: rows 0-7 and 8-15 of dims 16 jj .. + 7, then of the next 8
           const int r = (lane & 7) + (lane & 8);
@@ -669,18 +654,15 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
             uint32_t w[4];
             ldmatrix_x4_trans(w, tc::smem_addr(vt + chunk_at<C::ROWB>(r, 2 * jj + (lane >> 4))));
             if constexpr (!E4M3) {
-#pragma unroll
-              for (int x = 0; x < MT; ++x) {
-                mma16(o[x][2 * jj], pa[x], w[0], w[1]);
-                mma16(o[x][2 * jj + 1], pa[x], w[2], w[3]);
-              }
+              mma16(o[0][2 * jj], pa, w[0], w[1]);
+              mma16(o[0][2 * jj + 1], pa, w[2], w[3]);
             }
           }
         }
       }
       tc::cp_async_wait<0>();
 
-      // ---------------- the four warps' results of the unit
+      // ---------------- the groups' results of the unit
 #pragma unroll
       for (int k = 0; k < HB; ++k) {
         l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
@@ -692,13 +674,13 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
         }
       }
       __syncthreads();
-      float* part = reinterpret_cast<float*>(ring);  // [rows][D]: the ring is drained
+      float* part = reinterpret_cast<float*>(ring_all + warp * C::RING);  // [RW][D]: the rings are drained
 #pragma unroll
       for (int k = 0; k < HB; ++k) {
         const int r = g + 8 * k;
         float on = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) on = fmaxf(on, sm.mo[w][r]);
+        for (int w = 0; w < NG; ++w) on = fmaxf(on, sm.mo[w * PW + mw][r]);
         const float f = mo[k] == -INFINITY ? 0.f : tc::ex2_approx(mo[k] - on);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -714,28 +696,29 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
       const int slot = 2 * blockIdx.x + (at == first ? 0 : 1);
       for (int x = tid; x < rows * (D / 4); x += THREADS) {
         const int r = x / (D / 4), d4 = x % (D / 4);
+        const int rm = r / RW, rl = r % RW;  // the row's warp in a group, its place there
         float mn = -INFINITY, on = -INFINITY, ls = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          mn = fmaxf(mn, sm.m[w][r]);
-          on = fmaxf(on, sm.mo[w][r]);
-          const float4 v = reinterpret_cast<const float4*>(ring_all + w * C::RING)[r * (D / 4) + d4];
+        for (int w = 0; w < NG; ++w) {
+          mn = fmaxf(mn, sm.m[w * PW + rm][rl]);
+          on = fmaxf(on, sm.mo[w * PW + rm][rl]);
+          const float4 v = reinterpret_cast<const float4*>(ring_all + (w * PW + rm) * C::RING)[rl * (D / 4) + d4];
           acc.x += v.x;
           acc.y += v.y;
           acc.z += v.z;
           acc.w += v.w;
         }
 #pragma unroll
-        for (int w = 0; w < NW; ++w)
-          if (sm.m[w][r] > -INFINITY) ls += sm.l[w][r] * tc::ex2_approx(sm.m[w][r] - mn);
+        for (int w = 0; w < NG; ++w)
+          if (sm.m[w * PW + rm][rl] > -INFINITY) ls += sm.l[w * PW + rm][rl] * tc::ex2_approx(sm.m[w * PW + rm][rl] - mn);
         if (whole) {
           const int head = h * group + r % group;
           const int64_t row = (int64_t)(u.s.t0 + r / group) * p.q_heads + head;
           const float f = finish_scale(p, row, head, mn, ls, on, d4 == 0);
           store4<D>(p, row, d4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
         } else if (a.cs) {
-          reinterpret_cast<float4*>(ring_all)[x] = acc;  // (over warp 0's, which this thread has read here)
+          reinterpret_cast<float4*>(ring_all + rm * C::RING)[rl * (D / 4) + d4] = acc;  // (over group 0's, which this thread has read)
           if (d4 == 0) sm.cml[r] = make_float4(mn, ls, on, 0.f);
         } else {
           reinterpret_cast<float4*>(a.o_part)[((int64_t)slot * a.rows + r) * (D / 4) + d4] = acc;
@@ -759,7 +742,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
     cl.sync();
     const int unit = blockIdx.x / a.cs, rank = blockIdx.x % a.cs;
     const Unit u = unit_of<SR>(p, unit / p.kv_heads);
-    const int rows = u.s.n * group;
+    const int h = unit % p.kv_heads, rows = u.s.n * group;
     for (int x = rank * THREADS + tid; x < rows * (D / 4); x += a.cs * THREADS) {
       const int r = x / (D / 4), d4 = x % (D / 4);
       float4 ml[MAX_CLUSTER], v[MAX_CLUSTER];
@@ -770,7 +753,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
         v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i < a.cs) {
           ml[i] = cl.map_shared_rank(sm.cml, i)[r];
-          v[i] = cl.map_shared_rank(reinterpret_cast<float4*>(ring_all), i)[x];
+          v[i] = cl.map_shared_rank(reinterpret_cast<float4*>(ring_all + r / RW * C::RING), i)[r % RW * (D / 4) + d4];
         }
       }
 #pragma unroll
@@ -789,7 +772,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB>::CTAS) decode_kernel
         acc.z = fmaf(v[i].z, f, acc.z);
         acc.w = fmaf(v[i].w, f, acc.w);
       }
-      const int head = unit % p.kv_heads * group + r % group;
+      const int head = h * group + r % group;
       const int64_t row = (int64_t)(u.s.t0 + r / group) * p.q_heads + head;
       const float f = finish_scale(p, row, head, mn, ls, on, d4 == 0);
       store4<D>(p, row, d4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
@@ -863,7 +846,7 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(Args a) {
 }
 
 struct Plan {
-  int hb, rows, G, cs;
+  int hb, pw, rows, G, cs;
   size_t ml_off, unit_off, total;
 };
 
@@ -873,14 +856,16 @@ static Plan plan(const dsv4_gqa_attention_params& p) {
   Plan L;
   const int max_n = p.max_q_len < p.T ? p.max_q_len : p.T;
   L.rows = max_n * (p.q_heads / p.kv_heads);
-  L.hb = L.rows <= 8 ? 1 : L.rows <= 16 ? 2 : 4;
-  L.rows = 8 * L.hb;
+  L.hb = L.rows <= 8 ? 1 : 2;
+  L.pw = L.rows <= 16 ? 1 : 2;
+  L.rows = 8 * L.hb * L.pw;
   const int ctas = ctas_per_sm(p.head_dim, p.cache_dtype == DSV4_E4M3_PAGE, L.hb);
   const int64_t pieces = ((int64_t)p.B * p.kv_heads * (p.max_kv_len + 2 * 32) + MIN_ROWS - 1) / MIN_ROWS;
   L.G = num_sms() * ctas;
   if (pieces < L.G) L.G = (int)pieces;
   // A cluster a unit where the batch is small enough for all units' clusters to be resident and a warp to have
-  // few stages: its join costs less than a second kernel.  (Else, evenly cut pieces; beyond MAX_SCAN, a CTA a unit.)
+  // few stages: its join costs less than a second kernel (one token over 777 rows 8.8 us, 14.2 as pieces; 200 sequences
+  // of up to 1500 rows, one kv head, 21 and 28).  Else, evenly cut pieces; beyond MAX_SCAN, a CTA a unit.
   const int64_t units = (int64_t)p.B * p.kv_heads;
   int64_t seen = p.max_kv_len;
   if (p.window > 0 && (int64_t)p.window + max_n < seen) seen = (int64_t)p.window + max_n;
@@ -890,14 +875,14 @@ static Plan plan(const dsv4_gqa_attention_params& p) {
   const int64_t slots = L.cs == 0 ? 2LL * L.G : 0;
   L.ml_off = align_up((size_t)slots * L.rows * p.head_dim * 4, 256);
   L.unit_off = align_up(L.ml_off + (size_t)slots * L.rows * 16, 256);
-  L.total = align_up(L.unit_off + (size_t)p.B * p.kv_heads * 16, 256);
+  L.total = align_up(L.unit_off + (size_t)units * 16, 256);
   return L;
 }
 
-template <int D, bool E4M3, int HB>
+template <int D, bool E4M3, int HB, int PW>
 static cudaError_t launch(const Args& a, cudaStream_t s) {
-  using C = Cfg<D, E4M3, HB>;
-  const void* fn = reinterpret_cast<const void*>(decode_kernel<D, E4M3, HB>);
+  using C = Cfg<D, E4M3, HB, PW>;
+  const void* fn = reinterpret_cast<const void*>(decode_kernel<D, E4M3, HB, PW>);
   cudaError_t e = ensure_max_dynamic_smem(fn, C::SMEM);
   if (e != cudaSuccess) return e;
   const dsv4_gqa_attention_params& p = a.p;
@@ -917,14 +902,15 @@ static cudaError_t launch(const Args& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = count_launch(cudaLaunchKernelEx(&cfg, decode_kernel<D, E4M3, HB>, a));
+  e = count_launch(cudaLaunchKernelEx(&cfg, decode_kernel<D, E4M3, HB, PW>, a));
   if (e != cudaSuccess || a.cs) return e;
-  return launch_pdl(merge_kernel<D>, dim3((unsigned)units, 2 * HB), dim3(THREADS), 0, s, true, a);
+  return launch_pdl(merge_kernel<D>, dim3((unsigned)units, a.rows / NW), dim3(THREADS), 0, s, true, a);
 }
 
 template <int D, bool E4M3>
-static cudaError_t launch_hb(const Args& a, int hb, cudaStream_t s) {
-  return hb == 1 ? launch<D, E4M3, 1>(a, s) : hb == 2 ? launch<D, E4M3, 2>(a, s) : launch<D, E4M3, 4>(a, s);
+static cudaError_t launch_rows(const Args& a, const Plan& L, cudaStream_t s) {
+  if (L.hb == 1) return launch<D, E4M3, 1, 1>(a, s);
+  return L.pw == 2 ? launch<D, E4M3, 2, 2>(a, s) : launch<D, E4M3, 2, 1>(a, s);
 }
 
 }  // namespace dec
@@ -944,8 +930,8 @@ cudaError_t launch_decode(const dsv4_gqa_attention_params& p, cudaStream_t s) {
   a.cs = L.cs;
   const bool e4m3 = p.cache_dtype == DSV4_E4M3_PAGE;
   if (p.head_dim == 128)
-    return e4m3 ? dec::launch_hb<128, true>(a, L.hb, s) : dec::launch_hb<128, false>(a, L.hb, s);
-  return e4m3 ? dec::launch_hb<64, true>(a, L.hb, s) : dec::launch_hb<64, false>(a, L.hb, s);
+    return e4m3 ? dec::launch_rows<128, true>(a, L, s) : dec::launch_rows<128, false>(a, L, s);
+  return e4m3 ? dec::launch_rows<64, true>(a, L, s) : dec::launch_rows<64, false>(a, L, s);
 }
 
 }  // namespace gqa
