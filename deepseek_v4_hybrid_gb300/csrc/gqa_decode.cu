@@ -47,7 +47,8 @@ constexpr int BLK = 16;            // rows that lie in one page
 constexpr int MAX_SCAN = 1024;     // sequences whose stages are cut evenly; above, a CTA takes a whole unit
 constexpr int MAX_CLUSTER = 8;     // CTAs of a unit (portable cluster size)
 constexpr int MIN_ROWS = 128;      // rows of a piece, at least
-constexpr int CLUSTER_ROWS = 1024; // rows of a cluster's CTA, at most (512: 1 x 6000 rows 21 us for 15; 2048: 16 x 4000 43 for 35)
+// rows of a cluster's CTA, at most (512: one token over 6000 rows 21 us for 15; 2048: 16 x 4000 43 for 35)
+constexpr int CLUSTER_ROWS = 1024;
 constexpr float LAZY = 8.f;        // a running maximum moves when it is exceeded by more than 2^8
 
 struct Args {
@@ -121,7 +122,7 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
 }
 
 // Byte offset of 16-byte chunk ch of row r in a stage's K or V half: the chunks of a 128-byte line (one
-// row, half of one, or two) are exchanged so that the quarter-warps of both read patterns (rows 2k, 2k + 1
+// row, half of one, or two) are exchanged so that the share-warps of both read patterns (rows 2k, 2k + 1
 // with chunks c; rows 2c with the chunks of two lane groups) meet eight different ones.
 template <int ROWB>
 __device__ __forceinline__ int chunk_at(int r, int ch) {
@@ -781,68 +782,78 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB, PW>::CTAS) decode_ke
   }
 }
 
-// Units cut by a border between CTAs: a warp joins the partial results of one row.
-template <int D>
-__global__ void __launch_bounds__(THREADS) merge_kernel(Args a) {
+// Joins the partial results of the units that a piece's border cuts.  Q warps a row, each with every Qth eight of the
+// partials, all eight in flight: 4 where a unit has more than 8 partials on average (one warp a row: one token over
+// 16,000 rows 31 us for 22, 4 x 128k rows 180 for 174), else 1 (four: 32 x 8k rows 75 us for 69,
+// most of the warps idle).
+template <int D, int Q>
+__global__ void __launch_bounds__(Q * THREADS) merge_kernel(Args a) {
+  __shared__ float4 part[NW][Q][D / 4];
+  __shared__ float sums[NW][Q];
   pdl_wait();
   pdl_launch_dependents();
   const dsv4_gqa_attention_params& p = a.p;
   const int4 info = a.unit[blockIdx.x];
   if (info.w == 0) return;
   const int b = blockIdx.x / p.kv_heads, h = blockIdx.x % p.kv_heads, lane = threadIdx.x & 31;
+  const int wr = (threadIdx.x >> 5) / Q, share = (threadIdx.x >> 5) % Q, r = blockIdx.y * NW + wr;
   const Seq s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.max_kv_len);
   const int group = p.q_heads / p.kv_heads, rows = s.n * group, n = info.y - info.x + 1;
-  auto slot = [&](int i) { return 2 * (info.x + i) + (i == 0 ? info.z : 0); };
-  for (int r = blockIdx.y * NW + (threadIdx.x >> 5); r < rows; r += gridDim.y * NW) {
-    float mn = -INFINITY, on = -INFINITY;
+  auto slot = [&](int i) { return (int64_t)(2 * (info.x + i) + (i == 0 ? info.z : 0)) * a.rows + r; };
+  float mn = -INFINITY, on = -INFINITY;
+  if (r < rows) {
     for (int i = lane; i < n; i += 32) {
-      const float4 x = a.ml_part[(int64_t)slot(i) * a.rows + r];
+      const float4 x = a.ml_part[slot(i)];
       mn = fmaxf(mn, x.x);
       on = fmaxf(on, x.z);
     }
     mn = warp_max(mn);
     on = warp_max(on);
     float ls = 0.f;
-    constexpr int E = D / 32;  // dims of a lane, from lane * E on
-    float acc[E];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 8;
+    for (int i0 = U * share; i0 < n; i0 += Q * U) {
+      float4 v[U], x[U];
 #pragma unroll
-    for (int k = 0; k < E; ++k) acc[k] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float f = 0.f;
-      if (i0 + lane < n) {
-        const float4 x = a.ml_part[(int64_t)slot(i0 + lane) * a.rows + r];
-        if (x.x > -INFINITY) {
-          ls += x.y * tc::ex2_approx(x.x - mn);
-          f = tc::ex2_approx(x.z - on);
+      for (int k = 0; k < U; ++k) {
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        x[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        if (i0 + k < n) {
+          x[k] = a.ml_part[slot(i0 + k)];
+          if (lane < D / 4) v[k] = reinterpret_cast<const float4*>(a.o_part)[slot(i0 + k) * (D / 4) + lane];
         }
       }
-      const int m = min(32, n - i0);
-#pragma unroll 4
-      for (int i = 0; i < m; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float2* src = reinterpret_cast<const float2*>(a.o_part + ((int64_t)slot(i0 + i) * a.rows + r) * D + lane * E);
 #pragma unroll
-        for (int k = 0; k < E; k += 2) {
-          const float2 v = src[k / 2];
-          acc[k] = fmaf(v.x, fi, acc[k]);
-          acc[k + 1] = fmaf(v.y, fi, acc[k + 1]);
+      for (int k = 0; k < U; ++k)
+        if (x[k].x > -INFINITY) {
+          const float f = tc::ex2_approx(x[k].z - on);
+          ls = fmaf(x[k].y, tc::ex2_approx(x[k].x - mn), ls);
+          acc.x = fmaf(v[k].x, f, acc.x);
+          acc.y = fmaf(v[k].y, f, acc.y);
+          acc.z = fmaf(v[k].z, f, acc.z);
+          acc.w = fmaf(v[k].w, f, acc.w);
         }
-      }
     }
-    ls = warp_sum(ls);
-    const int head = h * group + r % group;
-    const int64_t row = (int64_t)(s.t0 + r / group) * p.q_heads + head;
-    const float f = finish_scale(p, row, head, mn, ls, on, lane == 0);
-    if (p.out_dtype == DSV4_F32) {
-#pragma unroll
-      for (int k = 0; k < E; k += 2)
-        reinterpret_cast<float2*>(p.out)[(row * D + lane * E + k) / 2] = make_float2(acc[k] * f, acc[k + 1] * f);
-    } else {
-#pragma unroll
-      for (int k = 0; k < E; k += 2)
-        reinterpret_cast<uint32_t*>(p.out)[(row * D + lane * E + k) / 2] = float2_to_bf16x2_bits(acc[k] * f, acc[k + 1] * f);
-    }
+    if (lane < D / 4) part[wr][share][lane] = acc;
+    if (lane == 0) sums[wr][share] = ls;
   }
+  __syncthreads();
+  if (r >= rows || share != 0 || lane >= D / 4) return;
+  float ls = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int y = 0; y < Q; ++y) {
+    const float4 v = part[wr][y][lane];
+    ls += sums[wr][y];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+  }
+  const int head = h * group + r % group;
+  const int64_t row = (int64_t)(s.t0 + r / group) * p.q_heads + head;
+  const float f = finish_scale(p, row, head, mn, ls, on, lane == 0);
+  store4<D>(p, row, lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
 }
 
 struct Plan {
@@ -904,7 +915,9 @@ static cudaError_t launch(const Args& a, cudaStream_t s) {
   cfg.numAttrs = 2;
   e = count_launch(cudaLaunchKernelEx(&cfg, decode_kernel<D, E4M3, HB, PW>, a));
   if (e != cudaSuccess || a.cs) return e;
-  return launch_pdl(merge_kernel<D>, dim3((unsigned)units, a.rows / NW), dim3(THREADS), 0, s, true, a);
+  const dim3 grid((unsigned)units, a.rows / NW);
+  if (a.G > 8 * units) return launch_pdl(merge_kernel<D, 4>, grid, dim3(4 * THREADS), 0, s, true, a);
+  return launch_pdl(merge_kernel<D, 1>, grid, dim3(THREADS), 0, s, true, a);
 }
 
 template <int D, bool E4M3>
