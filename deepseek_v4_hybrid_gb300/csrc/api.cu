@@ -35,7 +35,7 @@ bool act_dtype(int d) { return d == DSV4_F32 || d == DSV4_BF16; }
 // What the two grouped-query calls share: the ragged batch, the caches and their exponents.
 template <typename P>
 int check_gqa(const P& p) {
-  CHECK(p.T >= 0 && p.B >= 0 && p.B <= 65535 && p.max_q_len >= 1, DSV4_ERR_INVALID);
+  CHECK(p.T >= 0 && p.T <= (1 << 30) && p.B >= 0 && p.B <= 65535 && p.max_q_len >= 1, DSV4_ERR_INVALID);
   CHECK(p.num_pages >= 0 && p.num_pages <= 0x7FFFFFFF && p.max_pages_per_seq > 0, DSV4_ERR_INVALID);
   CHECK(p.q_heads >= 1 && p.q_heads <= 1024 && p.kv_heads >= 1 && p.kv_heads <= 1024, DSV4_ERR_INVALID);
   CHECK(p.head_dim == 64 || p.head_dim == 128, DSV4_ERR_UNSUPPORTED);
@@ -255,6 +255,7 @@ int dsv4_gqa_append(const dsv4_gqa_append_params* p, dsv4_stream_t stream) {
     CHECK(token_strides(p->q_token_stride, p->q_head_stride) &&
               token_strides(p->q_out_token_stride, p->q_out_head_stride),
           DSV4_ERR_INVALID);
+    CHECK((p->q_out_token_stride > 0 || p->T == 1) && (p->q_out_head_stride > 0 || p->q_heads == 1), DSV4_ERR_INVALID);
     CHECK(p->q != p->q_out || (p->q_token_stride == p->q_out_token_stride && p->q_head_stride == p->q_out_head_stride),
           DSV4_ERR_INVALID);
   }
@@ -270,6 +271,7 @@ int check_gqa_attention(const dsv4_gqa_attention_params& p) {
   CHECK((int64_t)(p.max_q_len < p.T ? p.max_q_len : p.T) * (p.q_heads / p.kv_heads) <= (1 << 30), DSV4_ERR_UNSUPPORTED);
   CHECK(p.causal == 0 || p.causal == 1, DSV4_ERR_INVALID);
   CHECK(std::isfinite(p.softmax_scale) && std::isfinite(p.softcap) && p.softcap >= 0.f, DSV4_ERR_INVALID);
+  CHECK(p.softcap <= 1024.f && (p.softcap == 0.f || std::isfinite(4.f * p.softmax_scale / p.softcap)), DSV4_ERR_INVALID);
   CHECK(act_dtype(p.out_dtype), DSV4_ERR_UNSUPPORTED);
   return DSV4_OK;
 }

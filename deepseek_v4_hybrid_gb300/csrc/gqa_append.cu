@@ -126,7 +126,7 @@ __device__ __forceinline__ void rotate_queries(const dsv4_gqa_append_params& p, 
     lo += k * step;
     hi = min(hi, lo + step);
   }
-  const Seq s = sequence(p.q_start, p.kv_len, lo, p.T, p.max_q_len, p.cos_sin ? p.max_pos : -1);
+  const Seq s = sequence(p.q_start, p.kv_len, lo, p.T, p.max_q_len, p.cos_sin ? p.max_pos : MAX_ROWS);
   if (!s.ok || t >= s.t0 + s.n) return;  // padding behind the last sequence, or a skipped sequence
   Turn tr;
   turn_of(rope, c, s.kv - s.n + (t - s.t0), true, tr);
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? 8 : E4M3 ? 2 : 3)
   const bool is_v = item & 1;
   const int h = (item >> 1) % p.kv_heads, u = (item >> 1) / p.kv_heads;
   const int b = u / pages_per_seq, slot = u % pages_per_seq;
-  const Seq s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.cos_sin ? p.max_pos : -1);
+  const Seq s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.cos_sin ? p.max_pos : MAX_ROWS);
   if (!s.ok) {
     if (slot == 0 && h == 0 && tid == 0) atomicOr(&g_flags_ga, FLAG_PAGE);
     return;

@@ -21,7 +21,9 @@ struct Seq {
   bool ok;        // false: the sequence is skipped
 };
 
-// Sequence b of the batch; `kv_bound` < 0 means none.
+constexpr int MAX_ROWS = 1 << 30;  // of a sequence
+
+// Sequence b of the batch.
 __device__ __forceinline__ Seq sequence(const int32_t* q_start, const int32_t* kv_len, int b, int T, int max_q_len,
                                         int kv_bound) {
   Seq s;
@@ -30,7 +32,7 @@ __device__ __forceinline__ Seq sequence(const int32_t* q_start, const int32_t* k
   s.kv = kv_len[b];
   s.ok = s.t0 >= 0 && t1 >= s.t0 && t1 <= T;
   s.n = s.ok ? t1 - s.t0 : 0;
-  s.ok = s.ok && s.n <= max_q_len && s.kv >= s.n && (kv_bound < 0 || s.kv <= kv_bound);
+  s.ok = s.ok && s.n <= max_q_len && s.kv >= s.n && s.kv <= min(kv_bound, MAX_ROWS);
   return s;
 }
 

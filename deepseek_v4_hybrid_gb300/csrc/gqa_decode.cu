@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB, PW>::CTAS) decode_ke
 
       // rows g + 8 k of this lane
       int rlo[HB], rhi[HB];
-      float rmul[HB], slope[HB], rpos[HB];
+      float rmul[HB], slope[HB];
+      int rpos[HB];
       float m[HB], mo[HB], l[HB];
       int all_lo = 0, all_hi = 0x7FFFFFFF;  // rows that every token sees
       // Q's A fragments; e4m3: [K step][hi, lo], or both terms in one for 8 rows.
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB, PW>::CTAS) decode_ke
         rlo[k] = 0;
         rhi[k] = 0;
         slope[k] = 0.f;
-        rpos[k] = (float)pos;
+        rpos[k] = pos;
         rmul[k] = 0.f;
         m[k] = mo[k] = -INFINITY;
         l[k] = 0.f;
@@ -491,6 +492,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB, PW>::CTAS) decode_ke
 #pragma unroll
         for (int k2 = 0; k2 < HB; ++k2) {
           top[k2] = -INFINITY;
+          const float far = (float)(rpos[k2] - j0 - 2 * c);  // (near distances stay exact however long the cache)
 #pragma unroll
           for (int nt = 0; nt < 2 * SUB; ++nt)
 #pragma unroll
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D, E4M3, HB, PW>::CTAS) decode_ke
               const int j = j0 + 8 * nt + 2 * c + y;
               if (!plain) {
                 if (p.softcap > 0.f) v = cap_logit(v, p.softcap, rcap2);
-                v = v * LOG2E - slope[k2] * fabsf(rpos[k2] - (float)j);
+                v = v * LOG2E - slope[k2] * fabsf(far - (float)(8 * nt + y));
               }
               if (!inside && (!page_ok[nt / 2] || j < rlo[k2] || j >= rhi[k2])) v = -INFINITY;
               top[k2] = fmaxf(top[k2], v);

@@ -47,7 +47,7 @@ constexpr uint32_t FLAG_TIMEOUT = 4u;
 
 struct Args {
   dsv4_gqa_attention_params p;
-  int4* unit;        // [B * tps]: first row seen, end of the rows seen, key tiles of tile 0 and 1 (bit 30 of the
+  int4* unit;        // [B * tps] of the evenly cut list: first row seen, end of the rows seen, key tiles of tile 0 and 1 (bit 30 of the
                      // latter: some page is out of range)
   float4* o_part;    // [2 G][8 groups of 32 rows][D / 4][32 rows]: a warp stores and loads whole lines
   float2* ml_part;   // [2 G][256]
@@ -1041,7 +1041,7 @@ static Plan plan(const dsv4_gqa_attention_params& p) {
     at = align_up(at + bytes, 256);
     return x;
   };
-  L.unit = take((size_t)units * 16);
+  L.unit = take(L.even ? (size_t)units * 16 : 0);
   L.part = take(slots * UROWS * p.head_dim * 4);
   L.ml = take(slots * UROWS * 8);
   L.cut = take((size_t)L.G * 16);
@@ -1095,7 +1095,7 @@ static cudaError_t launch(const dsv4_gqa_attention_params& p, cudaStream_t s) {
   const int64_t ts = 2 * p.q_token_stride, hs = 2 * p.q_head_stride;
   a.q_tma = TILE % group == 0 && ts > 0 && hs > 0 && ts < (1LL << 40) && hs < (1LL << 40);
   if (a.q_tma) {
-    e = make_tmap_4d_bf16(&qmap, p.q, D, p.q_heads, p.T, 1, hs, ts, ts * p.T, 64, group, TILE / group);
+    e = make_tmap_4d_bf16(&qmap, p.q, D, p.q_heads, p.T, 1, hs, ts, ts, 64, group, TILE / group);
     if (e != cudaSuccess) a.q_tma = 0;
   }
   const int smem = (2 + NSLOT) * TILE * D * 2 + 4 * 2048 + (int)sizeof(Smem) + 1024;

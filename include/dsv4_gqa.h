@@ -16,7 +16,7 @@
  *    at position kv_len[b] - n_b + i.  n_b = 0 and kv_len[b] = 0 are allowed.  Tokens from q_start[B] on
  *    (the padding of a fixed-size batch) are not written, and what they hold does not matter.
  *  - A sequence with q_start not in 0 <= q_start[b] <= q_start[b+1] <= T, n_b > max_q_len,
- *    kv_len[b] < n_b or kv_len[b] over the call's bound is skipped (its outputs stay as they were) and
+ *    kv_len[b] < n_b or kv_len[b] over 2^30 or the call's bound is skipped (its outputs stay as they were) and
  *    flagged (bit 0).
  *  - Caches are [num_pages, kv_heads, page_size, head_dim] in any order of the first three (element
  *    strides are given; head_dim is contiguous).  Row j of sequence b lies in page
@@ -52,7 +52,8 @@ extern "C" {
  * call's first one are re-encoded: code' = RNE(code * 2^(old - new)), exact unless the result is
  * subnormal.  Then code = RNE(x * 2^-exponent).  NaN stays NaN; +-Inf saturates at code +-448 (and
  * sets the exponent to 120).
- * Distinct sequences must not store into the same page (its contents would be unspecified).
+ * A call must not store into one page twice, for two sequences or two table entries of one (its contents
+ * would be unspecified).
  * ------------------------------------------------------------------------------------------- */
 typedef struct dsv4_gqa_append_params {
   uint32_t struct_size;
@@ -60,7 +61,7 @@ typedef struct dsv4_gqa_append_params {
   const void* v_new;           /* the same */
   int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;  /* elements, multiples of 8 */
   const void* q;               /* [T, q_heads, head_dim] bf16, 16-byte aligned, or NULL: no queries */
-  void* q_out;                 /* bf16, 16-byte aligned; q itself (same strides: in place) or apart from it */
+  void* q_out;                 /* bf16, 16-byte aligned, strides > 0; q itself (same strides: in place) or apart */
   int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
   void* k_cache;               /* 16-byte aligned, in cache_dtype */
   void* v_cache;
@@ -69,7 +70,7 @@ typedef struct dsv4_gqa_append_params {
   uint8_t* k_exp;              /* [num_pages, kv_heads] (E4M3_PAGE only) */
   uint8_t* v_exp;
   int32_t cache_dtype;         /* DSV4_BF16 or DSV4_E4M3_PAGE */
-  int32_t T, B, q_heads, kv_heads, head_dim;  /* head_dim 64 or 128; heads 1 .. 1024; B <= 65535 */
+  int32_t T, B, q_heads, kv_heads, head_dim;  /* T <= 2^30; B <= 65535; heads 1 .. 1024; head_dim 64 or 128 */
   int32_t page_size;           /* 16, 32, 64, 128 or 256 */
   int64_t num_pages;           /* < 2^31 */
   const int32_t* block_table;  /* [B, max_pages_per_seq] */
@@ -95,9 +96,11 @@ int dsv4_gqa_append(const dsv4_gqa_append_params* p, dsv4_stream_t stream);
  * Row j is visible when  j < kv_len[b],  causal == 0 or j <= p or j < prefix_len[b],
  * window == 0 or j > p - window,  and j >= kv_start[t].  A token that sees no row gets out = 0 and
  * lse = sink[h] (-inf without a sink).
- * What rows no token of the sequence sees hold (rows from kv_len on, rows of other pages, rows before
- * every token's window) never matters, NaN included.  Rows that some token of the sequence sees must
- * hold finite values: a NaN or Inf among them may also reach the sequence's tokens that do not see it.
+ * What rows from kv_len on, rows of other pages and rows before the first one that any of the sequence's
+ * tokens sees hold never matters, NaN included.  The rows from that one on must hold finite values: a NaN
+ * or Inf among them may also reach tokens that do not see it.
+ * The workspace of an e4m3 call with more than 32 rows (token, head of the group) a sequence has room for
+ * bf16 copies of the batch's rows: 4 B kv_heads max_kv_len head_dim bytes, lengths rounded up to 128.
  * ------------------------------------------------------------------------------------------- */
 typedef struct dsv4_gqa_attention_params {
   uint32_t struct_size;
@@ -123,9 +126,10 @@ typedef struct dsv4_gqa_attention_params {
   const int32_t* prefix_len;   /* [B] rows visible to every token of the sequence, or NULL */
   const int32_t* kv_start;     /* [T] first visible row of each token, or NULL */
   int32_t window;              /* 0: none */
-  float softcap;               /* 0: none; >= 0, finite */
+  float softcap;               /* 0: none; at most 1024 (logits are off by up to softcap * 2^-22), and
+                                  4 softmax_scale / softcap finite */
   const float* slopes;         /* [q_heads] or NULL */
-  const float* sink;           /* [q_heads] or NULL (= -inf) */
+  const float* sink;           /* [q_heads], finite or -inf, or NULL (= -inf) */
   void* out;                   /* [T, q_heads, head_dim] contiguous, out_dtype BF16 or F32, 16-byte aligned */
   int32_t out_dtype;
   float* lse;                  /* [T, q_heads] or NULL */

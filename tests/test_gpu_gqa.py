@@ -477,3 +477,217 @@ def test_prompt_then_decode(M, cache):
         want, wlse, mag, size = G.attention(q64, want_c, want_e, table, q_start, kvl, scale)
         tol, _ = bounds(mag, size, want, wlse, False)
         assert (np.abs(out.double().cpu().numpy() - want) <= tol).all(), i
+
+
+# ------------------------------------------------------------------------------------------------
+# calls at the edges of what is allowed
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,D,n", [(8, 2, 64, 1), (12, 1, 128, 1), (8, 1, 64, 3)])
+def test_attention_of_more_sequences_than_the_list_holds(M, H, Hkv, D, n, cache):
+    """Over 1024 sequences a CTA takes a whole (sequence, kv head); 8, 12 and 24 rows a kv head, empty ones between."""
+    g = np.random.default_rng(3)
+    count = 1100
+    ns = np.where(g.random(count) < 0.9, 0, n)
+    ns[[0, 1023, 1024, count - 1]] = n
+    kv = np.where(ns > 0, n + g.integers(0, 150, count), g.integers(0, 3, count))
+    check_attention(M, Batch(ns, kv, H, Hkv, D, 16, cache, seed=1), sink=np.linspace(-1, 1, H))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_long_attention_of_more_units_than_the_list_holds(M, cache):
+    """Over 8192 units of 256 rows a CTA takes a whole one, whatever the lengths."""
+    g = np.random.default_rng(4)
+    count = 2100
+    ns = np.where(g.random(count) < 0.99, 0, 40)
+    ns[[0, count - 1]] = 90
+    kv = np.where(ns > 0, ns + g.integers(0, 150, count), g.integers(0, 3, count))
+    check_attention(M, Batch(ns, kv, 4, 2, 64, 32, cache, seed=1), max_q=600)
+
+
+@pytest.mark.parametrize("group", [3, 5, 7, 9, 48, 128, 200])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_attention_of_odd_groups(M, group, D):
+    """Query tiles whose 128 rows do not hold whole tokens, or less than one."""
+    check_attention(M, Batch([40, 3], [50, 200], group, 1, D, 64, "bf16", seed=group))
+
+
+@pytest.mark.parametrize("group", [3, 5, 7, 9, 11, 15, 20, 31, 32])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_single_token_attention_of_odd_groups(M, group, cache):
+    check_attention(M, Batch([1, 1, 0, 1], [1, 333, 0, 64], 2 * group, 2, 128, 32, cache, seed=group))
+
+
+@pytest.mark.parametrize("n,kv", [([2, 1, 0], [90, 40, 0]), ([70, 0, 40], [90, 0, 400])])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_padding_tokens_may_hold_anything(M, n, kv, cache):
+    """NaN in the padding's queries, keys and values; its outputs stay as they were."""
+    bt = Batch(n, kv, 8, 2, 64, 32, cache, seed=6, pad=200)
+    live = int(bt.q_start[-1])
+    bt.q[live:] = bt.k_new[live:] = bt.v_new[live:] = 0x7FC0
+    check_append(M, bt, cos_sin(400, 64))
+    check_attention(M, bt)
+
+
+@pytest.mark.parametrize("n,kv", [([4, 1], [100, 70]), ([40, 33], [100, 70])])
+def test_one_query_for_every_token_and_head(M, n, kv):
+    """Queries of stride 0: one row, read by all."""
+    bt = Batch(n, kv, 4, 2, 64, 32, "e4m3", seed=6)
+    bt.q[:] = bt.q[:1, :1]
+    kc, vc, ke, ve = dev(bt.caches[0]), dev(bt.caches[1]), dev(bt.exps[0]), dev(bt.exps[1])
+    out = torch.empty((bt.T, 4, 64), device="cuda")
+    q = dev(bt.q[:1, :1]).expand(bt.T, 4, 64)
+    p = M.gqa_attention_params(q, kc, vc, dev(bt.table), dev(bt.q_start), dev(bt.kv), bt.max_q, bt.max_kv, 0.125, out,
+                               k_scale=ke, v_scale=ve)
+    M.gqa_set_workspace(p, torch.empty(M.dsv4_gqa_attention_workspace_bytes(p), dtype=torch.uint8, device="cuda"))
+    M.dsv4_gqa_attention(p)
+    assert M.dsv4_read_device_flags() == 0
+    want, wlse, mag, size = G.attention(bt.q64(), bt.caches, bt.exps, bt.table, bt.q_start, bt.kv, 0.125)
+    assert (np.abs(out.double().cpu().numpy() - want) <= bounds(mag, size, want, wlse, False)[0]).all()
+
+
+@pytest.mark.parametrize("n", [1, 60])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_caches_and_positions_past_32_bits(M, n, cache):
+    """Pages whose offsets pass 2^32 elements, at positions beyond 2^24 (odd ones, which fp32 does not hold), in a window:
+    append, then attention with distance bias, against the oracle on the sequence's last pages."""
+    H, Hkv, D, page, pages, W = 4, 1, 128, 256, 140000, 300
+    e4m3 = cache == "e4m3"
+    dt = torch.uint8 if e4m3 else torch.bfloat16
+    kc, vc = (torch.empty((pages, Hkv, page, D), dtype=dt, device="cuda") for _ in range(2))
+    assert kc.numel() > 2 ** 32
+    base = 78200 * page                                   # 20,019,200 rows before those that are looked at
+    kv = base + 3 * page + 77                             # the window and the new rows lie in four pages
+    mine = [pages - 1, 5, pages - 3, pages - 2]
+    table = np.full((1, base // page + 4), -1, np.int32)
+    table[0, -4:] = mine
+    small = Batch([n], [kv - base], H, Hkv, D, page, cache, seed=3)
+    g = np.random.default_rng(1)
+    at = torch.tensor(mine, device="cuda")
+    fill, exps = [], None
+    for c in (kc, vc):
+        x = O.bf16_encode(g.standard_normal((4, Hkv, page, D)))
+        if e4m3:
+            x = O.e4m3_encode(np.clip(g.standard_normal((4, Hkv, page, D)) * 100, -448, 448))
+        fill.append(x)
+        c[at] = dev(x)
+    dev_e = [None, None]
+    if e4m3:
+        exps = [g.integers(117, 123, (4, Hkv)).astype(np.uint8) for _ in range(2)]
+        dev_e = [torch.zeros((pages, Hkv), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        for d, e in zip(dev_e, exps):
+            d[at] = dev(e)
+    tab, qs, kvl = dev(table), dev(small.q_start), dev(np.array([kv], np.int32))
+    ap = M.gqa_append_params(dev(small.k_new), dev(small.v_new), kc, vc, tab, qs, kvl, n, k_scale=dev_e[0], v_scale=dev_e[1])
+    M.dsv4_gqa_append(ap)
+    assert M.dsv4_read_device_flags() == 0
+    local = np.arange(4, dtype=np.int32)[None]
+    local_kv = np.array([kv - base], np.int32)
+    G.append(O.bf16_decode(small.k_new), O.bf16_decode(small.v_new), fill, exps, local, small.q_start, local_kv)
+    for c, want in zip((kc, vc), fill):
+        got = c[at]
+        np.testing.assert_array_equal(host(got), want)
+    out = torch.empty((n, H, D), device="cuda")
+    slopes = np.array([2.0, 0.5, 0.25, 0.0])
+    p = M.gqa_attention_params(dev(small.q), kc, vc, tab, qs, kvl, n, kv, 0.1, out, k_scale=dev_e[0], v_scale=dev_e[1],
+                               window=W, slopes=dev(slopes.astype(np.float32)))
+    size = M.dsv4_gqa_attention_workspace_bytes(p)
+    M.gqa_set_workspace(p, torch.empty(size, dtype=torch.uint8, device="cuda"))
+    M.dsv4_gqa_attention(p)
+    assert M.dsv4_read_device_flags() == 0
+    want, wlse, mag, size = G.attention(small.q64(), fill, exps, local, small.q_start, local_kv, 0.1, window=W, slopes=slopes)
+    tol = bounds(mag, size, want, wlse, False)[0]
+    worst = (np.abs(out.double().cpu().numpy() - want) / tol).max()
+    assert worst <= 1, worst
+
+
+def test_append_skips_lengths_over_two_to_thirty(M):
+    bt = Batch([1, 1], [20, 9], 2, 1, 64, 16, "bf16", seed=3)
+    kv = bt.kv.copy()
+    kv[0] = 2 ** 30 + 1
+    kc, vc = dev(bt.caches[0]), dev(bt.caches[1])
+    p = M.gqa_append_params(dev(bt.k_new), dev(bt.v_new), kc, vc, dev(bt.table), dev(bt.q_start), dev(kv), 1)
+    M.dsv4_gqa_append(p)
+    assert M.dsv4_read_device_flags() == 1
+    got = host(kc)
+    np.testing.assert_array_equal(got[bt.table[0]], bt.caches[0][bt.table[0]])
+    np.testing.assert_array_equal(got[bt.table[1, 0], :, 8], bt.k_new[1])
+
+
+def test_two_streams_with_workspaces_of_their_own(M):
+    """A long and a short call at once, twenty times over: the bits of the calls one after the other."""
+    runs = []
+    for n, kv in (([1] * 6, [3000, 40, 900, 77, 2000, 1]), ([90, 33], [1500, 700]), ([300, 2], [300, 900])):
+        bt = Batch(n, kv, 16, 2, 128, 64, "e4m3", seed=14)
+        p, out, _ = run_attention(M, bt)
+        runs.append((p, out, out.clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, out, _, s in runs:
+            with torch.cuda.stream(s):
+                out.fill_(7)
+                M.dsv4_gqa_attention(p)
+    torch.cuda.synchronize()
+    for _, out, want, _ in runs:
+        assert torch.equal(out, want)
+    assert M.dsv4_read_device_flags() == 0
+
+
+@pytest.mark.parametrize("n,max_q", [(1, 1), (4, 4), (40, 40)])
+def test_captured_steps_replay_with_other_lengths(M, n, max_q):
+    """Append and attention captured with no eager call before; the lengths, tables and rows change between replays."""
+    H, Hkv, D, page = 8, 2, 128, 32
+    a = Batch([n, n], [200, 130], H, Hkv, D, page, "e4m3", seed=1)
+    b = Batch([n, 0], [55, 64], H, Hkv, D, page, "e4m3", seed=2, pad=n)
+    width, pages = 8, 24
+    tab = torch.zeros((2, width), dtype=torch.int32, device="cuda")
+    qs, kvl = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    kc, vc = (torch.zeros((pages, Hkv, page, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ke, ve = (torch.zeros((pages, Hkv), dtype=torch.uint8, device="cuda") for _ in range(2))
+    x = torch.zeros((2 * n, H + 2 * Hkv, D), dtype=torch.bfloat16, device="cuda")
+    rot = torch.zeros((2 * n, H, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((2 * n, H, D), device="cuda")
+    rope = cos_sin(300, D)
+    ap = M.gqa_append_params(x[:, H:H + Hkv], x[:, H + Hkv:], kc, vc, tab, qs, kvl, max_q, k_scale=ke, v_scale=ve,
+                             cos_sin=dev(rope), q=x[:, :H], q_out=rot)
+    at = M.gqa_attention_params(rot, kc, vc, tab, qs, kvl, max_q, width * page, 0.1, out, k_scale=ke, v_scale=ve)
+    M.gqa_set_workspace(at, torch.empty(M.dsv4_gqa_attention_workspace_bytes(at), dtype=torch.uint8, device="cuda"))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        M.dsv4_gqa_append(ap)
+        M.dsv4_gqa_attention(at)
+    for bt in (a, b, a):
+        tab.fill_(-1)
+        tab[:, :bt.table.shape[1]] = dev(bt.table)
+        qs.copy_(dev(bt.q_start))
+        kvl.copy_(dev(bt.kv))
+        for c, e, hc, he in zip((kc, vc), (ke, ve), bt.caches, bt.exps):
+            c[:len(hc)] = dev(hc)
+            e[:len(he)] = dev(he)
+        x.copy_(torch.cat([dev(bt.q), dev(bt.k_new), dev(bt.v_new)], 1))
+        out.fill_(-3)
+        g.replay()
+        assert M.dsv4_read_device_flags() == 0
+        caches, exps = [c.copy() for c in bt.caches], [e.copy() for e in bt.exps]
+        G.append(O.bf16_decode(bt.k_new), O.bf16_decode(bt.v_new), caches, exps, bt.table, bt.q_start, bt.kv, rope)
+        for c, want in zip((kc, vc), caches):
+            np.testing.assert_array_equal(host(c)[:len(want)], want)
+        want, wlse, mag, size = G.attention(O.bf16_decode(host(rot)).astype(np.float64), caches, exps, bt.table, bt.q_start,
+                                            bt.kv, 0.1)
+        live = int(bt.q_start[-1])
+        tol = bounds(mag, size, want, wlse, False)[0]
+        got = out.double().cpu().numpy()
+        assert (np.abs(got - want)[:live] <= tol[:live]).all()
+        assert (got[live:] == -3).all()
+
+
+@pytest.mark.parametrize("n,kv", [([1, 3], [300, 65]), ([60, 70], [300, 70])])
+@pytest.mark.parametrize("cap", [300.0, 1000.0])
+def test_attention_wide_caps(M, n, kv, cap):
+    """Caps far above the logits: off by softcap * 2^-22 more than the bounds, which the weights feel twice."""
+    bt = Batch(n, kv, 8, 2, 128, 64, "bf16", seed=5, qscale=2.0)
+    _, out, _ = run_attention(M, bt, softcap=cap)
+    want, wlse, mag, size = G.attention(bt.q64(), bt.caches, bt.exps, bt.table, bt.q_start, bt.kv, bt.D ** -0.5, softcap=cap)
+    tol = bounds(mag, size, want, wlse, False)[0] + mag * 2 * np.expm1(cap * 2.0 ** -22)
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+    assert M.dsv4_read_device_flags() == 0

@@ -110,6 +110,22 @@ def test_attention_refusals(abi, kw, status):
     assert lib.dsv4_kernel_launches() == n0
 
 
+@pytest.mark.parametrize("kw", [dict(softcap=2000.0), dict(softcap=1e-39, softmax_scale=8.0), dict(T=(1 << 30) + 1)])
+def test_attention_refuses_caps_and_counts_out_of_range(abi, kw):
+    lib, n0 = abi.load(), abi.load().dsv4_kernel_launches()
+    assert lib.dsv4_gqa_attention(attention_params(abi, **kw), None) == -1
+    assert lib.dsv4_gqa_attention_workspace_bytes(attention_params(abi, **kw)) == 0
+    assert lib.dsv4_kernel_launches() == n0
+
+
+@pytest.mark.parametrize("kw", [dict(q_out_token_stride=0), dict(q_out_head_stride=0)])
+def test_append_refuses_queries_written_over_one_another(abi, kw):
+    lib, n0 = abi.load(), abi.load().dsv4_kernel_launches()
+    assert lib.dsv4_gqa_append(append_params(abi, q=0x20000, q_out=0x30000, **kw), None) == -1
+    assert lib.dsv4_gqa_append(append_params(abi, T=(1 << 30) + 1), None) == -1
+    assert lib.dsv4_kernel_launches() == n0
+
+
 def test_workspace_is_zero_for_refused_params_and_empty_calls_pass(abi):
     lib = abi.load()
     assert lib.dsv4_gqa_attention_workspace_bytes(attention_params(abi)) > 0
