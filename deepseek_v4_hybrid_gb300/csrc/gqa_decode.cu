@@ -47,7 +47,7 @@ constexpr int BLK = 16;            // rows that lie in one page
 constexpr int MAX_SCAN = 1024;     // sequences whose stages are cut evenly; above, a CTA takes a whole unit
 constexpr int MAX_CLUSTER = 8;     // CTAs of a unit (portable cluster size)
 constexpr int MIN_ROWS = 128;      // rows of a piece, at least
-// rows of a cluster's CTA, at most (512: one token over 6000 rows 21 us for 15; 2048: 16 x 4000 43 for 35)
+// rows of a cluster's CTA, at most (16 sequences of up to 2000 e4m3 rows 21.7 us, 23.8 at 512; up to 4000 rows 32, 43 at 2048)
 constexpr int CLUSTER_ROWS = 1024;
 // Stages that a unit's start and end (lengths, queries, the drained and refilled rings, its merge) weigh in the list: pieces
 // of many short units end with those of few long ones (128 sequences of 100 to 1000 e4m3 rows, 8 kv heads: 63 us at 0, 51 at
@@ -887,8 +887,8 @@ static Plan plan(const dsv4_gqa_attention_params& p) {
   L.G = num_sms() * ctas;
   if (pieces < L.G) L.G = (int)pieces;
   // A cluster a unit where the batch is small enough for all units' clusters to be resident and a warp to have
-  // few stages: its join costs less than a second kernel (one token over 777 rows 8.8 us, 14.2 as pieces; 200 sequences
-  // of up to 1500 rows, one kv head, 21 and 28).  Else, evenly cut pieces; beyond MAX_SCAN, a CTA a unit.
+  // few stages: its join costs less than a second kernel (one token over 777 rows 8.8 us, 10.1 as pieces; 48 x 4
+  // tokens in a window of 1024 38 and 42; 200 sequences of up to 1500 rows, one kv head, 21.2 and 22.2).  Else, evenly cut pieces; beyond MAX_SCAN, a CTA a unit.
   const int64_t units = (int64_t)p.B * p.kv_heads;
   int64_t seen = p.max_kv_len;
   if (p.window > 0 && (int64_t)p.window + max_n < seen) seen = (int64_t)p.window + max_n;

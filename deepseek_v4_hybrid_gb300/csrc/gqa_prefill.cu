@@ -14,8 +14,8 @@
 //   Warps 14 and 15 load the tiles' queries: by TMA where the group divides 128 (a box of tokens x heads is
 //   128 rows), else by cp.async.
 // Bound by the softmax between the products, about 1450 cycles a warpgroup and tile of 128 x 128 beside 1024 of MMAs, and
-// at head_dim 64 or with capped scores by the exponentials: 8192 tokens of 64 heads of 128, causal, 834 us, 1320 TFLOP/s
-// (71 % of the measured cuBLAS rate).
+// at head_dim 64 or with capped scores by the exponentials: 8192 tokens of 64 heads of 128, causal, 823 us, 1340 TFLOP/s
+// (72 % of the measured cuBLAS rate).
 //
 // The work of a batch is one list of key tiles, ordered (sequence, kv head, unit), a unit weighing its tiles
 // plus UNIT_COST (its queries' load and output), cut evenly over one persistent CTA per SM: ragged batches,
@@ -40,7 +40,9 @@ constexpr int W_OUT = 8, W_LOAD = 12, W_MMA = 13, W_QUERY = 14, THREADS = 512;
 // Registers a thread: 512 x 128 at launch = 256 x 136 (softmax) + 128 x 120 (output) + 128 x 120 (the rest).
 constexpr int REGS_SOFTMAX = 136, REGS_OUT = 120, REGS_REST = 120;
 constexpr int NSLOT = 4;
-constexpr int UNIT_COST = 3;
+// Key tiles that a unit's queries and output weigh in the list (8 x up to 2048 tokens over up to 1000 rows: 270 us at 1, 266 at
+// 2, 271 at 3, 279 at 5; 8192 tokens 854, 823, 831, 850).
+constexpr int UNIT_COST = 2;
 constexpr int FEW_ROWS = 1024;
 constexpr int MAX_UNITS = 8192;   // units of the evenly cut list (its sums fill the ring's 64 KB); above, a CTA a unit
 constexpr float LAZY = 8.f;
