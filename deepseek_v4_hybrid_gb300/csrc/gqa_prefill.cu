@@ -51,8 +51,8 @@ constexpr uint32_t FLAG_TIMEOUT = 4u;
 
 struct Args {
   dsv4_gqa_attention_params p;
-  int4* unit;        // [B * tps] of the evenly cut list: first row seen, end of the rows seen, key tiles of tile 0 and 1 (bit 30 of the
-                     // latter: some page is out of range)
+  int4* unit;        // [B * tps] of the evenly cut list: first row seen, end of the rows seen, key tiles of tile 0 and 1
+                     // (bit 30 of the latter: some page is out of range)
   float4* o_part;    // [2 G][8 groups of 32 rows][D / 4][32 rows]: a warp stores and loads whole lines
   float2* ml_part;   // [2 G][256]
   int4* cut;         // [G]: unit, kv head, last CTA (-1: no unit that begins here goes on), slot here
@@ -280,9 +280,9 @@ struct WarpWalk {
   }
 };
 
-// x = cap2 tanh(x to_exp / (2 log2 e)) - m for 32 columns, cap2 = cap log2(e), to_exp = 2 log2(e) scale / cap: tanh t = 1 - 2 / (1 +
-// e^2t), one reciprocal for two columns.  Bound by the special-function unit: 10 cycles an element with the weight's
-// exponential.  (A degree-13 polynomial in packed fp32 was no faster: fp32 pairs issue at half rate.)
+// x = cap2 tanh(x to_exp / (2 log2 e)) - m for 32 columns, cap2 = cap log2(e), to_exp = 2 log2(e) scale / cap:
+// tanh t = 1 - 2 / (1 + e^2t), one reciprocal for two columns.  Bound by the special-function unit: 10 cycles an element
+// with the weight's exponential.  (A degree-13 polynomial in packed fp32 was no faster: fp32 pairs issue at half rate.)
 __device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float to_exp, float cap2, float m) {
   const float c0 = cap2 - m, c1 = -2.f * cap2;
 #pragma unroll
@@ -456,242 +456,242 @@ __global__ void __launch_bounds__(THREADS, 1)
   WarpWalk& ww = sm->walk[warp];
   const Segment& g = ww.g;
   if (lane == 0) {
-  Walk& walk = ww.w;
-  walk.unit = a.unit;
-  walk.one = a.even ? nullptr : &sm->one;
-  walk.tps = a.tps;
-  walk.heads = p.kv_heads;
-  walk.B = p.B;
-  walk.box = a.box;
-  walk.b = sm->b;
-  walk.h = sm->h;
-  walk.tile = sm->tile;
-  walk.u0 = sm->u0;
-  walk.first = sm->first;
-  walk.last = sm->last;
+    Walk& walk = ww.w;
+    walk.unit = a.unit;
+    walk.one = a.even ? nullptr : &sm->one;
+    walk.tps = a.tps;
+    walk.heads = p.kv_heads;
+    walk.B = p.B;
+    walk.box = a.box;
+    walk.b = sm->b;
+    walk.h = sm->h;
+    walk.tile = sm->tile;
+    walk.u0 = sm->u0;
+    walk.first = sm->first;
+    walk.last = sm->last;
   }
 
   if (warp >= W_LOAD) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
-  if (warp == W_LOAD) {
-    // ---------------- TMA loads
-    int it = 0, armed = 0;  // tiles handed out, tiles armed on their own barrier
-    bool raw = false;       // a tile is on its way to vraw
-    bool ok = true;
-    uint32_t raw_phase = 0;
-    if (lane == 0) {
-      tc::tma_prefetch_desc(&kmap);
-      tc::tma_prefetch_desc(&vmap);
-    }
-    const int nbox = TILE / a.box;
-    const bool expanded = a.bf_k != nullptr;
-    while (ok && ww.next(lane)) {
-      for (int k = g.k0; k < g.k1 && ok; ++k) {
-        const int t0 = g.start + k * TILE;
-        // box `lane` of the tile: its page (out of range, so that zeros come, where it has none) and row
-        int page = expanded ? g.b : (int)max(p.num_pages, (int64_t)1), y = expanded ? t0 : 0;
-        if (!expanded && lane < nbox) {
-          const int r = t0 + lane * a.box, lp = r / p.page_size;
-          if (r < g.end && lp < p.max_pages_per_seq) {
-            const int x = p.block_table[(int64_t)g.b * p.max_pages_per_seq + lp];
-            if (x >= 0 && x < p.num_pages) page = x;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+    if (warp == W_LOAD) {
+      // ---------------- TMA loads
+      int it = 0, armed = 0;  // tiles handed out, tiles armed on their own barrier
+      bool raw = false;       // a tile is on its way to vraw
+      bool ok = true;
+      uint32_t raw_phase = 0;
+      if (lane == 0) {
+        tc::tma_prefetch_desc(&kmap);
+        tc::tma_prefetch_desc(&vmap);
+      }
+      const int nbox = TILE / a.box;
+      const bool expanded = a.bf_k != nullptr;
+      while (ok && ww.next(lane)) {
+        for (int k = g.k0; k < g.k1 && ok; ++k) {
+          const int t0 = g.start + k * TILE;
+          // box `lane` of the tile: its page (out of range, so that zeros come, where it has none) and row
+          int page = expanded ? g.b : (int)max(p.num_pages, (int64_t)1), y = expanded ? t0 : 0;
+          if (!expanded && lane < nbox) {
+            const int r = t0 + lane * a.box, lp = r / p.page_size;
+            if (r < g.end && lp < p.max_pages_per_seq) {
+              const int x = p.block_table[(int64_t)g.b * p.max_pages_per_seq + lp];
+              if (x >= 0 && x < p.num_pages) page = x;
+            }
+            y = r & (p.page_size - 1);
           }
-          y = r & (p.page_size - 1);
-        }
-        for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
-          const int slot = it % NSLOT;
-          if (it >= NSLOT) ok = tc::mbar_wait_bounded(&sm->empty[slot], ((it / NSLOT) & 1) ^ 1, abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          uint8_t* dst = kv_mem + slot * QT;
-          // value rows that no row of the unit sees may hold anything, and 0 x NaN would reach the output:
-          // such a tile lands on a barrier of this warp's, which clears the rows before handing it over
-          // (expanded rows from kv_len on are zeros already)
-          const bool clear = kv == 1 && (t0 < g.lo || (!expanded && t0 + TILE > g.end));
-          uint64_t* bar = clear ? &sm->vraw : &sm->full[slot];
-          if (lane == 0) tc::mbar_arrive_expect_tx(bar, QT);
-          raw = clear;
-          if (!clear) armed = it + 1;
-          __syncwarp();
-          if (lane < nbox) {
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_4d(dst + c * HB + lane * a.box * 128, kv ? &vmap : &kmap, c * 64, y, g.h, page, bar);
-          }
-          if (clear) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->vraw, raw_phase, abort));
+          for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
+            const int slot = it % NSLOT;
+            if (it >= NSLOT) ok = tc::mbar_wait_bounded(&sm->empty[slot], ((it / NSLOT) & 1) ^ 1, abort);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            raw_phase ^= 1u;
-            raw = false;
-            armed = it + 1;
-            for (int r = lane; r < TILE; r += 32) {
-              if (t0 + r >= g.lo && t0 + r < g.end) continue;
+            uint8_t* dst = kv_mem + slot * QT;
+            // value rows that no row of the unit sees may hold anything, and 0 x NaN would reach the output:
+            // such a tile lands on a barrier of this warp's, which clears the rows before handing it over
+            // (expanded rows from kv_len on are zeros already)
+            const bool clear = kv == 1 && (t0 < g.lo || (!expanded && t0 + TILE > g.end));
+            uint64_t* bar = clear ? &sm->vraw : &sm->full[slot];
+            if (lane == 0) tc::mbar_arrive_expect_tx(bar, QT);
+            raw = clear;
+            if (!clear) armed = it + 1;
+            __syncwarp();
+            if (lane < nbox) {
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                  *reinterpret_cast<uint4*>(dst + c * HB + r * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                tma_load_4d(dst + c * HB + lane * a.box * 128, kv ? &vmap : &kmap, c * 64, y, g.h, page, bar);
             }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm->full[slot]);
-          }
-        }
-      }
-    }
-    if (!ok) {  // gave up: no copy may still be on its way when the CTA ends
-      volatile int none = 0;
-      for (int x = max(0, armed - NSLOT); x < armed; ++x)
-        tc::mbar_wait_bounded(&sm->full[x % NSLOT], (x / NSLOT) & 1, &none, 50000000ull);
-      if (raw) tc::mbar_wait_bounded(&sm->vraw, raw_phase, &none, 50000000ull);
-    }
-  } else if (warp == W_MMA) {
-    // ---------------- MMAs
-    const uint32_t idesc_s = tc::idesc_bf16_f32(TILE, TILE), idesc_o = tc::idesc_bf16_f32_bmn(TILE, D);
-    const uint32_t tm = (uint32_t)uniform((int)tmem);
-    const uint64_t qd = tc::sdesc_k_sw128(tc::smem_addr(q_mem)), kd = tc::sdesc_k_sw128(tc::smem_addr(kv_mem));
-    const uint64_t vd = tc::sdesc_mn_sw128(tc::smem_addr(kv_mem), HB, 1024);
-    int it = 0;
-    uint32_t qph[2] = {0, 0}, pph[2] = {0, 0}, oph[2] = {1, 1};  // (ofree: nothing to wait for the first time)
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t phase) {
-      ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_bounded(bar, phase, abort));
-      tc::tc_fence_after();
-    };
-    auto wait_full = [&](int x) { wait(&sm->full[x % NSLOT], (x / NSLOT) & 1); };
-    auto scores = [&](int i, int x, bool last_one) {
-      const uint64_t kb = kd + (uint64_t)((x % NSLOT) * QT >> 4), qb = qd + (uint64_t)(i * QT >> 4);
-      if (elect_one()) {
+            if (clear) {
+              ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->vraw, raw_phase, abort));
+              if (!ok) break;
+              raw_phase ^= 1u;
+              raw = false;
+              armed = it + 1;
+              for (int r = lane; r < TILE; r += 32) {
+                if (t0 + r >= g.lo && t0 + r < g.end) continue;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
+                for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-            tc::mma_bf16(tm + 128 * i, qb + (uint64_t)((c * HB + s * 32) >> 4), kb + (uint64_t)((c * HB + s * 32) >> 4),
-                         idesc_s, (c | s) != 0);
-        tc::mma_commit(&sm->sfull[i]);
-        if (last_one) tc::mma_commit(&sm->qfree[i]);
-      }
-      __syncwarp();
-    };
-    auto values = [&](int i, int x, int half, bool more, bool done) {
-      const uint64_t vb = vd + (uint64_t)((x % NSLOT) * QT >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          tc::mma_bf16_ts(tm + COL_O + D * i, tm + 128 * i + 8 * (4 * half + y),
-                          vb + (uint64_t)((4 * half + y) * 2048 >> 4), idesc_o, (more || y) ? 1u : 0u);
-        if (done) tc::mma_commit(&sm->odone[i]);
-      }
-      __syncwarp();
-    };
-    auto release = [&](int x) {
-      if (elect_one()) tc::mma_commit(&sm->empty[x % NSLOT]);
-      __syncwarp();
-    };
-    while (ok && ww.next(lane)) {
-      const int cnt[2] = {uniform(g.count(0)), uniform(g.count(1))}, n = uniform(g.k1 - g.k0);
-      it = uniform(it);
-      wait_full(it);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (cnt[i] && ok) {
-          wait(&sm->qfull[i], qph[i]);
-          qph[i] ^= 1u;
-          if (ok) scores(i, it, cnt[i] == 1);
-        }
-      if (!ok) break;
-      release(it);
-      for (int k = 0; k < n && ok; ++k, it += 2) {
-        wait_full(it + 1);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (ok && k < cnt[i]) {
-            if (k == 0) {
-              wait(&sm->ofree[i], oph[i]);  // the output of the unit before has been read
-              oph[i] ^= 1u;
+                  for (int x = 0; x < 8; ++x)
+                    *reinterpret_cast<uint4*>(dst + c * HB + r * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+              }
+              tc::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&sm->full[slot]);
             }
-            wait(&sm->phalf[i], pph[i]);
-            if (!ok) break;
-            values(i, it + 1, 0, k > 0, false);
-            wait(&sm->pfull[i], pph[i]);
-            if (!ok) break;
-            values(i, it + 1, 1, true, k == cnt[i] - 1);
-            pph[i] ^= 1u;
-          }
-          if (ok && k + 1 < n) {
-            if (i == 0) wait_full(it + 2);
-            if (ok && k + 1 < cnt[i]) scores(i, it + 2, k + 2 == cnt[i]);
           }
         }
-        if (!ok) break;
-        release(it + 1);
-        if (k + 1 < n) release(it + 2);
       }
-    }
-    if (!ok) {  // gave up: no MMA may still run when tensor memory is returned
-      volatile int none = 0;
-      if (elect_one()) tc::mma_commit(&sm->drain);
-      __syncwarp();
-      tc::mbar_wait_bounded(&sm->drain, 0, &none, 50000000ull);
-    }
-  } else if (warp >= W_QUERY) {
-    // ---------------- queries of row tile i
-    const int i = warp - W_QUERY;
-    constexpr int CPR = D / 8, RPI = 32 / CPR;
-    const uint32_t group = p.q_heads / p.kv_heads, rpi_q = RPI / group, rpi_r = RPI % group;
-    uint32_t fph = 1, armed = 0;  // (qfree: nothing to wait for the first time)
-    bool ok = true;
-    while (ok && ww.next(lane)) {
-      if (!g.count(i)) continue;
-      const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
-      const uint32_t r0 = (uint32_t)g.tile * UROWS + i * TILE;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->qfree[i], fph, abort));
-      fph ^= 1u;
-      if (!ok) break;
-      if (a.q_tma) {
-        // (rows of tokens behind the sequence's: another's, or zeros; their output is not written)
-        if (lane == 0) {
-          tc::mbar_arrive_expect_tx(&sm->qfull[i], QT);
+      if (!ok) {  // gave up: no copy may still be on its way when the CTA ends
+        volatile int none = 0;
+        for (int x = max(0, armed - NSLOT); x < armed; ++x)
+          tc::mbar_wait_bounded(&sm->full[x % NSLOT], (x / NSLOT) & 1, &none, 50000000ull);
+        if (raw) tc::mbar_wait_bounded(&sm->vraw, raw_phase, &none, 50000000ull);
+      }
+    } else if (warp == W_MMA) {
+      // ---------------- MMAs
+      const uint32_t idesc_s = tc::idesc_bf16_f32(TILE, TILE), idesc_o = tc::idesc_bf16_f32_bmn(TILE, D);
+      const uint32_t tm = (uint32_t)uniform((int)tmem);
+      const uint64_t qd = tc::sdesc_k_sw128(tc::smem_addr(q_mem)), kd = tc::sdesc_k_sw128(tc::smem_addr(kv_mem));
+      const uint64_t vd = tc::sdesc_mn_sw128(tc::smem_addr(kv_mem), HB, 1024);
+      int it = 0;
+      uint32_t qph[2] = {0, 0}, pph[2] = {0, 0}, oph[2] = {1, 1};  // (ofree: nothing to wait for the first time)
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_bounded(bar, phase, abort));
+        tc::tc_fence_after();
+      };
+      auto wait_full = [&](int x) { wait(&sm->full[x % NSLOT], (x / NSLOT) & 1); };
+      auto scores = [&](int i, int x, bool last_one) {
+        const uint64_t kb = kd + (uint64_t)((x % NSLOT) * QT >> 4), qb = qd + (uint64_t)(i * QT >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(q_mem + i * QT + c * HB, &qmap, c * 64, g.h * (int)group, s.t0 + (int)(r0 / group), 0, &sm->qfull[i]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              tc::mma_bf16(tm + 128 * i, qb + (uint64_t)((c * HB + s * 32) >> 4), kb + (uint64_t)((c * HB + s * 32) >> 4),
+                           idesc_s, (c | s) != 0);
+          tc::mma_commit(&sm->sfull[i]);
+          if (last_one) tc::mma_commit(&sm->qfree[i]);
         }
-        ++armed;
         __syncwarp();
-        continue;
-      }
-      const uint32_t r = r0 + lane / CPR, rows = (uint32_t)s.n * group;
-      uint32_t tok = r / group, head = r % group;  // of this lane's first row; then RPI rows on each time
-      const int ch = lane % CPR;
-      uint8_t* dst = q_mem + i * QT + (ch >> 3) * HB;
-      const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)s.t0 * p.q_token_stride +
-                                 (int64_t)g.h * group * p.q_head_stride + 8 * ch;
-#pragma unroll 4
-      for (int x = 0; x < TILE / RPI; ++x) {
-        const int R = x * RPI + lane / CPR;
-        const bool in = r + x * RPI < rows;
-        tc::cp_async16(dst + R * 128 + (((ch & 7) ^ (R & 7)) << 4),
-                       in ? src + (int64_t)tok * p.q_token_stride + (int64_t)head * p.q_head_stride
-                          : reinterpret_cast<const __nv_bfloat16*>(p.q),
-                       in ? 16u : 0u);
-        head += rpi_r;
-        tok += rpi_q;
-        if (head >= group) {
-          head -= group;
-          ++tok;
+      };
+      auto values = [&](int i, int x, int half, bool more, bool done) {
+        const uint64_t vb = vd + (uint64_t)((x % NSLOT) * QT >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            tc::mma_bf16_ts(tm + COL_O + D * i, tm + 128 * i + 8 * (4 * half + y),
+                            vb + (uint64_t)((4 * half + y) * 2048 >> 4), idesc_o, (more || y) ? 1u : 0u);
+          if (done) tc::mma_commit(&sm->odone[i]);
+        }
+        __syncwarp();
+      };
+      auto release = [&](int x) {
+        if (elect_one()) tc::mma_commit(&sm->empty[x % NSLOT]);
+        __syncwarp();
+      };
+      while (ok && ww.next(lane)) {
+        const int cnt[2] = {uniform(g.count(0)), uniform(g.count(1))}, n = uniform(g.k1 - g.k0);
+        it = uniform(it);
+        wait_full(it);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (cnt[i] && ok) {
+            wait(&sm->qfull[i], qph[i]);
+            qph[i] ^= 1u;
+            if (ok) scores(i, it, cnt[i] == 1);
+          }
+        if (!ok) break;
+        release(it);
+        for (int k = 0; k < n && ok; ++k, it += 2) {
+          wait_full(it + 1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (ok && k < cnt[i]) {
+              if (k == 0) {
+                wait(&sm->ofree[i], oph[i]);  // the output of the unit before has been read
+                oph[i] ^= 1u;
+              }
+              wait(&sm->phalf[i], pph[i]);
+              if (!ok) break;
+              values(i, it + 1, 0, k > 0, false);
+              wait(&sm->pfull[i], pph[i]);
+              if (!ok) break;
+              values(i, it + 1, 1, true, k == cnt[i] - 1);
+              pph[i] ^= 1u;
+            }
+            if (ok && k + 1 < n) {
+              if (i == 0) wait_full(it + 2);
+              if (ok && k + 1 < cnt[i]) scores(i, it + 2, k + 2 == cnt[i]);
+            }
+          }
+          if (!ok) break;
+          release(it + 1);
+          if (k + 1 < n) release(it + 2);
         }
       }
-      tc::cp_async_commit();
-      tc::cp_async_wait<0>();
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm->qfull[i]);
+      if (!ok) {  // gave up: no MMA may still run when tensor memory is returned
+        volatile int none = 0;
+        if (elect_one()) tc::mma_commit(&sm->drain);
+        __syncwarp();
+        tc::mbar_wait_bounded(&sm->drain, 0, &none, 50000000ull);
+      }
+    } else if (warp >= W_QUERY) {
+      // ---------------- queries of row tile i
+      const int i = warp - W_QUERY;
+      constexpr int CPR = D / 8, RPI = 32 / CPR;
+      const uint32_t group = p.q_heads / p.kv_heads, rpi_q = RPI / group, rpi_r = RPI % group;
+      uint32_t fph = 1, armed = 0;  // (qfree: nothing to wait for the first time)
+      bool ok = true;
+      while (ok && ww.next(lane)) {
+        if (!g.count(i)) continue;
+        const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
+        const uint32_t r0 = (uint32_t)g.tile * UROWS + i * TILE;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->qfree[i], fph, abort));
+        fph ^= 1u;
+        if (!ok) break;
+        if (a.q_tma) {
+          // (rows of tokens behind the sequence's: another's, or zeros; their output is not written)
+          if (lane == 0) {
+            tc::mbar_arrive_expect_tx(&sm->qfull[i], QT);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d(q_mem + i * QT + c * HB, &qmap, c * 64, g.h * (int)group, s.t0 + (int)(r0 / group), 0, &sm->qfull[i]);
+          }
+          ++armed;
+          __syncwarp();
+          continue;
+        }
+        const uint32_t r = r0 + lane / CPR, rows = (uint32_t)s.n * group;
+        uint32_t tok = r / group, head = r % group;  // of this lane's first row; then RPI rows on each time
+        const int ch = lane % CPR;
+        uint8_t* dst = q_mem + i * QT + (ch >> 3) * HB;
+        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)s.t0 * p.q_token_stride +
+                                   (int64_t)g.h * group * p.q_head_stride + 8 * ch;
+#pragma unroll 4
+        for (int x = 0; x < TILE / RPI; ++x) {
+          const int R = x * RPI + lane / CPR;
+          const bool in = r + x * RPI < rows;
+          tc::cp_async16(dst + R * 128 + (((ch & 7) ^ (R & 7)) << 4),
+                         in ? src + (int64_t)tok * p.q_token_stride + (int64_t)head * p.q_head_stride
+                            : reinterpret_cast<const __nv_bfloat16*>(p.q),
+                         in ? 16u : 0u);
+          head += rpi_r;
+          tok += rpi_q;
+          if (head >= group) {
+            head -= group;
+            ++tok;
+          }
+        }
+        tc::cp_async_commit();
+        tc::cp_async_wait<0>();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm->qfull[i]);
+      }
+      if (!ok && armed) {  // gave up: no copy may still be on its way when the CTA ends
+        volatile int none = 0;
+        tc::mbar_wait_bounded(&sm->qfull[i], (armed - 1) & 1, &none, 50000000ull);
+      }
     }
-    if (!ok && armed) {  // gave up: no copy may still be on its way when the CTA ends
-      volatile int none = 0;
-      tc::mbar_wait_bounded(&sm->qfull[i], (armed - 1) & 1, &none, 50000000ull);
-    }
-  }
   } else if (warp >= W_OUT) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OUT));
     // ---------------- output: warp W_OUT + y writes rows 32 y .. 32 y + 31 of both tiles
