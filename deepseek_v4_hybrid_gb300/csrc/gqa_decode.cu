@@ -1,7 +1,8 @@
 // Grouped-query attention of few new tokens a sequence (at most 32 rows of (token, head) per kv head).
 //
-// Bound by HBM: every visible row of the cache is read once for all rows of its kv head, and the rows of
-// a kv head together are far below the tensor cores' rate, so the products run on warp-level MMAs from
+// Bound by HBM where contexts are long (4 x 128k e4m3 rows, 64 query and 8 kv heads of 128: 173 us, 5.9 TB/s), by its warps'
+// chains of instructions where they are ragged and shorter (32 x 8k 65 us, 4.7 TB/s).  Every visible row of the
+// cache is read once for all rows of its kv head, and these together are far below the tensor cores' rate, so the products run on warp-level MMAs from
 // registers (tcgen05 would spend 128 rows on at most 32) and the design is about the stream of rows:
 //  - The visible rows of all (sequence, kv head) units form one list of stages (16 rows, e4m3 32) that is cut into
 //    equal pieces, one per CTA, whatever the lengths; a unit cut by a piece's border leaves partial
@@ -10,8 +11,8 @@
 //    ring of cp.async copies, with one barrier of theirs a stage; these groups stream their own stages and keep their
 //    own running maximum, sum and output: no barrier between them until a unit ends.  (All 32 rows in one warp took
 //    two CTAs' registers of three, each warp waiting on its own chain of MMAs: at 32 rows a kv head, 48 sequences of
-//    up to 4000 rows, 4 kv heads of 128, e4m3 142 us and 98 so, capped bf16 in a window of 1024 41.7 and 39.2; plain
-//    bf16 67 and 75.  8 rows a warp, four warps a group: e4m3 111 us, and 16 rows of 64-wide heads 28 for 21 us.)
+//    up to 4000 rows, 4 kv heads of 128, e4m3 142 us and 102 so, capped bf16 in a window of 1024 41.7 and 38.1; plain
+//    bf16 67 and 73.  8 rows a warp, four warps a group: e4m3 111 us, and 16 rows of 64-wide heads 28 for 21 us.)
 //  - S = Q K^T has the rows of a kv head as its M (16) and 8 cache rows as its N; its result is, register
 //    for register, the A operand of O += P V.  The order of a contraction's terms is free, so a lane
 //    reads 16 contiguous bytes of a row and Q's fragments are laid out to match; for P V a lane holds 16
