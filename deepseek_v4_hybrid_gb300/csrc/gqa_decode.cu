@@ -1,9 +1,10 @@
 // Grouped-query attention of few new tokens a sequence (at most 32 rows of (token, head) per kv head).
 //
-// Bound by HBM where contexts are long (4 x 128k e4m3 rows, 64 query and 8 kv heads of 128: 173 us, 5.9 TB/s), by its warps'
-// chains of instructions where they are ragged and shorter (32 x 8k 65 us, 4.7 TB/s).  Every visible row of the
-// cache is read once for all rows of its kv head, and these together are far below the tensor cores' rate, so the products run on warp-level MMAs from
-// registers (tcgen05 would spend 128 rows on at most 32) and the design is about the stream of rows:
+// Bound by HBM where contexts are long (4 x 128k e4m3 rows, 64 query and 8 kv heads of 128: 173 us, 5.9 TB/s), by its
+// warps' chains of instructions where they are ragged and shorter (32 x 8k 65 us, 4.7 TB/s).  Every visible row of
+// the cache is read once for all rows of its kv head, and these together are far below the tensor cores' rate, so the
+// products run on warp-level MMAs from registers (tcgen05 would spend 128 rows on at most 32) and the design is
+// about the stream of rows:
 //  - The visible rows of all (sequence, kv head) units form one list of stages (16 rows, e4m3 32) that is cut into
 //    equal pieces, one per CTA, whatever the lengths; a unit cut by a piece's border leaves partial
 //    results that a second kernel merges.
