@@ -32,17 +32,17 @@ __device__ __forceinline__ float cap_logit(float z, float cap, float rcap2) {
   return cap - 2.f * cap * rcp_approx(1.f + tc::ex2_approx(z * rcap2));
 }
 
-// A row's sums: m the logits' reference (log2 units), l their sum against it, mo the reference that the
-// output's sum is taken against.  Returns the output's factor, writes lse when `write` is set.
+// A row's sums: m the reference (log2 units) that its weights are taken against, l their sum.  Returns the factor
+// of the output's sum, writes lse when `write` is set.
 __device__ __forceinline__ float finish_scale(const dsv4_gqa_attention_params& p, int64_t row, int head, float m, float l,
-                                              float mo, bool write) {
+                                              bool write) {
   const float sink = p.sink ? p.sink[head] * LOG2E : -INFINITY;
   const float mf = fmaxf(m, sink);
-  float L = 0.f;
-  if (m > -INFINITY) L = l * tc::ex2_approx(m - mf);
+  const float f = m > -INFINITY ? tc::ex2_approx(m - mf) : 0.f;
+  float L = l * f;
   if (sink > -INFINITY) L += tc::ex2_approx(sink - mf);
   if (write && p.lse) p.lse[row] = mf > -INFINITY ? (mf + __log2f(L)) * LN2 : -INFINITY;
-  return mo > -INFINITY ? tc::ex2_approx(mo - mf) * rcp_approx(L) : 0.f;
+  return m > -INFINITY ? f * rcp_approx(L) : 0.f;
 }
 
 // Stores 4 consecutive dims of an output row.

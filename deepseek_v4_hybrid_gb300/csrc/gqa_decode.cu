@@ -23,11 +23,14 @@
 //    most 8 rows the two terms are the two halves of the MMA's 16 rows, and the second one costs nothing.
 //      Queries, brought to at most 448 by a power of two a row, s = 4: a bf16 query's 8 bits are hi's 4 and lo's
 //      4, exact down to 2^-15 of the row's largest element, off by 2^-23 of it at most below that.
-//      Weights, taken against the stage's own maximum (and its larger V exponent) and scaled to at most 256, s =
-//      5: off by 2^-8 of themselves or 2^-23 of the stage's largest; the stage's product is added to the running
-//      fp32 output with its factor, so a flat tail behind one large weight keeps its precision.
-//    V's exponent is part of the reference that the output is taken against, so pages of very different scales lose
-//    nothing.  The values' bytes are transposed in registers, 4 rows by 4 dims with 8 byte permutes.
+//      Weights, taken against the stage's own maximum and scaled to at most 256, s = 5: off by 2^-8 of themselves or
+//      2^-23 of the stage's largest; the stage's product is added to the running fp32 output with its factor, so a
+//      flat tail behind one large weight keeps its precision.
+//    A page's V exponent goes onto its product in fp32, apart from the weights' rounding, so a page whose scale is far
+//    above the others' takes nothing from them, seen or not.  Two pages of 16 rows in one stage share a product while
+//    their exponents lie within NEAR_EXP of one another (the lower one's weights are then off by 2^-19 of the stage's
+//    largest, at most); else the stage is gone through once for each of them.
+//    The values' bytes are transposed in registers, 4 rows by 4 dims with 8 byte permutes.
 //  - bf16 caches: P is rounded to bf16, against a maximum that moves when it is exceeded by more than 2^8.
 #include <cooperative_groups.h>
 
@@ -45,7 +48,6 @@ namespace gqa {
 namespace dec {
 
 constexpr int NW = 4, THREADS = 32 * NW;
-constexpr int BLK = 16;            // rows that lie in one page
 constexpr int MAX_SCAN = 1024;     // sequences whose stages are cut evenly; above, a CTA takes a whole unit
 constexpr int MAX_CLUSTER = 8;     // CTAs of a unit (portable cluster size)
 constexpr int MIN_ROWS = 128;      // rows of a piece, at least
@@ -56,11 +58,16 @@ constexpr int CLUSTER_ROWS = 1024;
 // 5, 48 at 8 and 12, 49 at 18; 32 x 8k 68.7, 66.4, 65.1 at 12, 66.1 at 18).
 constexpr int UNIT_COST = 12;
 constexpr float LAZY = 8.f;        // a running maximum moves when it is exceeded by more than 2^8
+constexpr int NEAR_EXP = 4;        // V exponents of one product
+
+// Caches: bf16, e4m3, and e4m3 in pages of 16 rows, two of them a stage.  (Pages of 64 rows as if they were two a
+// stage: 4 x 128k rows 182 us for 165, 32 x 8k 68.3 for 64.7.)
+enum Kind { BF, E4, E4P16 };
 
 struct Args {
   dsv4_gqa_attention_params p;
   float* o_part;    // [2 G][rows][D]
-  float4* ml_part;  // [2 G][rows]: maximum of the logits, sum, maximum that O is taken against (log2 units)
+  float2* ml_part;  // [2 G][rows]: maximum of the logits (log2 units), sum
   int4* unit;       // [B * heads]: first and last CTA of the unit, slot in the first, 0 / 1 = merge
   int G, rows;      // CTAs, rows of a partial
   int cs;           // 0: equal pieces of the list; else CTAs (a cluster) of each unit
@@ -73,11 +80,12 @@ __host__ __device__ constexpr int ctas_per_sm(int D, bool e4m3, int HB) {
   return D == 128 && e4m3 && HB == 2 ? 2 : D == 64 && HB == 1 ? 4 : 3;
 }
 
-template <int D, bool E4M3, int HB, int PW, int CTAS>
+template <int D, Kind KIND, int HB, int PW, int CTAS>
 struct Cfg {
+  static constexpr bool E4M3 = KIND != BF;
   static constexpr int ROWB = E4M3 ? D : 2 * D;
-  static constexpr int SUB = E4M3 ? 2 : 1;     // blocks of a stage: an MMA's K, 32 or 16 rows
-  static constexpr int SR = BLK * SUB;
+  static constexpr int SR = E4M3 ? 32 : 16;    // rows of a stage: an MMA's K
+  static constexpr int PG = KIND == E4P16 ? 2 : 1, PB = SR / PG;  // its pages, their rows
   static constexpr int STAGE = 2 * SR * ROWB;  // K then V
   static constexpr int RING = CTAS == 4 ? 12288 : CTAS == 3 ? 16384 : 24576;  // of a warp; a group's are one
   static constexpr int NST = PW * RING / STAGE;
@@ -87,9 +95,9 @@ struct Cfg {
 };
 
 struct Shared {
-  float m[NW][16], l[NW][16], mo[NW][16];
-  float4 cml[32];     // cluster: this CTA's (maximum, sum, reference) of each row
-  int2 meta[NW][32];  // [group][block of the ring]: page usable, (k exponent byte | v exponent byte << 8)
+  float m[NW][16], l[NW][16];
+  float2 cml[32];     // cluster: this CTA's (maximum, sum) of each row
+  int2 meta[NW][32];  // [group][page of the ring]: usable, (k exponent byte | v exponent byte << 8)
 };
 
 // c += a b (m16n8k16), bf16.
@@ -164,11 +172,12 @@ __device__ __forceinline__ Unit unit_of(const dsv4_gqa_attention_params& p, int 
   return u;
 }
 
-template <int D, bool E4M3, int HB, int PW, int CTAS>
+template <int D, Kind KIND, int HB, int PW, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
-  using C = Cfg<D, E4M3, HB, PW, CTAS>;
+  using C = Cfg<D, KIND, HB, PW, CTAS>;
+  constexpr bool E4M3 = C::E4M3;
   constexpr int RW = 8 * HB, NG = NW / PW;               // rows of a warp; groups of warps with stages of their own
-  constexpr int NT = D / 8, SR = C::SR, SUB = C::SUB;
+  constexpr int NT = D / 8, SR = C::SR, PG = C::PG, PB = C::PB;
   constexpr int KS = E4M3 ? D / 32 : D / 16;             // K steps of Q K^T
   constexpr int NQ = E4M3 && HB > 1 ? 2 * KS : KS;       // A fragments of an MMA tile of Q (two terms apart)
   extern __shared__ __align__(1024) uint8_t ring_all[];
@@ -243,7 +252,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
     first = (int64_t)(unit % p.kv_heads) * u.stages;
     last = first + min((int64_t)u.stages, (rank + 1) * per);
     first += min((int64_t)u.stages, rank * per);
-    if (tid < 32) sm.cml[tid] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    if (tid < 32) sm.cml[tid] = make_float2(-INFINITY, 0.f);
     __syncthreads();
   }
 
@@ -273,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
       int rlo[HB], rhi[HB];
       float rmul[HB], slope[HB];
       int rpos[HB];
-      float m[HB], mo[HB], l[HB];
+      float m[HB], l[HB];
       int all_lo = 0, all_hi = 0x7FFFFFFF;  // rows that every token sees
       // Q's A fragments; e4m3: [K step][hi, lo], or both terms in one for 8 rows.
       uint32_t q[NQ][4];
@@ -291,7 +300,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
         slope[k] = 0.f;
         rpos[k] = pos;
         rmul[k] = 0.f;
-        m[k] = mo[k] = -INFINITY;
+        m[k] = -INFINITY;
         l[k] = 0.f;
         const int head = h * group + r % group;
         if (live) {
@@ -379,8 +388,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
       for (int i = 0; i < NU; ++i) doff[i] = chunk_at<C::ROWB>(i * RPI + r_in, gl % CPR);
       auto fill = [&](int k) {
         if (k < count) {
-          if ((k * SUB & 31) == 0) {  // pages and exponents of the next 32 blocks, one a lane
-            const int ks = k + lane / SUB, j = u.lo + (s0 + gw + ks * NG) * SR + lane % SUB * BLK;
+          if ((k * PG & 31) == 0) {  // the next 32 pages and their exponents, one a lane
+            const int ks = k + lane / PG, j = u.lo + (s0 + gw + ks * NG) * SR + lane % PG * PB;
             pid = -1;
             pexp = 0;
             if (ks < count && j < u.s.kv) {
@@ -397,24 +406,24 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
           }
           const int slot = k % C::NST, js = u.lo + (s0 + gw + k * NG) * SR;
           uint8_t* dst = ring + slot * C::STAGE;
-          constexpr int PER = RPI < BLK ? BLK / RPI : 1;  // pieces that a thread copies of a block
-          static_assert(NU % PER == 0 && C::NST * SUB <= 32, "whole blocks; the ring's lie in sm.meta");
+          constexpr int PER = RPI < PB ? PB / RPI : 1;  // pieces that a thread copies of a page
+          static_assert(NU % PER == 0 && C::NST * PG <= 32, "whole pages; the ring's lie in sm.meta");
 #pragma unroll
-          for (int sub = 0; sub < SUB; ++sub) {
-            const int page = __shfl_sync(0xffffffffu, pid, (k * SUB + sub) & 31);
-            const int ex = __shfl_sync(0xffffffffu, pexp, (k * SUB + sub) & 31);
-            if (mw == 0 && lane == 0) sm.meta[gw][slot * SUB + sub] = make_int2(page >= 0, ex);
+          for (int y = 0; y < PG; ++y) {
+            const int page = __shfl_sync(0xffffffffu, pid, (k * PG + y) & 31);
+            const int ex = __shfl_sync(0xffffffffu, pexp, (k * PG + y) & 31);
+            if (mw == 0 && lane == 0) sm.meta[gw][slot * PG + y] = make_int2(page >= 0, ex);
           }
 #pragma unroll
           for (int nb = 0; nb < NU; nb += PER) {
-            const int rb = nb * RPI + r_in;  // the first of PER rows in one block
-            const int page = __shfl_sync(0xffffffffu, pid, (k * SUB + rb / BLK) & 31);
+            const int rb = nb * RPI + r_in;  // the first of PER rows in one page
+            const int page = __shfl_sync(0xffffffffu, pid, (k * PG + rb / PB) & 31);
             const int j0 = js + rb;
             const int row = j0 & (p.page_size - 1);
             const uint8_t* kr = k_base + ES * ((int64_t)max(page, 0) * p.k_page_stride + (int64_t)row * p.k_row_stride);
             const uint8_t* vr = v_base + ES * ((int64_t)max(page, 0) * p.v_page_stride + (int64_t)row * p.v_row_stride);
-            const int jb = j0 & ~(BLK - 1);
-            if (page >= 0 && jb >= u.vlo && jb + BLK <= u.s.kv) {
+            const int jb = j0 & ~(PB - 1);
+            if (page >= 0 && jb >= u.vlo && jb + PB <= u.s.kv) {
 #pragma unroll
               for (int i = 0; i < PER; ++i) {
                 tc::cp_async16(dst + doff[nb + i], kr + i * k_step, 16u);
@@ -442,20 +451,31 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
 #pragma unroll 1
       for (int k = 0; k < C::NST - 1; ++k) fill(k);
 
+      // only -1: the stage's rows together; 0, then 1: those of one page (V exponents too far apart for one product)
+      int only = -1;
 #pragma unroll 1
-      for (int k = 0; k < count; ++k) {
-        tc::cp_async_wait<C::NST - 2>();
-        group_sync();  // the stage is there for all, and the one before is read
-        fill(k + C::NST - 1);
-        if (row0 >= rows) continue;  // (a warp with no rows only copies)
+      for (int k = 0; k < count;) {
+        if (PG == 1 || only != 0) {
+          tc::cp_async_wait<C::NST - 2>();
+          group_sync();  // the stage is there for all, and the one before is read
+          fill(k + C::NST - 1);
+        }
+        if (row0 >= rows) {  // a warp with no rows only copies
+          ++k;
+          continue;
+        }
         const int slot = k % C::NST, j0 = u.lo + (s0 + gw + k * NG) * SR;
         const uint8_t* kt = ring + slot * C::STAGE;
         const uint8_t* vt = kt + SR * C::ROWB;
 
+        if (PG > 1) {
+          const int2 m0 = sm.meta[gw][slot * PG], m1 = sm.meta[gw][slot * PG + PG - 1];
+          only = only == 0 ? 1 : m0.x && m1.x && abs((m0.y >> 8) - (m1.y >> 8)) > NEAR_EXP ? 0 : -1;
+        }
         // ---- S = Q K^T: z[row half][tile of 8 rows][row 2c, 2c + 1 of it]
-        float z[HB][2 * SUB][2];
+        float z[HB][SR / 8][2];
 #pragma unroll
-        for (int nt = 0; nt < 2 * SUB; ++nt) {
+        for (int nt = 0; nt < SR / 8; ++nt) {
           constexpr int KCH = C::ROWB / 64;  // 16-byte chunks a lane holds of a row
           float s[4], s_lo[4];
 #pragma unroll
@@ -489,44 +509,49 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
         }
 
         // ---- logits in log2 units, masks, the stage's maximum of each row (this lane's part)
-        float top[HB], vexp[SUB];
+        float top[HB];
+        int vbyte[PG];
         bool inside = j0 >= all_lo && j0 + SR <= all_hi;
-        float kmul[SUB];
-        bool page_ok[SUB];
+        float kmul[PG];
+        bool page_ok[PG];
 #pragma unroll
-        for (int sub = 0; sub < SUB; ++sub) {
-          const int2 meta = sm.meta[gw][slot * SUB + sub];
-          page_ok[sub] = meta.x != 0;
-          inside = inside && page_ok[sub];
-          kmul[sub] = E4M3 ? ue8m0_scale((uint8_t)(meta.y & 255)) : 1.f;
-          vexp[sub] = (float)((meta.y >> 8) - 127);
+        for (int y = 0; y < PG; ++y) {
+          const int2 meta = sm.meta[gw][slot * PG + y];
+          page_ok[y] = meta.x != 0 && (PG == 1 || only < 0 || only == y);
+          inside = inside && page_ok[y];
+          kmul[y] = E4M3 ? ue8m0_scale((uint8_t)(meta.y & 255)) : 1.f;
+          vbyte[y] = meta.y >> 8;
         }
 #pragma unroll
         for (int k2 = 0; k2 < HB; ++k2) {
           top[k2] = -INFINITY;
           const float far = (float)(rpos[k2] - j0 - 2 * c);  // (near distances stay exact however long the cache)
 #pragma unroll
-          for (int nt = 0; nt < 2 * SUB; ++nt)
+          for (int nt = 0; nt < SR / 8; ++nt)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               float& v = z[k2][nt][y];
-              v = E4M3 ? v * kmul[nt / 2] * rmul[k2] : v * rmul[k2];
+              v = E4M3 ? v * kmul[nt * 8 / PB] * rmul[k2] : v * rmul[k2];
               const int j = j0 + 8 * nt + 2 * c + y;
               if (!plain) {
                 if (p.softcap > 0.f) v = cap_logit(v, p.softcap, rcap2);
                 v = v * LOG2E - slope[k2] * fabsf(far - (float)(8 * nt + y));
               }
-              if (!inside && (!page_ok[nt / 2] || j < rlo[k2] || j >= rhi[k2])) v = -INFINITY;
+              if (!inside && (!page_ok[nt * 8 / PB] || j < rlo[k2] || j >= rhi[k2])) v = -INFINITY;
               top[k2] = fmaxf(top[k2], v);
             }
         }
 
         if (E4M3) {
-          // ---- weights against the stage's maximum, in two e4m3 terms
-          const float vtop = fmaxf(page_ok[0] ? vexp[0] : -127.f, page_ok[SUB - 1] ? vexp[SUB - 1] : -127.f);
-          float vf[SUB];
+          // ---- weights against the stage's maximum, in two e4m3 terms; its V exponent
+          int vtop = vbyte[0];
+          float vf[PG];  // a page's weights in its product
+          if (PG > 1) {
+            vtop = max(page_ok[0] ? vbyte[0] : 0, page_ok[PG - 1] ? vbyte[PG - 1] : 0);
 #pragma unroll
-          for (int sub = 0; sub < SUB; ++sub) vf[sub] = page_ok[sub] ? tc::ex2_approx(vexp[sub] - vtop + 8.f) : 0.f;
+            for (int y = 0; y < PG; ++y) vf[y] = page_ok[y] ? exp2_neg_int(vtop - vbyte[y]) : 0.f;
+          }
+          const float vscale = ue8m0_scale((uint8_t)vtop);
           uint32_t hi[HB][2], lo[HB][2];
           float fs[HB];
           bool move = false;
@@ -536,16 +561,16 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
             float t = top[k2];
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-            const float ref = t == -INFINITY ? 0.f : t;
+            const float ref = (t == -INFINITY ? 0.f : t) - 8.f;  // (weights of at most 256, and their sum so)
             float sum = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < 2 * SUB; ++nt)
+            for (int nt = 0; nt < SR / 8; ++nt)
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 float& v = z[k2][nt][y];
                 v = tc::ex2_approx(v - ref);
                 sum += v;
-                v *= vf[nt / 2];
+                if (PG > 1) v *= vf[nt * 8 / PB];
               }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -553,14 +578,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
               hi[k2][x] = w.x;
               lo[k2][x] = w.y;
             }
-            const float mn = fmaxf(m[k2], t), on = fmaxf(mo[k2], t + vtop);
-            const float mr = mn == -INFINITY ? 0.f : mn, orf = on == -INFINITY ? 0.f : on;
-            l[k2] = fmaf(l[k2], tc::ex2_approx(m[k2] - mr), sum * tc::ex2_approx(t - mr));
-            fo[k2] = tc::ex2_approx(mo[k2] - orf);
-            fs[k2] = tc::ex2_approx(t + vtop - 8.f - orf);
-            move |= on > mo[k2];
+            const float mn = fmaxf(m[k2], t), mr = mn == -INFINITY ? 0.f : mn;
+            fo[k2] = tc::ex2_approx(m[k2] - mr);
+            const float ft = tc::ex2_approx(t - mr) * 0x1p-8f;
+            l[k2] = fmaf(l[k2], fo[k2], sum * ft);
+            fs[k2] = ft * vscale;
+            move |= mn > m[k2];
             m[k2] = mn;
-            mo[k2] = on;
           }
           if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -642,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
               const float mn = fmaxf(m[k2], t);
               const float f = m[k2] == -INFINITY ? 0.f : tc::ex2_approx(m[k2] - mn);
               l[k2] *= f;
-              m[k2] = mo[k2] = mn;
+              m[k2] = mn;
 #pragma unroll
               for (int j = 0; j < NT; ++j) {
                 out(k2, j, 0) *= f;
@@ -674,6 +698,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
             }
           }
         }
+        if (PG == 1 || only != 0) ++k;
       }
       tc::cp_async_wait<0>();
 
@@ -685,7 +710,6 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
         if (c == 0) {
           sm.m[warp][g + 8 * k] = m[k];
           sm.l[warp][g + 8 * k] = l[k];
-          sm.mo[warp][g + 8 * k] = mo[k];
         }
       }
       __syncthreads();
@@ -693,10 +717,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
 #pragma unroll
       for (int k = 0; k < HB; ++k) {
         const int r = g + 8 * k;
-        float on = -INFINITY;
+        float mn = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < NG; ++w) on = fmaxf(on, sm.mo[w * PW + mw][r]);
-        const float f = mo[k] == -INFINITY ? 0.f : tc::ex2_approx(mo[k] - on);
+        for (int w = 0; w < NG; ++w) mn = fmaxf(mn, sm.m[w * PW + mw][r]);
+        const float f = m[k] == -INFINITY ? 0.f : tc::ex2_approx(m[k] - mn);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           // column n of tile j is dim 16 f(n) + j, f(n) the chunk of lane group n (e4m3, D = 128), 8 n + j (D = 64)
@@ -712,12 +736,11 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
       for (int x = tid; x < rows * (D / 4); x += THREADS) {
         const int r = x / (D / 4), d4 = x % (D / 4);
         const int rm = r / RW, rl = r % RW;  // the row's warp in a group, its place there
-        float mn = -INFINITY, on = -INFINITY, ls = 0.f;
+        float mn = -INFINITY, ls = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < NG; ++w) {
           mn = fmaxf(mn, sm.m[w * PW + rm][rl]);
-          on = fmaxf(on, sm.mo[w * PW + rm][rl]);
           const float4 v = reinterpret_cast<const float4*>(ring_all + (w * PW + rm) * C::RING)[rl * (D / 4) + d4];
           acc.x += v.x;
           acc.y += v.y;
@@ -730,14 +753,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
         if (whole) {
           const int head = h * group + r % group;
           const int64_t row = (int64_t)(u.s.t0 + r / group) * p.q_heads + head;
-          const float f = finish_scale(p, row, head, mn, ls, on, d4 == 0);
+          const float f = finish_scale(p, row, head, mn, ls, d4 == 0);
           store4<D>(p, row, d4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
         } else if (a.cs) {
           reinterpret_cast<float4*>(ring_all + rm * C::RING)[rl * (D / 4) + d4] = acc;  // (over group 0's, which this thread has read)
-          if (d4 == 0) sm.cml[r] = make_float4(mn, ls, on, 0.f);
+          if (d4 == 0) sm.cml[r] = make_float2(mn, ls);
         } else {
           reinterpret_cast<float4*>(a.o_part)[((int64_t)slot * a.rows + r) * (D / 4) + d4] = acc;
-          if (d4 == 0) a.ml_part[(int64_t)slot * a.rows + r] = make_float4(mn, ls, on, 0.f);
+          if (d4 == 0) a.ml_part[(int64_t)slot * a.rows + r] = make_float2(mn, ls);
         }
       }
       if (tid == 0 && s0 == 0 && a.cs == 0)
@@ -760,11 +783,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
     const int h = unit % p.kv_heads, rows = u.s.n * group;
     for (int x = rank * THREADS + tid; x < rows * (D / 4); x += a.cs * THREADS) {
       const int r = x / (D / 4), d4 = x % (D / 4);
-      float4 ml[MAX_CLUSTER], v[MAX_CLUSTER];
-      float mn = -INFINITY, on = -INFINITY, ls = 0.f;
+      float2 ml[MAX_CLUSTER];
+      float4 v[MAX_CLUSTER];
+      float mn = -INFINITY, ls = 0.f;
 #pragma unroll
       for (int i = 0; i < MAX_CLUSTER; ++i) {  // (all at once: one latency)
-        ml[i] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        ml[i] = make_float2(-INFINITY, 0.f);
         v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i < a.cs) {
           ml[i] = cl.map_shared_rank(sm.cml, i)[r];
@@ -772,16 +796,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
         }
       }
 #pragma unroll
-      for (int i = 0; i < MAX_CLUSTER; ++i) {
-        mn = fmaxf(mn, ml[i].x);
-        on = fmaxf(on, ml[i].z);
-      }
+      for (int i = 0; i < MAX_CLUSTER; ++i) mn = fmaxf(mn, ml[i].x);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < MAX_CLUSTER; ++i) {
         if (ml[i].x == -INFINITY) continue;  // (a piece without visible rows: its sums may not have been written)
-        ls += ml[i].y * tc::ex2_approx(ml[i].x - mn);
-        const float f = tc::ex2_approx(ml[i].z - on);
+        const float f = tc::ex2_approx(ml[i].x - mn);
+        ls = fmaf(ml[i].y, f, ls);
         acc.x = fmaf(v[i].x, f, acc.x);
         acc.y = fmaf(v[i].y, f, acc.y);
         acc.z = fmaf(v[i].z, f, acc.z);
@@ -789,7 +810,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
       }
       const int head = h * group + r % group;
       const int64_t row = (int64_t)(u.s.t0 + r / group) * p.q_heads + head;
-      const float f = finish_scale(p, row, head, mn, ls, on, d4 == 0);
+      const float f = finish_scale(p, row, head, mn, ls, d4 == 0);
       store4<D>(p, row, d4, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
     }
     cl.sync();  // no CTA leaves while its shared memory is read
@@ -814,40 +835,34 @@ __global__ void __launch_bounds__(Q * THREADS) merge_kernel(Args a) {
   const Seq s = sequence(p.q_start, p.kv_len, b, p.T, p.max_q_len, p.max_kv_len);
   const int group = p.q_heads / p.kv_heads, rows = s.n * group, n = info.y - info.x + 1;
   auto slot = [&](int i) { return (int64_t)(2 * (info.x + i) + (i == 0 ? info.z : 0)) * a.rows + r; };
-  float mn = -INFINITY, on = -INFINITY;
+  float mn = -INFINITY;
   if (r < rows) {
-    for (int i = lane; i < n; i += 32) {
-      const float4 x = a.ml_part[slot(i)];
-      mn = fmaxf(mn, x.x);
-      on = fmaxf(on, x.z);
-    }
+    for (int i = lane; i < n; i += 32) mn = fmaxf(mn, a.ml_part[slot(i)].x);
     mn = warp_max(mn);
-    on = warp_max(on);
     float ls = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 8;
     for (int i0 = U * share; i0 < n; i0 += Q * U) {
-      float4 v[U], x[U];
+      float4 v[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        x[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-        if (i0 + k < n) {
-          x[k] = a.ml_part[slot(i0 + k)];
-          if (lane < D / 4) v[k] = reinterpret_cast<const float4*>(a.o_part)[slot(i0 + k) * (D / 4) + lane];
-        }
+        if (i0 + k < n && lane < D / 4) v[k] = reinterpret_cast<const float4*>(a.o_part)[slot(i0 + k) * (D / 4) + lane];
       }
+      float2 x = make_float2(-INFINITY, 0.f);  // lane k's: partial k's
+      if (lane < U && i0 + lane < n) x = a.ml_part[slot(i0 + lane)];
+      const float f = x.x > -INFINITY ? tc::ex2_approx(x.x - mn) : 0.f;  // (else its sums are zeros)
+      ls = fmaf(x.y, f, ls);
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (x[k].x > -INFINITY) {
-          const float f = tc::ex2_approx(x[k].z - on);
-          ls = fmaf(x[k].y, tc::ex2_approx(x[k].x - mn), ls);
-          acc.x = fmaf(v[k].x, f, acc.x);
-          acc.y = fmaf(v[k].y, f, acc.y);
-          acc.z = fmaf(v[k].z, f, acc.z);
-          acc.w = fmaf(v[k].w, f, acc.w);
-        }
+      for (int k = 0; k < U; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        acc.x = fmaf(v[k].x, fk, acc.x);
+        acc.y = fmaf(v[k].y, fk, acc.y);
+        acc.z = fmaf(v[k].z, fk, acc.z);
+        acc.w = fmaf(v[k].w, fk, acc.w);
+      }
     }
+    ls = warp_sum(ls);
     if (lane < D / 4) part[wr][share][lane] = acc;
     if (lane == 0) sums[wr][share] = ls;
   }
@@ -866,7 +881,7 @@ __global__ void __launch_bounds__(Q * THREADS) merge_kernel(Args a) {
   }
   const int head = h * group + r % group;
   const int64_t row = (int64_t)(s.t0 + r / group) * p.q_heads + head;
-  const float f = finish_scale(p, row, head, mn, ls, on, lane == 0);
+  const float f = finish_scale(p, row, head, mn, ls, lane == 0);
   store4<D>(p, row, lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
 }
 
@@ -899,15 +914,15 @@ static Plan plan(const dsv4_gqa_attention_params& p) {
     if (units * cs <= (int64_t)num_sms() * ctas && seen <= (int64_t)CLUSTER_ROWS * cs) L.cs = cs;
   const int64_t slots = L.cs == 0 ? 2LL * L.G : 0;
   L.ml_off = align_up((size_t)slots * L.rows * p.head_dim * 4, 256);
-  L.unit_off = align_up(L.ml_off + (size_t)slots * L.rows * 16, 256);
+  L.unit_off = align_up(L.ml_off + (size_t)slots * L.rows * 8, 256);
   L.total = align_up(L.unit_off + (size_t)units * 16, 256);
   return L;
 }
 
-template <int D, bool E4M3, int HB, int PW, int CTAS>
+template <int D, Kind KIND, int HB, int PW, int CTAS>
 static cudaError_t launch(const Args& a, cudaStream_t s) {
-  using C = Cfg<D, E4M3, HB, PW, CTAS>;
-  const void* fn = reinterpret_cast<const void*>(decode_kernel<D, E4M3, HB, PW, CTAS>);
+  using C = Cfg<D, KIND, HB, PW, CTAS>;
+  const void* fn = reinterpret_cast<const void*>(decode_kernel<D, KIND, HB, PW, CTAS>);
   cudaError_t e = ensure_max_dynamic_smem(fn, C::SMEM);
   if (e != cudaSuccess) return e;
   const dsv4_gqa_attention_params& p = a.p;
@@ -927,7 +942,7 @@ static cudaError_t launch(const Args& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = count_launch(cudaLaunchKernelEx(&cfg, decode_kernel<D, E4M3, HB, PW, CTAS>, a));
+  e = count_launch(cudaLaunchKernelEx(&cfg, decode_kernel<D, KIND, HB, PW, CTAS>, a));
   if (e != cudaSuccess || a.cs) return e;
   const dim3 grid((unsigned)units, a.rows / NW);
   if (a.G > 8 * units) return launch_pdl(merge_kernel<D, 4>, grid, dim3(4 * THREADS), 0, s, true, a);
@@ -936,18 +951,24 @@ static cudaError_t launch(const Args& a, cudaStream_t s) {
 
 // Where at most two CTAs an SM have work, they are built for two: deeper rings, more registers (8 kv heads, 16
 // sequences of up to 2000 rows: e4m3 26.5 us for 21.4, bf16 26.5 for 23.2; one token over 6000 bf16 rows 17.2 for 13.4).
-template <int D, bool E4M3, int HB, int PW>
+template <int D, Kind KIND, int HB, int PW>
 static cudaError_t launch_ctas(const Args& a, cudaStream_t s) {
   const int64_t ctas = a.cs ? (int64_t)a.p.B * a.p.kv_heads * a.cs : a.G;
-  constexpr int most = ctas_per_sm(D, E4M3, HB);
-  if (most > 2 && ctas <= 2LL * num_sms()) return launch<D, E4M3, HB, PW, 2>(a, s);
-  return launch<D, E4M3, HB, PW, most>(a, s);
+  constexpr int most = ctas_per_sm(D, KIND != BF, HB);
+  if (most > 2 && ctas <= 2LL * num_sms()) return launch<D, KIND, HB, PW, 2>(a, s);
+  return launch<D, KIND, HB, PW, most>(a, s);
 }
 
-template <int D, bool E4M3>
+template <int D, Kind KIND>
 static cudaError_t launch_rows(const Args& a, const Plan& L, cudaStream_t s) {
-  if (L.hb == 1) return launch_ctas<D, E4M3, 1, 1>(a, s);
-  return L.pw == 2 ? launch_ctas<D, E4M3, 2, 2>(a, s) : launch_ctas<D, E4M3, 2, 1>(a, s);
+  if (L.hb == 1) return launch_ctas<D, KIND, 1, 1>(a, s);
+  return L.pw == 2 ? launch_ctas<D, KIND, 2, 2>(a, s) : launch_ctas<D, KIND, 2, 1>(a, s);
+}
+
+template <int D>
+static cudaError_t launch_kind(const Args& a, Kind kind, const Plan& L, cudaStream_t s) {
+  if (kind == BF) return launch_rows<D, BF>(a, L, s);
+  return kind == E4 ? launch_rows<D, E4>(a, L, s) : launch_rows<D, E4P16>(a, L, s);
 }
 
 }  // namespace dec
@@ -960,15 +981,13 @@ cudaError_t launch_decode(const dsv4_gqa_attention_params& p, cudaStream_t s) {
   a.p = p;
   uint8_t* ws = reinterpret_cast<uint8_t*>(p.workspace);
   a.o_part = reinterpret_cast<float*>(ws);
-  a.ml_part = reinterpret_cast<float4*>(ws + L.ml_off);
+  a.ml_part = reinterpret_cast<float2*>(ws + L.ml_off);
   a.unit = reinterpret_cast<int4*>(ws + L.unit_off);
   a.G = L.G;
   a.rows = L.rows;
   a.cs = L.cs;
-  const bool e4m3 = p.cache_dtype == DSV4_E4M3_PAGE;
-  if (p.head_dim == 128)
-    return e4m3 ? dec::launch_rows<128, true>(a, L, s) : dec::launch_rows<128, false>(a, L, s);
-  return e4m3 ? dec::launch_rows<64, true>(a, L, s) : dec::launch_rows<64, false>(a, L, s);
+  const dec::Kind kind = p.cache_dtype != DSV4_E4M3_PAGE ? dec::BF : p.page_size == 16 ? dec::E4P16 : dec::E4;
+  return p.head_dim == 128 ? dec::launch_kind<128>(a, kind, L, s) : dec::launch_kind<64>(a, kind, L, s);
 }
 
 }  // namespace gqa

@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool some = m > -INFINITY;  // (a row that saw nothing: what O holds does not matter)
         float f = 1.f;
         if (g.whole) {
-          if (live) f = finish_scale(p, row, head, m, l, m, true);
+          if (live) f = finish_scale(p, row, head, m, l, true);
         } else {
           a.ml_part[(int64_t)slot * UROWS + r] = make_float2(m, l);
         }
@@ -1015,7 +1015,7 @@ __global__ void __launch_bounds__(256) join_kernel(Args a) {
   }
   const int head = cut.y * (int)group + (int)(r % group);
   const int64_t row = (int64_t)(s.t0 + (int)(r / group)) * p.q_heads + head;
-  const float f = finish_scale(p, row, head, m, l, m, warp == 0);
+  const float f = finish_scale(p, row, head, m, l, warp == 0);
 #pragma unroll
   for (int k = 0; k < E; ++k)
     store4<D>(p, row, warp * E + k, make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f));
