@@ -149,7 +149,7 @@ __device__ __forceinline__ int chunk_at(int r, int ch) {
 struct Unit {
   Seq s;
   int lo, stages;  // first row read (a multiple of SR), stages (0: nothing to do)
-  int vlo;         // first row any token sees
+  int vlo;         // first row any token sees (the number of rows: none sees any)
 };
 
 template <int SR>
@@ -159,14 +159,15 @@ __device__ __forceinline__ Unit unit_of(const dsv4_gqa_attention_params& p, int 
   u.stages = 0;
   u.lo = u.vlo = 0;
   if (!u.s.ok || u.s.n == 0) return u;
-  int lo = 0;
-  if (p.window > 0) lo = max(0, u.s.kv - u.s.n - p.window + 1);
   if (p.kv_start) {
-    int first = 0x7FFFFFFF;
-    for (int i = 0; i < u.s.n; ++i) first = min(first, p.kv_start[u.s.t0 + i]);
-    lo = max(lo, first);
+    u.vlo = u.s.kv;
+    for (int i = 0; i < u.s.n; ++i) {
+      const int2 v = visible_rows(p, b, u.s.t0 + i, u.s.kv - u.s.n + i, u.s.kv);
+      if (v.x < v.y) u.vlo = min(u.vlo, v.x);
+    }
+  } else if (p.window > 0) {
+    u.vlo = max(0, u.s.kv - u.s.n - p.window + 1);
   }
-  u.vlo = min(lo, u.s.kv);
   u.lo = u.vlo & ~(SR - 1);
   u.stages = max(1, (u.s.kv - u.lo + SR - 1) / SR);  // (one empty stage where nothing is visible)
   return u;

@@ -68,3 +68,31 @@ def test_scales_of_any_size_in_every_page(M, page, n):
     check_attention(M, bt, window=77, sink=np.linspace(-3, 3, 8))
 
 
+# ------------------------------------------------------------------------------------------------
+# rows that no token sees
+# ------------------------------------------------------------------------------------------------
+HIDDEN = [  # n, kv, window, kv_start of the sequence's first tokens (the rest: 0), first row that a token sees
+    (2, 100, 50, [80, 0], 50), (2, 100, 0, [2 ** 30, 60], 60), (3, 130, 40, [2 ** 30, 2 ** 30, 0], 90),
+    (4, 200, 33, [196, 170, 199, 180], 170), (1, 77, 30, [60], 60), (1, 77, 30, [5], 47),
+    (60, 300, 50, [290, 250, 260], 194), (40, 300, 64, [2 ** 30] * 30 + [0] * 10, 227)]
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("n,kv,window,starts,first", HIDDEN, ids=[f"n{h[0]}_kv{h[1]}_w{h[2]}_{h[4]}" for h in HIDDEN])
+def test_rows_before_the_first_seen_one_hold_nan(M, n, kv, window, starts, first, page, cache):
+    """The first row that any token sees is the least over those that see something, of the later of the token's
+    window and its kv_start; NaN in all rows before it changes no bit."""
+    start = np.r_[starts, np.zeros(n - len(starts), np.int64), 3]
+    pos = kv - n + np.arange(n)
+    lo = np.maximum(start[:n], pos - window + 1 if window else 0)
+    assert lo[lo <= pos].min() == first
+    clean, bt = (Batch([n, 1], [kv, 20], 4, 2, 64, page, cache, seed=8) for _ in range(2))
+    for j in range(first):
+        for c in bt.caches:
+            c[bt.table[0, j // page], :, j % page] = E4M3_NAN if cache == "e4m3" else BF16_NAN
+    _, out, lse = run_attention(M, bt, window=window, kv_start=start)
+    _, want, wlse = check_attention(M, clean, window=window, kv_start=start)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
