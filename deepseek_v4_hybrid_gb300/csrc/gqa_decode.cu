@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) decode_kernel(Args a) {
             const int ks = k + lane / PG, j = u.lo + (s0 + gw + ks * NG) * SR + lane % PG * PB;
             pid = -1;
             pexp = 0;
-            if (ks < count && j < u.s.kv) {
+            if (ks < count && j + PB > u.vlo && j < u.s.kv) {  // (pages that no token sees are not looked at)
               const int lp = j / p.page_size;
               pid = lp < p.max_pages_per_seq ? p.block_table[(int64_t)b * p.max_pages_per_seq + lp] : -1;
               if (pid < 0 || pid >= p.num_pages) {

@@ -107,7 +107,7 @@ __device__ __forceinline__ int4 plan_unit(const Args& a, int u) {
     if (live[0]) n[0] = max(n[0], 1);  // (a unit that sees nothing still writes its output)
     const int end = max(hi[0], hi[1]);
     bool bad = false;
-    for (int lp = start / p.page_size + lane; (int64_t)lp * p.page_size < end; lp += 32) {
+    for (int lp = lo / p.page_size + lane; (int64_t)lp * p.page_size < end; lp += 32) {
       const int page = lp < p.max_pages_per_seq ? p.block_table[(int64_t)b * p.max_pages_per_seq + lp] : -1;
       bad |= page < 0 || page >= p.num_pages;
     }

@@ -97,8 +97,9 @@ int dsv4_gqa_append(const dsv4_gqa_append_params* p, dsv4_stream_t stream);
  * window == 0 or j > p - window,  and j >= kv_start[t].  A token that sees no row gets out = 0 and
  * lse = sink[h] (-inf without a sink).
  * What rows from kv_len on, rows of other pages and rows before the first one that any of the sequence's
- * tokens sees hold never matters, NaN included.  The rows from that one on must hold finite values: a NaN
- * or Inf among them may also reach tokens that do not see it.
+ * tokens sees hold never matters, NaN included; nor do the table entries of pages with no other rows.  The
+ * rows from that one on must hold finite values: a NaN or Inf among them may also reach tokens that do not
+ * see it.
  * The workspace of an e4m3 call with more than 32 rows (token, head of the group) a sequence has room for
  * bf16 copies of the batch's rows: 4 B kv_heads max_kv_len head_dim bytes, lengths rounded up to 128.
  * ------------------------------------------------------------------------------------------- */

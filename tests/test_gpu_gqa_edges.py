@@ -96,3 +96,25 @@ def test_rows_before_the_first_seen_one_hold_nan(M, n, kv, window, starts, first
     assert torch.equal(out, want) and torch.equal(lse, wlse)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 32, 64, 256])
+@pytest.mark.parametrize("n,kv,window,start", [(1, 100, 20, 0), (1, 101, 0, 81), (4, 700, 33, 0), (60, 300, 33, 0),
+                                               (60, 900, 0, 700), (200, 500, 60, 0)])
+def test_pages_before_the_first_seen_row_are_not_looked_at(M, n, kv, window, start, page, cache):
+    """Entries of pages that lie before every token's window or start (a cache that lets go of them) may hold
+    anything: not flagged, and no bit changes."""
+    kv_start = np.r_[np.full(n, start), 0]
+    first = max(start, kv - n - window + 1 if window else 0)
+    clean, bt = (Batch([n, 1], [kv, 20], 4, 2, 64, page, cache, seed=8) for _ in range(2))
+    _, want, wlse = check_attention(M, clean, window=window, kv_start=kv_start)
+    for entry in (-1, 2 ** 31 - 1):
+        bt.table[0, :first // page] = entry
+        _, out, lse = run_attention(M, bt, window=window, kv_start=kv_start)
+        assert M.dsv4_read_device_flags() == 0
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+    if first // page < (kv - 1) // page:  # the page of the first seen row is
+        bt.table[0, first // page] = -1
+        run_attention(M, bt, window=window, kv_start=kv_start)
+        assert M.dsv4_read_device_flags() == 1
+
+
