@@ -27,7 +27,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// cap * tanh(z / cap) with rcap2 = 2 log2(e) / cap: tanh x = 1 - 2 / (1 + e^2x), off by some 2^-23 cap.
+// cap * tanh(z / cap) with rcap2 = 2 log2(e) / cap: tanh x = 1 - 2 / (1 + e^2x), off by less than 2^-20 cap.
 __device__ __forceinline__ float cap_logit(float z, float cap, float rcap2) {
   return cap - 2.f * cap * rcp_approx(1.f + tc::ex2_approx(z * rcap2));
 }

@@ -46,7 +46,11 @@ constexpr int UNIT_COST = 2;
 constexpr int FEW_ROWS = 1024;
 constexpr int MAX_UNITS = 8192;   // units of the evenly cut list (its sums fill the ring's 64 KB); above, a CTA a unit
 constexpr float LAZY = 8.f;
-constexpr float CAP_ROOM = 80.f;  // (2^80 x 2^20 rows x values up to 2^20 stay in fp32)
+// Capped logits lie at most at cap2 = cap log2(e).  A row's reference is put up to 2^CAP_RAISE above its largest logit so
+// far, so that cap2 is at most CAP_ROOM above it: then no weight passes 2^20 whatever the rows to come hold (fp32 holds
+// 2^20 x rows x values up to 2^107), the largest is at least 2^-60 (its product with values of 2^-40 still has 26
+// binary orders of normal numbers below it), and no maximum is needed any more.
+constexpr float CAP_ROOM = 20.f, CAP_RAISE = 60.f;
 constexpr uint32_t FLAG_TIMEOUT = 4u;
 
 struct Args {
@@ -281,7 +285,8 @@ struct WarpWalk {
 };
 
 // x = cap2 tanh(x to_exp / (2 log2 e)) - m for 32 columns, cap2 = cap log2(e), to_exp = 2 log2(e) scale / cap:
-// tanh t = 1 - 2 / (1 + e^2t), one reciprocal for two columns.  Bound by the special-function unit: 10 cycles an element
+// tanh t = 1 - 2 / (1 + e^2t), one reciprocal for two columns; off by at most 2^-20 cap: 2 cap times five roundings of
+// the quotient (the reciprocal's counts twice), 10 steps of 2^-24, and 3.3 of the scales' and the exponential's.  Bound by the special-function unit: 10 cycles an element
 // with the weight's exponential.  (A degree-13 polynomial in packed fp32 was no faster: fp32 pairs issue at half rate.)
 __device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float to_exp, float cap2, float m) {
   const float c0 = cap2 - m, c1 = -2.f * cap2;
@@ -825,8 +830,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         float mul = cl;
         const bool all = __all_sync(0xffffffffu, inside && !g.bad);
         if (capped && all && __all_sync(0xffffffffu, cap2 - m <= CAP_ROOM)) {
-          // Capped logits lie at most at cap2 (log2 units), here at most CAP_ROOM above every row's reference: no maximum
-          // is needed, and the tile is read once.  (Rolled: this code is long, and instruction fetch counts.)
+          // No maximum is needed, and the tile is read once.  (Rolled: this code is long, and instruction fetch counts.)
           uint64_t sum2[2] = {0, 0};
           tc::tmem_ld32_nowait(t_s, xa);
           tc::tmem_wait_ld_regs<32>(xa);
@@ -905,9 +909,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc::tmem_wait_st();
         }
         const float top = mul * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        const bool move = top > m + (capped && cap2 - m > CAP_ROOM ? 0.f : LAZY);
+        const float want = capped ? fmaxf(top, fminf(cap2 - CAP_ROOM, top + CAP_RAISE)) : top;
+        const bool move = capped && cap2 - m > CAP_ROOM ? want > m : top > m + LAZY;
         if (__any_sync(0xffffffffu, move)) {
-          const float mn = move ? top : m;
+          const float mn = move ? want : m;
           const float f = m == -INFINITY ? 0.f : tc::ex2_approx(m - mn);
           m = mn;
           l *= f;

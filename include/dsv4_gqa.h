@@ -99,7 +99,9 @@ int dsv4_gqa_append(const dsv4_gqa_append_params* p, dsv4_stream_t stream);
  * What rows from kv_len on, rows of other pages and rows before the first one that any of the sequence's
  * tokens sees hold never matters, NaN included; nor do the table entries of pages with no other rows.  The
  * rows from that one on must hold finite values: a NaN or Inf among them may also reach tokens that do not
- * see it.
+ * see it.  Sums over the rows are fp32 and divided at the end: |v| times the rows seen has to stay below
+ * 2^100, with softcap values below 2^-40 may lose bits, and weights below 2^-100 of a token's total may count
+ * as zeros.
  * The workspace of an e4m3 call with more than 32 rows (token, head of the group) a sequence has room for
  * bf16 copies of the batch's rows: 4 B kv_heads max_kv_len head_dim bytes, lengths rounded up to 128.
  * ------------------------------------------------------------------------------------------- */
@@ -127,7 +129,7 @@ typedef struct dsv4_gqa_attention_params {
   const int32_t* prefix_len;   /* [B] rows visible to every token of the sequence, or NULL */
   const int32_t* kv_start;     /* [T] first visible row of each token, or NULL */
   int32_t window;              /* 0: none */
-  float softcap;               /* 0: none; at most 1024 (logits are off by up to softcap * 2^-22), and
+  float softcap;               /* 0: none; at most 1024 (logits are off by up to softcap * 2^-20), and
                                   4 softmax_scale / softcap finite */
   const float* slopes;         /* [q_heads] or NULL */
   const float* sink;           /* [q_heads], finite or -inf, or NULL (= -inf) */

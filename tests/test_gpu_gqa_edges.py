@@ -118,3 +118,42 @@ def test_pages_before_the_first_seen_row_are_not_looked_at(M, n, kv, window, sta
         assert M.dsv4_read_device_flags() == 1
 
 
+# ------------------------------------------------------------------------------------------------
+# capped scores
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("sink", [False, True])
+@pytest.mark.parametrize("gain", [2.0 ** 90, 2.0 ** 40, 2.0 ** -40])
+@pytest.mark.parametrize("cap", [12.0, 27.0, 30.0, 50.0, 500.0])
+@pytest.mark.parametrize("n,causal", [(1, True), (60, True), (200, False)])
+def test_capped_logits_from_end_to_end(M, n, causal, cap, gain, sink):
+    """Rows whose logits lie at -cap in the first tiles, then at 0, then at +cap, over large and small values: the
+    running softmax holds every weight in fp32 (2^100 over |v| times the rows seen is the range it promises).
+    Bounds: those of the other calls, and the cap's own softcap * 2^-20."""
+    bt = Batch([n, 3], [700, 300], 4, 2, 128, 64, "bf16", seed=3)
+    bt.q[:] = O.bf16_encode(np.ones(bt.q.shape))
+    bt.q[:, 1] = O.bf16_encode(-np.ones(bt.q.shape[2]))
+    scale = 128 ** -0.5
+    bt.caches[1][:] = np.where(bt.caches[1] == BF16_NAN, BF16_NAN,
+                               O.bf16_encode(O.bf16_decode(bt.caches[1]).astype(np.float64) * gain))
+    for b, kv in enumerate(bt.kv):
+        for j in range(kv):
+            z = (-4 if j < 300 else 0.01 * (j % 7) if j < 560 else 4) * cap
+            bt.caches[0][bt.table[b, j // 64], :, j % 64] = O.bf16_encode(z / (128 * scale))
+    kw = {"sink": cap * np.linspace(-1.5, 1, 4)} if sink else {}
+    _, out, lse = run_attention(M, bt, softcap=cap, causal=causal, **kw)
+    assert M.dsv4_read_device_flags() == 0
+    want, wlse, mag, size = G.attention(bt.q64(), bt.caches, None, bt.table, bt.q_start, bt.kv, scale, causal=causal,
+                                        softcap=cap, **kw)
+    tol, ltol = bounds(mag, np.minimum(size, cap), want, wlse, False)
+    off = cap * 2.0 ** -20
+    tol, ltol = tol + mag * 2 * np.expm1(off), ltol + off
+    # Beside a sink, the factor 2^(m - sink) of a row's sums is an fp32 number, 0 below 2^-126; the weights it stands for
+    # are at most 2^20 above the reference m: each is then below 2^-106 of the total (here e^-100 = 2^-144).
+    vmax = np.nanmax(np.abs(O.bf16_decode(bt.caches[1])).astype(np.float64))
+    tol = tol + bt.max_kv * 2.0 ** -106 * vmax
+    worst = np.max(np.abs(out.double().cpu().numpy() - want) / tol)
+    assert worst <= 1, worst
+    worst = np.max(np.abs(lse.double().cpu().numpy() - wlse) / ltol)
+    assert worst <= 1, worst
+
+
