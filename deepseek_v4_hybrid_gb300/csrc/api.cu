@@ -243,7 +243,8 @@ int dsv4_gqa_append(const dsv4_gqa_append_params* p, dsv4_stream_t stream) {
   CHECK(st == DSV4_OK, st);
   if (p->cos_sin != nullptr) {
     CHECK(p->max_pos > 0 && p->rope_first >= 0 && p->rope_first % 8 == 0 && p->rope_dim >= 16 &&
-              p->rope_dim % 16 == 0 && p->rope_first + p->rope_dim <= p->head_dim && aligned(p->cos_sin, 16),
+              p->rope_dim % 16 == 0 && p->rope_dim <= p->head_dim && p->rope_first <= p->head_dim - p->rope_dim &&
+              aligned(p->cos_sin, 16),
           DSV4_ERR_INVALID);
   }
   if (p->T == 0 || p->B == 0) return DSV4_OK;
