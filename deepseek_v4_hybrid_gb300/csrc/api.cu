@@ -272,7 +272,9 @@ int check_gqa_attention(const dsv4_gqa_attention_params& p) {
   CHECK((int64_t)(p.max_q_len < p.T ? p.max_q_len : p.T) * (p.q_heads / p.kv_heads) <= (1 << 30), DSV4_ERR_UNSUPPORTED);
   CHECK(p.causal == 0 || p.causal == 1, DSV4_ERR_INVALID);
   CHECK(std::isfinite(p.softmax_scale) && std::isfinite(p.softcap) && p.softcap >= 0.f, DSV4_ERR_INVALID);
-  CHECK(p.softcap <= 1024.f && (p.softcap == 0.f || std::isfinite(4.f * p.softmax_scale / p.softcap)), DSV4_ERR_INVALID);
+  CHECK(std::isfinite(4.f * p.softmax_scale) && p.softcap <= 1024.f, DSV4_ERR_INVALID);
+  if (p.softcap > 0.f)
+    CHECK(std::isfinite(4.f / p.softcap) && std::isfinite(4.f * p.softmax_scale / p.softcap), DSV4_ERR_INVALID);
   CHECK(act_dtype(p.out_dtype), DSV4_ERR_UNSUPPORTED);
   return DSV4_OK;
 }

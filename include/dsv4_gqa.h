@@ -124,13 +124,13 @@ typedef struct dsv4_gqa_attention_params {
   const int32_t* kv_len;       /* [B] */
   int32_t max_q_len;           /* host bound on n_b, >= 1 (choose the kernels and the grid) */
   int32_t max_kv_len;          /* host bound on kv_len[b], 0 .. 2^30 */
-  float softmax_scale;         /* finite */
+  float softmax_scale;         /* 4 softmax_scale finite */
   int32_t causal;              /* 1: rows after the token are hidden (but for the prefix), 0: all visible */
   const int32_t* prefix_len;   /* [B] rows visible to every token of the sequence, or NULL */
   const int32_t* kv_start;     /* [T] first visible row of each token, or NULL */
   int32_t window;              /* 0: none */
   float softcap;               /* 0: none; at most 1024 (logits are off by up to softcap * 2^-20), and
-                                  4 softmax_scale / softcap finite */
+                                  4 / softcap and 4 softmax_scale / softcap finite */
   const float* slopes;         /* [q_heads] or NULL */
   const float* sink;           /* [q_heads], finite or -inf, or NULL (= -inf) */
   void* out;                   /* [T, q_heads, head_dim] contiguous, out_dtype BF16 or F32, 16-byte aligned */
