@@ -52,6 +52,10 @@ constexpr float LAZY = 8.f;
 // binary orders of normal numbers below it), and no maximum is needed any more.
 constexpr float CAP_ROOM = 20.f, CAP_RAISE = 60.f;
 constexpr uint32_t FLAG_TIMEOUT = 4u;
+// Longest waits: a tile's 250 ms; those that may span the CTA's whole piece (queries, output, a tile of rows with no work in
+// some units) as much and 50 us a key tile that the call's bounds let it hold (a pair of tiles takes 2 us, masked, capped and
+// biased 6).
+constexpr uint64_t WAIT_NS = 250000000, WAIT_TILE_NS = 50000;
 
 struct Args {
   dsv4_gqa_attention_params p;
@@ -68,6 +72,7 @@ struct Args {
   int even;          // 1: the list is cut evenly, 0: a CTA takes a whole unit
   int box;           // cache rows of a TMA box
   int q_tma;         // 1: queries by TMA
+  uint64_t piece_ns; // limit of the waits that may span a CTA's piece
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!g.count(i)) continue;
         const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
         const uint32_t r0 = (uint32_t)g.tile * UROWS + i * TILE;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->qfree[i], fph, abort));
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sm->qfree[i], fph, abort, a.piece_ns));
         fph ^= 1u;
         if (!ok) break;
         if (a.q_tma) {
@@ -718,7 +723,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int cnt = g.count(i);
         float m = -INFINITY, l = 0.f;
         if (cnt) {
-          ok = tc::mbar_wait_bounded(&sm->stats[i], oph[i], abort) && tc::mbar_wait_bounded(&sm->odone[i], oph[i], abort);
+          ok = tc::mbar_wait_bounded(&sm->stats[i], oph[i], abort, a.piece_ns) &&
+               tc::mbar_wait_bounded(&sm->odone[i], oph[i], abort);
           ok = __all_sync(0xffffffffu, ok);
           oph[i] ^= 1u;
           if (!ok) break;
@@ -816,7 +822,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < cnt; ++k) {
-        ok = tc::mbar_wait_bounded(&sm->sfull[i], sph, abort);
+        ok = tc::mbar_wait_bounded(&sm->sfull[i], sph, abort, a.piece_ns);
         sph ^= 1u;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -1084,6 +1090,8 @@ static cudaError_t launch(const dsv4_gqa_attention_params& p, cudaStream_t s) {
   const int64_t plan_ctas = L.even ? (units + PREP_THREADS / 32 - 1) / (PREP_THREADS / 32) : 0;
   const int64_t expand = e4m3 ? (int64_t)p.B * p.kv_heads * (L.kv_pad / EXPAND_ROWS) : 0;
   const int64_t ctas = L.even ? L.G : units * p.kv_heads;
+  const int64_t weight = p.max_kv_len / TILE + 2 + UNIT_COST;  // of a unit, at most
+  a.piece_ns = WAIT_NS + WAIT_TILE_NS * (uint64_t)(L.even ? units * p.kv_heads * weight / L.G + weight : weight);
   if (plan_ctas + expand > 0x7FFFFFFF || ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   CUtensorMap kmap, vmap;
   cudaError_t e;

@@ -157,3 +157,34 @@ def test_capped_logits_from_end_to_end(M, n, causal, cap, gain, sink):
     assert worst <= 1, worst
 
 
+# ------------------------------------------------------------------------------------------------
+# very long sequences
+# ------------------------------------------------------------------------------------------------
+def long_run(M, n, H, kv, cache, page=256):
+    """One kv head of 128 over kv rows that are one page again and again; the outputs and logsumexps, and the exact ones
+    (each row of the page weighs as often as a token sees it) with the bounds' magnitudes."""
+    bt = Batch([n], [page], H, 1, 128, page, cache, seed=5)
+    at = bt.table[0, 0]
+    bt.table = np.full((1, kv // page), at, np.int32)
+    bt.kv[:] = kv
+    bt.max_kv = kv
+    _, out, lse = run_attention(M, bt)
+    assert M.dsv4_read_device_flags() == 0
+    k, v = (G.rows_of(c, None if bt.exps is None else e, np.array([at]), 0, page)
+            for c, e in zip(bt.caches, bt.exps or (None, None)))
+    z = np.einsum("thd,jd->thj", bt.q64(), k) * 128 ** -0.5
+    size = (np.einsum("thd,jd->thj", np.abs(bt.q64()), np.abs(k)) * 128 ** -0.5).max(-1)
+    seen = kv - n + np.arange(n)[:, None] + 1
+    count = seen // page + (np.arange(page) < seen % page)
+    w = np.exp(z - z.max(-1, keepdims=True)) * count[:, None]
+    total = w.sum(-1)
+    want, mag = (np.einsum("thj,jd->thd", w / total[..., None], x) for x in (v, np.abs(v)))
+    return out.double().cpu().numpy(), lse.double().cpu().numpy(), want, z.max(-1) + np.log(total), mag, size
+
+
+def test_a_piece_of_many_tiles_is_waited_for(M):
+    """2^25 rows for a unit of 256 queries on each SM: a CTA's piece takes half a second, and no wait gives up."""
+    out, lse, *_ = long_run(M, 304, 128, 2 ** 25, "bf16")
+    assert (out != -3).all() and (lse != -3).all()
+
+
