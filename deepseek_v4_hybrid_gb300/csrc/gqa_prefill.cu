@@ -44,6 +44,12 @@ constexpr int NSLOT = 4;
 // 2, 271 at 3, 279 at 5; 8192 tokens 854, 823, 831, 850).
 constexpr int UNIT_COST = 2;
 constexpr int FEW_ROWS = 1024;
+// Key tiles that are summed into one accumulator.  Adding drops what lies below the accumulator's last bit: the sums lose
+// 2^-30 a row or so (outputs 0.13 % low after 2^20 rows, 4.3 % after 2^25), so longer runs are added up in fp32 in the
+// workspace.  (A CTA a unit has no place there: calls of more than MAX_UNITS units keep one accumulator.)  Calls whose
+// lengths allow such runs take kernels of their own: with that code in the others, 8192 tokens took 834 us for 820, the
+// capped documents 162 for 152.
+constexpr int MAX_RUN = 2048;
 constexpr int MAX_UNITS = 8192;   // units of the evenly cut list (its sums fill the ring's 64 KB); above, a CTA a unit
 constexpr float LAZY = 8.f;
 // Capped logits lie at most at cap2 = cap log2(e).  A row's reference is put up to 2^CAP_RAISE above its largest logit so
@@ -226,8 +232,9 @@ struct Segment {
   int lo, end;         // rows seen by the unit: lo .. end - 1
   int start;           // cache row of key tile 0
   int k0, k1, n[2];    // this CTA's key tiles k0 .. k1 - 1; tiles of the two row tiles
-  bool bad, whole;
-  int slot;            // of a cut unit's partial results in this CTA
+  bool bad, whole;     // whole: the segment has all tiles of the unit
+  bool add, mine;      // add: to the partial results of the segment before; mine: whole, but for MAX_RUN
+  int slot;            // of the unit's partial results in this CTA
   int64_t u0, w;       // the unit's place and weight in the list
   __device__ int count(int i) const { return max(0, min(k1, n[i]) - k0); }
 };
@@ -239,7 +246,14 @@ struct Walk {
   int tps, heads, B, box;
   int b, h, tile;
   int64_t u0, first, last;
-  __device__ __forceinline__ bool next(Segment& g) {
+  template <bool LONG>
+  __device__ __forceinline__ bool next(Segment& g, int& kend) {  // kend: the CTA's tiles of the unit end there (LONG)
+    if (LONG && g.k1 < kend) {
+      g.k0 = g.k1;
+      g.k1 = min(kend, g.k0 + MAX_RUN);
+      g.add = true;
+      return true;
+    }
     while (u0 < last && b < B) {
       const int4 e = one ? *one : unit[(int64_t)b * tps + tile];
       g.n[0] = e.z;
@@ -268,6 +282,12 @@ struct Walk {
       g.k0 = (int)max((int64_t)0, x0 - UNIT_COST);
       g.k1 = (int)max((int64_t)0, x1 - UNIT_COST);
       if (g.k0 >= g.k1) continue;
+      if (LONG) {
+        kend = g.k1;
+        g.k1 = min(g.k1, g.k0 + MAX_RUN);
+        g.mine = g.k0 == 0 && kend == n;
+        g.add = false;
+      }
       g.whole = g.k0 == 0 && g.k1 == n;
       g.slot = g.u0 <= first ? 0 : 1;
       return true;
@@ -280,10 +300,11 @@ struct Walk {
 struct WarpWalk {
   Walk w;
   Segment g;
-  int have;
+  int have, kend;
+  template <bool LONG>
   __device__ __forceinline__ bool next(int lane) {
     __syncwarp();
-    if (lane == 0) have = w.next(g);
+    if (lane == 0) have = w.next<LONG>(g, kend);
     __syncwarp();
     return have;
   }
@@ -339,7 +360,8 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // PLAIN: the logits are the scaled scores, the scale positive (its code is half as long, and its loops fetch faster).
-template <int D, bool PLAIN>
+// LONG: a CTA may have more than MAX_RUN key tiles of a unit.
+template <int D, bool PLAIN, bool LONG>
 __global__ void __launch_bounds__(THREADS, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap qmap, Args a) {
@@ -479,6 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     walk.u0 = sm->u0;
     walk.first = sm->first;
     walk.last = sm->last;
+    if (LONG) ww.g.k1 = ww.kend = 0;
   }
 
   if (warp >= W_LOAD) {
@@ -495,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       const int nbox = TILE / a.box;
       const bool expanded = a.bf_k != nullptr;
-      while (ok && ww.next(lane)) {
+      while (ok && ww.next<LONG>(lane)) {
         for (int k = g.k0; k < g.k1 && ok; ++k) {
           const int t0 = g.start + k * TILE;
           // box `lane` of the tile: its page (out of range, so that zeros come, where it has none) and row
@@ -598,7 +621,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (elect_one()) tc::mma_commit(&sm->empty[x % NSLOT]);
         __syncwarp();
       };
-      while (ok && ww.next(lane)) {
+      while (ok && ww.next<LONG>(lane)) {
         const int cnt[2] = {uniform(g.count(0)), uniform(g.count(1))}, n = uniform(g.k1 - g.k0);
         it = uniform(it);
         wait_full(it);
@@ -651,7 +674,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t group = p.q_heads / p.kv_heads, rpi_q = RPI / group, rpi_r = RPI % group;
       uint32_t fph = 1, armed = 0;  // (qfree: nothing to wait for the first time)
       bool ok = true;
-      while (ok && ww.next(lane)) {
+      while (ok && ww.next<LONG>(lane)) {
         if (!g.count(i)) continue;
         const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
         const uint32_t r0 = (uint32_t)g.tile * UROWS + i * TILE;
@@ -708,7 +731,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t group = p.q_heads / p.kv_heads;
     uint32_t oph[2] = {0, 0};
     bool ok = true;
-    while (ok && ww.next(lane)) {
+    while (ok && ww.next<LONG>(lane)) {
       const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
       const int slot = 2 * blockIdx.x + g.slot;
       const uint32_t n_rows = (uint32_t)s.n * group;
@@ -734,11 +757,20 @@ __global__ void __launch_bounds__(THREADS, 1)
           l = ml.y;
         }
         const bool some = m > -INFINITY;  // (a row that saw nothing: what O holds does not matter)
-        float f = 1.f;
+        float f = 1.f, f0 = 0.f;          // f0: the factor of the partial results so far
         if (g.whole) {
           if (live) f = finish_scale(p, row, head, m, l, true);
         } else {
-          a.ml_part[(int64_t)slot * UROWS + r] = make_float2(m, l);
+          float2* ml = a.ml_part + (int64_t)slot * UROWS + r;
+          if (LONG && g.add) {
+            const float2 x = *ml;
+            const float mn = fmaxf(m, x.x);
+            f = some ? tc::ex2_approx(m - mn) : 0.f;
+            f0 = x.x > -INFINITY ? tc::ex2_approx(x.x - mn) : 0.f;
+            l = l * f + x.y * f0;
+            m = mn;
+          }
+          *ml = make_float2(m, l);
         }
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -752,9 +784,18 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!g.whole) {
             float4* dst = a.o_part + (((int64_t)slot * 8 + i * 4 + (warp & 3)) * (D / 4) + c / 4) * 32 + lane;
 #pragma unroll
-            for (int d = 0; d < 32; d += 4)
-              dst[d * 8] = make_float4(__uint_as_float(o[d]), __uint_as_float(o[d + 1]), __uint_as_float(o[d + 2]),
-                                       __uint_as_float(o[d + 3]));
+            for (int d = 0; d < 32; d += 4) {
+              float4 v = make_float4(__uint_as_float(o[d]), __uint_as_float(o[d + 1]), __uint_as_float(o[d + 2]),
+                                     __uint_as_float(o[d + 3]));
+              if (LONG && g.add) {
+                const float4 x = dst[d * 8];
+                v.x = fmaf(x.x, f0, v.x);
+                v.y = fmaf(x.y, f0, v.y);
+                v.z = fmaf(x.z, f0, v.z);
+                v.w = fmaf(x.w, f0, v.w);
+              }
+              dst[d * 8] = v;
+            }
           } else if (p.out_dtype == DSV4_F32) {
             if (live) {
 #pragma unroll
@@ -789,8 +830,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::tc_fence_before();
         __syncwarp();
         if (cnt && lane == 0) tc::mbar_arrive(&sm->ofree[i]);
+        if (LONG && g.mine && g.add && g.k1 == ww.kend && live) {  // the sums of a unit of several segments are complete
+          const float y = finish_scale(p, row, head, m, l, true);
+          const float4* src = a.o_part + ((int64_t)slot * 8 + i * 4 + (warp & 3)) * (D / 4) * 32 + lane;
+#pragma unroll 1
+          for (int d4 = 0; d4 < D / 4; ++d4) {
+            const float4 x = src[d4 * 32];
+            store4<D>(p, row, d4, make_float4(x.x * y, x.y * y, x.z * y, x.w * y));
+          }
+        }
       }
-      if (warp == W_OUT && lane == 0 && !g.whole && g.k0 == 0)
+      if (warp == W_OUT && lane == 0 && !(LONG ? g.mine : g.whole) && g.k0 == 0)
         // the unit's first piece: it goes on up to the CTA of its last tile
         a.cut[blockIdx.x] = make_int4(g.b * a.tps + g.tile, g.h, (int)((g.u0 + g.w - 1) / sm->per), g.slot);
     }
@@ -807,7 +857,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float to_exp = p.softcap > 0.f ? 2.f * LOG2E * p.softmax_scale / p.softcap : 0.f;
     uint32_t sph = 0, fph = 1;  // (ofree: nothing to wait for the first time)
     bool ok = true;
-    while (ok && ww.next(lane)) {
+    while (ok && ww.next<LONG>(lane)) {
       const int cnt = g.count(i);
       if (!cnt) continue;
       const Seq s = sequence(p.q_start, p.kv_len, g.b, p.T, p.max_q_len, p.max_kv_len);
@@ -1119,7 +1169,9 @@ static cudaError_t launch(const dsv4_gqa_attention_params& p, cudaStream_t s) {
   }
   const int smem = (2 + NSLOT) * TILE * D * 2 + 4 * 2048 + (int)sizeof(Smem) + 1024;
   const bool plain = p.softcap == 0.f && p.slopes == nullptr && p.softmax_scale > 0.f;
-  const auto kernel = plain ? prefill_kernel<D, true> : prefill_kernel<D, false>;
+  const bool lng = L.even && p.max_kv_len > MAX_RUN * TILE;
+  const auto kernel = plain ? (lng ? prefill_kernel<D, true, true> : prefill_kernel<D, true, false>)
+                            : (lng ? prefill_kernel<D, false, true> : prefill_kernel<D, false, false>);
   e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   if (plan_ctas + expand > 0) {

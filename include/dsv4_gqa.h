@@ -101,7 +101,8 @@ int dsv4_gqa_append(const dsv4_gqa_append_params* p, dsv4_stream_t stream);
  * rows from that one on must hold finite values: a NaN or Inf among them may also reach tokens that do not
  * see it.  Sums over the rows are fp32 and divided at the end: |v| times the rows seen has to stay below
  * 2^100, with softcap values below 2^-40 may lose bits, and weights below 2^-100 of a token's total may count
- * as zeros.
+ * as zeros.  Calls of more than 8192 blocks of 256 rows (token, head of the group; B ceil(max_q_len group / 256))
+ * add up a token's rows in one run, whose rounding takes about rows * 2^-29 of an output.
  * The workspace of an e4m3 call with more than 32 rows (token, head of the group) a sequence has room for
  * bf16 copies of the batch's rows: 4 B kv_heads max_kv_len head_dim bytes, lengths rounded up to 128.
  * ------------------------------------------------------------------------------------------- */

@@ -188,3 +188,14 @@ def test_a_piece_of_many_tiles_is_waited_for(M):
     assert (out != -3).all() and (lse != -3).all()
 
 
+@pytest.mark.parametrize("kv", [2 ** 17, 2 ** 20, 2 ** 22, 2 ** 25])
+@pytest.mark.parametrize("cache,n,H", [("bf16", 304, 128), ("bf16", 700, 128), ("bf16", 9, 40), ("e4m3", 9, 40), ("bf16", 1, 8),
+                                        ("e4m3", 1, 8)])
+def test_sums_over_many_rows(M, cache, n, H, kv):
+    """As close as the sums over few rows."""
+    out, lse, want, wlse, mag, size = long_run(M, n, H, kv, cache)
+    tol, ltol = bounds(mag, size, want, wlse, False)
+    worst = np.max(np.abs(out - want) / tol), np.max(np.abs(lse - wlse) / ltol)
+    assert max(worst) <= 1, worst
+
+
