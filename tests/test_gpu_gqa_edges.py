@@ -160,24 +160,29 @@ def test_capped_logits_from_end_to_end(M, n, causal, cap, gain, sink):
 # ------------------------------------------------------------------------------------------------
 # very long sequences
 # ------------------------------------------------------------------------------------------------
-def long_run(M, n, H, kv, cache, page=256):
-    """One kv head of 128 over kv rows that are one page again and again; the outputs and logsumexps, and the exact ones
+def long_run(M, n, H, kv, cache, page=256, D=128, kv_start=None, softcap=0.0, sink=None, out_dtype=torch.float32):
+    """One kv head over kv rows that are one page again and again; the outputs and logsumexps, and the exact ones
     (each row of the page weighs as often as a token sees it) with the bounds' magnitudes."""
-    bt = Batch([n], [page], H, 1, 128, page, cache, seed=5)
+    bt = Batch([n], [page], H, 1, D, page, cache, seed=5)
     at = bt.table[0, 0]
     bt.table = np.full((1, kv // page), at, np.int32)
     bt.kv[:] = kv
     bt.max_kv = kv
-    _, out, lse = run_attention(M, bt)
+    _, out, lse = run_attention(M, bt, kv_start=kv_start, softcap=softcap, sink=sink, out_dtype=out_dtype)
     assert M.dsv4_read_device_flags() == 0
     k, v = (G.rows_of(c, None if bt.exps is None else e, np.array([at]), 0, page)
             for c, e in zip(bt.caches, bt.exps or (None, None)))
-    z = np.einsum("thd,jd->thj", bt.q64(), k) * 128 ** -0.5
-    size = (np.einsum("thd,jd->thj", np.abs(bt.q64()), np.abs(k)) * 128 ** -0.5).max(-1)
-    seen = kv - n + np.arange(n)[:, None] + 1
-    count = seen // page + (np.arange(page) < seen % page)
+    z = np.einsum("thd,jd->thj", bt.q64(), k) * D ** -0.5
+    size = (np.einsum("thd,jd->thj", np.abs(bt.q64()), np.abs(k)) * D ** -0.5).max(-1)
+    if softcap:
+        z = softcap * np.tanh(z / softcap)
+
+    def rows_up_to(x):
+        return x[:, None] // page + (np.arange(page) < x[:, None] % page)
+
+    count = rows_up_to(kv - n + np.arange(n) + 1) - (rows_up_to(kv_start) if kv_start is not None else 0)
     w = np.exp(z - z.max(-1, keepdims=True)) * count[:, None]
-    total = w.sum(-1)
+    total = w.sum(-1) + (0 if sink is None else np.exp(sink - z.max(-1)))
     want, mag = (np.einsum("thj,jd->thd", w / total[..., None], x) for x in (v, np.abs(v)))
     return out.double().cpu().numpy(), lse.double().cpu().numpy(), want, z.max(-1) + np.log(total), mag, size
 
@@ -199,3 +204,23 @@ def test_sums_over_many_rows(M, cache, n, H, kv):
     assert max(worst) <= 1, worst
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_sums_over_many_rows_of_some_tokens(M, softcap, D, out_dtype):
+    """Tokens that see from 2^18 rows down to a few: of a unit's two row tiles one may go on for many runs without the
+    other.  With a cap, its own softcap * 2^-20 more."""
+    kv, n, H = 2 ** 20, 800, 96
+    g = np.random.default_rng(7)
+    start = kv - n + np.arange(n) - np.exp2(g.uniform(0, 18, n)).astype(np.int64)
+    start[100:140] = kv - 5 * 2 ** 17 - 77
+    start[300:303] = 0
+    start[600:] = np.sort(start[600:])
+    sink = np.linspace(-4, 14, H)
+    out, lse, want, wlse, mag, size = long_run(M, n, H, kv, "bf16", D=D, kv_start=start, softcap=softcap, sink=sink,
+                                               out_dtype=out_dtype)
+    tol, ltol = bounds(mag, size, want, wlse, out_dtype == torch.bfloat16)
+    off = softcap * 2.0 ** -20
+    tol, ltol = tol + mag * 2 * np.expm1(off), ltol + off
+    worst = np.max(np.abs(out - want) / tol), np.max(np.abs(lse - wlse) / ltol)
+    assert max(worst) <= 1, worst
