@@ -1,8 +1,9 @@
 // Grouped-query attention of few new tokens a sequence (at most 32 rows of (token, head) per kv head).
 //
-// Bound by HBM where contexts are long (4 x 128k e4m3 rows, 64 query and 8 kv heads of 128: 173 us, 5.9 TB/s), by its
-// warps' chains of instructions where they are ragged and shorter (32 x 8k 65 us, 4.7 TB/s).  Every visible row of
-// the cache is read once for all rows of its kv head, and these together are far below the tensor cores' rate, so the
+// Bound by HBM where contexts are long (4 x 128k rows, 64 query and 8 kv heads of 128: e4m3 164 us, 6.3 TB/s, bf16
+// 295, 7.0), by its warps' chains of instructions where they are ragged and shorter (32 x 8k e4m3 63 us, 4.8 TB/s, bf16
+// 100, 6.0).  The pairs of times beside the rules below are those of the step that chose them.  Every visible row of the
+// cache is read once for all rows of its kv head, and these together are far below the tensor cores' rate, so the
 // products run on warp-level MMAs from registers (tcgen05 would spend 128 rows on at most 32) and the design is
 // about the stream of rows:
 //  - The visible rows of all (sequence, kv head) units form one list of stages (16 rows, e4m3 32) that is cut into
@@ -48,7 +49,10 @@ namespace gqa {
 namespace dec {
 
 constexpr int NW = 4, THREADS = 32 * NW;
-constexpr int MAX_SCAN = 1024;     // sequences whose stages are cut evenly; above, a CTA takes a whole unit
+// Sequences whose stages are cut evenly; above, a CTA takes a whole unit: they even out by their number, and every CTA
+// would sum up all lengths (1100 sequences of up to 300 e4m3 rows 172 us, 183 as a list; of up to 1500 rows 360 and 387, with
+// one kv head of 64 60 and 71; 2000 of up to 4000 rows of that 203 and 215).
+constexpr int MAX_SCAN = 1024;
 constexpr int MAX_CLUSTER = 8;     // CTAs of a unit (portable cluster size)
 constexpr int MIN_ROWS = 128;      // rows of a piece, at least
 // rows of a cluster's CTA, at most (16 sequences of up to 2000 e4m3 rows 21.7 us, 23.8 at 512; up to 4000 rows 32, 43 at 2048)

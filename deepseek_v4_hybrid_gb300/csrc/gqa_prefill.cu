@@ -13,9 +13,10 @@
 //   work on one tile while the other's softmax runs.  (Two warps, one a tile, mix the tiles' MMAs and lost 12 %.)
 //   Warps 14 and 15 load the tiles' queries: by TMA where the group divides 128 (a box of tokens x heads is
 //   128 rows), else by cp.async.
-// Bound by the softmax between the products, about 1450 cycles a warpgroup and tile of 128 x 128 beside 1024 of MMAs, and
-// at head_dim 64 or with capped scores by the exponentials: 8192 tokens of 64 heads of 128, causal, 823 us, 1340 TFLOP/s
-// (72 % of the measured cuBLAS rate).
+// Bound by the softmax between the products, about 1450 cycles a warpgroup and tile of 128 x 128 beside 1024 of MMAs:
+// 8192 tokens of 64 heads of 128, causal, 824 us, 1330 TFLOP/s (72 % of the measured cuBLAS rate).  Short documents
+// are bound by the starts and ends of units of about five tiles and by masked tiles, which read S twice (two prompts of 4096
+// tokens of 32 heads in documents of 1100: 103 us, capped 152, the special-function unit active 29 % of it).
 //
 // The work of a batch is one list of key tiles, ordered (sequence, kv head, unit), a unit weighing its tiles
 // plus UNIT_COST (its queries' load and output), cut evenly over one persistent CTA per SM: ragged batches,
@@ -50,7 +51,10 @@ constexpr int FEW_ROWS = 1024;
 // lengths allow such runs take kernels of their own: with that code in the others, 8192 tokens took 834 us for 820, the
 // capped documents 162 for 152.
 constexpr int MAX_RUN = 2048;
-constexpr int MAX_UNITS = 8192;   // units of the evenly cut list (its sums fill the ring's 64 KB); above, a CTA a unit
+// Units of the evenly cut list: its sums fill the ring's 64 KB.  Above, a CTA takes a whole unit, which costs more (2000
+// x 32 tokens over up to 200 rows, e4m3, 1340 us as a list, 1818 so; 1000 x up to 256 over 1000 rows 4.8 ms and 6.7; 32 x up
+// to 4096 tokens, bf16, 3.5 and 4.1).
+constexpr int MAX_UNITS = 8192;
 constexpr float LAZY = 8.f;
 // Capped logits lie at most at cap2 = cap log2(e).  A row's reference is put up to 2^CAP_RAISE above its largest logit so
 // far, so that cap2 is at most CAP_ROOM above it: then no weight passes 2^20 whatever the rows to come hold (fp32 holds
@@ -312,8 +316,8 @@ struct WarpWalk {
 
 // x = cap2 tanh(x to_exp / (2 log2 e)) - m for 32 columns, cap2 = cap log2(e), to_exp = 2 log2(e) scale / cap:
 // tanh t = 1 - 2 / (1 + e^2t), one reciprocal for two columns; off by at most 2^-20 cap: 2 cap times five roundings of
-// the quotient (the reciprocal's counts twice), 10 steps of 2^-24, and 3.3 of the scales' and the exponential's.  Bound by the special-function unit: 10 cycles an element
-// with the weight's exponential.  (A degree-13 polynomial in packed fp32 was no faster: fp32 pairs issue at half rate.)
+// the quotient (the reciprocal's counts twice), 10 steps of 2^-24, and 3.3 of the scales' and the exponential's.  With the weight's
+// exponential 10 cycles of the special-function unit a warp and column.  (A degree-13 polynomial in packed fp32 was no faster: fp32 pairs issue at half rate.)
 __device__ __forceinline__ void cap_logits(uint32_t (&x)[32], float to_exp, float cap2, float m) {
   const float c0 = cap2 - m, c1 = -2.f * cap2;
 #pragma unroll

@@ -9,8 +9,9 @@
  *
  * The conventions of dsv4.h hold (device pointers, caller-owned memory, asynchronous on `stream`,
  * graph-capturable, struct_size, host validation before any launch, device range checks that skip the
- * access and raise dsv4_read_device_flags() bits, bounded waits).  Both calls wait for the kernel before
- * them on the stream.  Further:
+ * access and raise dsv4_read_device_flags() bits, bounded waits: where one may last through a block of
+ * queries, 50 us longer for each 128 rows that the call's bounds let a CTA go through).  Both calls wait for the
+ * kernel before them on the stream.  Further:
  *  - Batches are ragged: q_start[B + 1] holds the first flat token of each sequence; sequence b has
  *    n_b = q_start[b+1] - q_start[b] new tokens, and kv_len[b] rows INCLUDING them, so its token i is
  *    at position kv_len[b] - n_b + i.  n_b = 0 and kv_len[b] = 0 are allowed.  Tokens from q_start[B] on
@@ -98,11 +99,18 @@ int dsv4_gqa_append(const dsv4_gqa_append_params* p, dsv4_stream_t stream);
  * lse = sink[h] (-inf without a sink).
  * What rows from kv_len on, rows of other pages and rows before the first one that any of the sequence's
  * tokens sees hold never matters, NaN included; nor do the table entries of pages with no other rows.  The
- * rows from that one on must hold finite values: a NaN or Inf among them may also reach tokens that do not
- * see it.  Sums over the rows are fp32 and divided at the end: |v| times the rows seen has to stay below
- * 2^100, with softcap values below 2^-40 may lose bits, and weights below 2^-100 of a token's total may count
- * as zeros.  Calls of more than 8192 blocks of 256 rows (token, head of the group; B ceil(max_q_len group / 256))
- * add up a token's rows in one run, whose rounding takes about rows * 2^-29 of an output.
+ * rows from that one on must hold finite values, as bf16 (e4m3: code times scale): a NaN or Inf among them
+ * may also reach tokens that do not see it.
+ * Sums over the rows are fp32 and divided at the end: |v| times the rows seen has to stay below 2^100, with
+ * softcap values below 2^-40 may lose bits, and weights below 2^-100 of a token's total may count as zeros.
+ * Calls of more than 8192 blocks of 256 rows (token, head of the group; B ceil(max_q_len group / 256)) add up
+ * a token's rows in one run, whose rounding takes about rows * 2^-29 of an output.
+ * Weights are rounded before their product with V whatever out_dtype is: to bf16 (2^-8 of themselves), or, over
+ * e4m3 caches with at most 32 rows (token, head of the group) a sequence, to two e4m3 terms (2^-8 of
+ * themselves, or 2^-19 of the largest among 32 neighbouring ones).  Their sum is that of the unrounded ones.
+ * max_q_len and max_kv_len choose the kernels, the grid and the workspace for the whole call.  Over e4m3
+ * caches, a step that mixes prompt chunks with single tokens is better made as two calls, one for each kind
+ * (512 tokens beside 31 single ones over up to 8k rows: 151 us for 337, and 61 MB of workspace for 1.1 GB).
  * The workspace of an e4m3 call with more than 32 rows (token, head of the group) a sequence has room for
  * bf16 copies of the batch's rows: 4 B kv_heads max_kv_len head_dim bytes, lengths rounded up to 128.
  * ------------------------------------------------------------------------------------------- */
