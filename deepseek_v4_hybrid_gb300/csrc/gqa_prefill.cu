@@ -59,8 +59,10 @@ constexpr float LAZY = 8.f;
 // Capped logits lie at most at cap2 = cap log2(e).  A row's reference is put up to 2^CAP_RAISE above its largest logit so
 // far, so that cap2 is at most CAP_ROOM above it: then no weight passes 2^20 whatever the rows to come hold (fp32 holds
 // 2^20 x rows x values up to 2^107), the largest is at least 2^-60 (its product with values of 2^-40 still has 26
-// binary orders of normal numbers below it), and no maximum is needed any more.
-constexpr float CAP_ROOM = 20.f, CAP_RAISE = 60.f;
+// binary orders of normal numbers below it), and no maximum is needed any more.  It is raised by whole binary orders, so
+// that the largest weight is still a power of two and is not rounded (outputs of the capped documents off by 0.0023 with
+// a reference at cap2 - 20, 0.0021 so).
+constexpr float CAP_ROOM = 20.f, CAP_RAISE = 60.f, CAP_NEAR = CAP_ROOM + 0.5f;
 constexpr uint32_t FLAG_TIMEOUT = 4u;
 // Longest waits: a tile's 250 ms; those that may span the CTA's whole piece (queries, output, a tile of rows with no work in
 // some units) as much and 50 us a key tile that the call's bounds let it hold (a pair of tiles takes 2 us, masked, capped and
@@ -889,7 +891,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         float mul = cl;
         const bool all = __all_sync(0xffffffffu, inside && !g.bad);
-        if (capped && all && __all_sync(0xffffffffu, cap2 - m <= CAP_ROOM)) {
+        if (capped && all && __all_sync(0xffffffffu, cap2 - m <= CAP_NEAR)) {
           // No maximum is needed, and the tile is read once.  (Rolled: this code is long, and instruction fetch counts.)
           uint64_t sum2[2] = {0, 0};
           tc::tmem_ld32_nowait(t_s, xa);
@@ -969,8 +971,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc::tmem_wait_st();
         }
         const float top = mul * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        const float want = capped ? fmaxf(top, fminf(cap2 - CAP_ROOM, top + CAP_RAISE)) : top;
-        const bool move = capped && cap2 - m > CAP_ROOM ? want > m : top > m + LAZY;
+        const float want = capped ? top + fminf(fmaxf(ceilf(cap2 - CAP_ROOM - top), 0.f), CAP_RAISE) : top;
+        const bool move = capped && cap2 - m > CAP_NEAR ? want > m : top > m + LAZY;
         if (__any_sync(0xffffffffu, move)) {
           const float mn = move ? want : m;
           const float f = m == -INFINITY ? 0.f : tc::ex2_approx(m - mn);

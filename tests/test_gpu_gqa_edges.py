@@ -224,3 +224,20 @@ def test_sums_over_many_rows_of_some_tokens(M, softcap, D, out_dtype):
     tol, ltol = tol + mag * 2 * np.expm1(off), ltol + off
     worst = np.max(np.abs(out - want) / tol), np.max(np.abs(lse - wlse) / ltol)
     assert max(worst) <= 1, worst
+
+
+@pytest.mark.parametrize("cap", [20.0, 30.0, 50.0])
+@pytest.mark.parametrize("n", [1, 60])
+def test_capped_weight_of_one_row_is_not_rounded(M, n, cap):
+    """A row far above the others in a token's first tile weighs a power of two, so the output is its value: the others
+    together weigh under 600 e^-16 = 2^-13.8 of it, the sums and the division a few steps of 2^-23."""
+    bt = Batch([n], [700], 8, 1, 128, 64, "bf16", seed=3)
+    bt.q[:] = O.bf16_encode(np.linspace(1, 1.7, 8)[:, None] * np.ones(bt.q.shape))
+    for j in range(700):
+        z = 14.0 if j == 40 else -14.0     # caps of 20 and more leave at least 11.9 of it, and 16 between any two
+        bt.caches[0][bt.table[0, j // 64], :, j % 64] = O.bf16_encode(z / 128 ** 0.5)
+    _, out, _ = run_attention(M, bt, softcap=cap)
+    v = O.bf16_decode(bt.caches[1][bt.table[0, 0], 0, 40]).astype(np.float64)
+    big = np.abs(O.bf16_decode(bt.caches[1][bt.table[0]].view(np.uint16))).astype(np.float64)
+    off = np.abs(out.double().cpu().numpy() - v)
+    assert (off <= 2.0 ** -13 * np.nanmax(big) + 2.0 ** -20 * np.abs(v)).all(), off.max()
