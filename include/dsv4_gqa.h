@@ -101,8 +101,9 @@ int dsv4_gqa_append(const dsv4_gqa_append_params* p, dsv4_stream_t stream);
  * tokens sees hold never matters, NaN included; nor do the table entries of pages with no other rows.  The
  * rows from that one on must hold finite values, as bf16 (e4m3: code times scale): a NaN or Inf among them
  * may also reach tokens that do not see it.
- * Sums over the rows are fp32 and divided at the end: |v| times the rows seen has to stay below 2^100, with
- * softcap values below 2^-40 may lose bits, and weights below 2^-100 of a token's total may count as zeros.
+ * Sums over the rows are fp32 and divided at the end: |v| times the rows seen has to stay below 2^100, and
+ * weights below 2^-100 of a token's total may count as zeros (with softcap: below 2^-60, and values below
+ * 2^-40 may lose bits).
  * Calls of more than 8192 blocks of 256 rows (token, head of the group; B ceil(max_q_len group / 256)) add up
  * a token's rows in one run, whose rounding takes about rows * 2^-29 of an output.
  * Weights are rounded before their product with V whatever out_dtype is: to bf16 (2^-8 of themselves), or, over
