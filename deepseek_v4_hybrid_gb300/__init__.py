@@ -1,11 +1,13 @@
 """DeepSeek-V4 hybrid compressed-attention decode step on one GB300 (sm_103a).
 
-Thin Python binding of libdsv4.so (include/dsv4.h, include/dsv4_gqa.h).  The functions below take torch CUDA tensors,
+Thin Python binding of libdsv4.so (include/dsv4.h, dsv4_gqa.h, dsv4_loop.h).  The functions below take torch CUDA tensors,
 fill the C parameter structs and call the library on the current torch stream; every step of the
 decode path runs in the library's CUDA kernels.  There is no CPU fallback: the import fails if
 the library is not built.
 """
 from __future__ import annotations
+
+import ctypes as C
 
 import torch
 
@@ -260,7 +262,7 @@ def gqa_set_workspace(params, workspace):
     params.workspace_tensor = workspace
 
 
-def _gqa_call(name, fn, params, stream):
+def _call(name, fn, params, stream):
     dev = params.device
     if dev.index is not None and dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -272,12 +274,195 @@ def _gqa_call(name, fn, params, stream):
 
 def dsv4_gqa_append(params, stream=None):
     """Rotates and stores the new tokens' keys and values, and rotates their queries (see include/dsv4_gqa.h)."""
-    _gqa_call("dsv4_gqa_append", _lib.dsv4_gqa_append, params, stream)
+    _call("dsv4_gqa_append", _lib.dsv4_gqa_append, params, stream)
 
 
 def dsv4_gqa_attention(params, stream=None):
     """Attention of the new tokens over the paged per-head caches into params' out and lse (see include/dsv4_gqa.h)."""
-    _gqa_call("dsv4_gqa_attention", _lib.dsv4_gqa_attention, params, stream)
+    _call("dsv4_gqa_attention", _lib.dsv4_gqa_attention, params, stream)
+
+
+# ---------------------------------------------------------------------------------------------------------
+# what surrounds the layers of a decode step (include/dsv4_loop.h): like the grouped-query calls, over parameter
+# structs that are built once and keep their tensors alive.
+# ---------------------------------------------------------------------------------------------------------
+def rope_freqs(rope_dim, theta=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0, beta_slow=1.0,
+               low_turns=1.0, high_turns=4.0, device="cuda"):
+    """Frequencies of rope_params and rope_table_params: [rope_dim / 2] int64 on the device, scaled for long contexts
+    by "none", "linear", "base", "yarn" or "bands" (see include/dsv4_loop.h)."""
+    _need(scaling in _abi.ROPE_SCALINGS, f"scaling: {scaling!r} is none of {tuple(_abi.ROPE_SCALINGS)}")
+    _need(isinstance(rope_dim, int) and 2 <= rope_dim <= 1024, f"rope_dim: {rope_dim}")
+    out = torch.empty(rope_dim // 2, dtype=torch.int64)
+    p = _abi.make(_abi.RopeFreqsParams, rope_dim=rope_dim, scaling=_abi.ROPE_SCALINGS[scaling], theta=theta,
+                  factor=factor, original_len=original_len, beta_fast=beta_fast, beta_slow=beta_slow,
+                  low_turns=low_turns, high_turns=high_turns)
+    _abi.check("dsv4_rope_freqs", _lib.dsv4_rope_freqs(p, C.cast(out.data_ptr(), C.POINTER(C.c_uint64))))
+    return out.to(device)
+
+
+def _act(t, name):
+    _need(isinstance(t, torch.Tensor) and t.dtype in (torch.bfloat16, torch.float32),
+          f"{name}: dtype {getattr(t, 'dtype', type(t))} is neither bfloat16 nor float32")
+    _need(t.device.type == "cuda", f"{name}: on {t.device}, wanted a CUDA device")
+    return BF16 if t.dtype == torch.bfloat16 else F32
+
+
+def rope_params(x, out, positions, freqs, x2=None, out2=None, rope_first=0, rope_halves=False, inverse=False,
+                scale=1.0):
+    """Parameter struct of dsv4_rope.  x, out [T, heads, dim] and x2, out2 [T, heads2, dim] bf16 or fp32, rows of
+    any strides (slices of a fused projection); out is x itself (in place) or apart; positions [T] int32 (negative:
+    skipped); freqs of rope_freqs; inverse turns back (the gradient)."""
+    dt, dev = _act(x, "x"), x.device
+    _need(x.dim() == 3, f"x: shape {tuple(x.shape)}, wanted three dimensions")
+    T, heads, dim = x.shape
+    _need((x2 is None) == (out2 is None), "x2 and out2 go together")
+    _need_tensor(x, "x", (x.dtype,), (T, heads, dim), dev)
+    _need_tensor(out, "out", (x.dtype,), (T, heads, dim), dev)
+    _need_flat(positions, "positions", torch.int32, (T,), dev)
+    _need_flat(freqs, "freqs", torch.int64, (None,), dev)
+    p = _abi.make(_abi.RopeParams, x=_ptr(x), y=_ptr(out), x_token_stride=x.stride(0), x_head_stride=x.stride(1),
+                  y_token_stride=out.stride(0), y_head_stride=out.stride(1), heads=heads, heads2=1, dtype=dt, T=T,
+                  head_dim=dim, positions=_ptr(positions), freqs=_ptr(freqs), rope_first=rope_first,
+                  rope_dim=2 * freqs.shape[0], rope_halves=int(rope_halves), inverse=int(inverse), scale=scale)
+    if x2 is not None:
+        _need_tensor(x2, "x2", (x.dtype,), (T, None, dim), dev)
+        _need_tensor(out2, "out2", (x.dtype,), (T, x2.shape[1], dim), dev)
+        p.x2, p.y2, p.heads2 = _ptr(x2), _ptr(out2), x2.shape[1]
+        p.x2_token_stride, p.x2_head_stride = x2.stride(0), x2.stride(1)
+        p.y2_token_stride, p.y2_head_stride = out2.stride(0), out2.stride(1)
+    p.device = dev
+    p.tensors = (x, out, positions, freqs, x2, out2)
+    return p
+
+
+def dsv4_rope(params, stream=None):
+    """Turns rows by their tokens' positions (see include/dsv4_loop.h)."""
+    _call("dsv4_rope", _lib.dsv4_rope, params, stream)
+
+
+def rope_table_params(table, freqs, first_position=0, scale=1.0):
+    """Parameter struct of dsv4_rope_table: table [rows, rope_dim] fp32 becomes the cos_sin table of the positions from
+    first_position on."""
+    _need(isinstance(table, torch.Tensor) and table.device.type == "cuda", "table: wanted a tensor on a CUDA device")
+    _need_flat(freqs, "freqs", torch.int64, (None,), table.device)
+    _need_flat(table, "table", torch.float32, (None, 2 * freqs.shape[0]), table.device)
+    p = _abi.make(_abi.RopeTableParams, table=_ptr(table), rows=table.shape[0], rope_dim=table.shape[1],
+                  first_position=first_position, scale=scale, freqs=_ptr(freqs))
+    p.device = table.device
+    p.tensors = (table, freqs)
+    return p
+
+
+def dsv4_rope_table(params, stream=None):
+    """Writes a cos_sin table (see include/dsv4_loop.h)."""
+    _call("dsv4_rope_table", _lib.dsv4_rope_table, params, stream)
+
+
+def plan_cache(block_table, held, free_pages, free_count, page_size, held_out=None, free_count_out=None, ratio=1,
+               window=0, first=None, first_out=None, slots=None):
+    """One paged cache of batch_plan_params: block_table [B, n], held [B], free_pages [num_pages] and free_count [1] int32;
+    window: with first [B], the begin of each request's table entries; slots [T] int64.  The outputs are
+    the inputs themselves where they are not given (held, first and free_count then advance in place)."""
+    held_out = held if held_out is None else held_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    first_out = first if first_out is None else first_out
+    _need(isinstance(block_table, torch.Tensor) and block_table.device.type == "cuda",
+          "block_table: wanted a tensor on a CUDA device")
+    dev = block_table.device
+    _need_flat(block_table, "block_table", torch.int32, (None, None), dev)
+    B = block_table.shape[0]
+    for t, name in ((held, "held"), (held_out, "held_out"), (first, "first"), (first_out, "first_out")):
+        if t is not None or name.startswith("held"):
+            _need_flat(t, name, torch.int32, (B,), dev)
+    _need_flat(free_pages, "free_pages", torch.int32, (None,), dev)
+    _need_flat(free_count, "free_count", torch.int32, (1,), dev)
+    _need_flat(free_count_out, "free_count_out", torch.int32, (1,), dev)
+    if slots is not None:
+        _need_flat(slots, "slots", torch.int64, (None,), dev)
+    c = _abi.PlanCache(page_size=page_size, ratio=ratio, window=window, max_pages_per_seq=block_table.shape[1],
+                       num_pages=free_pages.shape[0], block_table=_ptr(block_table), held=_ptr(held),
+                       held_out=_ptr(held_out), first=_ptr(first), first_out=_ptr(first_out),
+                       free_pages=_ptr(free_pages), free_count=_ptr(free_count), free_count_out=_ptr(free_count_out),
+                       slots=_ptr(slots))
+    c.shape, c.device = (B, None if slots is None else slots.shape[0]), dev
+    c.tensors = (block_table, held, held_out, first, first_out, free_pages, free_count, free_count_out, slots)
+    return c
+
+
+def batch_plan_params(ctx, n_new, q_start, kv_len, caches, ctx_add=None, ctx_out=None, positions=None, token_seq=None,
+                      max_tokens=None):
+    """Parameter struct of dsv4_batch_plan.  ctx, n_new, kv_len, ctx_add, ctx_out [B], q_start [B + 1], positions and
+    token_seq [T] int32; caches: 1 to 4 of plan_cache; max_tokens: T, where neither positions, token_seq nor
+    slots say it."""
+    _need(isinstance(ctx, torch.Tensor) and ctx.device.type == "cuda", "ctx: wanted a tensor on a CUDA device")
+    dev, B = ctx.device, ctx.shape[0]
+    _need(1 <= len(caches) <= _abi.PLAN_MAX_CACHES, f"caches: {len(caches)}, wanted 1 to {_abi.PLAN_MAX_CACHES}")
+    for t, name, shape in ((ctx, "ctx", (B,)), (n_new, "n_new", (B,)), (q_start, "q_start", (B + 1,)),
+                           (kv_len, "kv_len", (B,)), (ctx_add, "ctx_add", (B,)), (ctx_out, "ctx_out", (B,)),
+                           (positions, "positions", (None,)), (token_seq, "token_seq", (None,))):
+        if t is not None or name in ("ctx", "n_new", "q_start", "kv_len"):
+            _need_flat(t, name, torch.int32, shape, dev)
+    sizes = {t.shape[0] for t in (positions, token_seq) if t is not None}
+    sizes |= {c.shape[1] for c in caches if c.shape[1] is not None} | ({max_tokens} if max_tokens is not None else set())
+    _need(len(sizes) == 1, f"positions, token_seq, slots and max_tokens: sizes {sorted(sizes)}, wanted one")
+    for c in caches:
+        _need(c.device == dev and c.shape[0] == B, f"cache: {c.shape[0]} requests on {c.device}, wanted {B} on {dev}")
+    p = _abi.make(_abi.BatchPlanParams, B=B, T=sizes.pop(), num_caches=len(caches), ctx=_ptr(ctx), ctx_add=_ptr(ctx_add),
+                  n_new=_ptr(n_new), ctx_out=_ptr(ctx_out), q_start=_ptr(q_start), kv_len=_ptr(kv_len),
+                  positions=_ptr(positions), token_seq=_ptr(token_seq))
+    for i, c in enumerate(caches):
+        p.caches[i] = c
+    p.device = dev
+    p.tensors = (ctx, n_new, q_start, kv_len, ctx_add, ctx_out, positions, token_seq, tuple(c.tensors for c in caches))
+    return p
+
+
+def dsv4_batch_plan(params, stream=None):
+    """Gives back and takes pages and writes the next step's tables, slots and positions (see include/dsv4_loop.h)."""
+    _call("dsv4_batch_plan", _lib.dsv4_batch_plan, params, stream)
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def draft_verify_params(target, tokens, q_start, max_q_len, out_tokens, n_out, draft=None, draft_row=None,
+                        temperature=None, u=None, noise=None, logp=None, target_probs=False, draft_probs=False):
+    """Parameter struct of dsv4_draft_verify.  target [T, vocab] logits (or probabilities) and draft [rows, vocab], bf16
+    or fp32, rows of any stride; tokens, draft_row [T], q_start [B + 1], out_tokens [B, max_q_len], n_out [B] int32;
+    temperature [B], u [T], noise [B, vocab], logp [B, max_q_len] fp32."""
+    dt, dev = _act(target, "target"), target.device
+    _need_tensor(target, "target", (target.dtype,), (None, None), dev)
+    T, V = target.shape
+    _need_flat(n_out, "n_out", torch.int32, (None,), dev)
+    B = n_out.shape[0]
+    _need_flat(q_start, "q_start", torch.int32, (B + 1,), dev)
+    _need_flat(tokens, "tokens", torch.int32, (T,), dev)
+    _need_flat(out_tokens, "out_tokens", torch.int32, (B, max_q_len), dev)
+    for t, name, dtype, shape in ((draft_row, "draft_row", torch.int32, (T,)), (temperature, "temperature", torch.float32, (B,)),
+                                  (u, "u", torch.float32, (T,)), (logp, "logp", torch.float32, (B, max_q_len))):
+        if t is not None:
+            _need_flat(t, name, dtype, shape, dev)
+    _need((u is None) == (noise is None), "u and noise go together")
+    p = _abi.make(_abi.DraftVerifyParams, target=_ptr(target), target_stride=_row_stride(target), target_dtype=dt,
+                  target_probs=int(target_probs), draft_row=_ptr(draft_row), tokens=_ptr(tokens), q_start=_ptr(q_start),
+                  T=T, B=B, vocab=V, max_q_len=max_q_len, temperature=_ptr(temperature), u=_ptr(u), noise=_ptr(noise),
+                  out_tokens=_ptr(out_tokens), n_out=_ptr(n_out), logp=_ptr(logp), draft_probs=int(draft_probs))
+    if draft is not None:
+        p.draft_dtype = _act(draft, "draft")
+        _need_tensor(draft, "draft", (draft.dtype,), (None, V), dev)
+        p.draft, p.draft_rows, p.draft_stride = _ptr(draft), draft.shape[0], _row_stride(draft)
+    if noise is not None:
+        _need_tensor(noise, "noise", (torch.float32,), (B, V), dev)
+        p.noise_stride = _row_stride(noise)
+    p.device = dev
+    p.tensors = (target, tokens, q_start, out_tokens, n_out, draft, draft_row, temperature, u, noise, logp)
+    return p
+
+
+def dsv4_draft_verify(params, stream=None):
+    """Verifies drafted tokens and draws the token that follows them (see include/dsv4_loop.h)."""
+    _call("dsv4_draft_verify", _lib.dsv4_draft_verify, params, stream)
 
 
 def dsv4_kernel_launches() -> int:

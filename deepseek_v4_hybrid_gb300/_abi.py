@@ -1,4 +1,4 @@
-"""ctypes mirror of include/dsv4.h and the loader of the in-tree libdsv4.so.
+"""ctypes mirror of include/dsv4.h, dsv4_gqa.h and dsv4_loop.h, and the loader of the in-tree libdsv4.so.
 
 Argument marshalling only: every step of the decode path runs in the library's CUDA kernels.
 Importing this module fails loudly if the library has not been built.
@@ -17,7 +17,7 @@ OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_BOUNDS, ERR_TIMEOUT = 0, -1, -2,
 LATENT_DIM, VALUE_DIM, ROPE_DIM, FP8_DS_MLA_BYTES = 576, 512, 64, 656
 ABI_VERSION = 3
 
-vp, i32, i64, u32, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_uint32, C.c_float
+vp, i32, i64, u32, f32, f64 = C.c_void_p, C.c_int32, C.c_int64, C.c_uint32, C.c_float, C.c_double
 
 
 class KvInsertParams(C.Structure):
@@ -88,6 +88,47 @@ class GqaAttentionParams(C.Structure):
                 ("lse", vp), ("workspace", vp), ("workspace_bytes", C.c_size_t)]
 
 
+class RopeFreqsParams(C.Structure):
+    _fields_ = [("struct_size", u32), ("rope_dim", i32), ("scaling", i32), ("theta", f64), ("factor", f64),
+                ("original_len", f64), ("beta_fast", f64), ("beta_slow", f64), ("low_turns", f64), ("high_turns", f64)]
+
+
+class RopeParams(C.Structure):
+    _fields_ = [("struct_size", u32), ("x", vp), ("y", vp), ("x_token_stride", i64), ("x_head_stride", i64),
+                ("y_token_stride", i64), ("y_head_stride", i64), ("x2", vp), ("y2", vp), ("x2_token_stride", i64),
+                ("x2_head_stride", i64), ("y2_token_stride", i64), ("y2_head_stride", i64), ("heads", i32),
+                ("heads2", i32), ("dtype", i32), ("T", i32), ("head_dim", i32), ("positions", vp), ("freqs", vp),
+                ("rope_first", i32), ("rope_dim", i32), ("rope_halves", i32), ("inverse", i32), ("scale", f32)]
+
+
+class RopeTableParams(C.Structure):
+    _fields_ = [("struct_size", u32), ("table", vp), ("rows", i32), ("rope_dim", i32), ("first_position", i32),
+                ("scale", f32), ("freqs", vp)]
+
+
+class PlanCache(C.Structure):
+    _fields_ = [("page_size", i32), ("ratio", i32), ("window", i32), ("max_pages_per_seq", i32), ("num_pages", i64),
+                ("block_table", vp), ("held", vp), ("held_out", vp), ("first", vp), ("first_out", vp),
+                ("free_pages", vp), ("free_count", vp), ("free_count_out", vp), ("slots", vp)]
+
+
+PLAN_MAX_CACHES, PLAN_MAX_REQUESTS, PLAN_MAX_TOKENS = 4, 4096, 1 << 19
+
+
+class BatchPlanParams(C.Structure):
+    _fields_ = [("struct_size", u32), ("B", i32), ("T", i32), ("num_caches", i32), ("ctx", vp), ("ctx_add", vp),
+                ("n_new", vp), ("ctx_out", vp), ("q_start", vp), ("kv_len", vp), ("positions", vp),
+                ("token_seq", vp), ("caches", PlanCache * PLAN_MAX_CACHES)]
+
+
+class DraftVerifyParams(C.Structure):
+    _fields_ = [("struct_size", u32), ("target", vp), ("target_stride", i64), ("target_dtype", i32),
+                ("target_probs", i32), ("draft", vp), ("draft_stride", i64), ("draft_rows", i64),
+                ("draft_dtype", i32), ("draft_probs", i32), ("draft_row", vp), ("tokens", vp), ("q_start", vp),
+                ("T", i32), ("B", i32), ("vocab", i32), ("max_q_len", i32), ("temperature", vp), ("u", vp),
+                ("noise", vp), ("noise_stride", i64), ("out_tokens", vp), ("n_out", vp), ("logp", vp)]
+
+
 EXPORTS = ["dsv4_kv_insert", "dsv4_compress_update", "dsv4_indexer_topk_workspace_bytes", "dsv4_indexer_topk",
            "dsv4_sparse_mla_decode_workspace_bytes", "dsv4_sparse_mla_decode", "dsv4_abi_version",
            "dsv4_status_string", "dsv4_last_cuda_error", "dsv4_read_device_flags", "dsv4_indexer_topk_noalloc",
@@ -95,6 +136,10 @@ EXPORTS = ["dsv4_kv_insert", "dsv4_compress_update", "dsv4_indexer_topk_workspac
 
 # the grouped-query calls (include/dsv4_gqa.h)
 GQA_EXPORTS = ["dsv4_gqa_append", "dsv4_gqa_attention_workspace_bytes", "dsv4_gqa_attention"]
+
+# the calls around the layers (include/dsv4_loop.h)
+LOOP_EXPORTS = ["dsv4_rope_freqs", "dsv4_rope", "dsv4_rope_table", "dsv4_batch_plan", "dsv4_draft_verify"]
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "yarn": 3, "bands": 4}
 
 # bytes of the scratch array built into the library for dsv4_indexer_topk_noalloc
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -115,7 +160,9 @@ def load(path: str = LIB_PATH) -> C.CDLL:
                      ("dsv4_qnorm_rope_kv_insert", QnormRopeKvInsertParams),
                      ("dsv4_indexer_topk", IndexerTopkParams), ("dsv4_sparse_mla_decode", SparseMlaDecodeParams),
                      ("dsv4_indexer_topk_noalloc", IndexerTopkParams), ("dsv4_gqa_append", GqaAppendParams),
-                     ("dsv4_gqa_attention", GqaAttentionParams)):
+                     ("dsv4_gqa_attention", GqaAttentionParams), ("dsv4_rope", RopeParams),
+                     ("dsv4_rope_table", RopeTableParams), ("dsv4_batch_plan", BatchPlanParams),
+                     ("dsv4_draft_verify", DraftVerifyParams)):
         fn = getattr(lib, name)
         fn.argtypes = [C.POINTER(st), vp]
         fn.restype = C.c_int
@@ -125,6 +172,8 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         fn = getattr(lib, name)
         fn.argtypes = [C.POINTER(st)]
         fn.restype = C.c_size_t
+    lib.dsv4_rope_freqs.argtypes = [C.POINTER(RopeFreqsParams), C.POINTER(C.c_uint64)]
+    lib.dsv4_rope_freqs.restype = C.c_int
     lib.dsv4_padded_num_q_heads.argtypes = [C.c_int, C.c_int]
     lib.dsv4_padded_num_q_heads.restype = C.c_int
     lib.dsv4_abi_version.restype = C.c_int

@@ -12,7 +12,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libdsv4.so")
 SOURCES = ["api.cu", "insert_compress.cu", "indexer_topk.cu", "attention.cu", "noalloc.cu", "tmap.cu",
-           "gqa_append.cu", "gqa_attention.cu", "gqa_decode.cu", "gqa_prefill.cu"]
+           "gqa_append.cu", "gqa_attention.cu", "gqa_decode.cu", "gqa_prefill.cu",
+           "loop_api.cu", "loop_rope.cu", "loop_plan.cu", "loop_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]

@@ -8,6 +8,7 @@
 #include "dsv4_common.cuh"
 #include "dsv4_launch.h"
 #include "gqa_common.cuh"
+#include "loop_common.cuh"
 
 using namespace dsv4;
 
@@ -103,6 +104,10 @@ int dsv4_read_device_flags(uint32_t* flags) {
   st = cuda_status(read_flags_gqa_prefill(flags));
   if (st != DSV4_OK) return st;
   st = cuda_status(read_flags_gqa_decode(flags));
+  if (st != DSV4_OK) return st;
+  st = cuda_status(read_flags_loop_plan(flags));
+  if (st != DSV4_OK) return st;
+  st = cuda_status(read_flags_loop_verify(flags));
   if (st != DSV4_OK) return st;
   if (*flags & 4u) return DSV4_ERR_TIMEOUT;
   return *flags ? DSV4_ERR_BOUNDS : DSV4_OK;
