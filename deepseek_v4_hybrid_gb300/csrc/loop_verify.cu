@@ -1,10 +1,10 @@
 // Verification of drafted tokens.
 //
 // A cluster of CTAs takes a sequence, each CTA the same slice of the vocabulary of every row.  Rows are taken in groups:
-// the warps go over the slices of a group's rows once, with the running maximum and the sum of e^(z - max) of a
+// the warps go over the slices of a group's rows once, with a reference and the sum of e^(z - reference) of a
 // softmax (in 32-bit floats), the CTAs exchange these through distributed shared memory, and every CTA
 // finds by itself how far the drafted tokens stand.  The row where they end is read once more, from the L2 cache,
-// for the race argmax r(x) / noise(x), whose winners are exchanged the same way.  Rows behind that one are not read.
+// for the race argmax r(x) / noise(x), whose winners are exchanged the same way.  Rows behind that group are not read.
 #include <cooperative_groups.h>
 
 #include "loop_common.cuh"
@@ -19,13 +19,13 @@ namespace loop {
 
 namespace cg = cooperative_groups;
 
-constexpr int NT = 512, NW = NT / 32;
-constexpr int MAX_CLUSTER = 8;
-constexpr int MAX_ROWS = NW / 2;  // rows of a group: a warp at least for each row of target and draft
+constexpr int MAX_CLUSTER = 8, MAX_ROWS = 8;  // rows of a group
 constexpr float LOG2E_HI = 1.44269502162933349609375f, LOG2E_LO = 1.92596299112661746887e-8f, LN2F = 0.69314718055994531f;
-constexpr float MAX_F32 = 3.4028234663852886e38f;
+constexpr float MAX_F32 = 3.4028234663852886e38f, MAX_BF16 = 3.3895313892515355e38f;
+constexpr int NOWHERE = 0x7FFFFFFF;
 
-// Maximum, its first index, and the sum of 2^((z - m) c) of a part of a row.
+// Sums of a part of a row of logits: s = sum of 2^((z - m) c) against the reference m, one of the row's logits (-inf: the
+// part leaves nothing), and, for greedy sequences, whose m is the maximum, its first index.
 struct Stat {
   float m, s;
   int idx;
@@ -42,8 +42,9 @@ __device__ __forceinline__ void merge(Stat& a, const Stat& b, float c) {
   }
 }
 
-// A logit as it counts: NaN as -inf, +inf as the largest value.
-__device__ __forceinline__ float logit(float x) { return fminf(fmaxf(x, -INFINITY), MAX_F32); }
+// A logit as it counts: NaN as -inf, +inf as the type's largest value.
+__device__ __forceinline__ float largest(bool f32) { return f32 ? MAX_F32 : MAX_BF16; }
+__device__ __forceinline__ float logit(float x, bool f32) { return fminf(fmaxf(x, -INFINITY), largest(f32)); }
 // A probability: NaN and negative ones as 0.
 __device__ __forceinline__ float prob(float x) { return fminf(fmaxf(x, 0.f), MAX_F32); }
 
@@ -59,89 +60,219 @@ __device__ __forceinline__ const void* at(const void* base, int64_t i, bool f32)
   return reinterpret_cast<const uint8_t*>(base) + i * (f32 ? 4 : 2);
 }
 
-// Adds N logits with indices index(0) < index(1) < ... to st.
-template <int N, typename I>
-__device__ __forceinline__ void add(Stat& st, const float (&z)[N], float c, I index) {
-  float top = z[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) top = fmaxf(top, z[i]);
-  if (top > st.m) {
-    st.s = st.m == -INFINITY ? 0.f : st.s * tc::ex2_approx((st.m - top) * c);
-    st.m = top;
-#pragma unroll
-    for (int i = N - 1; i >= 0; --i)
-      if (z[i] == top) st.idx = index(i);
-  }
-  if (st.m == -INFINITY) return;
-#pragma unroll
-  for (int i = 0; i < N; ++i) st.s += tc::ex2_approx((z[i] - st.m) * c);
+// Two floats in one register pair, for the packed instructions.
+__device__ __forceinline__ uint64_t pack(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
-// Elements [lo, hi) of a row of logits, by lane `lane` of `lanes` threads.
+// 16 bytes of a row.
 template <bool F32>
-__device__ __forceinline__ Stat scan_row(const void* row, int lo, int hi, int lane, int lanes, float c) {
-  constexpr int E = F32 ? 4 : 8, U = F32 ? 4 : 2;  // elements of 16 bytes, loads in flight
-  Stat st = {-INFINITY, 0.f, 0x7FFFFFFF};
-  const uintptr_t a = reinterpret_cast<uintptr_t>(at(row, lo, F32));
-  const int head = min(hi - lo, (int)((16 - (a & 15)) & 15) / (F32 ? 4 : 2));  // elements before the first whole 16 bytes
-  if (lane < head) {
-    const float z[1] = {logit(element<F32>(row, lo + lane))};
-    add<1>(st, z, c, [&](int) { return lo + lane; });
+struct Vec {
+  static constexpr int E = F32 ? 4 : 8;
+  uint32_t w[4];
+  __device__ __forceinline__ void set(const uint4& r) { w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w; }
+  __device__ __forceinline__ float get(int i) const {
+    if (F32) return __uint_as_float(w[i]);
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
   }
-  const int from = lo + head, vecs = (hi - from) / E;
-  const uint4* v = reinterpret_cast<const uint4*>(at(row, from, F32));
-  for (int j = lane; j < vecs; j += U * lanes) {
-    uint4 raw[U];
+};
+template <bool F32>
+constexpr uint32_t NONE = F32 ? 0xFF800000u : 0xFF80FF80u;  // elements of -inf
+
+// The largest of the elements (NaN is passed over).
+template <bool F32, int N>
+__device__ __forceinline__ float top_of(const Vec<F32> (&v)[N]) {
+  if (F32) {
+    float top = v[0].get(0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t none = F32 ? 0xFF800000u : 0xFF80FF80u;
-      raw[u] = make_uint4(none, none, none, none);
-      if (j + u * lanes < vecs) raw[u] = v[j + u * lanes];
-    }
-    float z[U * E];
+    for (int i = 1; i < N * 4; ++i) top = fmaxf(top, v[i / 4].get(i % 4));
+    return top;
+  }
+  __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&v[0].w[0]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+  for (int i = 1; i < N * 4; ++i) y = __hmax2(y, *reinterpret_cast<const __nv_bfloat162*>(&v[i / 4].w[i % 4]));
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&y);
+  return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Order-preserving map of floats (no NaN) to integers and back.
+__device__ __forceinline__ int ordered(float x) {
+  const int b = __float_as_int(x);
+  return b < 0 ? b ^ 0x7FFFFFFF : b;
+}
+__device__ __forceinline__ float from_ordered(int k) { return __int_as_float(k < 0 ? k ^ 0x7FFFFFFF : k); }
+__device__ __forceinline__ float warp_top(float x) { return from_ordered(__reduce_max_sync(0xffffffffu, ordered(x))); }
+
+// Each thread streams its vectors through a ring of its own in shared memory: groups of asynchronous 16-byte copies,
+// all but one of them ahead of the one in use.  Nobody else reads them, so no barrier is needed.
+constexpr int U = 4;  // vectors of a group (scan)
+
+// The running numbers of a warp over a row: the reference m, r = the integer next to m c (or -2^21, when m c is less), and
+// the lane's sum of 2^(z c - r).  With an integer the exponent's argument is one fused product, and a new reference
+// rescales the sums by a power of two: neither rounds anything that the logits' size could make large.
+// Greedy sequences keep m at the maximum and each lane's first index of it; the others change it only when a sum
+// says that a logit lies far above (2^40), which spares the search.
+// Elements are taken as they are.  NaN, +inf and references beyond +-2^21 / c show in the result, and the part is then
+// done again by the careful form.
+constexpr float LEAST = -2097152.f, FAR = 1099511627776.f;
+
+struct Run {
+  float m, r, s;
+  int idx;
+};
+
+template <bool F32, int N>
+__device__ __forceinline__ float weights(const Vec<F32> (&v)[N], float c, float r) {
+  constexpr int E = Vec<F32>::E;
+  const uint64_t c2 = pack(c, c), r2 = pack(-r, -r);
+  uint64_t sum = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (F32) {
-          z[u * E + i] = logit(__uint_as_float(w[i]));
-        } else {
-          z[u * E + 2 * i] = logit(__uint_as_float(w[i] << 16));
-          z[u * E + (2 * i + 1) % E] = logit(__uint_as_float(w[i] & 0xFFFF0000u));
-        }
+  for (int i = 0; i < N * E; i += 2) {
+    const uint64_t y = fma2(pack(v[i / E].get(i % E), v[i / E].get(i % E + 1)), c2, r2);
+    sum = add2(sum, pack(tc::ex2_approx(low(y)), tc::ex2_approx(high(y))));
+  }
+  return low(sum) + high(sum);
+}
+
+template <bool F32, bool GREEDY, int N, typename I>
+__device__ __forceinline__ void add(Run& st, const Vec<F32> (&v)[N], float c, I index) {
+  constexpr int E = Vec<F32>::E;
+  float sum = 0.f;
+  bool renew;
+  if (GREEDY || st.m == -INFINITY) {
+    renew = __any_sync(0xffffffffu, top_of<F32, N>(v) > st.m);
+  } else {
+    sum = weights<F32, N>(v, c, st.r);
+    renew = __any_sync(0xffffffffu, sum > FAR);
+  }
+  if (renew) {
+    const float top = top_of<F32, N>(v), m = warp_top(fmaxf(top, st.m)), r = fmaxf(rintf(m * c), LEAST);
+    st.s *= tc::ex2_approx(st.r - r);
+    st.m = m, st.r = r;
+    if (GREEDY) {
+      st.idx = NOWHERE;
+      if (top == m) {
+#pragma unroll
+        for (int i = N * E - 1; i >= 0; --i)
+          if (v[i / E].get(i % E) == m) st.idx = index(i);
       }
     }
-    add<U * E>(st, z, c, [&](int i) { return from + (j + i / E * lanes) * E + i % E; });
   }
-  const int tail = from + vecs * E + lane;
-  if (tail < hi) {
-    const float z[1] = {logit(element<F32>(row, tail))};
-    add<1>(st, z, c, [&](int) { return tail; });
-  }
-  return st;
+  if (GREEDY || renew) sum = weights<F32, N>(v, c, st.r);
+  st.s += sum;
 }
 
-__device__ __forceinline__ Stat warp_merge(Stat st, float c) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stat y;
-    y.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    y.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    y.idx = __shfl_xor_sync(0xffffffffu, st.idx, o);
-    // (both lanes of a pair merge in the same order, so that they agree)
-    Stat lo = (threadIdx.x & o) ? y : st;
-    merge(lo, (threadIdx.x & o) ? st : y, c);
-    st = lo;
+// The careful form: one element, as it counts; s goes with m itself, the maximum.
+__device__ __forceinline__ void add_careful(Stat& st, float z, int i, float c) {
+  if (z == -INFINITY) return;
+  if (z > st.m) {
+    st.s = (st.m == -INFINITY ? 0.f : st.s * tc::ex2_approx((st.m - z) * c)) + 1.f;
+    st.m = z, st.idx = i;
+  } else {
+    st.s += tc::ex2_approx((z - st.m) * c);
   }
-  return st;
+}
+
+// Elements [lo, hi) of a row of logits: warp `share` of `shares` takes its part, blocks of U * 32 vectors, and returns its
+// numbers in every lane.
+template <int NT, int DEPTH, bool F32, bool GREEDY>
+__device__ __noinline__ Stat scan_row(const void* row, int lo, int hi, int share, int shares, float c, uint4* ring) {
+  constexpr int E = Vec<F32>::E, BLOCK = U * 32;
+  const int lane = threadIdx.x & 31;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(at(row, lo, F32));
+  const int head = min(hi - lo, (int)((16 - (a & 15)) & 15) / (F32 ? 4 : 2));  // elements before the first whole 16 bytes
+  const int from = lo + head, vecs = (hi - from) / E, step = BLOCK * shares;
+  const uint4* v = reinterpret_cast<const uint4*>(at(row, from, F32)) + lane;
+  uint4* mine = ring + threadIdx.x;
+  const auto fetch = [&](int j0, int group) {  // the block from vector j0 on
+    uint4* to = mine + group * (U * NT);
+    if (j0 + BLOCK <= vecs) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) tc::cp_async16(to + u * NT, v + j0 + u * 32, 16);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j0 + u * 32 + lane < vecs) tc::cp_async16(to + u * NT, v + j0 + u * 32, 16);
+    }
+    tc::cp_async_commit();
+  };
+  int j0 = share * BLOCK, ahead = j0, to = 0, use = 0;
+#pragma unroll
+  for (int g = 0; g < DEPTH - 1; ++g, ahead += step, ++to) fetch(ahead, to);
+  Run st = {-INFINITY, LEAST, 0.f, NOWHERE};
+  const auto one = [&](int i, bool there) {
+    Vec<F32> z[1];
+    z[0].set(make_uint4(NONE<F32>, NONE<F32>, NONE<F32>, NONE<F32>));
+    if (there) z[0].w[0] = F32 ? reinterpret_cast<const uint32_t*>(row)[i] : 0xFF800000u | reinterpret_cast<const uint16_t*>(row)[i];
+    add<F32, GREEDY, 1>(st, z, c, [&](int) { return i; });
+  };
+  if (share == 0 && head > 0) one(lo + lane, lane < head);
+  for (; j0 < vecs; j0 += step, ahead += step) {
+    fetch(ahead, to);
+    to = to == DEPTH - 1 ? 0 : to + 1;
+    tc::cp_async_wait<DEPTH - 1>();
+    const uint4* block = mine + use * (U * NT);
+    use = use == DEPTH - 1 ? 0 : use + 1;
+    Vec<F32> z[U];
+    if (j0 + BLOCK <= vecs) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) z[u].set(block[u * NT]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        z[u].set(make_uint4(NONE<F32>, NONE<F32>, NONE<F32>, NONE<F32>));
+        if (j0 + u * 32 + lane < vecs) z[u].set(block[u * NT]);
+      }
+    }
+    add<F32, GREEDY, U>(st, z, c, [&](int i) { return from + (j0 + i / E * 32 + lane) * E + i % E; });
+  }
+  tc::cp_async_wait<0>();
+  const int tail = from + vecs * E;
+  if (share == 0 && tail < hi) one(tail + lane, tail + lane < hi);
+  const float s = warp_sum(st.s);
+  if (st.m == -INFINITY) {
+    if (s == 0.f) return Stat{-INFINITY, 0.f, NOWHERE};  // (else a NaN was among them, which the careful form passes over)
+  } else if (s == s && fabsf(st.m * c) < -LEAST) {
+    return Stat{st.m, s * tc::ex2_approx(-fmaf(st.m, c, -st.r)),
+                GREEDY ? (int)__reduce_min_sync(0xffffffffu, (unsigned)st.idx) : NOWHERE};
+  }
+  Stat slow = {-INFINITY, 0.f, NOWHERE}, out;
+  const auto careful = [&](int i) { add_careful(slow, logit(element<F32>(row, i), F32), i, c); };
+  if (share == 0 && lane < head) careful(lo + lane);
+  for (int block = share * BLOCK; block < vecs; block += step)  // (the same part)
+    for (int j = block; j < min(block + BLOCK, vecs - lane); j += 32) {
+      Vec<F32> z;
+      z.set(v[j]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) add_careful(slow, logit(z.get(i), F32), from + (j + lane) * E + i, c);
+    }
+  if (share == 0 && tail + lane < hi) careful(tail + lane);
+  __syncwarp();
+  out.m = warp_top(slow.m);
+  out.s = warp_sum(slow.m == -INFINITY ? 0.f : slow.s * tc::ex2_approx((slow.m - out.m) * c));
+  out.idx = (int)__reduce_min_sync(0xffffffffu, slow.m == out.m ? (unsigned)slow.idx : (unsigned)NOWHERE);
+  return out;
 }
 
 // What turns an element of a row into its probability.
 struct Law {
   const void* row;
   bool f32, probs;
-  float m, inv;  // maximum and 1 / sum (logits)
+  float m, inv;  // reference and 1 / sum (logits)
 };
 
 // log2(e) / temperature in two floats.
@@ -149,8 +280,7 @@ struct Rate {
   float hi, lo;
 };
 
-// 2^((z - m) rate): the argument's rounding is carried along, as the special-function unit's input has 24 bits of
-// arguments up to 2^7.
+// 2^((z - m) rate): the roundings of the argument are carried along (an argument of 2^7 has steps of 2^-17).
 __device__ __forceinline__ float weight(float z, float m, const Rate& r) {
   const float d = z - m, y = d * r.hi;
   if (!(y > -150.f)) return 0.f;
@@ -169,7 +299,7 @@ __device__ __forceinline__ bool keeps(float u, float z, const Stat& p, float y, 
 
 __device__ __forceinline__ float law_of(const Law& l, float x, const Rate& r) {
   if (l.probs) return prob(x);
-  return l.m == -INFINITY ? 0.f : weight(logit(x), l.m, r) * l.inv;
+  return l.m == -INFINITY ? 0.f : weight(logit(x, l.f32), l.m, r) * l.inv;
 }
 
 struct Best {
@@ -181,17 +311,183 @@ __device__ __forceinline__ void take(Best& a, const Best& b) {
   if (b.key > a.key || (b.key == a.key && b.idx < a.idx)) a = b;
 }
 
-// The race over elements [lo, hi): r(x) / noise(x), r = p, max(p - q, 0) or p without `skip`.
-__device__ __forceinline__ Best race(const Law& p, const Law& q, bool minus, int skip, const float* noise, int lo, int hi,
-                                     const Rate& r) {
-  Best best = {0.f, 0x7FFFFFFF, 0.f};
-  for (int i = lo + (int)threadIdx.x; i < hi; i += NT) {
-    const float x = element(p.row, i, p.f32);
-    float w = law_of(p, x, r);
-    if (minus) w -= law_of(q, element(q.row, i, q.f32), r);
-    if (i == skip) w = 0.f;
-    const float key = __fdividef(w, noise[i]);
-    if (key > best.key) best = Best{key, i, x};
+// A law's quick weight: 2^(x c - ref) or x itself, times `scale`, is the probability but for 2^-10 of it.
+struct Quick {
+  bool probs, holds;
+  float ref, scale;
+  __device__ __forceinline__ explicit Quick(const Law& l, float c) {
+    probs = l.probs;
+    holds = l.probs || l.m == -INFINITY || fabsf(l.m * c) < -LEAST;
+    ref = l.m == -INFINITY ? 0.f : rintf(l.m * c);
+    scale = l.probs ? 1.f : l.m == -INFINITY ? 0.f : l.inv * tc::ex2_approx(-fmaf(l.m, c, -ref));
+  }
+  __device__ __forceinline__ float operator()(float x, float c) const {
+    return probs ? x : tc::ex2_approx(fmaf(x, c, -ref));
+  }
+};
+
+// The race over elements [lo, hi): r(x) / noise(x), r = p, p without `skip`, or (minus) max(p - q, 0).  Of most elements
+// only a quick upper bound of p is computed: it has to pass the best key of the CTA so far, and the draft's row is
+// read for those that do.  `top` (shared, 0 at first) holds that key's bits.
+struct Runner {
+  Law p, q;
+  bool minus;
+  int skip;
+  const float* noise;
+  int lo, hi;
+  Rate r;
+  uint4* ring;
+  int* top;
+};
+
+template <int NT, int RING, bool F32>
+__device__ __noinline__ Best race(const Runner& a) {
+  constexpr float MORE = 1.f + 0x1p-10f, LESS = 1.f - 0x1p-10f;
+  // A warp takes chunks of 8 elements, H of them a lane, as many vectors as four groups and more of them leave room for.
+  constexpr int H = F32 ? 1 : 2, E = 8 * H, STEP = 32 * E, SIZE = F32 ? 4 : 2, GROUP = STEP * (SIZE + 4);
+  constexpr int GROUPS = RING / GROUP, STRIDE = NT / 32 * STEP;
+  Best best = {0.f, NOWHERE, 0.f};
+  if (!a.p.probs && a.p.m == -INFINITY) return best;
+  const float c = a.r.hi;
+  const Quick wp(a.p, c);
+  const bool quick = wp.holds && (!a.minus || Quick(a.q, c).holds);  // (else every element is a candidate)
+  const float unit = 1.f / (wp.scale * MORE);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float* noise = a.noise;
+  int* top = a.top;
+
+  const auto key_of = [&](int i, float x, float e) {
+    float w = law_of(a.p, x, a.r);
+    if (a.minus) w -= law_of(a.q, element(a.q.row, i, a.q.f32), a.r);
+    return i == a.skip ? 0.f : __fdividef(w, e);
+  };
+  const auto enter = [&](int i, float x, float e) {
+    const float key = key_of(i, x, e);
+    if (key > best.key || (key == best.key && key > 0.f && i < best.idx)) best = Best{key, i, x};
+  };
+  const auto share = [&](float key) {
+    const int t = __reduce_max_sync(0xffffffffu, __float_as_int(key));
+    if (lane == 0) atomicMax(top, t);
+    __syncwarp();
+  };
+
+  // the part whose vectors are whole, in chunks of 8 elements
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(at(a.p.row, a.lo, F32));
+  const int from = min(a.hi, a.lo + (int)((16 - (begin & 15)) & 15) / SIZE), chunks = (a.hi - from) / 8;
+  const uint8_t* prow = reinterpret_cast<const uint8_t*>(at(a.p.row, from, F32));
+  const float* nrow = noise + from;
+  const bool whole = (reinterpret_cast<uintptr_t>(nrow) & 15) == 0;
+  uint8_t* mine = reinterpret_cast<uint8_t*>(a.ring) + warp * RING;
+  const int count = chunks * 8;
+  // (elements as they lie in memory: the target's, then the noise's, which is copied word by word where its row begins
+  // off the target's boundaries)
+  const auto fetch = [&](int i, int group) {
+    uint8_t* to = mine + group * GROUP;
+    if (i < count) {
+      const int n = min(STEP, count - i);
+#pragma unroll
+      for (int u = 0; u < STEP * SIZE / 512; ++u)
+        if ((u * 32 + lane) * (16 / SIZE) < n)
+          tc::cp_async16(to + u * 512 + lane * 16, prow + (int64_t)i * SIZE + u * 512 + lane * 16, 16);
+      to += STEP * SIZE;
+      if (whole) {
+#pragma unroll
+        for (int u = 0; u < STEP / 128; ++u)
+          if (u * 128 + lane * 4 < n) tc::cp_async16(to + u * 512 + lane * 16, nrow + i + u * 128 + lane * 4, 16);
+      } else {
+#pragma unroll
+        for (int u = 0; u < STEP / 32; ++u)
+          if (u * 32 + lane < n) tc::cp_async4(to + u * 128 + lane * 4, nrow + i + u * 32 + lane);
+      }
+    }
+    tc::cp_async_commit();
+  };
+  const uint64_t c2 = pack(c, c), ref2 = pack(-wp.ref, -wp.ref);
+  int ahead = warp * STEP, to = 0, use = 0;
+#pragma unroll 1
+  for (; to < GROUPS - 1; ++to, ahead += STRIDE) fetch(ahead, to);
+  bool begun = false;
+  for (int i0 = warp * STEP; i0 < count; i0 += STRIDE, ahead += STRIDE) {
+    __syncwarp();  // (the group that is filled now has been read by every lane)
+    fetch(ahead, to);
+    to = to == GROUPS - 1 ? 0 : to + 1;
+    tc::cp_async_wait<GROUPS - 1>();
+    __syncwarp();
+    const uint8_t* group = mine + use * GROUP;
+    use = use == GROUPS - 1 ? 0 : use + 1;
+    // (chunk h of the lane: elements i0 + 256 h + 8 lane on; one behind the end holds what it held before)
+    const uint8_t* gx = group + lane * 8 * SIZE;
+    const float* ge = reinterpret_cast<const float*>(group + STEP * SIZE) + lane * 8;
+    const int n = count - i0 - lane * 8;  // the lane's chunk h is there if h * 256 < n
+    const auto bounds = [&](float bar) {  // elements whose bound passes
+      const uint64_t bar2 = pack(-bar * unit, -bar * unit);
+      uint32_t good = 0;
+      float most = 0.f;
+      uint64_t over[E / 2];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        Vec<F32> x[SIZE / 2];
+#pragma unroll
+        for (int v = 0; v < SIZE / 2; ++v) x[v].set(*reinterpret_cast<const uint4*>(gx + h * 256 * SIZE + v * 16));
+        const float4 e0 = *reinterpret_cast<const float4*>(ge + h * 256), e1 = *reinterpret_cast<const float4*>(ge + h * 256 + 4);
+        const uint64_t e[4] = {pack(e0.x, e0.y), pack(e0.z, e0.w), pack(e1.x, e1.y), pack(e1.z, e1.w)};
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+          constexpr int PER = 16 / SIZE;
+          const uint64_t z = pack(x[k / PER].get(k % PER), x[k / PER].get(k % PER + 1));
+          uint64_t w = z;
+          if (!wp.probs) {
+            const uint64_t y = fma2(z, c2, ref2);
+            w = pack(tc::ex2_approx(low(y)), tc::ex2_approx(high(y)));
+          }
+          w = fma2(e[k / 2], bar2, w);
+          over[h * 4 + k / 2] = w;
+          if (h * 256 < n) most = fmaxf(most, fmaxf(low(w), high(w)));
+        }
+      }
+      if (__any_sync(0xffffffffu, most > 0.f || !quick)) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          const float w = k & 1 ? high(over[k / 2]) : low(over[k / 2]);
+          if (k / 8 * 256 < n && (w > 0.f || !quick)) good |= 1u << k;
+        }
+      }
+      return good;
+    };
+    uint32_t good = bounds(__int_as_float(*(volatile int*)top));
+    if (!__any_sync(0xffffffffu, good)) continue;
+    const auto index = [&](int k) { return from + i0 + k / 8 * 256 + lane * 8 + k % 8; };
+    const auto xs = [&](int k) { return element<F32>(gx, k / 8 * 256 + k % 8); };
+    const auto es = [&](int k) { return ge[k / 8 * 256 + k % 8]; };
+    if (!begun && quick) {  // the first keys, or lower bounds of them, make a bar
+      begun = true;
+      const Quick wq(a.minus ? a.q : a.p, c);
+      float least = 0.f, y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = a.minus && (good >> k & 1) ? element(a.q.row, index(k), a.q.f32) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = wp(xs(k), c) * (wp.scale * LESS) - (a.minus ? fmaxf(wq(y[k], c), 0.f) * (wq.scale * MORE) : 0.f);
+        if ((good >> k & 1) && index(k) != a.skip) least = fmaxf(least, __fdividef(w, es(k)));
+      }
+      share(least < MAX_F32 ? least * LESS : 0.f);
+      good = bounds(__int_as_float(*(volatile int*)top));
+    }
+    while (good) {
+      const int k = __ffs(good) - 1;
+      good &= good - 1;
+      enter(index(k), xs(k), es(k));
+    }
+    __syncwarp();
+    share(best.key);
+  }
+  tc::cp_async_wait<0>();
+  __syncwarp();
+  // the elements before and behind the chunks, fewer than 8 each
+  const int front = from - a.lo, rest = from + count, edge = front + a.hi - rest;
+  if ((int)threadIdx.x < edge) {
+    const int i = (int)threadIdx.x < front ? a.lo + (int)threadIdx.x : rest + (int)threadIdx.x - front;
+    enter(i, element<F32>(a.p.row, i), noise[i]);
   }
   return best;
 }
@@ -201,18 +497,23 @@ struct Args {
   int rows;  // of a group
 };
 
-__global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Args a) {
+template <int NT, int DEPTH, int CTAS>
+__global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant__ Args a) {
+  constexpr int NW = NT / 32;
   const dsv4_draft_verify_params& p = a.p;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), rank = cluster.block_rank(), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / C;
+  extern __shared__ uint4 ring[];
   __shared__ Stat part[NW], got[2][2 * MAX_ROWS][MAX_CLUSTER];
   __shared__ Best bpart[NW], bgot[2][MAX_CLUSTER];
   __shared__ Stat fin[2 * MAX_ROWS];
-  __shared__ int stands[MAX_ROWS];
+  __shared__ int stands[MAX_ROWS], top_key;
+  if (tid == 0) top_key = 0;
   pdl_wait();
   pdl_launch_dependents();
   const int t0 = p.q_start[b], t1 = p.q_start[b + 1];
+  float temp = p.temperature ? p.temperature[b] : 1.f;
   if (t0 < 0 || t1 < t0 || t1 > p.T || t1 - t0 > p.max_q_len) {  // (the same for the whole cluster)
     if (rank == 0 && tid == 0) atomicOr(&g_flags_vf, FLAG_PAGE);
     return;
@@ -231,7 +532,6 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Args
     return;
   }
   cluster.sync();  // every CTA's shared memory is there to be written
-  float temp = p.temperature ? p.temperature[b] : 1.f;
   const bool greedy = p.noise == nullptr || !(temp > 0.f);
   temp = greedy ? 1.f : fminf(fmaxf(temp, 1e-30f), 1e30f);
   Rate rate;
@@ -240,13 +540,13 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Args
   const bool tf32 = p.target_dtype == DSV4_F32, df32 = p.draft_dtype == DSV4_F32;
   const bool drafted_law = p.draft != nullptr && !greedy;
   const int per = ((p.vocab + C - 1) / C + 7) & ~7, lo = min(p.vocab, rank * per), hi = min(p.vocab, lo + per);
-  const int tasks_a_row = (!p.target_probs || greedy ? 1 : 0) + (drafted_law && !p.draft_probs ? 1 : 0);
-  const bool target_task = !p.target_probs || greedy;
+  const bool target_task = !p.target_probs || greedy, draft_task = drafted_law && !p.draft_probs;
+  const int tasks_a_row = (target_task ? 1 : 0) + (draft_task ? 1 : 0);
 
   int last = -1, par = 0;  // the row that the sequence's last token comes from
-  bool all = false, excluded = false;
+  bool all = false, residual = false;
   Law lp = {}, lq = {};
-  int best_idx = 0;
+  Best best = {0.f, NOWHERE, 0.f};
   for (int i0 = 0; last < 0; i0 += a.rows) {
     const int rows = min(a.rows, n - i0), tasks = rows * tasks_a_row;
     // each row's drafted successor
@@ -268,31 +568,41 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Args
       if (!in) x = -1;
     }
     if (tasks > 0) {
-      // warp w works on task w % tasks
-      const int k = warp % tasks, share = warp / tasks, shares = (NW - 1 - k) / tasks + 1;
-      const int i = i0 + k / tasks_a_row;
-      const bool is_target = target_task && k % tasks_a_row == 0;
-      Stat st = {-INFINITY, 0.f, 0x7FFFFFFF};
-      const int64_t t = t0 + i;
-      if (is_target) {
-        const void* row = at(p.target, t * p.target_stride, tf32);
-        st = tf32 ? scan_row<true>(row, lo, hi, share * 32 + lane, shares * 32, rate.hi)
-                  : scan_row<false>(row, lo, hi, share * 32 + lane, shares * 32, rate.hi);
-      } else if (i + 1 < n) {
-        const int64_t d = p.draft_row ? p.draft_row[t + 1] : t - b;
-        if (d >= 0 && d < p.draft_rows) {
-          const void* row = at(p.draft, d * p.draft_stride, df32);
-          st = df32 ? scan_row<true>(row, lo, hi, share * 32 + lane, shares * 32, rate.hi)
-                    : scan_row<false>(row, lo, hi, share * 32 + lane, shares * 32, rate.hi);
+      // warp w works on task w % tasks (where there are more tasks than warps, on every NW-th)
+      for (int k = tasks < NW ? warp % tasks : warp; k < tasks; k += NW) {
+        const int share = tasks < NW ? warp / tasks : 0, shares = tasks < NW ? (NW - 1 - k) / tasks + 1 : 1;
+        const int i = i0 + k / tasks_a_row;
+        const int64_t t = t0 + i;
+        const bool is_target = target_task && k % tasks_a_row == 0;
+        int64_t d = 0;
+        if (!is_target) {
+          d = i + 1 < n ? (p.draft_row ? p.draft_row[t + 1] : t - b) : -1;
+          if (d >= p.draft_rows) d = -1;
+        }
+        const bool f32 = is_target ? tf32 : df32;
+        const void* row = is_target ? at(p.target, t * p.target_stride, tf32) : at(p.draft, d * p.draft_stride, df32);
+        Stat st = {-INFINITY, 0.f, NOWHERE};
+        if (d >= 0) {
+          if (greedy)
+            st = f32 ? scan_row<NT, DEPTH, true, true>(row, lo, hi, share, shares, rate.hi, ring)
+                     : scan_row<NT, DEPTH, false, true>(row, lo, hi, share, shares, rate.hi, ring);
+          else
+            st = f32 ? scan_row<NT, DEPTH, true, false>(row, lo, hi, share, shares, rate.hi, ring)
+                     : scan_row<NT, DEPTH, false, false>(row, lo, hi, share, shares, rate.hi, ring);
+        }
+        if (tasks < NW) {
+          if (lane == 0) part[warp] = st;
+        } else if (lane < C) {
+          *cluster.map_shared_rank(&got[par][k][rank], lane) = st;
         }
       }
-      st = warp_merge(st, rate.hi);
-      if (lane == 0) part[warp] = st;
-      __syncthreads();
-      if (tid < tasks) {
-        Stat sum = part[tid];
-        for (int w = tid + tasks; w < NW; w += tasks) merge(sum, part[w], rate.hi);
-        for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&got[par][tid][rank], r) = sum;
+      if (tasks < NW) {
+        __syncthreads();
+        if (tid < tasks) {
+          Stat sum = part[tid];
+          for (int w = tid + tasks; w < NW; w += tasks) merge(sum, part[w], rate.hi);
+          for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&got[par][tid][rank], r) = sum;
+        }
       }
       cluster.sync();
       if (tid < tasks) {
@@ -303,60 +613,64 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Args
       __syncthreads();
       par ^= 1;
     }
+    float l_m = 0.f, l_s = 1.f;
     if (tid < rows) {
       const Stat ts = target_task ? fin[tid * tasks_a_row] : Stat{};
-      const Stat ds = drafted_law && !p.draft_probs ? fin[tid * tasks_a_row + tasks_a_row - 1] : Stat{};
+      const Stat ds = draft_task ? fin[tid * tasks_a_row + tasks_a_row - 1] : Stat{};
+      l_m = ts.m, l_s = ts.s;
       bool ok = false;
-      float l = 0.f;
       if (x >= 0) {
-        const Law law = {nullptr, tf32, p.target_probs != 0, ts.m, ts.s > 0.f ? 1.f / ts.s : 0.f};
-        const float px = law_of(law, zx, rate);
-        l = p.target_probs ? logf(px) : (logit(zx) - ts.m) / temp - logf(ts.s);
         if (greedy) {
           ok = ts.m > (p.target_probs ? 0.f : -INFINITY) && x == ts.idx;
-        } else if (!drafted_law) {
-          ok = ux < px || (ux == 0.f && !p.target_probs && logit(zx) > -INFINITY);
-        } else if (qrow >= 0) {
-          const Law dlaw = {nullptr, df32, p.draft_probs != 0, ds.m, ds.s > 0.f ? 1.f / ds.s : 0.f};
-          ok = p.target_probs || p.draft_probs ? ux * law_of(dlaw, yx, rate) < px
-                                               : keeps(ux, logit(zx), ts, logit(yx), ds, rate);
-        }
-        if (ok && rank == 0) {
-          // (written whether or not an earlier one falls: what follows the last token is overwritten below)
-          out[i0 + tid] = x;
-          if (logp) logp[i0 + tid] = l;
+        } else if (draft_task && !p.target_probs) {
+          ok = qrow >= 0 && keeps(ux, logit(zx, tf32), ts, logit(yx, df32), ds, rate);
+        } else {
+          const Law law = {nullptr, tf32, p.target_probs != 0, ts.m, ts.s > 0.f ? 1.f / ts.s : 0.f};
+          const float px = law_of(law, zx, rate);
+          if (!drafted_law) {
+            ok = ux < px || (ux == 0.f && !p.target_probs && logit(zx, tf32) > -INFINITY);
+          } else if (qrow >= 0) {
+            const Law dlaw = {nullptr, df32, p.draft_probs != 0, ds.m, ds.s > 0.f ? 1.f / ds.s : 0.f};
+            ok = ux * law_of(dlaw, yx, rate) < px;
+          }
         }
       }
       stands[tid] = ok;
     }
     __syncthreads();
-    for (int j = 0; j < rows; ++j) {
-      if (stands[j]) continue;
-      last = i0 + j;
+    int stay = 0;
+    while (stay < rows && stands[stay]) ++stay;
+    if (stay < rows) {
+      last = i0 + stay;
       const int64_t t = t0 + last;
       all = last == n - 1;
-      const Stat ts = target_task ? fin[j * tasks_a_row] : Stat{};
-      best_idx = ts.m > (p.target_probs ? 0.f : -INFINITY) ? ts.idx : 0x7FFFFFFF;
+      const Stat ts = target_task ? fin[stay * tasks_a_row] : Stat{};
+      if (greedy && ts.m > (p.target_probs ? 0.f : -INFINITY)) best = Best{0.f, ts.idx, ts.m};
       lp = Law{at(p.target, t * p.target_stride, tf32), tf32, p.target_probs != 0, ts.m, ts.s > 0.f ? 1.f / ts.s : 0.f};
       if (drafted_law && !all) {
         const int64_t d = p.draft_row ? p.draft_row[t + 1] : t - b;
         if (d >= 0 && d < p.draft_rows) {
-          const Stat ds = p.draft_probs ? Stat{} : fin[j * tasks_a_row + tasks_a_row - 1];
+          const Stat ds = draft_task ? fin[stay * tasks_a_row + tasks_a_row - 1] : Stat{};
           lq = Law{at(p.draft, d * p.draft_stride, df32), df32, p.draft_probs != 0, ds.m, ds.s > 0.f ? 1.f / ds.s : 0.f};
-          excluded = true;
+          residual = true;
         }
       }
-      break;
+    }
+    if (rank == 0 && tid < stay) {
+      out[i0 + tid] = x;
+      if (logp) logp[i0 + tid] = p.target_probs ? logf(prob(zx)) : (logit(zx, tf32) - l_m) / temp - logf(l_s);
     }
     __syncthreads();  // fin and stands are free again
   }
 
-  Best best = {0.f, best_idx, 0.f};
   if (!greedy) {
     const float* noise = p.noise + (int64_t)b * p.noise_stride;
     const int skip = !all && p.draft == nullptr ? p.tokens[t0 + last + 1] : -1;
-    for (int round = excluded || skip >= 0 ? 0 : 1; round < 2; ++round) {
-      Best mine = race(lp, lq, excluded && round == 0, round == 0 ? skip : -1, noise, lo, hi, rate);
+    for (int round = residual || skip >= 0 ? 0 : 1; round < 2; ++round) {
+      const bool minus = residual && round == 0;
+      const int not_this = round == 0 ? skip : -1;
+      const Runner run = {lp, lq, minus, not_this, noise, lo, hi, rate, ring, &top_key};
+      Best mine = tf32 ? race<NT, U * DEPTH * 512, true>(run) : race<NT, U * DEPTH * 512, false>(run);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const Best y = {__shfl_xor_sync(0xffffffffu, mine.key, o), __shfl_xor_sync(0xffffffffu, mine.idx, o),
@@ -365,9 +679,10 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Args
       }
       if (lane == 0) bpart[warp] = mine;
       __syncthreads();
-      if (tid == 0) {
+      if (tid < C) {
+        mine = bpart[0];
         for (int w = 1; w < NW; ++w) take(mine, bpart[w]);
-        for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&bgot[round][rank], r) = mine;
+        *cluster.map_shared_rank(&bgot[round][rank], tid) = mine;
       }
       cluster.sync();
       best = bgot[round][0];
@@ -376,30 +691,25 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Args
     }
   }
   if (rank != 0) return;
-  const bool found = best.idx != 0x7FFFFFFF;
+  const bool found = best.idx != NOWHERE;
   for (int i = last + tid; i < p.max_q_len; i += NT) {
-    int token = -1;
-    float l = 0.f;
-    if (i == last && found) {
-      token = best.idx;
-      const float x = element(lp.row, token, tf32);
-      l = p.target_probs ? logf(prob(x)) : (logit(x) - lp.m) / temp - logf(1.f / lp.inv);
-    }
-    out[i] = token;
-    if (logp) logp[i] = l;
+    const bool here = i == last && found;
+    out[i] = here ? best.idx : -1;
+    if (logp)
+      logp[i] = !here ? 0.f : p.target_probs ? logf(prob(best.x)) : (logit(best.x, tf32) - lp.m) / temp + logf(lp.inv);
   }
   if (tid == 0) p.n_out[b] = last + (found ? 1 : 0);
 }
 
-}  // namespace loop
-
-cudaError_t launch_draft_verify(const dsv4_draft_verify_params& p, cudaStream_t s) {
-  if (p.B == 0) return cudaSuccess;
-  loop::Args a = {p, 1};
+template <int NT, int DEPTH, int CTAS>
+cudaError_t launch(const Args& a, int cluster, cudaStream_t s) {
+  constexpr int RING = NT * U * DEPTH * 16;
+  const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(verify_kernel<NT, DEPTH, CTAS>), RING);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int cluster = 1;
-  cfg.gridDim = dim3((unsigned)p.B * cluster);
-  cfg.blockDim = dim3(loop::NT);
+  cfg.gridDim = dim3((unsigned)a.p.B * cluster);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = RING;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -409,7 +719,22 @@ cudaError_t launch_draft_verify(const dsv4_draft_verify_params& p, cudaStream_t 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return count_launch(cudaLaunchKernelEx(&cfg, loop::verify_kernel, a));
+  return count_launch(cudaLaunchKernelEx(&cfg, verify_kernel<NT, DEPTH, CTAS>, a));
+}
+
+}  // namespace loop
+
+cudaError_t launch_draft_verify(const dsv4_draft_verify_params& p, cudaStream_t s) {
+  if (p.B == 0) return cudaSuccess;
+  // As many CTAs a sequence as two an SM can hold at once (2 sequences of 32000 logits: 8 CTAs 11.8 us, 1 25; 64 of 131072
+  // with probabilities of the draft: 4 CTAs 40 us, 2 41, 8 51; 256 of 131072: 1 CTA 130 us, 2 145).
+  int cluster = 1;
+  while (cluster < loop::MAX_CLUSTER && (int64_t)p.B * cluster * 2 <= 2 * num_sms()) cluster *= 2;
+  // Rows in one group share the exchange between the CTAs and their waits (400 sequences of 8000 logits, four rows each:
+  // 8 rows a group 37 us, 1 51), but all of them are read (256 of 131072, five rows each: 164 us, one 130): rows of
+  // 131072 logits a CTA in all.
+  const int slice = (p.vocab + cluster - 1) / cluster, rows = 131072 / slice;
+  return loop::launch<256, 6, 2>({p, rows < 1 ? 1 : rows > loop::MAX_ROWS ? loop::MAX_ROWS : rows}, cluster, s);
 }
 
 cudaError_t read_flags_loop_verify(uint32_t* f) {
