@@ -5,6 +5,15 @@
 // softmax (in 32-bit floats), the CTAs exchange these through distributed shared memory, and every CTA
 // finds by itself how far the drafted tokens stand.  The row where they end is read once more, from the L2 cache,
 // for the race argmax r(x) / noise(x), whose winners are exchanged the same way.  Rows behind that group are not read.
+//
+// Two CTAs of 256 threads an SM with six groups of copies on their way each (512 threads, four groups: 256 x 5 rows of
+// 131072 logits 158 us for 126, 64 x 4 rows 33 for 35.5; three CTAs with four groups 159 and 42).  Large batches are bound
+// by HBM: 256 x 5 rows of 131072 bf16 logits of both models 126 us, of which the 700 MB that the drafts that stand make it
+// read take 103 at the copy rate.  Smaller ones by a chain of phases, each waiting for the one before: launch and first
+// loads (2 us), rows, exchange and decision (3 us), race, exchange; 2 x 4 rows of 32000 fp32 logits 10.6 us, 64 x 4 rows of
+// 131072 bf16 logits with fp32 probabilities of the draft 35.5 us (104 MB), 200 x up to 3 rows of 100003 42 us.
+// Code that runs once a sequence waits for its instructions to be fetched: parts that were inlined twice are loops
+// (256 x 5 rows 131 -> 126 us, 400 x 4 rows of 8000 37 -> 30).
 #include <cooperative_groups.h>
 
 #include "loop_common.cuh"
@@ -151,29 +160,31 @@ __device__ __forceinline__ float weights(const Vec<F32> (&v)[N], float c, float 
 template <bool F32, bool GREEDY, int N, typename I>
 __device__ __forceinline__ void add(Run& st, const Vec<F32> (&v)[N], float c, I index) {
   constexpr int E = Vec<F32>::E;
-  float sum = 0.f;
-  bool renew;
-  if (GREEDY || st.m == -INFINITY) {
-    renew = __any_sync(0xffffffffu, top_of<F32, N>(v) > st.m);
-  } else {
-    sum = weights<F32, N>(v, c, st.r);
-    renew = __any_sync(0xffffffffu, sum > FAR);
-  }
-  if (renew) {
-    const float top = top_of<F32, N>(v), m = warp_top(fmaxf(top, st.m)), r = fmaxf(rintf(m * c), LEAST);
-    st.s *= tc::ex2_approx(st.r - r);
-    st.m = m, st.r = r;
-    if (GREEDY) {
-      st.idx = NOWHERE;
-      if (top == m) {
+  bool look = GREEDY || st.m == -INFINITY;
+  while (true) {  // (a loop, so that each part of the code is there once: what runs once a row waits for its instructions)
+    if (look) {
+      const float top = top_of<F32, N>(v);
+      if (__any_sync(0xffffffffu, top > st.m)) {
+        const float m = warp_top(fmaxf(top, st.m)), r = fmaxf(rintf(m * c), LEAST);
+        st.s *= tc::ex2_approx(st.r - r);
+        st.m = m, st.r = r;
+        if (GREEDY) {
+          st.idx = NOWHERE;
+          if (top == m) {
 #pragma unroll
-        for (int i = N * E - 1; i >= 0; --i)
-          if (v[i / E].get(i % E) == m) st.idx = index(i);
+            for (int i = N * E - 1; i >= 0; --i)
+              if (v[i / E].get(i % E) == m) st.idx = index(i);
+          }
+        }
       }
     }
+    const float sum = weights<F32, N>(v, c, st.r);
+    if (look || !__any_sync(0xffffffffu, sum > FAR)) {
+      st.s += sum;
+      return;
+    }
+    look = true;
   }
-  if (GREEDY || renew) sum = weights<F32, N>(v, c, st.r);
-  st.s += sum;
 }
 
 // The careful form: one element, as it counts; s goes with m itself, the maximum.
@@ -311,84 +322,46 @@ __device__ __forceinline__ void take(Best& a, const Best& b) {
   if (b.key > a.key || (b.key == a.key && b.idx < a.idx)) a = b;
 }
 
-// A law's quick weight: 2^(x c - ref) or x itself, times `scale`, is the probability but for 2^-10 of it.
-struct Quick {
-  bool probs, holds;
-  float ref, scale;
-  __device__ __forceinline__ explicit Quick(const Law& l, float c) {
-    probs = l.probs;
-    holds = l.probs || l.m == -INFINITY || fabsf(l.m * c) < -LEAST;
-    ref = l.m == -INFINITY ? 0.f : rintf(l.m * c);
-    scale = l.probs ? 1.f : l.m == -INFINITY ? 0.f : l.inv * tc::ex2_approx(-fmaf(l.m, c, -ref));
-  }
-  __device__ __forceinline__ float operator()(float x, float c) const {
-    return probs ? x : tc::ex2_approx(fmaf(x, c, -ref));
-  }
-};
-
 // The race over elements [lo, hi): r(x) / noise(x), r = p, p without `skip`, or (minus) max(p - q, 0).  Of most elements
 // only a quick upper bound of p is computed: it has to pass the best key of the CTA so far, and the draft's row is
 // read for those that do.  `top` (shared, 0 at first) holds that key's bits.
-struct Runner {
-  Law p, q;
-  bool minus;
-  int skip;
-  const float* noise;
-  int lo, hi;
-  Rate r;
-  uint4* ring;
-  int* top;
-};
-
 template <int NT, int RING, bool F32>
-__device__ __noinline__ Best race(const Runner& a) {
-  constexpr float MORE = 1.f + 0x1p-10f, LESS = 1.f - 0x1p-10f;
+__device__ __forceinline__ Best race(const Law& p, const Law& q, bool minus, int skip, const float* noise, int lo, int hi,
+                                     const Rate& r, uint4* ring, int* top) {
   // A warp takes chunks of 8 elements, H of them a lane, as many vectors as four groups and more of them leave room for.
   constexpr int H = F32 ? 1 : 2, E = 8 * H, STEP = 32 * E, SIZE = F32 ? 4 : 2, GROUP = STEP * (SIZE + 4);
   constexpr int GROUPS = RING / GROUP, STRIDE = NT / 32 * STEP;
   Best best = {0.f, NOWHERE, 0.f};
-  if (!a.p.probs && a.p.m == -INFINITY) return best;
-  const float c = a.r.hi;
-  const Quick wp(a.p, c);
-  const bool quick = wp.holds && (!a.minus || Quick(a.q, c).holds);  // (else every element is a candidate)
-  const float unit = 1.f / (wp.scale * MORE);
+  if (!p.probs && p.m == -INFINITY) return best;
+  // An element's quick weight is x itself, or 2^(x c - ref); times scale it is its probability but for 2^-11 of it.
+  const float c = r.hi, ref = rintf(p.m * c);
+  const bool quick = p.probs || fabsf(p.m * c) < -LEAST;  // (else every element is a candidate)
+  const float unit = (1.f - 0x1p-10f) / (p.probs ? 1.f : p.inv * tc::ex2_approx(-fmaf(p.m, c, -ref)));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float* noise = a.noise;
-  int* top = a.top;
 
-  const auto key_of = [&](int i, float x, float e) {
-    float w = law_of(a.p, x, a.r);
-    if (a.minus) w -= law_of(a.q, element(a.q.row, i, a.q.f32), a.r);
-    return i == a.skip ? 0.f : __fdividef(w, e);
-  };
   const auto enter = [&](int i, float x, float e) {
-    const float key = key_of(i, x, e);
+    float w = law_of(p, x, r);
+    if (minus) w -= law_of(q, element(q.row, i, q.f32), r);
+    const float key = i == skip ? 0.f : __fdividef(w, e);
     if (key > best.key || (key == best.key && key > 0.f && i < best.idx)) best = Best{key, i, x};
-  };
-  const auto share = [&](float key) {
-    const int t = __reduce_max_sync(0xffffffffu, __float_as_int(key));
-    if (lane == 0) atomicMax(top, t);
-    __syncwarp();
   };
 
   // the part whose vectors are whole, in chunks of 8 elements
-  const uintptr_t begin = reinterpret_cast<uintptr_t>(at(a.p.row, a.lo, F32));
-  const int from = min(a.hi, a.lo + (int)((16 - (begin & 15)) & 15) / SIZE), chunks = (a.hi - from) / 8;
-  const uint8_t* prow = reinterpret_cast<const uint8_t*>(at(a.p.row, from, F32));
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(at(p.row, lo, F32));
+  const int from = min(hi, lo + (int)((16 - (begin & 15)) & 15) / SIZE), count = (hi - from) / 8 * 8;
+  const uint8_t* prow = reinterpret_cast<const uint8_t*>(at(p.row, from, F32)) + lane * 16;
   const float* nrow = noise + from;
   const bool whole = (reinterpret_cast<uintptr_t>(nrow) & 15) == 0;
-  uint8_t* mine = reinterpret_cast<uint8_t*>(a.ring) + warp * RING;
-  const int count = chunks * 8;
+  uint8_t* mine = reinterpret_cast<uint8_t*>(ring) + warp * RING;
   // (elements as they lie in memory: the target's, then the noise's, which is copied word by word where its row begins
   // off the target's boundaries)
   const auto fetch = [&](int i, int group) {
     uint8_t* to = mine + group * GROUP;
-    if (i < count) {
-      const int n = min(STEP, count - i);
+    const int n = min(STEP, count - i);
+    if (n > 0) {
 #pragma unroll
       for (int u = 0; u < STEP * SIZE / 512; ++u)
-        if ((u * 32 + lane) * (16 / SIZE) < n)
-          tc::cp_async16(to + u * 512 + lane * 16, prow + (int64_t)i * SIZE + u * 512 + lane * 16, 16);
+        if ((u * 32 + lane) * (16 / SIZE) < n) tc::cp_async16(to + u * 512 + lane * 16, prow + (int64_t)i * SIZE + u * 512, 16);
       to += STEP * SIZE;
       if (whole) {
 #pragma unroll
@@ -402,28 +375,27 @@ __device__ __noinline__ Best race(const Runner& a) {
     }
     tc::cp_async_commit();
   };
-  const uint64_t c2 = pack(c, c), ref2 = pack(-wp.ref, -wp.ref);
-  int ahead = warp * STEP, to = 0, use = 0;
-#pragma unroll 1
-  for (; to < GROUPS - 1; ++to, ahead += STRIDE) fetch(ahead, to);
-  bool begun = false;
-  for (int i0 = warp * STEP; i0 < count; i0 += STRIDE, ahead += STRIDE) {
+  const uint64_t c2 = pack(c, c), ref2 = pack(-ref, -ref);
+  int to = 0, use = 0;
+  for (int i0 = warp * STEP - (GROUPS - 1) * STRIDE; i0 < count; i0 += STRIDE) {
     __syncwarp();  // (the group that is filled now has been read by every lane)
-    fetch(ahead, to);
+    fetch(i0 + (GROUPS - 1) * STRIDE, to);
     to = to == GROUPS - 1 ? 0 : to + 1;
+    if (i0 < 0) continue;  // (the first groups)
     tc::cp_async_wait<GROUPS - 1>();
     __syncwarp();
     const uint8_t* group = mine + use * GROUP;
     use = use == GROUPS - 1 ? 0 : use + 1;
-    // (chunk h of the lane: elements i0 + 256 h + 8 lane on; one behind the end holds what it held before)
+    // (chunk h of the lane: elements i0 + 256 h + 8 lane on, there if h * 256 < n)
     const uint8_t* gx = group + lane * 8 * SIZE;
     const float* ge = reinterpret_cast<const float*>(group + STEP * SIZE) + lane * 8;
-    const int n = count - i0 - lane * 8;  // the lane's chunk h is there if h * 256 < n
-    const auto bounds = [&](float bar) {  // elements whose bound passes
-      const uint64_t bar2 = pack(-bar * unit, -bar * unit);
-      uint32_t good = 0;
-      float most = 0.f;
+    const int n = count - i0 - lane * 8;
+    uint32_t done = 0;  // candidates that have been looked at
+    while (true) {
+      const float bar = __int_as_float(*(volatile int*)top) * unit;
+      const uint64_t bar2 = pack(-bar, -bar);
       uint64_t over[E / 2];
+      float most = 0.f;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         Vec<F32> x[SIZE / 2];
@@ -434,10 +406,9 @@ __device__ __noinline__ Best race(const Runner& a) {
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
           constexpr int PER = 16 / SIZE;
-          const uint64_t z = pack(x[k / PER].get(k % PER), x[k / PER].get(k % PER + 1));
-          uint64_t w = z;
-          if (!wp.probs) {
-            const uint64_t y = fma2(z, c2, ref2);
+          uint64_t w = pack(x[k / PER].get(k % PER), x[k / PER].get(k % PER + 1));
+          if (!p.probs) {
+            const uint64_t y = fma2(w, c2, ref2);
             w = pack(tc::ex2_approx(low(y)), tc::ex2_approx(high(y)));
           }
           w = fma2(e[k / 2], bar2, w);
@@ -445,49 +416,33 @@ __device__ __noinline__ Best race(const Runner& a) {
           if (h * 256 < n) most = fmaxf(most, fmaxf(low(w), high(w)));
         }
       }
-      if (__any_sync(0xffffffffu, most > 0.f || !quick)) {
+      if (!__any_sync(0xffffffffu, most > 0.f || !quick)) break;
+      // each lane looks at the candidate that lies farthest over the bar, which may raise it for the others
+      int pick = -1;
+      most = 0.f;
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          const float w = k & 1 ? high(over[k / 2]) : low(over[k / 2]);
-          if (k / 8 * 256 < n && (w > 0.f || !quick)) good |= 1u << k;
-        }
+      for (int k = 0; k < E; ++k) {
+        const float w = quick ? (k & 1 ? high(over[k / 2]) : low(over[k / 2])) : 1.f;
+        if (w > most && k / 8 * 256 < n && !(done >> k & 1)) most = w, pick = k;
       }
-      return good;
-    };
-    uint32_t good = bounds(__int_as_float(*(volatile int*)top));
-    if (!__any_sync(0xffffffffu, good)) continue;
-    const auto index = [&](int k) { return from + i0 + k / 8 * 256 + lane * 8 + k % 8; };
-    const auto xs = [&](int k) { return element<F32>(gx, k / 8 * 256 + k % 8); };
-    const auto es = [&](int k) { return ge[k / 8 * 256 + k % 8]; };
-    if (!begun && quick) {  // the first keys, or lower bounds of them, make a bar
-      begun = true;
-      const Quick wq(a.minus ? a.q : a.p, c);
-      float least = 0.f, y[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = a.minus && (good >> k & 1) ? element(a.q.row, index(k), a.q.f32) : 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float w = wp(xs(k), c) * (wp.scale * LESS) - (a.minus ? fmaxf(wq(y[k], c), 0.f) * (wq.scale * MORE) : 0.f);
-        if ((good >> k & 1) && index(k) != a.skip) least = fmaxf(least, __fdividef(w, es(k)));
+      if (!__any_sync(0xffffffffu, pick >= 0)) break;
+      if (pick >= 0) {
+        done |= 1u << pick;
+        const int k = pick / 8 * 256 + pick % 8;
+        enter(from + i0 + lane * 8 + k, element<F32>(gx, k), ge[k]);
       }
-      share(least < MAX_F32 ? least * LESS : 0.f);
-      good = bounds(__int_as_float(*(volatile int*)top));
+      const int t = __reduce_max_sync(0xffffffffu, __float_as_int(best.key));
+      if (lane == 0) atomicMax(top, t);
+      __syncwarp();
     }
-    while (good) {
-      const int k = __ffs(good) - 1;
-      good &= good - 1;
-      enter(index(k), xs(k), es(k));
-    }
-    __syncwarp();
-    share(best.key);
   }
   tc::cp_async_wait<0>();
   __syncwarp();
   // the elements before and behind the chunks, fewer than 8 each
-  const int front = from - a.lo, rest = from + count, edge = front + a.hi - rest;
+  const int front = from - lo, rest = from + count, edge = front + hi - rest;
   if ((int)threadIdx.x < edge) {
-    const int i = (int)threadIdx.x < front ? a.lo + (int)threadIdx.x : rest + (int)threadIdx.x - front;
-    enter(i, element<F32>(a.p.row, i), noise[i]);
+    const int i = (int)threadIdx.x < front ? lo + (int)threadIdx.x : rest + (int)threadIdx.x - front;
+    enter(i, element<F32>(p.row, i), noise[i]);
   }
   return best;
 }
@@ -497,7 +452,7 @@ struct Args {
   int rows;  // of a group
 };
 
-template <int NT, int DEPTH, int CTAS>
+template <int NT, int DEPTH, int CTAS, bool F32>
 __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant__ Args a) {
   constexpr int NW = NT / 32;
   const dsv4_draft_verify_params& p = a.p;
@@ -537,7 +492,8 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
   Rate rate;
   rate.hi = LOG2E_HI / temp;
   rate.lo = rate.hi < 1e30f ? (fmaf(-rate.hi, temp, LOG2E_HI) + LOG2E_LO) / temp : 0.f;
-  const bool tf32 = p.target_dtype == DSV4_F32, df32 = p.draft_dtype == DSV4_F32;
+  constexpr bool tf32 = F32;
+  const bool df32 = p.draft_dtype == DSV4_F32;
   const bool drafted_law = p.draft != nullptr && !greedy;
   const int per = ((p.vocab + C - 1) / C + 7) & ~7, lo = min(p.vocab, rank * per), hi = min(p.vocab, lo + per);
   const bool target_task = !p.target_probs || greedy, draft_task = drafted_law && !p.draft_probs;
@@ -669,8 +625,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
     for (int round = residual || skip >= 0 ? 0 : 1; round < 2; ++round) {
       const bool minus = residual && round == 0;
       const int not_this = round == 0 ? skip : -1;
-      const Runner run = {lp, lq, minus, not_this, noise, lo, hi, rate, ring, &top_key};
-      Best mine = tf32 ? race<NT, U * DEPTH * 512, true>(run) : race<NT, U * DEPTH * 512, false>(run);
+      Best mine = race<NT, U * DEPTH * 512, F32>(lp, lq, minus, not_this, noise, lo, hi, rate, ring, &top_key);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const Best y = {__shfl_xor_sync(0xffffffffu, mine.key, o), __shfl_xor_sync(0xffffffffu, mine.idx, o),
@@ -701,10 +656,10 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
   if (tid == 0) p.n_out[b] = last + (found ? 1 : 0);
 }
 
-template <int NT, int DEPTH, int CTAS>
+template <int NT, int DEPTH, int CTAS, bool F32>
 cudaError_t launch(const Args& a, int cluster, cudaStream_t s) {
   constexpr int RING = NT * U * DEPTH * 16;
-  const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(verify_kernel<NT, DEPTH, CTAS>), RING);
+  const cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(verify_kernel<NT, DEPTH, CTAS, F32>), RING);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.p.B * cluster);
@@ -719,22 +674,23 @@ cudaError_t launch(const Args& a, int cluster, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return count_launch(cudaLaunchKernelEx(&cfg, verify_kernel<NT, DEPTH, CTAS>, a));
+  return count_launch(cudaLaunchKernelEx(&cfg, verify_kernel<NT, DEPTH, CTAS, F32>, a));
 }
 
 }  // namespace loop
 
 cudaError_t launch_draft_verify(const dsv4_draft_verify_params& p, cudaStream_t s) {
   if (p.B == 0) return cudaSuccess;
-  // As many CTAs a sequence as two an SM can hold at once (2 sequences of 32000 logits: 8 CTAs 11.8 us, 1 25; 64 of 131072
-  // with probabilities of the draft: 4 CTAs 40 us, 2 41, 8 51; 256 of 131072: 1 CTA 130 us, 2 145).
+  // As many CTAs a sequence as the SMs can hold at once, two each (2 sequences of 32000 logits: 8 CTAs 10.6 us, 1 26; 64 of
+  // 131072 with probabilities of the draft: 4 CTAs 35.5 us, 2 37, 8 43; 200 of 131072: 1 CTA 98 us, 2 109).
   int cluster = 1;
   while (cluster < loop::MAX_CLUSTER && (int64_t)p.B * cluster * 2 <= 2 * num_sms()) cluster *= 2;
   // Rows in one group share the exchange between the CTAs and their waits (400 sequences of 8000 logits, four rows each:
-  // 8 rows a group 37 us, 1 51), but all of them are read (256 of 131072, five rows each: 164 us, one 130): rows of
-  // 131072 logits a CTA in all.
+  // 8 rows a group 30 us, 1 45), but all of them are read (256 of 131072, five rows each: 8 rows a group 153 us, 1 126):
+  // rows of 131072 logits a CTA in all.
   const int slice = (p.vocab + cluster - 1) / cluster, rows = 131072 / slice;
-  return loop::launch<256, 6, 2>({p, rows < 1 ? 1 : rows > loop::MAX_ROWS ? loop::MAX_ROWS : rows}, cluster, s);
+  const loop::Args a = {p, rows < 1 ? 1 : rows > loop::MAX_ROWS ? loop::MAX_ROWS : rows};
+  return p.target_dtype == DSV4_F32 ? loop::launch<256, 6, 2, true>(a, cluster, s) : loop::launch<256, 6, 2, false>(a, cluster, s);
 }
 
 cudaError_t read_flags_loop_verify(uint32_t* f) {
