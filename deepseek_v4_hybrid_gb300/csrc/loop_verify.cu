@@ -682,9 +682,10 @@ cudaError_t launch(const Args& a, int cluster, cudaStream_t s) {
 cudaError_t launch_draft_verify(const dsv4_draft_verify_params& p, cudaStream_t s) {
   if (p.B == 0) return cudaSuccess;
   // As many CTAs a sequence as the SMs can hold at once, two each (2 sequences of 32000 logits: 8 CTAs 10.6 us, 1 26; 64 of
-  // 131072 with probabilities of the draft: 4 CTAs 35.5 us, 2 37, 8 43; 200 of 131072: 1 CTA 98 us, 2 109).
+  // 131072 with probabilities of the draft: 4 CTAs 35.5 us, 2 37, 8 43; 200 of 131072: 1 CTA 98 us, 2 109),
+  // of 4000 logits a row at least (22 sequences of 4000: 1 CTA 9.4 us, 8 13.5; of 16000: 4 CTAs 11.6, 8 12.0, 1 16.3).
   int cluster = 1;
-  while (cluster < loop::MAX_CLUSTER && (int64_t)p.B * cluster * 2 <= 2 * num_sms()) cluster *= 2;
+  while (cluster < loop::MAX_CLUSTER && (int64_t)p.B * cluster * 2 <= 2 * num_sms() && p.vocab >= 8000 * cluster) cluster *= 2;
   // Rows in one group share the exchange between the CTAs and their waits (400 sequences of 8000 logits, four rows each:
   // 8 rows a group 30 us, 1 45), but all of them are read (256 of 131072, five rows each: 8 rows a group 153 us, 1 126):
   // rows of 131072 logits a CTA in all.
