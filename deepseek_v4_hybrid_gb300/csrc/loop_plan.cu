@@ -5,7 +5,8 @@
 // cluster, whose items find their request by a binary search.  Two cluster barriers: pages given back lie on the stack
 // before pages are taken from it, and tables are complete before slots are read from them.
 // Bound by latency: a launch, the loads of a request's numbers, the sums, page, table and slot in turn.  64 requests with
-// four tokens each 6.2 us; 1000 requests in three caches 15 us; 65k prompt tokens 11 us (1 MB written).
+// four tokens each 5.4 us; 1000 requests in three caches 13.3 us (15.3 with the caches one after the other); 65k prompt
+// tokens 11.3 us (1 MB written).
 #include <cooperative_groups.h>
 
 #include "loop_common.cuh"
@@ -231,32 +232,45 @@ __global__ void __launch_bounds__(1024) plan_kernel(const __grid_constant__ Args
   }
   __syncthreads();
 
-  // given back
-  uint32_t given = 0;
+  // given back (the loads of all caches side by side, here and below)
+  uint32_t gives = 0, takes = 0;  // of the longest list
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const dsv4_plan_cache& k = p.caches[g];
-    const uint32_t* first_of = give0 + g * S;
-    given |= total[1 + G + g];
-    for (uint32_t j = me; j < total[1 + G + g]; j += all_threads) {
-      const int b = owner(first_of, B, j);
-      const int i = (int)(j - first_of[b]), front = (int)fronts[g * S + b];
+  for (int g = 0; g < G; ++g) gives = max(gives, total[1 + G + g]), takes = max(takes, run_total[1 + g]);
+  for (uint32_t j = me; j < gives; j += all_threads) {
+    int page[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (j >= total[1 + G + g]) continue;
+      const dsv4_plan_cache& k = p.caches[g];
+      const uint32_t* first_of = give0 + g * S;
+      const int b = owner(first_of, B, j), i = (int)(j - first_of[b]), front = (int)fronts[g * S + b];
       const int entry = i < front ? k.first[b] + i : k.held[b] - (int)(first_of[b + 1] - first_of[b]) + i;
-      if (count[g] + (uint64_t)j < (uint64_t)k.num_pages)
-        k.free_pages[count[g] + j] = k.block_table[(int64_t)b * k.max_pages_per_seq + entry];
+      page[g] = k.block_table[(int64_t)b * k.max_pages_per_seq + entry];
     }
-  }
-  if (given) cluster.sync();
-  // taken (what lies on the stack may have been put there by another CTA: read past L1)
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const dsv4_plan_cache& k = p.caches[g];
-    const uint32_t* first_of = take0 + g * S;
-    for (uint32_t j = me; j < run_total[1 + g]; j += all_threads) {
+    for (int g = 0; g < G; ++g)
+      if (j < total[1 + G + g] && count[g] + (uint64_t)j < (uint64_t)p.caches[g].num_pages)
+        p.caches[g].free_pages[count[g] + j] = page[g];
+  }
+  if (gives) cluster.sync();
+  // taken (what lies on the stack may have been put there by another CTA: read past L1)
+  for (uint32_t j = me; j < takes; j += all_threads) {
+    int page[G];
+    int64_t to[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (j >= run_total[1 + g]) continue;
+      const dsv4_plan_cache& k = p.caches[g];
+      page[g] = __ldcg(k.free_pages + (level[g] - 1 - j));
+      const uint32_t* first_of = take0 + g * S;
       const int b = owner(first_of, B, j);
-      const int page = __ldcg(k.free_pages + (level[g] - 1 - j));
-      k.block_table[(int64_t)b * k.max_pages_per_seq + k.held[b] + (j - first_of[b])] = page;
-      bad |= page < 0 || page >= k.num_pages;
+      to[g] = (int64_t)b * k.max_pages_per_seq + k.held[b] + (j - first_of[b]);
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (j >= run_total[1 + g]) continue;
+      p.caches[g].block_table[to[g]] = page[g];
+      bad |= page[g] < 0 || page[g] >= p.caches[g].num_pages;
     }
   }
   if (bad) atomicOr(&g_flags_pl, FLAG_PAGE);
@@ -289,7 +303,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const __grid_constant__ Args
   const uint32_t tokens = token0[B];
   for (uint32_t t = 4 * me; t < T; t += 4 * all_threads) {
     int b = t < tokens ? owner(token0, B, t) : 0;
-    int pos[4], seq[4];
+    int pos[4], seq[4], page[G][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool real = t + i < tokens;
@@ -297,6 +311,14 @@ __global__ void __launch_bounds__(1024) plan_kernel(const __grid_constant__ Args
         while (token0[b + 1] <= t + i) ++b;
       pos[i] = real ? kept[b] + (int)(t + i - token0[b]) : -1;
       seq[i] = real ? b : -1;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const dsv4_plan_cache& k = p.caches[g];
+        const int entry = a.ratio[g].quotient(pos[i] + 1) - 1;  // (of a token that completes it)
+        page[g][i] = -1;
+        if (k.slots && real && (entry + 1) * k.ratio == pos[i] + 1)
+          page[g][i] = __ldcg(k.block_table + (int64_t)b * k.max_pages_per_seq + a.page[g].quotient(entry));
+      }
     }
     const bool four = t + 4 <= T;
     if (four) {
@@ -315,13 +337,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const __grid_constant__ Args
       int64_t slot[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        slot[i] = -1;
-        const int entry = a.ratio[g].quotient(pos[i] + 1) - 1;  // (of a token that completes it)
-        if (pos[i] >= 0 && (entry + 1) * k.ratio == pos[i] + 1) {
-          const int at_page = a.page[g].quotient(entry);
-          const int page = __ldcg(k.block_table + (int64_t)seq[i] * k.max_pages_per_seq + at_page);
-          if (page >= 0 && page < k.num_pages) slot[i] = (int64_t)page * k.page_size + entry - at_page * k.page_size;
-        }
+        const int entry = a.ratio[g].quotient(pos[i] + 1) - 1;
+        const bool good = page[g][i] >= 0 && page[g][i] < k.num_pages;
+        slot[i] = good ? (int64_t)page[g][i] * k.page_size + entry - a.page[g].quotient(entry) * k.page_size : -1;
       }
       if (four) {
         *reinterpret_cast<longlong2*>(k.slots + t) = make_longlong2(slot[0], slot[1]);
@@ -365,9 +383,9 @@ cudaError_t launch_batch_plan(const dsv4_batch_plan_params& p, cudaStream_t s) {
     a.page[g] = loop::Div::by(p.caches[g].page_size);
     a.ratio[g] = loop::Div::by(p.caches[g].ratio);
   }
-  // Eight CTAs whatever the size (64 requests with four tokens each 6.2 us, 6.5 with one CTA; 65k tokens of 300 prompts 11.4
-  // and 45), of more threads where lists are long (4000 requests 20 us with 1024 threads a CTA, 38 with 256; 64 requests 6.9
-  // and 6.2, the barriers of idle warps).
+  // Eight CTAs whatever the size (64 requests with four tokens each 0.3 us less than with one CTA; 65k tokens of 300 prompts
+  // 11 us, 45 with one), of more threads where lists are long (4000 requests 20 us with 1024 threads a CTA, 38 with 256;
+  // 64 requests 0.7 us more, the barriers of idle warps).
   const int cluster = 8, threads = p.B > 2048 || p.T > 32768 ? 1024 : p.B > 512 || p.T > 16384 ? 512 : 256;
   switch (p.num_caches) {
     case 1: return launch_plan<1>(a, cluster, threads, s);
