@@ -22,8 +22,10 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # (the handle itself: making a stream object of it costs more than a kernel's launch, 2.8 us of a call's 5.9)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def dsv4_kv_insert(kv_new, kv_dtype, slot_mapping, cache, cache_dtype, page_size, positions=None, cos_sin=None,
