@@ -453,7 +453,8 @@ def draft_verify_params(target, tokens, q_start, max_q_len, out_tokens, n_out, d
     if draft is not None:
         p.draft_dtype = _act(draft, "draft")
         _need_tensor(draft, "draft", (draft.dtype,), (None, V), dev)
-        p.draft, p.draft_rows, p.draft_stride = _ptr(draft), draft.shape[0], _row_stride(draft)
+        # (an empty tensor has no address, which would mean that there is no draft; nothing is read from it)
+        p.draft, p.draft_rows, p.draft_stride = _ptr(draft) or 16, draft.shape[0], _row_stride(draft)
     if noise is not None:
         _need_tensor(noise, "noise", (torch.float32,), (B, V), dev)
         p.noise_stride = _row_stride(noise)

@@ -136,6 +136,13 @@ int dsv4_batch_plan(const dsv4_batch_plan_params* p, dsv4_stream_t stream) {
       CHECK(c.block_table && c.held && c.held_out && aligned(c.block_table, 4) && aligned(c.held, 4) &&
                 aligned(c.held_out, 4) && aligned(c.first, 4) && aligned(c.first_out, 4),
             DSV4_ERR_INVALID);
+    for (int h = 0; h < g; ++h) {  // what a cache writes is its own
+      const dsv4_plan_cache& o = p->caches[h];
+      CHECK(c.free_count_out != o.free_count_out && (c.num_pages == 0 || c.free_pages != o.free_pages) &&
+                (c.slots == nullptr || c.slots != o.slots) && (p->B == 0 || (c.block_table != o.block_table && c.held_out != o.held_out)) &&
+                (c.first_out == nullptr || c.first_out != o.first_out),
+            DSV4_ERR_INVALID);
+    }
   }
   return cuda_status(launch_batch_plan(*p, (cudaStream_t)stream));
 }
@@ -146,7 +153,6 @@ int dsv4_draft_verify(const dsv4_draft_verify_params* p, dsv4_stream_t stream) {
   CHECK(p->vocab >= 1 && p->vocab <= (1 << 24), DSV4_ERR_INVALID);
   CHECK(act_dtype(p->target_dtype) && (p->draft == nullptr || act_dtype(p->draft_dtype)), DSV4_ERR_UNSUPPORTED);
   CHECK((p->target_probs == 0 || p->target_probs == 1) && (p->draft_probs == 0 || p->draft_probs == 1), DSV4_ERR_INVALID);
-  CHECK((p->u == nullptr) == (p->noise == nullptr), DSV4_ERR_INVALID);
   if (p->B == 0) return DSV4_OK;
   CHECK(p->q_start && p->n_out && p->out_tokens && aligned(p->q_start, 4) && aligned(p->n_out, 4) &&
             aligned(p->out_tokens, 4) && aligned(p->logp, 4),
@@ -155,6 +161,7 @@ int dsv4_draft_verify(const dsv4_draft_verify_params* p, dsv4_stream_t stream) {
     CHECK(p->target && p->tokens && aligned(p->target, p->target_dtype == DSV4_F32 ? 4 : 2) && aligned(p->tokens, 4),
           DSV4_ERR_INVALID);
     CHECK(p->target_stride >= p->vocab, DSV4_ERR_INVALID);
+    CHECK((p->u == nullptr) == (p->noise == nullptr), DSV4_ERR_INVALID);
   }
   CHECK(aligned(p->temperature, 4) && aligned(p->u, 4) && aligned(p->noise, 4) && aligned(p->draft_row, 4), DSV4_ERR_INVALID);
   CHECK(p->noise == nullptr || p->noise_stride >= p->vocab, DSV4_ERR_INVALID);

@@ -69,7 +69,8 @@ int dsv4_rope_freqs(const dsv4_rope_freqs_params* p, uint64_t* freqs);
  * the gradient of the forward one: it turns the gradient of y into that of x.
  * A token with a negative position is skipped: its rows of y stay as they are.
  * A second tensor (the keys beside the queries) is turned in the same launch when x2 is given.
- * y is x itself (same strides: in place) or lies apart from x, x2 and y2; rows of one buffer may alternate.
+ * y is x itself (same strides: in place) or lies apart from x, x2 and y2; rows of one buffer may alternate.  Strides of x
+ * may be 0 (a row for several heads or tokens).
  * ------------------------------------------------------------------------------------------- */
 typedef struct dsv4_rope_params {
   uint32_t struct_size;
@@ -128,7 +129,7 @@ int dsv4_rope_table(const dsv4_rope_table_params* p, dsv4_stream_t stream);
  *     ((position + 1) % ratio = 0), else -1.  From q_start[B] to T: -1 in all of them (dsv4_kv_insert skips
  *     such slots, dsv4_rope such positions).  Table entries that are given back stay as they were.
  * Every *_out may be its input (in place) or lie apart; apart from its input, the same call can be made again with
- * the same result.
+ * the same result.  Each cache has tables, counts, stack and slots of its own: two that name the same are refused.
  * A request with ctx, ctx_add or n_new that gives c_b < 0, n_b < 0 or c_b + n_b over 2^30, more pages than
  * max_pages_per_seq, first and held not in 0 <= first <= held <= max_pages_per_seq, or a window that reaches rows before
  * first is flagged (bit 0) and left alone: no token, kv_len 0, ctx_out = ctx, nothing given back or taken.  A
@@ -152,7 +153,7 @@ typedef struct dsv4_plan_cache {
   int32_t* free_pages;         /* [num_pages] */
   const int32_t* free_count;   /* [1] */
   int32_t* free_count_out;
-  int64_t* slots;              /* [T] or NULL */
+  int64_t* slots;              /* [T], 16-byte aligned, or NULL */
 } dsv4_plan_cache;
 
 typedef struct dsv4_batch_plan_params {
@@ -166,8 +167,8 @@ typedef struct dsv4_batch_plan_params {
   int32_t* ctx_out;            /* [B] or NULL */
   int32_t* q_start;            /* [B + 1] */
   int32_t* kv_len;             /* [B] */
-  int32_t* positions;          /* [T] or NULL */
-  int32_t* token_seq;          /* [T] or NULL */
+  int32_t* positions;          /* [T], 16-byte aligned, or NULL */
+  int32_t* token_seq;          /* the same */
   dsv4_plan_cache caches[DSV4_PLAN_MAX_CACHES];
 } dsv4_batch_plan_params;
 

@@ -613,6 +613,99 @@ def test_verify_offsets_past_32_bits(M):
     d.run(M)
 
 
+@pytest.mark.parametrize("shift", [-1e7, -3000.0, 3000.0, 1e7, 1e30])
+@pytest.mark.parametrize("V", [100, 40000])
+def test_verify_logits_far_from_zero(M, shift, V):
+    """Exponents beyond the range of the quick sums, and rows that lie there altogether."""
+    d = Drafts(30, [3] * 6, V, F32, F32, greedy=0.2)
+    d.target += shift
+    d.draft -= shift
+    d.run(M, telling=False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("order", ["up", "down", "late", "jumps"])
+def test_verify_logits_that_rise_along_the_row(M, dtype, order):
+    """The reference of the sums is found at the row's begin and has to follow what comes later."""
+    V = 30000
+    d = Drafts(31, [3] * 6, V, dtype, dtype, greedy=0.2)
+    at = torch.arange(V, device="cuda").float() / V
+    slope = {"up": 150 * at, "down": -150 * at, "late": torch.where(at > 0.999, 300.0, 0.0),
+             "jumps": 60 * torch.floor(at * 7)}[order]
+    d.target.copy_((d.target.float() + slope).to(dtype))
+    d.draft.copy_((d.draft.float() + slope).to(dtype))
+    d.run(M, telling=False)
+
+
+def test_verify_masked_stretches(M):
+    """Most of the vocabulary masked, by -inf and by the lowest value: slices of CTAs and warps with nothing left."""
+    for dtype in (BF16, F32):
+        for mask in (-math.inf, torch.finfo(dtype).min):
+            for keep in (slice(0, 7), slice(29990, 30000), slice(15000, 15003), slice(8, 29992, 4000)):
+                d = Drafts(32, [3] * 4, 30000, dtype, dtype, greedy=0.3)
+                kept = d.target[:, keep].clone()
+                d.target.fill_(mask)
+                d.target[:, keep] = kept
+                d.run(M, telling=False)
+
+
+def test_verify_ties_of_the_race_go_to_the_first(M):
+    """Equal probabilities over equal noise: the lowest index, wherever the others are."""
+    V = 60000
+    d = Drafts(33, [1] * 4, V, F32, None)
+    d.target.fill_(-5.0)
+    d.noise.fill_(1.0)
+    for b, places in enumerate(([5, 6], [59999, 31], [30000, 29999, 15000], [7500, 52499, 8])):
+        d.target[b, places] = 2.0
+    out, count = d.run(M, telling=False)
+    assert list(out[:, 0]) == [5, 31, 15000, 8]
+
+
+def test_verify_empty_inputs(M):
+    """No tokens at all, and drafted tokens whose draft has no row."""
+    d = Drafts(34, [0, 0, 0], 100)
+    p, t = d.device(M)
+    M.dsv4_draft_verify(p)
+    assert torch.all(t["count"] == 0) and torch.all(t["out"] == -1) and M.dsv4_read_device_flags() == 0
+    d = Drafts(35, [2, 2], 100)
+    d.draft = d.draft[:0]
+    out, count = d.run(M, flags=1)
+    assert np.all(count == 1)
+
+
+def test_verify_a_million_logits(M):
+    Drafts(36, [3, 1], 1 << 20, BF16, BF16, stride=5).run(M)
+
+
+def test_two_streams_at_once(M):
+    """Calls of each kind side by side on two streams, each over its own buffers."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ds = [Drafts(40 + i, [4] * 10, 20000) for i in range(2)]
+    qs = [Requests(50 + i, 100, [(16, 1, 0), (16, 4, 0)], 300, 4, 200) for i in range(2)]
+    vs, ps = [d.device(M) for d in ds], [q.device(M) for q in qs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            M.dsv4_draft_verify(vs[i][0], stream=s)
+            M.dsv4_batch_plan(ps[i][0], stream=s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        ds[i].check(vs[i][1])
+        qs[i].check(ps[i][1])
+
+
+def test_rope_reads_broadcast_rows(M):
+    """One row for every head, and one token's rows for every token."""
+    x = torch.randn((5, 1, 64), device="cuda")
+    pos = ints([0, 3, 9, 100, 7])
+    freqs = M.rope_freqs(64)
+    for src in (x.expand(5, 6, 64), x[:1].expand(5, 1, 64)):
+        y = torch.empty(src.shape, device="cuda")
+        M.dsv4_rope(M.rope_params(src, y, pos, freqs))
+        want = L.rope(f64(src), pos.cpu().numpy(), freqs.cpu().numpy())
+        assert np.all(np.abs(f64(y) - want) <= rope_bound(f64(src), want, 0, 64, False, 1.0, F32))
+
+
 def test_verify_many_sequences(M):
     Drafts(28, [2, 1, 3, 0] * 2000, 64).run(M)
 

@@ -119,6 +119,17 @@ def test_plan_refusals(abi, kw):  # noqa: F811
     refused(abi, "dsv4_batch_plan", plan_params(abi, **kw))
 
 
+@pytest.mark.parametrize("shared", ["block_table", "held_out", "free_pages", "free_count_out", "slots", "first_out"])
+def test_plan_refuses_caches_that_share_what_they_write(abi, shared):  # noqa: F811
+    a = dict(page_size=64, ratio=1, window=8, max_pages_per_seq=8, num_pages=100, block_table=0x1000, held=0x2000,
+             held_out=0x2100, first=0x2200, first_out=0x2300, free_pages=0x3000, free_count=0x4000, free_count_out=0x4100,
+             slots=0x5000)
+    b = {k: v + 0x100000 if v >= 0x1000 else v for k, v in a.items()}
+    p = plan_params(abi, cache=a, num_caches=2)
+    p.caches[1] = abi.PlanCache(**dict(b, **{shared: a[shared]}))
+    refused(abi, "dsv4_batch_plan", p)
+
+
 def verify_params(abi, **kw):  # noqa: F811
     f = dict(target=0x10000, target_stride=100, target_dtype=abi.BF16, tokens=0x2000, q_start=0x3000, T=8, B=2, vocab=100,
              max_q_len=4, u=0x4000, noise=0x5000, noise_stride=100, out_tokens=0x6000, n_out=0x7000, draft_dtype=abi.BF16,
