@@ -8,12 +8,14 @@
 //
 // Two CTAs of 256 threads an SM with six groups of copies on their way each (512 threads, four groups: 256 x 5 rows of
 // 131072 logits 158 us for 126, 64 x 4 rows 33 for 35.5; three CTAs with four groups 159 and 42).  Large batches are bound
-// by HBM: 256 x 5 rows of 131072 bf16 logits of both models 126 us, of which the 700 MB that the drafts that stand make it
+// by HBM: 256 x 5 rows of 131072 bf16 logits of both models 130 us, of which the 700 MB that the drafts that stand make it
 // read take 103 at the copy rate.  Smaller ones by a chain of phases, each waiting for the one before: launch and first
 // loads (2 us), rows, exchange and decision (3 us), race, exchange; 2 x 4 rows of 32000 fp32 logits 10.6 us, 64 x 4 rows of
-// 131072 bf16 logits with fp32 probabilities of the draft 35.5 us (104 MB), 200 x up to 3 rows of 100003 42 us.
+// 131072 bf16 logits with fp32 probabilities of the draft 35.8 us (104 MB), 200 x up to 3 rows of 100003 42.6 us.
 // Code that runs once a sequence waits for its instructions to be fetched: parts that were inlined twice are loops
-// (256 x 5 rows 131 -> 126 us, 400 x 4 rows of 8000 37 -> 30).
+// (256 x 5 rows 131 -> 126 us, 400 x 4 rows of 8000 37 -> 30).  Exponents are taken of differences from a logit, in two
+// instructions for one fused product against an integer: 3 % of the largest call, but no range that logits or low
+// temperatures could leave (temperature 1e-6: 44 us for 441).
 #include <cooperative_groups.h>
 
 #include "loop_common.cuh"
@@ -82,6 +84,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -130,28 +137,25 @@ __device__ __forceinline__ float warp_top(float x) { return from_ordered(__reduc
 // all but one of them ahead of the one in use.  Nobody else reads them, so no barrier is needed.
 constexpr int U = 4;  // vectors of a group (scan)
 
-// The running numbers of a warp over a row: the reference m, r = the integer next to m c (or -2^21, when m c is less), and
-// the lane's sum of 2^(z c - r).  With an integer the exponent's argument is one fused product, and a new reference
-// rescales the sums by a power of two: neither rounds anything that the logits' size could make large.
+// The running numbers of a warp over a row: the reference m, one of its logits, and the lane's sum of 2^((z - m) c).
 // Greedy sequences keep m at the maximum and each lane's first index of it; the others change it only when a sum
 // says that a logit lies far above (2^40), which spares the search.
-// Elements are taken as they are.  NaN, +inf and references beyond +-2^21 / c show in the result, and the part is then
-// done again by the careful form.
-constexpr float LEAST = -2097152.f, FAR = 1099511627776.f;
+// Elements are taken as they are: NaN and +inf make the sum NaN, and the part is then done again by the careful form.
+constexpr float FAR = 1099511627776.f;
 
 struct Run {
-  float m, r, s;
+  float m, s;
   int idx;
 };
 
 template <bool F32, int N>
-__device__ __forceinline__ float weights(const Vec<F32> (&v)[N], float c, float r) {
+__device__ __forceinline__ float weights(const Vec<F32> (&v)[N], float c, float m) {
   constexpr int E = Vec<F32>::E;
-  const uint64_t c2 = pack(c, c), r2 = pack(-r, -r);
+  const uint64_t c2 = pack(c, c), m2 = pack(-m, -m);
   uint64_t sum = 0;
 #pragma unroll
   for (int i = 0; i < N * E; i += 2) {
-    const uint64_t y = fma2(pack(v[i / E].get(i % E), v[i / E].get(i % E + 1)), c2, r2);
+    const uint64_t y = mul2(add2(pack(v[i / E].get(i % E), v[i / E].get(i % E + 1)), m2), c2);
     sum = add2(sum, pack(tc::ex2_approx(low(y)), tc::ex2_approx(high(y))));
   }
   return low(sum) + high(sum);
@@ -165,9 +169,9 @@ __device__ __forceinline__ void add(Run& st, const Vec<F32> (&v)[N], float c, I 
     if (look) {
       const float top = top_of<F32, N>(v);
       if (__any_sync(0xffffffffu, top > st.m)) {
-        const float m = warp_top(fmaxf(top, st.m)), r = fmaxf(rintf(m * c), LEAST);
-        st.s *= tc::ex2_approx(st.r - r);
-        st.m = m, st.r = r;
+        const float m = warp_top(fmaxf(top, st.m));
+        if (st.m > -INFINITY) st.s *= tc::ex2_approx((st.m - m) * c);
+        st.m = m;
         if (GREEDY) {
           st.idx = NOWHERE;
           if (top == m) {
@@ -178,7 +182,7 @@ __device__ __forceinline__ void add(Run& st, const Vec<F32> (&v)[N], float c, I 
         }
       }
     }
-    const float sum = weights<F32, N>(v, c, st.r);
+    const float sum = weights<F32, N>(v, c, st.m == -INFINITY ? 0.f : st.m);
     if (look || !__any_sync(0xffffffffu, sum > FAR)) {
       st.s += sum;
       return;
@@ -224,7 +228,7 @@ __device__ __noinline__ Stat scan_row(const void* row, int lo, int hi, int share
   int j0 = share * BLOCK, ahead = j0, to = 0, use = 0;
 #pragma unroll
   for (int g = 0; g < DEPTH - 1; ++g, ahead += step, ++to) fetch(ahead, to);
-  Run st = {-INFINITY, LEAST, 0.f, NOWHERE};
+  Run st = {-INFINITY, 0.f, NOWHERE};
   const auto one = [&](int i, bool there) {
     Vec<F32> z[1];
     z[0].set(make_uint4(NONE<F32>, NONE<F32>, NONE<F32>, NONE<F32>));
@@ -255,12 +259,7 @@ __device__ __noinline__ Stat scan_row(const void* row, int lo, int hi, int share
   const int tail = from + vecs * E;
   if (share == 0 && tail < hi) one(tail + lane, tail + lane < hi);
   const float s = warp_sum(st.s);
-  if (st.m == -INFINITY) {
-    if (s == 0.f) return Stat{-INFINITY, 0.f, NOWHERE};  // (else a NaN was among them, which the careful form passes over)
-  } else if (s == s && fabsf(st.m * c) < -LEAST) {
-    return Stat{st.m, s * tc::ex2_approx(-fmaf(st.m, c, -st.r)),
-                GREEDY ? (int)__reduce_min_sync(0xffffffffu, (unsigned)st.idx) : NOWHERE};
-  }
+  if (s == s) return Stat{st.m, s, GREEDY ? (int)__reduce_min_sync(0xffffffffu, (unsigned)st.idx) : NOWHERE};
   Stat slow = {-INFINITY, 0.f, NOWHERE}, out;
   const auto careful = [&](int i) { add_careful(slow, logit(element<F32>(row, i), F32), i, c); };
   if (share == 0 && lane < head) careful(lo + lane);
@@ -333,10 +332,8 @@ __device__ __forceinline__ Best race(const Law& p, const Law& q, bool minus, int
   constexpr int GROUPS = RING / GROUP, STRIDE = NT / 32 * STEP;
   Best best = {0.f, NOWHERE, 0.f};
   if (!p.probs && p.m == -INFINITY) return best;
-  // An element's quick weight is x itself, or 2^(x c - ref); times scale it is its probability but for 2^-11 of it.
-  const float c = r.hi, ref = rintf(p.m * c);
-  const bool quick = p.probs || fabsf(p.m * c) < -LEAST;  // (else every element is a candidate)
-  const float unit = (1.f - 0x1p-10f) / (p.probs ? 1.f : p.inv * tc::ex2_approx(-fmaf(p.m, c, -ref)));
+  // An element's quick weight is x itself, or 2^((x - m) c); times scale it is its probability but for 2^-11 of it.
+  const float c = r.hi, unit = (1.f - 0x1p-10f) / (p.probs ? 1.f : p.inv);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   const auto enter = [&](int i, float x, float e) {
@@ -375,7 +372,7 @@ __device__ __forceinline__ Best race(const Law& p, const Law& q, bool minus, int
     }
     tc::cp_async_commit();
   };
-  const uint64_t c2 = pack(c, c), ref2 = pack(-ref, -ref);
+  const uint64_t c2 = pack(c, c), m2 = pack(-p.m, -p.m);
   int to = 0, use = 0;
   for (int i0 = warp * STEP - (GROUPS - 1) * STRIDE; i0 < count; i0 += STRIDE) {
     __syncwarp();  // (the group that is filled now has been read by every lane)
@@ -408,7 +405,7 @@ __device__ __forceinline__ Best race(const Law& p, const Law& q, bool minus, int
           constexpr int PER = 16 / SIZE;
           uint64_t w = pack(x[k / PER].get(k % PER), x[k / PER].get(k % PER + 1));
           if (!p.probs) {
-            const uint64_t y = fma2(w, c2, ref2);
+            const uint64_t y = mul2(add2(w, m2), c2);
             w = pack(tc::ex2_approx(low(y)), tc::ex2_approx(high(y)));
           }
           w = fma2(e[k / 2], bar2, w);
@@ -416,13 +413,13 @@ __device__ __forceinline__ Best race(const Law& p, const Law& q, bool minus, int
           if (h * 256 < n) most = fmaxf(most, fmaxf(low(w), high(w)));
         }
       }
-      if (!__any_sync(0xffffffffu, most > 0.f || !quick)) break;
+      if (!__any_sync(0xffffffffu, most > 0.f)) break;
       // each lane looks at the candidate that lies farthest over the bar, which may raise it for the others
       int pick = -1;
       most = 0.f;
 #pragma unroll
       for (int k = 0; k < E; ++k) {
-        const float w = quick ? (k & 1 ? high(over[k / 2]) : low(over[k / 2])) : 1.f;
+        const float w = k & 1 ? high(over[k / 2]) : low(over[k / 2]);
         if (w > most && k / 8 * 256 < n && !(done >> k & 1)) most = w, pick = k;
       }
       if (!__any_sync(0xffffffffu, pick >= 0)) break;
