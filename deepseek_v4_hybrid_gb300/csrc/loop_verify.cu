@@ -31,7 +31,8 @@ namespace loop {
 namespace cg = cooperative_groups;
 
 constexpr int MAX_CLUSTER = 8, MAX_ROWS = 8;  // rows of a group
-constexpr float LOG2E_HI = 1.44269502162933349609375f, LOG2E_LO = 1.92596299112661746887e-8f, LN2F = 0.69314718055994531f;
+constexpr double LOG2E = 1.4426950408889634;  // in two floats:
+constexpr float LOG2E_HI = (float)LOG2E, LOG2E_LO = (float)(LOG2E - (double)LOG2E_HI), LN2F = 0.69314718055994531f;
 constexpr float MAX_F32 = 3.4028234663852886e38f, MAX_BF16 = 3.3895313892515355e38f;
 constexpr int NOWHERE = 0x7FFFFFFF;
 
