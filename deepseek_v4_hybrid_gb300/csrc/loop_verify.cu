@@ -490,7 +490,6 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
   Rate rate;
   rate.hi = LOG2E_HI / temp;
   rate.lo = rate.hi < 1e30f ? (fmaf(-rate.hi, temp, LOG2E_HI) + LOG2E_LO) / temp : 0.f;
-  constexpr bool tf32 = F32;
   const bool df32 = p.draft_dtype == DSV4_F32;
   const bool drafted_law = p.draft != nullptr && !greedy;
   const int per = ((p.vocab + C - 1) / C + 7) & ~7, lo = min(p.vocab, rank * per), hi = min(p.vocab, lo + per);
@@ -511,7 +510,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
       const int t = t0 + i0 + tid;
       x = p.tokens[t + 1];
       const bool in = x >= 0 && x < p.vocab;
-      if (in) zx = element(p.target, (int64_t)t * p.target_stride + x, tf32);
+      if (in) zx = element(p.target, (int64_t)t * p.target_stride + x, F32);
       if (!greedy) ux = p.u[t + 1];
       if (drafted_law) {
         qrow = p.draft_row ? p.draft_row[t + 1] : t - b;
@@ -533,8 +532,8 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
           d = i + 1 < n ? (p.draft_row ? p.draft_row[t + 1] : t - b) : -1;
           if (d >= p.draft_rows) d = -1;
         }
-        const bool f32 = is_target ? tf32 : df32;
-        const void* row = is_target ? at(p.target, t * p.target_stride, tf32) : at(p.draft, d * p.draft_stride, df32);
+        const bool f32 = is_target ? F32 : df32;
+        const void* row = is_target ? at(p.target, t * p.target_stride, F32) : at(p.draft, d * p.draft_stride, df32);
         Stat st = {-INFINITY, 0.f, NOWHERE};
         if (d >= 0) {
           if (greedy)
@@ -577,12 +576,12 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
         if (greedy) {
           ok = ts.m > (p.target_probs ? 0.f : -INFINITY) && x == ts.idx;
         } else if (draft_task && !p.target_probs) {
-          ok = qrow >= 0 && keeps(ux, logit(zx, tf32), ts, logit(yx, df32), ds, rate);
+          ok = qrow >= 0 && keeps(ux, logit(zx, F32), ts, logit(yx, df32), ds, rate);
         } else {
-          const Law law = {nullptr, tf32, p.target_probs != 0, ts.m, ts.s > 0.f ? 1.f / ts.s : 0.f};
+          const Law law = {nullptr, F32, p.target_probs != 0, ts.m, ts.s > 0.f ? 1.f / ts.s : 0.f};
           const float px = law_of(law, zx, rate);
           if (!drafted_law) {
-            ok = ux < px || (ux == 0.f && !p.target_probs && logit(zx, tf32) > -INFINITY);
+            ok = ux < px || (ux == 0.f && !p.target_probs && logit(zx, F32) > -INFINITY);
           } else if (qrow >= 0) {
             const Law dlaw = {nullptr, df32, p.draft_probs != 0, ds.m, ds.s > 0.f ? 1.f / ds.s : 0.f};
             ok = ux * law_of(dlaw, yx, rate) < px;
@@ -600,7 +599,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
       all = last == n - 1;
       const Stat ts = target_task ? fin[stay * tasks_a_row] : Stat{};
       if (greedy && ts.m > (p.target_probs ? 0.f : -INFINITY)) best = Best{0.f, ts.idx, ts.m};
-      lp = Law{at(p.target, t * p.target_stride, tf32), tf32, p.target_probs != 0, ts.m, ts.s > 0.f ? 1.f / ts.s : 0.f};
+      lp = Law{at(p.target, t * p.target_stride, F32), F32, p.target_probs != 0, ts.m, ts.s > 0.f ? 1.f / ts.s : 0.f};
       if (drafted_law && !all) {
         const int64_t d = p.draft_row ? p.draft_row[t + 1] : t - b;
         if (d >= 0 && d < p.draft_rows) {
@@ -612,7 +611,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
     }
     if (rank == 0 && tid < stay) {
       out[i0 + tid] = x;
-      if (logp) logp[i0 + tid] = p.target_probs ? logf(prob(zx)) : (logit(zx, tf32) - l_m) / temp - logf(l_s);
+      if (logp) logp[i0 + tid] = p.target_probs ? logf(prob(zx)) : (logit(zx, F32) - l_m) / temp - logf(l_s);
     }
     __syncthreads();  // fin and stands are free again
   }
@@ -649,7 +648,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
     const bool here = i == last && found;
     out[i] = here ? best.idx : -1;
     if (logp)
-      logp[i] = !here ? 0.f : p.target_probs ? logf(prob(best.x)) : (logit(best.x, tf32) - lp.m) / temp + logf(lp.inv);
+      logp[i] = !here ? 0.f : p.target_probs ? logf(prob(best.x)) : (logit(best.x, F32) - lp.m) / temp + logf(lp.inv);
   }
   if (tid == 0) p.n_out[b] = last + (found ? 1 : 0);
 }

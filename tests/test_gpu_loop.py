@@ -51,7 +51,7 @@ ROPES = [  # T, heads, heads2, dim, first, rope_dim, halves
     (1, 1, 0, 16, 0, 16, False), (1, 64, 8, 128, 0, 128, False), (3, 5, 1, 64, 32, 32, True), (70, 20, 4, 64, 0, 64, True),
     (33, 7, 3, 80, 48, 32, False), (129, 1, 0, 576, 512, 64, False), (5, 3, 2, 1024, 0, 1024, True),
     (9, 128, 1, 192, 128, 64, False), (1000, 1, 1, 256, 8, 48, True), (17, 300, 0, 96, 0, 96, False),
-    (40, 2, 2, 24, 8, 16, True),
+    (40, 2, 2, 24, 8, 16, True), (3, 2, 0, 1024, 0, 1024, False), (2, 1024, 1, 32, 0, 32, False),
 ]
 
 
@@ -242,7 +242,8 @@ PLANS = [  # B, caches (page, ratio, window), ctx, n_max, free pages
     (64, [(64, 1, 128), (64, 4, 0)], 900, 4, 40), (300, [(64, 1, 0)], 3000, 4, 5), (65, [(1, 1, 3)], 20, 6, 600),
     (33, [(128, 1, 500), (256, 4, 0), (64, 128, 0)], 4000, 700, 60), (1000, [(32, 1, 0), (16, 4, 0)], 300, 3, 30),
     (1025, [(16, 1, 40), (8, 3, 0), (64, 128, 0), (5, 7, 0)], 500, 9, 700), (4096, [(64, 1, 0)], 2000, 6, 300),
-    (2500, [(16, 1, 0)], 30, 100, 20000),
+    (2500, [(16, 1, 0)], 30, 100, 20000), (4096, [(16, 1, 9), (32, 1, 70), (8, 1, 33), (64, 1, 128)], 90, 3, 5000),
+    (40, [(64, 1, 0)], 9000, 13000, 9000),
 ]
 
 
@@ -271,6 +272,14 @@ def test_plan_with_less_room_than_tokens(M, T):
     M.dsv4_batch_plan(p)
     r = q.check(t)
     assert r["q_start"][-1] <= T
+
+
+def test_plan_of_the_largest_step(M):
+    """Room for 2^19 tokens, nearly all of them taken."""
+    q = Requests(10, 60, [(256, 1, 0)], 2000, 17000, 3000, T=1 << 19, ended=0.0)
+    p, t = q.device(M)
+    M.dsv4_batch_plan(p)
+    assert q.check(t)["q_start"][-1] > 1 << 18
 
 
 def test_plan_empty_batches(M):
