@@ -32,9 +32,9 @@ def ints(a, dtype=torch.int32):
 # rotary positions
 # ------------------------------------------------------------------------------------------------
 def rope_bound(x, want, first, dim, halves, scale, dtype):
-    """An angle's float conversion moves it by pi 2^-24 at most, sincospi by two steps of 2^-24, the factor's product by
-    half a step; two products and a sum round once or twice each: |a| and |b| times 8 * 2^-24 in all.  Then
-    the output's rounding; dims that are copied are exact."""
+    """An angle's float conversion moves it by pi 2^-24 at most, the sums for sine and cosine by two steps of 2^-24, the
+    factor's product by half a step; two products and a sum round once or twice each: |a| and |b| times 8 * 2^-24 in all.
+    Then the output's rounding; dims that are copied are exact."""
     a = np.abs(x).copy()
     part = a[:, :, first:first + dim]
     pair = part.reshape(*part.shape[:2], 2, -1).sum(2) if halves else part.reshape(*part.shape[:2], -1, 2).sum(3)
@@ -130,7 +130,7 @@ def test_rope_table(M, rows, dim, first, scale):
     M.dsv4_rope_table(M.rope_table_params(table[:rows], freqs, first_position=first, scale=scale))
     w = L.angles(np.arange(first, first + rows), freqs.cpu().numpy())
     want = scale * np.concatenate([np.cos(w), np.sin(w)], 1)
-    # pi 2^-24 of the angle, two steps of sincospi, the factor's rounding
+    # pi 2^-24 of the angle, two steps of the sums, the factor's rounding
     assert np.abs(f64(table[:rows]) - want).max() <= abs(scale) * 7 * 2.0 ** -24
     small = np.abs(np.sin(w)) < 2.0 ** -9  # near 0 the sine is as exact relatively
     err = np.abs(f64(table[:rows])[:, dim // 2:] - want[:, dim // 2:])
