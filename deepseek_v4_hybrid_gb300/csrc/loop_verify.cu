@@ -139,10 +139,12 @@ __device__ __forceinline__ float warp_top(float x) { return from_ordered(__reduc
 constexpr int U = 4;  // vectors of a group (scan)
 
 // The running numbers of a warp over a row: the reference m, one of its logits, and the lane's sum of 2^((z - m) c).
-// Greedy sequences keep m at the maximum and each lane's first index of it; the others change it only when a sum
-// says that a logit lies far above (2^40), which spares the search.
+// Greedy sequences keep m at the maximum and each lane's first index of it; the others change it only when the sum of
+// a lane's 32 elements (16 of fp32) says that one lies above it by a binary order or two, which spares the search.  (An exponent's
+// argument y is off by |y| 2^-23, so the elements that make up the sum should have small ones: with logits 20 binary orders
+// above the reference, log-probabilities next to 0 were off by 8e-7.)
 // Elements are taken as they are: NaN and +inf make the sum NaN, and the part is then done again by the careful form.
-constexpr float FAR = 1099511627776.f;
+constexpr float FAR = 64.f;
 
 struct Run {
   float m, s;
@@ -311,6 +313,13 @@ __device__ __forceinline__ bool keeps(float u, float z, const Stat& p, float y, 
 __device__ __forceinline__ float law_of(const Law& l, float x, const Rate& r) {
   if (l.probs) return prob(x);
   return l.m == -INFINITY ? 0.f : weight(logit(x, l.f32), l.m, r) * l.inv;
+}
+
+// log p of an element: of the probability itself, whose error stays that of a weight (a difference of two logarithms has
+// the error of the larger, and p may be next to 1); where it is too small for that, of its parts.
+__device__ __forceinline__ float log_of(const Law& l, float x, const Rate& r, float temp) {
+  const float p = law_of(l, x, r);
+  return l.probs || p > 1e-30f ? logf(p) : (logit(x, l.f32) - l.m) / temp + logf(l.inv);
 }
 
 struct Best {
@@ -611,7 +620,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
     }
     if (rank == 0 && tid < stay) {
       out[i0 + tid] = x;
-      if (logp) logp[i0 + tid] = p.target_probs ? logf(prob(zx)) : (logit(zx, F32) - l_m) / temp - logf(l_s);
+      if (logp) logp[i0 + tid] = log_of(Law{nullptr, F32, p.target_probs != 0, l_m, __fdividef(1.f, l_s)}, zx, rate, temp);
     }
     __syncthreads();  // fin and stands are free again
   }
@@ -647,8 +656,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
   for (int i = last + tid; i < p.max_q_len; i += NT) {
     const bool here = i == last && found;
     out[i] = here ? best.idx : -1;
-    if (logp)
-      logp[i] = !here ? 0.f : p.target_probs ? logf(prob(best.x)) : (logit(best.x, F32) - lp.m) / temp + logf(lp.inv);
+    if (logp) logp[i] = here ? log_of(lp, best.x, rate, temp) : 0.f;
   }
   if (tid == 0) p.n_out[b] = last + (found ? 1 : 0);
 }
