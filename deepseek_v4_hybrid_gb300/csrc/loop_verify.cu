@@ -8,10 +8,10 @@
 //
 // Two CTAs of 256 threads an SM with six groups of copies on their way each (512 threads, four groups: 256 x 5 rows of
 // 131072 logits 158 us for 126, 64 x 4 rows 33 for 35.5; three CTAs with four groups 159 and 42).  Large batches are bound
-// by HBM: 256 x 5 rows of 131072 bf16 logits of both models 130 us, of which the 700 MB that the drafts that stand make it
-// read take 103 at the copy rate.  Smaller ones by a chain of phases, each waiting for the one before: launch and first
-// loads (2 us), rows, exchange and decision (3 us), race, exchange; 2 x 4 rows of 32000 fp32 logits 10.6 us, 64 x 4 rows of
-// 131072 bf16 logits with fp32 probabilities of the draft 35.8 us (104 MB), 200 x up to 3 rows of 100003 42.6 us.
+// by HBM: 256 x 5 rows of 131072 bf16 logits of both models 130 us, of which the 650 to 700 MB that the drafts that stand make
+// it read take 100 at the copy rate.  Smaller ones by a chain of phases, each waiting for the one before: launch and first
+// loads (2 us), rows, exchange and decision (3 us), race, exchange; 2 x 4 rows of 32000 fp32 logits 10.7 us, 64 x 4 rows of
+// 131072 bf16 logits with fp32 probabilities of the draft 35.8 us (104 MB), 200 x up to 3 rows of 100003 43.7 us.
 // Code that runs once a sequence waits for its instructions to be fetched: parts that were inlined twice are loops
 // (256 x 5 rows 131 -> 126 us, 400 x 4 rows of 8000 37 -> 30).  Exponents are taken of differences from a logit, in two
 // instructions for one fused product against an integer: 3 % of the largest call, but no range that logits or low
