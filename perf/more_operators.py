@@ -264,8 +264,7 @@ def _prepare_verify(c, g, seed):
         # a few words that fit, far above the rest; a drafter that mostly agrees
         z = torch.randn((m, V), generator=g, device=dev).mul_(2.0)
         top = torch.randint(0, V, (m, 12), generator=g, device=dev)
-        # (a word drawn twice keeps its larger value: which of two plain stores stays would not follow from the seed)
-        z.scatter_reduce_(1, top, 8.0 + 3.0 * torch.randn((m, 12), generator=g, device=dev), "amax", include_self=False)
+        z.scatter_(1, top, 8.0 + 3.0 * torch.randn((m, 12), generator=g, device=dev))
         y = z + 0.35 * torch.randn((m, V), generator=g, device=dev)
         if c["banned"]:
             z.masked_fill_(torch.rand((m, V), generator=g, device=dev) < c["banned"], -math.inf)
