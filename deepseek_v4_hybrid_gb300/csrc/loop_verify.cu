@@ -470,12 +470,22 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
   __shared__ Stat part[NW], got[2][2 * MAX_ROWS][MAX_CLUSTER];
   __shared__ Best bpart[NW], bgot[2][MAX_CLUSTER];
   __shared__ Stat fin[2 * MAX_ROWS];
-  __shared__ int stands[MAX_ROWS], top_key;
+  __shared__ int stands[MAX_ROWS], top_key, brought_part[NW];
   if (tid == 0) top_key = 0;
   pdl_wait();
   pdl_launch_dependents();
   const int t0 = p.q_start[b], t1 = p.q_start[b + 1];
   float temp = p.temperature ? p.temperature[b] : 1.f;
+  // Draft rows in order: one for every token but the first of each sequence, so the row of token t + 1 is t less the sequences
+  // before b that brought any token.  (The loads lie beside those above: 2 x 4 rows 10.8 to 11.1 us, 256 x 5 rows no change, 8000 x
+  // 2 rows of 100 logits 215 to 245.)
+  if (p.draft != nullptr && p.draft_row == nullptr) {
+    int brought = 0;
+#pragma unroll 8
+    for (int j = tid; j < b; j += NT) brought += p.q_start[j + 1] > p.q_start[j];
+    brought = __reduce_add_sync(0xffffffffu, brought);
+    if (lane == 0) brought_part[warp] = brought;
+  }
   if (t0 < 0 || t1 < t0 || t1 > p.T || t1 - t0 > p.max_q_len) {  // (the same for the whole cluster)
     if (rank == 0 && tid == 0) atomicOr(&g_flags_vf, FLAG_PAGE);
     return;
@@ -494,6 +504,10 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
     return;
   }
   cluster.sync();  // every CTA's shared memory is there to be written
+  int64_t brought = 0;
+  if (p.draft != nullptr && p.draft_row == nullptr)
+    for (int w = 0; w < NW; ++w) brought += brought_part[w];
+  const auto draft_row_of = [&](int64_t t) { return p.draft_row ? (int64_t)p.draft_row[t + 1] : t - brought; };
   const bool greedy = p.noise == nullptr || !(temp > 0.f);
   temp = greedy ? 1.f : fminf(fmaxf(temp, 1e-30f), 1e30f);
   Rate rate;
@@ -522,7 +536,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
       if (in) zx = element(p.target, (int64_t)t * p.target_stride + x, F32);
       if (!greedy) ux = p.u[t + 1];
       if (drafted_law) {
-        qrow = p.draft_row ? p.draft_row[t + 1] : t - b;
+        qrow = draft_row_of(t);
         if (qrow < 0 || qrow >= p.draft_rows) qrow = -1;
         if (in && qrow >= 0) yx = element(p.draft, qrow * p.draft_stride + x, df32);
       }
@@ -538,7 +552,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
         const bool is_target = target_task && k % tasks_a_row == 0;
         int64_t d = 0;
         if (!is_target) {
-          d = i + 1 < n ? (p.draft_row ? p.draft_row[t + 1] : t - b) : -1;
+          d = i + 1 < n ? draft_row_of(t) : -1;
           if (d >= p.draft_rows) d = -1;
         }
         const bool f32 = is_target ? F32 : df32;
@@ -610,7 +624,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
       if (greedy && ts.m > (p.target_probs ? 0.f : -INFINITY)) best = Best{0.f, ts.idx, ts.m};
       lp = Law{at(p.target, t * p.target_stride, F32), F32, p.target_probs != 0, ts.m, ts.s > 0.f ? 1.f / ts.s : 0.f};
       if (drafted_law && !all) {
-        const int64_t d = p.draft_row ? p.draft_row[t + 1] : t - b;
+        const int64_t d = draft_row_of(t);
         if (d >= 0 && d < p.draft_rows) {
           const Stat ds = draft_task ? fin[stay * tasks_a_row + tasks_a_row - 1] : Stat{};
           lq = Law{at(p.draft, d * p.draft_stride, df32), df32, p.draft_probs != 0, ds.m, ds.s > 0.f ? 1.f / ds.s : 0.f};

@@ -179,9 +179,9 @@ int dsv4_batch_plan(const dsv4_batch_plan_params* p, dsv4_stream_t stream);
  * n_b - 1 drafted ones.  Target row t = q_start[b] + i says how token t + 1 is distributed:
  *   logits         p = softmax(row / temperature[b])
  *   target_probs   p = row
- * and draft row of token t + 1 (draft_row[t + 1], or t - b when draft_row is NULL: the drafted tokens' rows in
- * order) the distribution q that it was drawn from, likewise; without a draft, q is 1 at the token (drafts that were
- * not drawn).  For i = 0, 1, ... the drafted token x = tokens[t + 1] stands if
+ * and draft row of token t + 1 (draft_row[t + 1]; when draft_row is NULL, t less the number of sequences before b that
+ * brought tokens: the drafted tokens' rows in order, sequences without tokens having none) the distribution q that it was
+ * drawn from, likewise; without a draft, q is 1 at the token (drafts that were not drawn).  For i = 0, 1, ... the drafted token x = tokens[t + 1] stands if
  *   u[t + 1] q(x) < p(x)
  * up to the first that does not; that one is replaced by argmax_x max(p(x) - q(x), 0) / noise[b][x] (without a
  * draft: of p(x) / noise[b][x] over the others), and when all stand, argmax_x p(x) / noise[b][x] of the last row

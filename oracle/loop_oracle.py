@@ -174,8 +174,11 @@ def verify(target, tokens, q_start, width, draft=None, draft_row=None, temperatu
     B, V = len(q_start) - 1, target.shape[1]
     out, logp = np.full((B, width), -1, np.int64), np.zeros((B, width))
     count, margin = np.zeros(B, np.int64), np.full(B, np.inf)
+    drafted = int(q_start[0])  # tokens drafted for the sequences before, whose rows lie before this one's
     for b in range(B):
         t0, n = int(q_start[b]), int(q_start[b + 1] - q_start[b])
+        row0 = drafted
+        drafted += max(n - 1, 0)
         temp = 1.0 if temperature is None else float(temperature[b])
         greedy = noise is None or not temp > 0
         for i in range(n):
@@ -186,7 +189,7 @@ def verify(target, tokens, q_start, width, draft=None, draft_row=None, temperatu
             if i + 1 < n:
                 known, q, lq = True, np.zeros(V), None
                 if draft is not None and not greedy:
-                    d = int(draft_row[t + 1]) if draft_row is not None else t - b
+                    d = int(draft_row[t + 1]) if draft_row is not None else row0 + i
                     known = 0 <= d < len(draft)
                     if known:
                         q, lq = law(draft[d], draft_probs, temp, largest)

@@ -1,0 +1,94 @@
+"""The calls around the layers where they can go wrong: what the tests beside their definitions pass over."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import loop_oracle as L
+from test_gpu_loop import BF16, F32, Drafts, M, Requests, f64, ints  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------------
+# draft rows behind sequences without tokens
+# ------------------------------------------------------------------------------------------------
+def rows_in_order(n):
+    """The draft row of every token, counted token by token (-3: not drafted)."""
+    row, at = [], 0
+    for k in n:
+        for i in range(k):
+            row.append(-3 if i == 0 else at)
+            at += i > 0
+    return np.array(row, np.int64)
+
+
+EMPTIES = [[0, 2], [0, 0, 2], [2, 0, 2], [4, 0, 4], [0, 3, 0, 0, 1, 5, 0, 2, 0], [1, 0, 1, 0, 3],
+           np.random.default_rng(0).integers(0, 4, 700).tolist(), [0] * 300 + [3] * 5 + [0] * 2100 + [2, 4]]
+
+
+@pytest.mark.parametrize("draft,draft_probs", [(BF16, False), (F32, True)], ids=["logits", "probs"])
+@pytest.mark.parametrize("n", EMPTIES, ids=lambda n: f"B{len(n)}_first{n[0]}_T{sum(n)}")
+def test_verify_draft_rows_behind_empty_sequences(M, n, draft, draft_probs):  # noqa: F811
+    """Drafts in order give what the same rows give by name."""
+    d = Drafts(len(n) + sum(n), n, 257, F32, draft, draft_probs=draft_probs)
+    row = rows_in_order(n)
+    assert row.max() + 1 == len(d.draft)
+    d.draft_row = row
+    named, t = d.device(M)
+    M.dsv4_draft_verify(named)
+    want = {k: v.clone() for k, v in t.items()}
+    d.check(t, telling=len(n) > 20)
+    d.draft_row = None
+    in_order, t = d.device(M)
+    M.dsv4_draft_verify(in_order)
+    assert M.dsv4_read_device_flags() == 0
+    for k in t:
+        assert torch.equal(t[k], want[k]), k
+
+
+def test_drafted_loop_with_requests_left_out(M):  # noqa: F811
+    """Plan and verification of one captured step: requests end, begin and are left out for want of pages, so that sequences
+    without tokens lie between the others; the drafts' rows follow one another."""
+    B, k, V, page = 24, 3, 300, 4
+    W = k + 1
+    q = Requests(3, B, [(page, 1, 0)], 20, W, 12, width=20, T=B * W)
+    p, t = q.device(M, in_place=True)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rng = np.random.default_rng(8)
+    target = torch.zeros((q.T, V), device="cuda")
+    draft = torch.zeros((q.T, V), device="cuda")
+    tokens, u, noise = torch.zeros(q.T, dtype=torch.int32, device="cuda"), torch.zeros(q.T, device="cuda"), torch.ones((B, V), device="cuda")
+    words = torch.zeros((B, W), dtype=torch.int32, device="cuda")
+    v = M.draft_verify_params(target, tokens, t["q_start"], W, words, t["add"], draft=draft, u=u, noise=noise)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.dsv4_batch_plan(p)
+        M.dsv4_draft_verify(v)
+    between = 0
+    for step in range(25):
+        target.normal_(generator=g).mul_(2)
+        draft.copy_(target.roll(1, 1) + 0.1)
+        noise.exponential_(generator=g).clamp_(min=1e-20)
+        u.uniform_(generator=g).mul_(0.2)
+        graph.replay()
+        r = q.check(t)
+        n = np.diff(r["q_start"])
+        between += int(np.any((n == 0)[:np.max(np.nonzero(n)[0], initial=0)]))
+        row = np.full(q.T, -3)
+        known = rows_in_order(n)
+        row[:len(known)] = known
+        out, count, _, margin = L.verify(f64(target), tokens.cpu().numpy(), r["q_start"], W, draft=f64(draft), draft_row=row,
+                                         u=f64(u), noise=f64(noise))
+        sure = margin > 2.0 ** -17
+        np.testing.assert_array_equal(words.cpu().numpy()[sure], out[sure])
+        np.testing.assert_array_equal(t["add"].cpu().numpy()[sure], count[sure])
+        q.ctx = r["ctx_out"].astype(np.int64)
+        q.add = t["add"].cpu().numpy().astype(np.int64)
+        q.n = np.where(q.n == 0, rng.integers(1, W + 1, B), rng.integers(1, W + 1, B))
+        end = (rng.random(B) < 0.15) | (q.ctx + q.add > 60)
+        q.ctx[end], q.add[end], q.n[end] = 0, 0, 0
+        for name in ("ctx", "add", "n"):
+            t[name].copy_(ints(getattr(q, name)))
+        # the next step's tokens, drawn from the rows that will be theirs
+        tokens.copy_(torch.randint(0, V, (q.T,), generator=g, device="cuda"))
+    assert between > 10 and M.dsv4_read_device_flags() == 0
