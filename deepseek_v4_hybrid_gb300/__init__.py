@@ -431,8 +431,9 @@ def _row_stride(t):
 def draft_verify_params(target, tokens, q_start, max_q_len, out_tokens, n_out, draft=None, draft_row=None,
                         temperature=None, u=None, noise=None, logp=None, target_probs=False, draft_probs=False):
     """Parameter struct of dsv4_draft_verify.  target [T, vocab] logits (or probabilities) and draft [rows, vocab], bf16
-    or fp32, rows of any stride (without draft_row: the drafted tokens' rows in order); tokens, draft_row [T], q_start [B + 1], out_tokens [B, max_q_len], n_out [B] int32;
-    temperature [B], u [T], noise [B, vocab], logp [B, max_q_len] fp32."""
+    or fp32, rows of any stride (without draft_row: the drafted tokens' rows in order); tokens, draft_row [T],
+    q_start [B + 1], out_tokens [B, max_q_len], n_out [B] int32; temperature [B], u [T], noise [B, vocab],
+    logp [B, max_q_len] fp32."""
     dt, dev = _act(target, "target"), target.device
     _need_tensor(target, "target", (target.dtype,), (None, None), dev)
     T, V = target.shape

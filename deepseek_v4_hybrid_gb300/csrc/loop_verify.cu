@@ -301,12 +301,17 @@ __device__ __forceinline__ float weight(float z, float m, const Rate& r) {
   return tc::ex2_approx(y) * fmaf(e, LN2F, 1.f);
 }
 // Whether u q(x) < p(x) for logits z of the target's row and y of the draft's, as u < p(x) / q(x): the quotient stands
-// where both probabilities are too small for a float.
+// where both probabilities are too small for a float.  Quotients of 2^150 and more or less, and those whose exponents leave fp32 (a
+// logit of -1e38 does so at temperature 1), are decided by the difference of the exponents in fp64, which holds any of them.
 __device__ __forceinline__ bool keeps(float u, float z, const Stat& p, float y, const Stat& q, const Rate& r) {
   if (z == -INFINITY) return false;
   if (y == -INFINITY) return true;
   const float dp = z - p.m, dq = y - q.m, a = dp * r.hi, b = dq * r.hi;
   const float e = (fmaf(dp, r.hi, -a) + dp * r.lo) - (fmaf(dq, r.hi, -b) + dq * r.lo), d = a - b, sum = d + e;
+  if (!(fabsf(sum) < 150.f)) {  // (NaN too)
+    const double far = (((double)z - p.m) - ((double)y - q.m)) * r.hi;
+    return u < tc::ex2_approx((float)fmin(fmax(far, -1000.0), 1000.0)) * (q.s / p.s);
+  }
   return u < tc::ex2_approx(sum) * fmaf((d - sum) + e, LN2F, 1.f) * (q.s / p.s);
 }
 

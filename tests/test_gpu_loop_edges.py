@@ -92,3 +92,53 @@ def test_drafted_loop_with_requests_left_out(M):  # noqa: F811
         # the next step's tokens, drawn from the rows that will be theirs
         tokens.copy_(torch.randint(0, V, (q.T,), generator=g, device="cuda"))
     assert between > 10 and M.dsv4_read_device_flags() == 0
+
+
+# ------------------------------------------------------------------------------------------------
+# drafted tokens far below the maximum of their draft row
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("temp", [1e-7, 0.4, 0.5, 1.0, 1.4, 2.0, 100.0])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+def test_verify_drafted_tokens_masked_in_the_draft(M, dtype, temp):  # noqa: F811
+    """A drafted token that is the target's maximum stands, however little the draft gave it: u q(x) < p(x) with q(x) next to
+    nothing.  (u is below 0.9 and p over 0.99 of what it could be.)"""
+    values = [-1e3, -1e6, -1e7, -3e7, -1e8, -1e9, -1e20, -1e30, torch.finfo(dtype).min]
+    d = Drafts(70, [2] * len(values), 300, dtype, dtype, spread=0.01 if temp > 10 else 2.0)
+    x = torch.arange(len(values), device="cuda") * 31 + 5
+    rows = torch.arange(len(values), device="cuda")
+    d.tokens[1::2] = x.cpu().numpy()
+    d.target[2 * rows, x] = 40.0 if temp < 10 else 3000.0
+    d.draft[rows, x] = torch.tensor(values, device="cuda").to(dtype)
+    d.temp.fill_(temp)
+    d.u.mul_(0.9)
+    out, count = d.run(M, telling=False)
+    assert np.all(count == 2)
+
+
+@pytest.mark.parametrize("low", [-1e6, -1e8, -1e30, None])
+def test_verify_drafted_tokens_masked_in_the_target(M, low):  # noqa: F811
+    """The other way round they fall: p(x) is next to nothing, q(x) is not."""
+    d = Drafts(71, [2] * 8, 300, F32, F32)
+    rows = torch.arange(8, device="cuda")
+    x = torch.from_numpy(d.tokens[1::2].copy()).cuda()
+    d.target[2 * rows, x] = torch.finfo(F32).min if low is None else low
+    d.u.clamp_(min=1e-3)
+    _, count = d.run(M, telling=False)
+    assert np.all(count == 1)
+
+
+def test_verify_drafted_tokens_far_down_in_both(M):  # noqa: F811
+    """Both probabilities are too small for a float, their quotient is not: equal rows keep every draft (u below 1)."""
+    d = Drafts(72, [2] * 6, 300, F32, F32)
+    x = torch.from_numpy(d.tokens[1::2].copy()).cuda()
+    rows = torch.arange(6, device="cuda")
+    d.draft.copy_(d.target[0::2])
+    for row, value in enumerate((-200.0, -1e4, -1e7, -1e9, -1e30, torch.finfo(F32).min)):
+        d.target[2 * row, x[row]] = d.draft[row, x[row]] = value
+    d.temp.fill_(0.7)
+    d.u.clamp_(max=0.999)
+    p, t = d.device(M)
+    M.dsv4_draft_verify(p)
+    d.check(t, telling=False)
+    # (beside 1e30 a float64 sum of logarithms loses log u: the definition's count says nothing there)
+    assert torch.all(t["count"] == 2) and M.dsv4_read_device_flags() == 0
