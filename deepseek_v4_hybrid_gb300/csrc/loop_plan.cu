@@ -124,7 +124,7 @@ __device__ __forceinline__ Wants<G> wants_of(const Args& a, int b) {
       const int lo = min(held[g], max(first[g], seen)), hi = min(held[g], max(need, lo));
       w.front[g] = lo - first[g];
       w.give[g] = w.front[g] + held[g] - hi;
-      w.take[g] = max(0, need - held[g]);
+      w.take[g] = w.n > 0 ? max(0, need - held[g]) : 0;
     }
   }
   w.c = ok ? (int)c : -1;

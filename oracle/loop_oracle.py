@@ -113,13 +113,13 @@ def plan(ctx, add, n_new, T, caches):
             tokens += n[b]
             run = n[b] == 0 or tokens <= T
             for g, k in enumerate(caches):
-                take = max(0, k.pages(rows[b] + n[b]) - int(held_before[g][b]))
+                take = max(0, k.pages(rows[b] + n[b]) - int(held_before[g][b])) if n[b] else 0
                 wanted[g] += take
                 run = run and (take == 0 or wanted[g] <= k.count)
         runs.append(run)
     for g, k in enumerate(caches):
         for b in range(B):
-            if not runs[b]:
+            if not runs[b] or n[b] == 0:
                 continue
             for j in range(int(held_before[g][b]), k.pages(rows[b] + n[b])):
                 k.count -= 1

@@ -142,3 +142,26 @@ def test_verify_drafted_tokens_far_down_in_both(M):  # noqa: F811
     d.check(t, telling=False)
     # (beside 1e30 a float64 sum of logarithms loses log u: the definition's count says nothing there)
     assert torch.all(t["count"] == 2) and M.dsv4_read_device_flags() == 0
+
+
+# ------------------------------------------------------------------------------------------------
+# requests without new tokens that hold too few pages
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("free", [1000, 3])
+def test_plan_requests_without_tokens_take_nothing(M, free):  # noqa: F811
+    """A request that brings no token takes no page and counts for nothing in the admission of those behind it, even where
+    it holds fewer pages than its rows need."""
+    q = Requests(60, 30, [(16, 1, 0), (8, 4, 0)], 500, 3, free, ended=0.0, fresh=0.0)
+    q.n[::3] = 0
+    q.T = int(q.n.sum()) + 5
+    for c in q.caches:
+        c.held[::3] = np.minimum(c.held[::3], 1)
+    held = [c.held.copy() for c in q.caches]
+    tables = [c.table.copy() for c in q.caches]
+    p, t = q.device(M)
+    M.dsv4_batch_plan(p)
+    q.check(t)
+    for i, d in enumerate(t["k"]):
+        np.testing.assert_array_equal(d["held_out"].cpu().numpy()[::3], held[i][::3])
+        np.testing.assert_array_equal(d["table"].cpu().numpy()[::3], tables[i][::3])
+    assert M.dsv4_read_device_flags() == 0
