@@ -23,11 +23,51 @@ int cuda_status(cudaError_t e) {
     if (!(cond)) return (code); \
   } while (0)
 
+// Rows of a dsv4_rope call: `heads` of each of T tokens, `row` bytes each (strides in bytes).
+struct Rows {
+  uintptr_t at;
+  int64_t token, head;
+  int T, heads;
+};
+
+// Whether rows of a and b share memory, for rows whose extents are apart, that begin at one place, or that have their strides
+// in common (parts of one buffer); rows of other buffers that are laid through one another are not looked into.
+bool rows_meet(Rows a, Rows b, int64_t row) {
+  const auto extent = [&](const Rows& r) { return (__int128)(r.T - 1) * r.token + (__int128)(r.heads - 1) * r.head + row; };
+  if (a.at + extent(a) <= b.at || b.at + extent(b) <= a.at) return false;
+  if (a.at == b.at) return true;
+  if (a.T == 1) a.token = b.token = INT64_MAX;
+  if (a.heads == 1) a.head = b.head;
+  if (b.heads == 1) b.head = a.head;
+  if (a.token != b.token || a.head != b.head || a.token <= 0) return false;
+  // the wider stride outside; b's rows against a's that lie j narrow strides on from the place where they would meet
+  const bool tokens_outside = a.token >= a.head;
+  const int64_t wide = tokens_outside ? a.token : a.head, narrow = tokens_outside ? a.head : a.token;
+  const int wide_a = tokens_outside ? a.T : a.heads, wide_b = tokens_outside ? b.T : b.heads;
+  const int narrow_a = tokens_outside ? a.heads : a.T, narrow_b = tokens_outside ? b.heads : b.T;
+  const int64_t off = (int64_t)(b.at - a.at), first = off / wide - (off % wide < 0);
+  for (int64_t k = first; k <= first + 1; ++k) {
+    if (k >= wide_a || -k >= wide_b) continue;
+    const int64_t rest = off - k * wide;  // between -wide and wide
+    if (narrow_a == 1 && narrow_b == 1) {
+      if (rest < row && -rest < row) return true;
+      continue;
+    }
+    if (narrow <= 0) return rest < row && -rest < row;
+    const int64_t j0 = rest / narrow - (rest % narrow < 0);
+    for (int64_t j = j0; j <= j0 + 1; ++j)
+      if (j < narrow_a && -j < narrow_b && rest - j * narrow < row && j * narrow - rest < row) return true;
+  }
+  return false;
+}
+
 // One tensor of a dsv4_rope call.
-int check_rope_rows(const void* x, const void* y, int heads, int T, const int64_t (&stride)[4]) {
+int check_rope_rows(const void* x, const void* y, int heads, int T, const int64_t (&stride)[4], int head_dim) {
   CHECK(heads >= 1 && heads <= 1024, DSV4_ERR_INVALID);
   for (int64_t s : stride) CHECK(s >= 0 && s % 8 == 0, DSV4_ERR_INVALID);
-  CHECK((stride[2] > 0 || T <= 1) && (stride[3] > 0 || heads == 1), DSV4_ERR_INVALID);
+  // rows of y lie apart from one another
+  CHECK((stride[2] >= head_dim || T <= 1) && (stride[3] >= head_dim || heads == 1), DSV4_ERR_INVALID);
+  CHECK(stride[2] != stride[3] || T <= 1 || heads == 1, DSV4_ERR_INVALID);
   if (T == 0) return DSV4_OK;
   CHECK(x && y && aligned(x, 16) && aligned(y, 16), DSV4_ERR_INVALID);
   CHECK(x != y || (stride[0] == stride[2] && stride[1] == stride[3]), DSV4_ERR_INVALID);
@@ -89,15 +129,26 @@ int dsv4_rope(const dsv4_rope_params* p, dsv4_stream_t stream) {
   CHECK((p->rope_halves == 0 || p->rope_halves == 1) && (p->inverse == 0 || p->inverse == 1), DSV4_ERR_INVALID);
   CHECK(std::isfinite(p->scale), DSV4_ERR_INVALID);
   int st = check_rope_rows(p->x, p->y, p->heads, p->T,
-                           {p->x_token_stride, p->x_head_stride, p->y_token_stride, p->y_head_stride});
+                           {p->x_token_stride, p->x_head_stride, p->y_token_stride, p->y_head_stride}, p->head_dim);
   CHECK(st == DSV4_OK, st);
   if (p->x2 != nullptr || p->y2 != nullptr) {
     st = check_rope_rows(p->x2, p->y2, p->heads2, p->T,
-                         {p->x2_token_stride, p->x2_head_stride, p->y2_token_stride, p->y2_head_stride});
+                         {p->x2_token_stride, p->x2_head_stride, p->y2_token_stride, p->y2_head_stride}, p->head_dim);
     CHECK(st == DSV4_OK, st);
-    CHECK(p->y != p->y2, DSV4_ERR_INVALID);
   }
   if (p->T == 0) return DSV4_OK;
+  const int64_t size = p->dtype == DSV4_F32 ? 4 : 2, row = p->head_dim * size;
+  const auto rows = [&](const void* at, int64_t token, int64_t head, int heads) {
+    return Rows{reinterpret_cast<uintptr_t>(at), token * size, head * size, p->T, heads};
+  };
+  const Rows x = rows(p->x, p->x_token_stride, p->x_head_stride, p->heads), y = rows(p->y, p->y_token_stride, p->y_head_stride, p->heads);
+  CHECK(p->x == p->y || !rows_meet(y, x, row), DSV4_ERR_INVALID);
+  if (p->x2 != nullptr) {
+    const Rows x2 = rows(p->x2, p->x2_token_stride, p->x2_head_stride, p->heads2);
+    const Rows y2 = rows(p->y2, p->y2_token_stride, p->y2_head_stride, p->heads2);
+    CHECK(p->x2 == p->y2 || !rows_meet(y2, x2, row), DSV4_ERR_INVALID);
+    CHECK(!rows_meet(y, x2, row) && !rows_meet(y2, x, row) && !rows_meet(y, y2, row), DSV4_ERR_INVALID);
+  }
   CHECK(p->positions && p->freqs && aligned(p->positions, 4) && aligned(p->freqs, 16), DSV4_ERR_INVALID);
   return cuda_status(launch_rope(*p, (cudaStream_t)stream));
 }

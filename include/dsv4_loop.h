@@ -69,14 +69,15 @@ int dsv4_rope_freqs(const dsv4_rope_freqs_params* p, uint64_t* freqs);
  * the gradient of the forward one: it turns the gradient of y into that of x.
  * A token with a negative position is skipped: its rows of y stay as they are.
  * A second tensor (the keys beside the queries) is turned in the same launch when x2 is given.
- * y is x itself (same strides: in place) or lies apart from x, x2 and y2; rows of one buffer may alternate.  Strides of x
- * may be 0 (a row for several heads or tokens).
+ * y is x itself (same strides: in place) or lies apart from x, x2 and y2, and y2 likewise; rows of one buffer may
+ * alternate.  Calls where they meet are refused where extents, or equal strides, tell.  Strides of x may be 0 (a row
+ * for several heads or tokens).
  * ------------------------------------------------------------------------------------------- */
 typedef struct dsv4_rope_params {
   uint32_t struct_size;
   const void* x;               /* [T, heads, head_dim] in dtype, 16-byte aligned */
   void* y;
-  int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride; /* elements, multiples of 8; y's over 0 */
+  int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride; /* elements, multiples of 8; y's head_dim or more */
   const void* x2;              /* [T, heads2, head_dim] or NULL */
   void* y2;
   int64_t x2_token_stride, x2_head_stride, y2_token_stride, y2_head_stride;
