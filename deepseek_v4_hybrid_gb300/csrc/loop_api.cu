@@ -193,6 +193,11 @@ int dsv4_batch_plan(const dsv4_batch_plan_params* p, dsv4_stream_t stream) {
                 (c.slots == nullptr || c.slots != o.slots) && (p->B == 0 || (c.block_table != o.block_table && c.held_out != o.held_out)) &&
                 (c.first_out == nullptr || c.first_out != o.first_out),
             DSV4_ERR_INVALID);
+      // ... and is not read for another: a request's numbers of all caches are read and written by one thread in turn
+      CHECK(c.free_count_out != o.free_count && o.free_count_out != c.free_count &&
+                (p->B == 0 || (c.held_out != o.held && o.held_out != c.held)) &&
+                (c.first == nullptr || c.first != o.first_out) && (o.first == nullptr || o.first != c.first_out),
+            DSV4_ERR_INVALID);
     }
   }
   return cuda_status(launch_batch_plan(*p, (cudaStream_t)stream));

@@ -130,7 +130,8 @@ int dsv4_rope_table(const dsv4_rope_table_params* p, dsv4_stream_t stream);
  *     ((position + 1) % ratio = 0), else -1.  From q_start[B] to T: -1 in all of them (dsv4_kv_insert skips
  *     such slots, dsv4_rope such positions).  Table entries that are given back stay as they were.
  * Every *_out may be its input (in place) or lie apart; apart from its input, the same call can be made again with
- * the same result.  Each cache has tables, counts, stack and slots of its own: two that name the same are refused.
+ * the same result.  What the call writes of a cache (table, held_out, first_out, stack, free_count_out, slots) belongs to
+ * no other: two that name the same, or one that reads what is written of another, are refused.
  * A request with ctx, ctx_add or n_new that gives c_b < 0, n_b < 0 or c_b + n_b over 2^30, more pages than
  * max_pages_per_seq, first and held not in 0 <= first <= held <= max_pages_per_seq, or a window that reaches rows before
  * first is flagged (bit 0) and left alone: no token, kv_len 0, ctx_out = ctx, nothing given back or taken.  A

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from test_gqa_abi import abi  # noqa: F401
-from test_loop_abi import refused, rope_params
+from test_loop_abi import plan_params, refused, rope_params
 
 BASE = 1 << 20
 
@@ -62,3 +62,23 @@ def test_rope_row_check_against_every_row(abi):  # noqa: F811
         assert status == (-1 if meet else -3), (T, nx, ny, head, token, off)
         seen[meet] += 1
     assert min(seen) > 500
+
+
+@pytest.mark.parametrize("in_place", [True, False], ids=["in place", "apart"])
+@pytest.mark.parametrize("order", [(0, 1), (1, 0)], ids=["first writes", "second writes"])
+@pytest.mark.parametrize("name", ["held", "first", "free_count"])
+def test_plan_refuses_caches_that_read_what_another_writes(abi, name, order, in_place):  # noqa: F811
+    """The numbers that one cache advances are the other's input (which is then read behind the store)."""
+    caches = []
+    for i in range(2):
+        at = 0x100000 * (i + 1)
+        caches.append(dict(page_size=64, ratio=1, window=8, max_pages_per_seq=8, num_pages=100, block_table=at + 0x1000,
+                           held=at + 0x2000, held_out=at + 0x2100, first=at + 0x2200, first_out=at + 0x2300,
+                           free_pages=at + 0x3000, free_count=at + 0x4000, free_count_out=at + 0x4100, slots=at + 0x5000))
+    writer, reader = caches[order[0]], caches[order[1]]
+    reader[name] = writer[name + "_out"]
+    if in_place:
+        writer[name] = writer[name + "_out"]
+    p = plan_params(abi, cache=caches[0], num_caches=2)
+    p.caches[1] = abi.PlanCache(**caches[1])
+    refused(abi, "dsv4_batch_plan", p)
