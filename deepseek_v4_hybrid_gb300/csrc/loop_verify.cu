@@ -36,22 +36,34 @@ constexpr float LOG2E_HI = (float)LOG2E, LOG2E_LO = (float)(LOG2E - (double)LOG2
 constexpr float MAX_F32 = 3.4028234663852886e38f, MAX_BF16 = 3.3895313892515355e38f;
 constexpr int NOWHERE = 0x7FFFFFFF;
 
-// Sums of a part of a row of logits: s = sum of 2^((z - m) c) against the reference m, one of the row's logits (-inf: the
-// part leaves nothing), and, for greedy sequences, whose m is the maximum, its first index.
-struct Stat {
-  float m, s;
-  int idx;
-};
+constexpr int U = 4;  // vectors of a block of a lane (scan), 32 vectors apart
 
-__device__ __forceinline__ void merge(Stat& a, const Stat& b, float c) {
+// Sums of a part of a row of logits, weights 2^((z - m) c) against the reference m, one of the row's logits (-inf: the part
+// leaves nothing): `top` of the lane's block that weighs most, s of all other elements.  A token of a probability p over a half
+// lies in that block, and -log p = log1p(rest / its weight): rest, the others' sum, would be lost in the roundings of a sum that
+// has the token in it.  `where` is the block's first element, and its vectors (0: that element alone) from bit 24 on.
+// For greedy sequences m is the maximum, and idx its first index.
+struct Stat {
+  float m, s, top;
+  int where, idx;
+};
+constexpr Stat NOTHING = {-INFINITY, 0.f, 0.f, 0, NOWHERE};
+
+__device__ __forceinline__ void merge(Stat& a, Stat b, float c) {
   if (b.m == -INFINITY) return;
+  if (a.m == -INFINITY) {
+    a = b;
+    return;
+  }
+  const float f = tc::ex2_approx(-fabsf(a.m - b.m) * c);
   if (b.m > a.m) {
-    a.s = b.s + (a.m == -INFINITY ? 0.f : a.s * tc::ex2_approx((a.m - b.m) * c));
-    a.m = b.m, a.idx = b.idx;
+    a.s *= f, a.top *= f, a.m = b.m, a.idx = b.idx;
   } else {
-    a.s += b.s * tc::ex2_approx((b.m - a.m) * c);
+    b.s *= f, b.top *= f;
     if (b.m == a.m) a.idx = min(a.idx, b.idx);
   }
+  a.s += b.s + fminf(a.top, b.top);
+  if (b.top > a.top) a.top = b.top, a.where = b.where;
 }
 
 // A logit as it counts: NaN as -inf, +inf as the type's largest value.
@@ -136,19 +148,19 @@ __device__ __forceinline__ float warp_top(float x) { return from_ordered(__reduc
 
 // Each thread streams its vectors through a ring of its own in shared memory: groups of asynchronous 16-byte copies,
 // all but one of them ahead of the one in use.  Nobody else reads them, so no barrier is needed.
-constexpr int U = 4;  // vectors of a group (scan)
 
-// The running numbers of a warp over a row: the reference m, one of its logits, and the lane's sum of 2^((z - m) c).
+// The running numbers of a warp over a row: the reference m, one of its logits, and the lane's sums of 2^((z - m) c): `top` of
+// the block of 32 elements (16 of fp32) that weighs most, begun at vector `at`, and s of the others.
 // Greedy sequences keep m at the maximum and each lane's first index of it; the others change it only when the sum of
-// a lane's 32 elements (16 of fp32) says that one lies above it by a binary order or two, which spares the search.  (An exponent's
-// argument y is off by |y| 2^-23, so the elements that make up the sum should have small ones: with logits 20 binary orders
-// above the reference, log-probabilities next to 0 were off by 8e-7.)
+// a block says that one lies above it by a binary order or two, which spares the search.  (An exponent's
+// argument y is off by |y| 2^-22, so the elements that make up the sum should have small ones.)
 // Elements are taken as they are: NaN and +inf make the sum NaN, and the part is then done again by the careful form.
 constexpr float FAR = 64.f;
+constexpr int FRONT = -1, BACK = -2;  // blocks of one element a lane, before and behind the whole vectors
 
 struct Run {
-  float m, s;
-  int idx;
+  float m, s, top;
+  int at, idx;
 };
 
 template <bool F32, int N>
@@ -165,7 +177,7 @@ __device__ __forceinline__ float weights(const Vec<F32> (&v)[N], float c, float 
 }
 
 template <bool F32, bool GREEDY, int N, typename I>
-__device__ __forceinline__ void add(Run& st, const Vec<F32> (&v)[N], float c, I index) {
+__device__ __forceinline__ void add(Run& st, const Vec<F32> (&v)[N], float c, int block, I index) {
   constexpr int E = Vec<F32>::E;
   bool look = GREEDY || st.m == -INFINITY;
   while (true) {  // (a loop, so that each part of the code is there once: what runs once a row waits for its instructions)
@@ -173,7 +185,10 @@ __device__ __forceinline__ void add(Run& st, const Vec<F32> (&v)[N], float c, I 
       const float top = top_of<F32, N>(v);
       if (__any_sync(0xffffffffu, top > st.m)) {
         const float m = warp_top(fmaxf(top, st.m));
-        if (st.m > -INFINITY) st.s *= tc::ex2_approx((st.m - m) * c);
+        if (st.m > -INFINITY) {
+          const float f = tc::ex2_approx((st.m - m) * c);
+          st.s *= f, st.top *= f;
+        }
         st.m = m;
         if (GREEDY) {
           st.idx = NOWHERE;
@@ -187,18 +202,20 @@ __device__ __forceinline__ void add(Run& st, const Vec<F32> (&v)[N], float c, I 
     }
     const float sum = weights<F32, N>(v, c, st.m == -INFINITY ? 0.f : st.m);
     if (look || !__any_sync(0xffffffffu, sum > FAR)) {
-      st.s += sum;
+      const bool higher = sum > st.top;
+      st.s += higher ? st.top : sum;
+      if (higher) st.top = sum, st.at = block;
       return;
     }
     look = true;
   }
 }
 
-// The careful form: one element, as it counts; s goes with m itself, the maximum.
+// The careful form: one element, as it counts; m is the maximum, and its first place the block of its own that is left out of s.
 __device__ __forceinline__ void add_careful(Stat& st, float z, int i, float c) {
   if (z == -INFINITY) return;
   if (z > st.m) {
-    st.s = (st.m == -INFINITY ? 0.f : st.s * tc::ex2_approx((st.m - z) * c)) + 1.f;
+    st.s = st.m == -INFINITY ? 0.f : (st.s + 1.f) * tc::ex2_approx((st.m - z) * c);
     st.m = z, st.idx = i;
   } else {
     st.s += tc::ex2_approx((z - st.m) * c);
@@ -231,14 +248,14 @@ __device__ __noinline__ Stat scan_row(const void* row, int lo, int hi, int share
   int j0 = share * BLOCK, ahead = j0, to = 0, use = 0;
 #pragma unroll
   for (int g = 0; g < DEPTH - 1; ++g, ahead += step, ++to) fetch(ahead, to);
-  Run st = {-INFINITY, 0.f, NOWHERE};
-  const auto one = [&](int i, bool there) {
+  Run st = {-INFINITY, 0.f, 0.f, FRONT, NOWHERE};
+  const auto one = [&](int i, bool there, int block) {
     Vec<F32> z[1];
     z[0].set(make_uint4(NONE<F32>, NONE<F32>, NONE<F32>, NONE<F32>));
     if (there) z[0].w[0] = F32 ? reinterpret_cast<const uint32_t*>(row)[i] : 0xFF800000u | reinterpret_cast<const uint16_t*>(row)[i];
-    add<F32, GREEDY, 1>(st, z, c, [&](int) { return i; });
+    add<F32, GREEDY, 1>(st, z, c, block, [&](int) { return i; });
   };
-  if (share == 0 && head > 0) one(lo + lane, lane < head);
+  if (share == 0 && head > 0) one(lo + lane, lane < head, FRONT);
   for (; j0 < vecs; j0 += step, ahead += step) {
     fetch(ahead, to);
     to = to == DEPTH - 1 ? 0 : to + 1;
@@ -256,14 +273,22 @@ __device__ __noinline__ Stat scan_row(const void* row, int lo, int hi, int share
         if (j0 + u * 32 + lane < vecs) z[u].set(block[u * NT]);
       }
     }
-    add<F32, GREEDY, U>(st, z, c, [&](int i) { return from + (j0 + i / E * 32 + lane) * E + i % E; });
+    add<F32, GREEDY, U>(st, z, c, j0, [&](int i) { return from + (j0 + i / E * 32 + lane) * E + i % E; });
   }
   tc::cp_async_wait<0>();
   const int tail = from + vecs * E;
-  if (share == 0 && tail < hi) one(tail + lane, tail + lane < hi);
-  const float s = warp_sum(st.s);
-  if (s == s) return Stat{st.m, s, GREEDY ? (int)__reduce_min_sync(0xffffffffu, (unsigned)st.idx) : NOWHERE};
-  Stat slow = {-INFINITY, 0.f, NOWHERE}, out;
+  if (share == 0 && tail < hi) one(tail + lane, tail + lane < hi, BACK);
+  const float top = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(st.top)));  // (none is negative or NaN)
+  const int owner = __ffs(__ballot_sync(0xffffffffu, st.top == top)) - 1;
+  const float s = warp_sum(lane == owner ? st.s : st.s + st.top);
+  if (s == s) {
+    const int first = st.at == FRONT ? lo + lane : st.at == BACK ? tail + lane : from + (st.at + lane) * E;
+    const int vectors = st.at < 0 ? 0 : min(U, (vecs - st.at - lane + 31) / 32);
+    const int where = __shfl_sync(0xffffffffu, first | vectors << 24, owner);
+    return Stat{st.m, s, top, top > 0.f ? where : 0,
+                GREEDY ? (int)__reduce_min_sync(0xffffffffu, (unsigned)st.idx) : NOWHERE};
+  }
+  Stat slow = NOTHING, out;
   const auto careful = [&](int i) { add_careful(slow, logit(element<F32>(row, i), F32), i, c); };
   if (share == 0 && lane < head) careful(lo + lane);
   for (int block = share * BLOCK; block < vecs; block += step)  // (the same part)
@@ -276,9 +301,23 @@ __device__ __noinline__ Stat scan_row(const void* row, int lo, int hi, int share
   if (share == 0 && tail + lane < hi) careful(tail + lane);
   __syncwarp();
   out.m = warp_top(slow.m);
-  out.s = warp_sum(slow.m == -INFINITY ? 0.f : slow.s * tc::ex2_approx((slow.m - out.m) * c));
-  out.idx = (int)__reduce_min_sync(0xffffffffu, slow.m == out.m ? (unsigned)slow.idx : (unsigned)NOWHERE);
+  const bool leads = slow.m == out.m && out.m > -INFINITY;
+  const int places = __popc(__ballot_sync(0xffffffffu, leads));  // (lanes that have the maximum)
+  const float others = leads ? slow.s : slow.m == -INFINITY ? 0.f : (slow.s + 1.f) * tc::ex2_approx((slow.m - out.m) * c);
+  out.s = warp_sum(others) + fmaxf((float)places - 1.f, 0.f);
+  out.top = places ? 1.f : 0.f;
+  out.idx = (int)__reduce_min_sync(0xffffffffu, leads ? (unsigned)slow.idx : (unsigned)NOWHERE);
+  out.where = places ? out.idx : 0;
   return out;
+}
+
+// What lane `lane` has of the block that weighs most in a row: the element's index (-1: none).
+template <bool F32>
+__device__ __forceinline__ int of_block(const Stat& st, int lane) {
+  constexpr int E = Vec<F32>::E;
+  const int first = st.where & 0xFFFFFF, vectors = st.where >> 24;
+  if (vectors == 0) return lane == 0 ? first : -1;
+  return lane / E < vectors ? first + lane / E * (32 * E) + lane % E : -1;
 }
 
 // What turns an element of a row into its probability.
@@ -310,9 +349,14 @@ __device__ __forceinline__ bool keeps(float u, float z, const Stat& p, float y, 
   const float e = (fmaf(dp, r.hi, -a) + dp * r.lo) - (fmaf(dq, r.hi, -b) + dq * r.lo), d = a - b, sum = d + e;
   if (!(fabsf(sum) < 150.f)) {  // (NaN too)
     const double far = (((double)z - p.m) - ((double)y - q.m)) * r.hi;
-    return u < tc::ex2_approx((float)fmin(fmax(far, -1000.0), 1000.0)) * (q.s / p.s);
+    return u < tc::ex2_approx((float)fmin(fmax(far, -1000.0), 1000.0)) * ((q.s + q.top) / (p.s + p.top));
   }
-  return u < tc::ex2_approx(sum) * fmaf((d - sum) + e, LN2F, 1.f) * (q.s / p.s);
+  return u < tc::ex2_approx(sum) * fmaf((d - sum) + e, LN2F, 1.f) * ((q.s + q.top) / (p.s + p.top));
+}
+
+__device__ __forceinline__ Law law_from(const void* row, bool f32, bool probs, const Stat& st) {
+  const float sum = st.s + st.top;
+  return Law{row, f32, probs, st.m, sum > 0.f ? 1.f / sum : 0.f};
 }
 
 __device__ __forceinline__ float law_of(const Law& l, float x, const Rate& r) {
@@ -320,10 +364,17 @@ __device__ __forceinline__ float law_of(const Law& l, float x, const Rate& r) {
   return l.m == -INFINITY ? 0.f : weight(logit(x, l.f32), l.m, r) * l.inv;
 }
 
-// log p of an element: of the probability itself, whose error stays that of a weight (a difference of two logarithms has
-// the error of the larger, and p may be next to 1); where it is too small for that, of its parts.
-__device__ __forceinline__ float log_of(const Law& l, float x, const Rate& r, float temp) {
+// log p of element i, x, by a warp: over a half from the sum of the other weights, for which each lane has an element y, of index
+// j, of the row's heaviest block (error against float64 5e-7 of log p at worst; 7e-4 where p is 0.9995 from a sum with p in it:
+// 2 x 4 rows 11.1 to 11.5 us, 256 x 5 rows 132 to 134, greedy ones 66 to 71); else of the probability itself, whose error stays that of a weight (a difference of two
+// logarithms has the error of the larger); where it is too small for that, of its parts.
+__device__ __noinline__ float log_of(bool f32, bool probs, Stat st, float x, int i, float y, int j, Rate r, float temp) {
+  const Law l = law_from(nullptr, f32, probs, st);
   const float p = law_of(l, x, r);
+  if (!l.probs && p > 0.5f && __any_sync(0xffffffffu, j == i)) {
+    const float rest = st.s + warp_sum(j < 0 || j == i ? 0.f : weight(y, st.m, r));
+    return -log1pf(rest / weight(logit(x, l.f32), st.m, r));
+  }
   return l.probs || p > 1e-30f ? logf(p) : (logit(x, l.f32) - l.m) / temp + logf(l.inv);
 }
 
@@ -475,7 +526,8 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
   __shared__ Stat part[NW], got[2][2 * MAX_ROWS][MAX_CLUSTER];
   __shared__ Best bpart[NW], bgot[2][MAX_CLUSTER];
   __shared__ Stat fin[2 * MAX_ROWS];
-  __shared__ int stands[MAX_ROWS], top_key, brought_part[NW];
+  __shared__ int stands[MAX_ROWS], top_key, brought_part[NW], drafted[MAX_ROWS];
+  __shared__ float drafted_x[MAX_ROWS];
   if (tid == 0) top_key = 0;
   pdl_wait();
   pdl_launch_dependents();
@@ -527,6 +579,15 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
   int last = -1, par = 0;  // the row that the sequence's last token comes from
   bool all = false, residual = false;
   Law lp = {}, lq = {};
+  const bool logs = rank == 0 && logp != nullptr && target_task;
+  int last_warp = 0, j = -1;
+  float y = 0.f;
+  const auto write = [&](int i, int token, float z) {  // a warp's row's token
+    if (lane == 0) out[i] = token;
+    if (!logp) return;
+    const float l = log_of(F32, p.target_probs != 0, target_task ? fin[warp * tasks_a_row] : Stat{}, z, token, y, j, rate, temp);
+    if (lane == 0) logp[i] = l;
+  };
   Best best = {0.f, NOWHERE, 0.f};
   for (int i0 = 0; last < 0; i0 += a.rows) {
     const int rows = min(a.rows, n - i0), tasks = rows * tasks_a_row;
@@ -562,7 +623,7 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
         }
         const bool f32 = is_target ? F32 : df32;
         const void* row = is_target ? at(p.target, t * p.target_stride, F32) : at(p.draft, d * p.draft_stride, df32);
-        Stat st = {-INFINITY, 0.f, NOWHERE};
+        Stat st = NOTHING;
         if (d >= 0) {
           if (greedy)
             st = f32 ? scan_row<NT, DEPTH, true, true>(row, lo, hi, share, shares, rate.hi, ring)
@@ -594,11 +655,15 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
       __syncthreads();
       par ^= 1;
     }
-    float l_m = 0.f, l_s = 1.f;
+    // warp w has row w's heaviest block brought, for the logarithm of the row's token
+    y = -INFINITY, j = -1;
+    if (logs && warp < rows) {
+      j = of_block<F32>(fin[warp * tasks_a_row], lane);
+      if (j >= 0) y = logit(element<F32>(at(p.target, (t0 + i0 + warp) * p.target_stride, F32), j), F32);
+    }
     if (tid < rows) {
       const Stat ts = target_task ? fin[tid * tasks_a_row] : Stat{};
       const Stat ds = draft_task ? fin[tid * tasks_a_row + tasks_a_row - 1] : Stat{};
-      l_m = ts.m, l_s = ts.s;
       bool ok = false;
       if (x >= 0) {
         if (greedy) {
@@ -606,17 +671,18 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
         } else if (draft_task && !p.target_probs) {
           ok = qrow >= 0 && keeps(ux, logit(zx, F32), ts, logit(yx, df32), ds, rate);
         } else {
-          const Law law = {nullptr, F32, p.target_probs != 0, ts.m, ts.s > 0.f ? 1.f / ts.s : 0.f};
+          const Law law = law_from(nullptr, F32, p.target_probs != 0, ts);
           const float px = law_of(law, zx, rate);
           if (!drafted_law) {
             ok = ux < px || (ux == 0.f && !p.target_probs && logit(zx, F32) > -INFINITY);
           } else if (qrow >= 0) {
-            const Law dlaw = {nullptr, df32, p.draft_probs != 0, ds.m, ds.s > 0.f ? 1.f / ds.s : 0.f};
+            const Law dlaw = law_from(nullptr, df32, p.draft_probs != 0, ds);
             ok = ux * law_of(dlaw, yx, rate) < px;
           }
         }
       }
       stands[tid] = ok;
+      drafted[tid] = x, drafted_x[tid] = zx;
     }
     __syncthreads();
     int stay = 0;
@@ -627,20 +693,18 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
       all = last == n - 1;
       const Stat ts = target_task ? fin[stay * tasks_a_row] : Stat{};
       if (greedy && ts.m > (p.target_probs ? 0.f : -INFINITY)) best = Best{0.f, ts.idx, ts.m};
-      lp = Law{at(p.target, t * p.target_stride, F32), F32, p.target_probs != 0, ts.m, ts.s > 0.f ? 1.f / ts.s : 0.f};
+      lp = law_from(at(p.target, t * p.target_stride, F32), F32, p.target_probs != 0, ts);
+      last_warp = stay;
       if (drafted_law && !all) {
         const int64_t d = draft_row_of(t);
         if (d >= 0 && d < p.draft_rows) {
           const Stat ds = draft_task ? fin[stay * tasks_a_row + tasks_a_row - 1] : Stat{};
-          lq = Law{at(p.draft, d * p.draft_stride, df32), df32, p.draft_probs != 0, ds.m, ds.s > 0.f ? 1.f / ds.s : 0.f};
+          lq = law_from(at(p.draft, d * p.draft_stride, df32), df32, p.draft_probs != 0, ds);
           residual = true;
         }
       }
     }
-    if (rank == 0 && tid < stay) {
-      out[i0 + tid] = x;
-      if (logp) logp[i0 + tid] = log_of(Law{nullptr, F32, p.target_probs != 0, l_m, __fdividef(1.f, l_s)}, zx, rate, temp);
-    }
+    if (last < 0 && rank == 0 && warp < rows) write(i0 + warp, drafted[warp], drafted_x[warp]);
     __syncthreads();  // fin and stands are free again
   }
 
@@ -672,10 +736,12 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
   }
   if (rank != 0) return;
   const bool found = best.idx != NOWHERE;
-  for (int i = last + tid; i < p.max_q_len; i += NT) {
-    const bool here = i == last && found;
-    out[i] = here ? best.idx : -1;
-    if (logp) logp[i] = here ? log_of(lp, best.x, rate, temp) : 0.f;
+  const bool kept = warp < last_warp;  // (of the last group, whose rows the warps still have)
+  if (kept || (warp == last_warp && found))
+    write(last - last_warp + warp, kept ? drafted[warp] : best.idx, kept ? drafted_x[warp] : best.x);
+  for (int i = last + found + tid; i < p.max_q_len; i += NT) {
+    out[i] = -1;
+    if (logp) logp[i] = 0.f;
   }
   if (tid == 0) p.n_out[b] = last + (found ? 1 : 0);
 }

@@ -165,3 +165,58 @@ def test_plan_requests_without_tokens_take_nothing(M, free):  # noqa: F811
         np.testing.assert_array_equal(d["held_out"].cpu().numpy()[::3], held[i][::3])
         np.testing.assert_array_equal(d["table"].cpu().numpy()[::3], tables[i][::3])
     assert M.dsv4_read_device_flags() == 0
+
+
+# ------------------------------------------------------------------------------------------------
+# log-probabilities next to 0
+# ------------------------------------------------------------------------------------------------
+def near_one(V, dtype, left, places, temp, stride=0, seed=80):
+    """Two sequences a case: a drafted token that is nearly certain, then a last row with a nearly certain token; `left` is
+    the probability of all others."""
+    n = [2] * len(places)
+    d = Drafts(seed, n, V, dtype, dtype, stride=stride)
+    d.temp.fill_(temp)
+    for b, x in enumerate(places):
+        for t, y in ((2 * b, x), (2 * b + 1, V - 1 - x)):
+            row = d.target[t].double() / temp
+            row[y] = -float("inf")
+            others = float(torch.logsumexp(row, 0))
+            top = (others + np.log((1 - left) / left)) * temp
+            d.target[t, y] = float(top)
+        d.tokens[2 * b + 1] = x
+        d.draft[b, x] = d.target[2 * b, x]
+    d.u.mul_(0.4)
+    return d
+
+
+@pytest.mark.parametrize("greedy", [False, True], ids=["drawn", "greedy"])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("left", [0.3, 0.02, 1e-3, 1e-5, 1e-8])
+@pytest.mark.parametrize("V,stride", [(40, 0), (2000, 3), (32000, 0), (100003, 1)])
+def test_verify_log_probabilities_near_0(M, V, stride, left, dtype, greedy):  # noqa: F811
+    """log p = -log(1 + rest / w) is as exact relatively as the other weights' sum.  Of each of these the exponent's
+    argument y is off by |y| 2^-22 (a difference, a factor and its own rounding), the special function by 2^-22; V / 512
+    additions a lane and 32 after them, the division and the logarithm round once or twice each."""
+    places = [0, 1, V - 1, V - 2, V // 2, 7, 8, V // 3]
+    d = near_one(V, dtype, left, places, 1.0 if greedy else 0.8, stride)
+    if greedy:
+        d.temp.fill_(0.0)
+    p, t = d.device(M)
+    M.dsv4_draft_verify(p)
+    out, count, lp, _ = d.want()
+    got = f64(t["logp"])
+    rows = f64(d.target)
+    sure = 0
+    for b in range(d.B):
+        if count[b] != 2 or int(t["count"][b]) != 2:
+            continue
+        np.testing.assert_array_equal(t["out"][b].cpu().numpy(), out[b])
+        for i in range(2):
+            if lp[b, i] < -0.69:
+                continue
+            z = rows[2 * b + i]
+            orders = (z.max() - z.min()) / (1.0 if greedy else 0.8) / np.log(2)
+            rel = 2.0 ** -20 + orders * np.log(2) * 2.0 ** -22 + (V / 512 + 40) * 2.0 ** -24
+            assert abs(got[b, i] - lp[b, i]) <= rel * abs(lp[b, i]), (b, i, got[b, i], lp[b, i])
+            sure += 1
+    assert sure >= (0 if left == 0.3 and dtype == BF16 else d.B)
