@@ -38,8 +38,10 @@ extern "C" {
  *                     c(b) = rope_dim ln(original_len / (2 pi b)) / (2 ln theta)
  *   DSV4_ROPE_BANDS   f_i ((1 - m_i) / factor + m_i),
  *                     m_i = clamp((original_len f_i / (2 pi) - low_turns) / (high_turns - low_turns), 0, 1)
- * freqs[i] = f_i / (2 pi) as a binary fraction of 64 bits: position * freqs[i] mod 2^64 is the angle, reduced to one
- * turn without a rounding, so an angle is off by position * f_i * 2^-51 at most, whatever the position.
+ * freqs[i] = f_i / (2 pi) as a binary fraction of 64 bits, cut: position * freqs[i] mod 2^64 is the angle, reduced to one
+ * turn without a rounding, so an angle is off by position * (k theta^(-2 i / rope_dim) 2^-53 + 2 pi 2^-64) at most, whatever
+ * the position, with k = 2 ln(theta) + 8 (theta as it is used; BANDS: times 1 + high_turns / (high_turns - low_turns)): the
+ * roundings of f_i in fp64, and a step of the fraction, which is the larger part for small frequencies.
  * ------------------------------------------------------------------------------------------- */
 #define DSV4_ROPE_NONE 0
 #define DSV4_ROPE_LINEAR 1
