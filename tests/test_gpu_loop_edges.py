@@ -220,3 +220,113 @@ def test_verify_log_probabilities_near_0(M, V, stride, left, dtype, greedy):  # 
             assert abs(got[b, i] - lp[b, i]) <= rel * abs(lp[b, i]), (b, i, got[b, i], lp[b, i])
             sure += 1
     assert sure >= (0 if left == 0.3 and dtype == BF16 else d.B)
+
+
+# ------------------------------------------------------------------------------------------------
+# offsets past 32 bits, and the plan under the layers that its ratios and windows are for
+# ------------------------------------------------------------------------------------------------
+def test_verify_every_operand_past_32_bits(M):  # noqa: F811
+    """Target, draft and noise rows that decide lie behind 2^32 elements each: indices wrapped to 32 bits, signed or
+    not, would read the rows of the others."""
+    V = 1000
+    d = Drafts(90, [3, 3, 3], V, BF16, BF16)
+    for name, stride in (("target", (1 << 29) + 8), ("draft", (1 << 30) - 8), ("noise", (1 << 31) + 4)):
+        x = getattr(d, name)
+        big = torch.empty((x.shape[0] - 1) * stride + V, dtype=x.dtype, device="cuda").as_strided(x.shape, (stride, 1))
+        big.copy_(x)
+        setattr(d, name, big)
+        assert (x.shape[0] - 1) * stride > 1 << 32
+    d.u.mul_(0.5)
+    _, count = d.run(M)
+    assert count[2] >= 2  # (the last sequence comes to its second draft, whose row is the last)
+
+
+@pytest.mark.parametrize("ratio,coff", [(4, 2), (128, 1)], ids=["ratio4", "ratio128"])
+def test_plan_under_the_compressed_layers(M, ratio, coff):  # noqa: F811
+    """Tables and slots of a windowed and a compressed cache under the layers that read them: the insert by slot, the
+    compressor, the attention over window and entries.  Beside the same calls over tables that give every sequence pages of
+    its own, where nothing is ever given back: rows that are seen, entries and outputs are the same bits, over a captured
+    step whose drafts are cut back, with a pool that just holds what the window needs and a request that makes place for another."""
+    B, n, page, window, steps, H = 3, 4, 64, 128, 110, 2
+    most, width = steps * n + n, steps * n // page + 2
+    T = B * n
+    g = torch.Generator(device="cuda").manual_seed(ratio)
+    rng = np.random.default_rng(ratio)
+    new = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    cos_sin = torch.empty((most + 1, 64), device="cuda")
+    M.dsv4_rope_table(M.rope_table_params(cos_sin, M.rope_freqs(64)))
+    ctx, add, count = new(B), new(B), torch.full((B,), n, dtype=torch.int32, device="cuda")
+    q_start, kv_len, pos = new(B + 1), new(B), new(T)
+    caches, sides = [], []
+    for r, w, pages in ((1, window, 4 * B), (ratio, 0, B * (most // ratio // page + 1))):
+        k = {"table": torch.full((B, width), -1, dtype=torch.int32, device="cuda"), "held": new(B), "first": new(B), "pages": pages,
+             "stack": torch.randperm(pages, generator=g, device="cuda").int(), "count": torch.tensor([pages], dtype=torch.int32, device="cuda"),
+             "slots": new(T, dt=torch.int64)}
+        caches.append(M.plan_cache(k["table"], k["held"], k["stack"], k["count"], page, ratio=r, window=w, slots=k["slots"],
+                                   first=k["first"] if w else None))
+        sides.append(k)
+    plan = M.batch_plan_params(ctx, count, q_start, kv_len, caches, ctx_add=add, ctx_out=ctx, positions=pos)
+    kv = new(T, 576, dt=BF16)
+    score, q = torch.empty((T, 2 * coff * 576), device="cuda"), new(T, H, 576, dt=BF16)
+    weight = torch.ones(576, device="cuda")
+
+    class Layer:
+        def __init__(self, tables, slots, pages):
+            self.tables, self.slots = tables, slots
+            self.swa, self.main = (torch.full((p, page, 576), float("nan"), dtype=BF16, device="cuda") for p in pages)
+            self.state = torch.zeros((B, coff * ratio, 2 * coff * 576), device="cuda")
+            self.out, self.lse = torch.zeros((T, H, 512), device="cuda"), torch.zeros((T, H), device="cuda")
+            self.p = M.sparse_mla_params(q, M.BF16, pos, n, self.swa, tables[0], self.main, tables[1], M.BF16, page, ratio, window,
+                                         None, None, 576 ** -0.5, self.out, M.F32, self.lse, most)
+            self.ws = torch.empty(max(256, M.dsv4_sparse_mla_decode_workspace_bytes(self.p)), dtype=torch.uint8, device="cuda")
+            self.p.workspace, self.p.workspace_bytes = self.ws.data_ptr(), self.ws.numel()
+
+        def run(self):
+            M.dsv4_kv_insert(kv, M.BF16, self.slots, self.swa, M.BF16, page, positions=pos, cos_sin=cos_sin)
+            M.dsv4_compress_update(score, pos, n, ratio, coff, self.state, None, weight, 1e-6, cos_sin, self.main, M.BF16,
+                                   self.tables[1], page)
+            M.dsv4_sparse_mla_decode(self.p)
+
+    planned = Layer([k["table"] for k in sides], sides[0]["slots"], [k["pages"] for k in sides])
+    own = torch.arange(B * width, dtype=torch.int32, device="cuda").view(B, width)
+    plain = Layer([own, own], new(T, dt=torch.int64), [B * width] * 2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.dsv4_batch_plan(plan)
+        planned.run()
+    kept, given = np.zeros(B, int), 0
+    for step in range(steps):
+        if step == steps // 2:  # sequence 1 ends; another takes its place
+            ctx[1], add[1], before = 0, 0, count.clone()
+            ctx.add_(add), add.zero_(), count.zero_()
+            M.dsv4_batch_plan(plan)
+            assert int(kv_len[1]) == 0 and int(sides[0]["held"][1]) == 0
+            count.copy_(before)
+            kept = ctx.cpu().numpy().astype(int)
+            for layer in (planned, plain):
+                layer.state[1] = 0
+        else:
+            kept = kept + add.cpu().numpy()
+        kv.normal_(generator=g), score.normal_(generator=g), q.normal_(generator=g)
+        graph.replay()
+        at = kept[:, None] + np.arange(n)
+        np.testing.assert_array_equal(pos.cpu().numpy().reshape(B, n), at)
+        plain.slots.copy_(ints((np.arange(B)[:, None] * width * page + at).ravel(), torch.int64))
+        plain.run()
+        tables = [k["table"].cpu().numpy() for k in sides]
+        for b in range(B):
+            seen = np.arange(max(0, kept[b] - window + 1), kept[b] + n)
+            entries = np.arange((kept[b] + n) // ratio)
+            for rows, table, mine, theirs in ((seen, tables[0], planned.swa, plain.swa), (entries, tables[1], planned.main, plain.main)):
+                x = mine[ints(table[b, rows // page], torch.long), ints(rows % page, torch.long)]
+                y = theirs[ints(own[b].cpu().numpy()[rows // page], torch.long), ints(rows % page, torch.long)]
+                assert torch.equal(x, y) and not x.isnan().any(), (step, b)
+        done = (at + 1) % ratio == 0
+        want = np.where(done, np.take_along_axis(tables[1], at // ratio // page, 1).astype(np.int64) * page + at // ratio % page, -1)
+        np.testing.assert_array_equal(sides[1]["slots"].cpu().numpy().reshape(B, n), want)
+        assert torch.equal(planned.out, plain.out) and torch.equal(planned.lse, plain.lse), step
+        given = max(given, int(sides[0]["first"].max()))
+        add.copy_(ints(rng.integers(2, n + 1, B)))
+    assert given >= 2 and M.dsv4_read_device_flags() == 0
+    for k in sides:
+        assert int(k["count"]) + int((k["held"] - k["first"]).sum()) == k["pages"]
