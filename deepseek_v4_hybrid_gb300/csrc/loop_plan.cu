@@ -5,8 +5,8 @@
 // cluster, whose items find their request by a binary search.  Two cluster barriers: pages given back lie on the stack
 // before pages are taken from it, and tables are complete before slots are read from them.
 // Bound by latency: a launch, the loads of a request's numbers, the sums, page, table and slot in turn.  64 requests with
-// four tokens each 5.4 us; 1000 requests in three caches 13.3 us (15.3 with the caches one after the other); 65k prompt
-// tokens 11.3 us (1 MB written).
+// four tokens each 5.5 us; 1000 requests in three caches 13.3 us (15.3 with the caches one after the other); 65k prompt
+// tokens 11.4 us (1 MB written, by eight SMs).
 #include <cooperative_groups.h>
 
 #include "loop_common.cuh"
@@ -383,9 +383,11 @@ cudaError_t launch_batch_plan(const dsv4_batch_plan_params& p, cudaStream_t s) {
     a.page[g] = loop::Div::by(p.caches[g].page_size);
     a.ratio[g] = loop::Div::by(p.caches[g].ratio);
   }
-  // Eight CTAs whatever the size (64 requests with four tokens each 0.3 us less than with one CTA; 65k tokens of 300 prompts
-  // 11 us, 45 with one), of more threads where lists are long (4000 requests 20 us with 1024 threads a CTA, 38 with 256;
-  // 64 requests 0.7 us more, the barriers of idle warps).
+  // Eight CTAs whatever the size (64 requests with four tokens each 5.45 us, 5.65 with one CTA; 65k tokens of 300 prompts 11.4,
+  // 16 with four and 44 with one), of more threads where lists are long; with 256, 512 and 1024 threads a CTA
+  //   requests of 4 tokens, one cache: 64 5.5, 5.7, 6.1 us; 512 6.6, 7.5, 8.2; 1000 7.8, 8.3, 10.9; 2048 12.3, 9.9, 12.1; 4000 25.6, 16.3, 14.9
+  //   1000 requests in three caches: 15.0, 13.3, 13.9
+  //   60 prompts of 8k tokens in all: 5.0, 5.5, 7.0; 16k 6.4, 5.8, 7.4; 20k 7.4, 7.0, 7.3; 32k 8.7, 7.1, 7.4; 65k 13.6, 9.7, 9.9; 131k 23.2, 15.5, 14.4
   const int cluster = 8, threads = p.B > 2048 || p.T > 32768 ? 1024 : p.B > 512 || p.T > 16384 ? 512 : 256;
   switch (p.num_caches) {
     case 1: return launch_plan<1>(a, cluster, threads, s);

@@ -8,7 +8,8 @@
 // A thread owns 16 bytes (with halves, and the 16 of their partners) of a token's heads and turns that chunk of head after
 // head; the block computes each token's angles once, while the first chunks are on their way.
 // Bound by HBM: 16384 tokens of 72 heads of 128 bf16 (604 MB) 88 us, 6.8 TB/s; 4096 of 32 heads of 128 fp32 (134 MB) 22 us; 9377
-// of 24 heads of 64, half turned (58 MB), 13 us; 48 tokens 2.8 us, a launch; a table of 131072 rows of 64 (34 MB) 8.6 us.
+// of 24 heads of 64, half turned (58 MB), 13 us; 48 tokens 2.8 us from a graph, a launch (called one by one from
+// Python 3.4, the host's time); a table of 131072 rows of 64 (34 MB) 8.6 us.
 #include "loop_common.cuh"
 
 namespace dsv4 {

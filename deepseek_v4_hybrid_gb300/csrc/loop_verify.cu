@@ -7,15 +7,14 @@
 // for the race argmax r(x) / noise(x), whose winners are exchanged the same way.  Rows behind that group are not read.
 //
 // Two CTAs of 256 threads an SM with six groups of copies on their way each (512 threads, four groups: 256 x 5 rows of
-// 131072 logits 158 us for 126, 64 x 4 rows 33 for 35.5; three CTAs with four groups 159 and 42).  Large batches are bound
-// by HBM: 256 x 5 rows of 131072 bf16 logits of both models 130 us, of which the 650 to 700 MB that the drafts that stand make
-// it read take 100 at the copy rate.  Smaller ones by a chain of phases, each waiting for the one before: launch and first
-// loads (2 us), rows, exchange and decision (3 us), race, exchange; 2 x 4 rows of 32000 fp32 logits 10.7 us, 64 x 4 rows of
-// 131072 bf16 logits with fp32 probabilities of the draft 35.8 us (104 MB), 200 x up to 3 rows of 100003 43.7 us.
-// Code that runs once a sequence waits for its instructions to be fetched: parts that were inlined twice are loops
-// (256 x 5 rows 131 -> 126 us, 400 x 4 rows of 8000 37 -> 30).  Exponents are taken of differences from a logit, in two
-// instructions for one fused product against an integer: 3 % of the largest call, but no range that logits or low
-// temperatures could leave (temperature 1e-6: 44 us for 441).
+// 131072 logits 171 us for 133, 64 x 4 rows 44 for 36; three CTAs with four groups 173 and 43).  Large batches are bound
+// by HBM: 256 x 5 rows of 131072 bf16 logits of both models 133 us, of which the 651 MB that the drafts that stand make
+// it read take 96 at the copy rate.  Smaller ones by a chain of phases, each waiting for the one before: launch and first
+// loads (2 us), rows, exchange and decision (3 us), race, exchange; 2 x 4 rows of 32000 fp32 logits 11.7 us, 64 x 4 rows of
+// 131072 bf16 logits with fp32 probabilities of the draft 36.4 us (103 MB), 200 x up to 3 rows of 100003 45.5 us.
+// Code that runs once a sequence waits for its instructions to be fetched: parts that would be inlined twice are loops.
+// Exponents are taken of differences from a logit, in two instructions for one fused product against an integer, which
+// leaves no range that logits or low temperatures could leave.
 #include <cooperative_groups.h>
 
 #include "loop_common.cuh"
@@ -366,7 +365,7 @@ __device__ __forceinline__ float law_of(const Law& l, float x, const Rate& r) {
 
 // log p of element i, x, by a warp: over a half from the sum of the other weights, for which each lane has an element y, of index
 // j, of the row's heaviest block (error against float64 5e-7 of log p at worst; 7e-4 where p is 0.9995 from a sum with p in it:
-// 2 x 4 rows 11.1 to 11.5 us, 256 x 5 rows 132 to 134, greedy ones 66 to 71); else of the probability itself, whose error stays that of a weight (a difference of two
+// 2 x 4 rows of 32000 0.6 us, 256 x 5 rows of 131072 2 of 133, greedy ones 5 of 71); else of the probability itself, whose error stays that of a weight (a difference of two
 // logarithms has the error of the larger); where it is too small for that, of its parts.
 __device__ __noinline__ float log_of(bool f32, bool probs, Stat st, float x, int i, float y, int j, Rate r, float temp) {
   const Law l = law_from(nullptr, f32, probs, st);
@@ -518,6 +517,7 @@ struct Args {
 template <int NT, int DEPTH, int CTAS, bool F32>
 __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant__ Args a) {
   constexpr int NW = NT / 32;
+  static_assert(MAX_ROWS <= NW, "a warp a row of a group");
   const dsv4_draft_verify_params& p = a.p;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), rank = cluster.block_rank(), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -534,8 +534,8 @@ __global__ void __launch_bounds__(NT, CTAS) verify_kernel(const __grid_constant_
   const int t0 = p.q_start[b], t1 = p.q_start[b + 1];
   float temp = p.temperature ? p.temperature[b] : 1.f;
   // Draft rows in order: one for every token but the first of each sequence, so the row of token t + 1 is t less the sequences
-  // before b that brought any token.  (The loads lie beside those above: 2 x 4 rows 10.8 to 11.1 us, 256 x 5 rows no change, 8000 x
-  // 2 rows of 100 logits 215 to 245.)
+  // before b that brought any token.  (The loads lie beside those above: 2 x 4 rows 0.3 us, 256 x 5 rows nothing, 8000 x 2 rows of 100
+  // logits 261 us for 239 with rows given by name.)
   if (p.draft != nullptr && p.draft_row == nullptr) {
     int brought = 0;
 #pragma unroll 8
@@ -771,13 +771,14 @@ cudaError_t launch(const Args& a, int cluster, cudaStream_t s) {
 
 cudaError_t launch_draft_verify(const dsv4_draft_verify_params& p, cudaStream_t s) {
   if (p.B == 0) return cudaSuccess;
-  // As many CTAs a sequence as the SMs can hold at once, two each (2 sequences of 32000 logits: 8 CTAs 10.6 us, 1 26; 64 of
-  // 131072 with probabilities of the draft: 4 CTAs 35.5 us, 2 37, 8 43; 200 of 131072: 1 CTA 98 us, 2 109),
-  // of 4000 logits a row at least (22 sequences of 4000: 1 CTA 9.4 us, 8 13.5; of 16000: 4 CTAs 11.6, 8 12.0, 1 16.3).
+  // As many CTAs a sequence as the SMs can hold at once, two each (2 sequences of 32000 logits: 8 CTAs 11.7 us, 4 14.0, 1 28;
+  // 64 of 131072 with probabilities of the draft: 4 CTAs 36.3 us, 2 41.7, 8 45.4; 200 x 4 rows of 131072: 1 CTA 103 us, 2 113, but 200
+  // x up to 3 rows of 100003, half of them greedy, 45 and 40),
+  // of 4000 logits a row at least (22 sequences of 4000: 1 CTA 10.1 us, 2 11.7, 8 14.5; of 16000: 4 CTAs 12.4, 8 13.1, 1 17.5).
   int cluster = 1;
   while (cluster < loop::MAX_CLUSTER && (int64_t)p.B * cluster * 2 <= 2 * num_sms() && p.vocab >= 8000 * cluster) cluster *= 2;
   // Rows in one group share the exchange between the CTAs and their waits (400 sequences of 8000 logits, four rows each:
-  // 8 rows a group 30 us, 1 45), but all of them are read (256 of 131072, five rows each: 8 rows a group 153 us, 1 126):
+  // 8 rows a group 31.8 us, 1 52.5), but all of them are read (256 of 131072, five rows each: 8 rows a group 159 us, 1 133):
   // rows of 131072 logits a CTA in all.
   const int slice = (p.vocab + cluster - 1) / cluster, rows = 131072 / slice;
   const loop::Args a = {p, rows < 1 ? 1 : rows > loop::MAX_ROWS ? loop::MAX_ROWS : rows};
