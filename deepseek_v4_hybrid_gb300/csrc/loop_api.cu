@@ -61,13 +61,24 @@ bool rows_meet(Rows a, Rows b, int64_t row) {
   return false;
 }
 
+// Whether rows of `dim` elements at t token + h head (strides of dim or more) lie apart from one another.
+bool rows_apart(int64_t token, int64_t head, int T, int heads, int dim) {
+  if (T <= 1 || heads == 1 || token / heads >= head || head / T >= token) return true;  // one stride holds all of the other's rows
+  for (int h = 1; h < heads; ++h) {
+    const __int128 at = (__int128)h * head;
+    const int64_t rest = (int64_t)(at % token);
+    const __int128 t = at / token;
+    if ((rest < dim && t < T) || (token - rest < dim && t + 1 < T)) return false;
+  }
+  return true;
+}
+
 // One tensor of a dsv4_rope call.
 int check_rope_rows(const void* x, const void* y, int heads, int T, const int64_t (&stride)[4], int head_dim) {
   CHECK(heads >= 1 && heads <= 1024, DSV4_ERR_INVALID);
   for (int64_t s : stride) CHECK(s >= 0 && s % 8 == 0, DSV4_ERR_INVALID);
-  // rows of y lie apart from one another
   CHECK((stride[2] >= head_dim || T <= 1) && (stride[3] >= head_dim || heads == 1), DSV4_ERR_INVALID);
-  CHECK(stride[2] != stride[3] || T <= 1 || heads == 1, DSV4_ERR_INVALID);
+  CHECK(rows_apart(stride[2], stride[3], T, heads, head_dim), DSV4_ERR_INVALID);
   if (T == 0) return DSV4_OK;
   CHECK(x && y && aligned(x, 16) && aligned(y, 16), DSV4_ERR_INVALID);
   CHECK(x != y || (stride[0] == stride[2] && stride[1] == stride[3]), DSV4_ERR_INVALID);

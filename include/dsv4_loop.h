@@ -72,8 +72,8 @@ int dsv4_rope_freqs(const dsv4_rope_freqs_params* p, uint64_t* freqs);
  * A token with a negative position is skipped: its rows of y stay as they are.
  * A second tensor (the keys beside the queries) is turned in the same launch when x2 is given.
  * y is x itself (same strides: in place) or lies apart from x, x2 and y2, and y2 likewise; rows of one buffer may
- * alternate.  Calls where they meet are refused where extents, or equal strides, tell.  Strides of x may be 0 (a row
- * for several heads or tokens).
+ * alternate.  Calls where they meet are refused where extents, or equal strides, tell.  Rows of y, and of y2, lie apart from
+ * one another (else refused).  Strides of x may be 0 (a row for several heads or tokens).
  * ------------------------------------------------------------------------------------------- */
 typedef struct dsv4_rope_params {
   uint32_t struct_size;

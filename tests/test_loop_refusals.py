@@ -44,6 +44,22 @@ def test_rope_refuses_rows_that_meet(abi, x, y, x2, y2):  # noqa: F811
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="calls that pass the check would be launched")
+def test_rope_rows_of_y_lie_apart(abi):  # noqa: F811
+    """Any strides of y: refused exactly where two of its rows share an element."""
+    g = np.random.default_rng(1)
+    lib, seen = abi.load(), [0, 0]
+    for _ in range(6000):
+        T, heads, D = int(g.integers(1, 7)), int(g.integers(1, 6)), 16
+        token, head = 8 * int(g.integers(2, 14)), 8 * int(g.integers(2, 14))
+        at = sorted(t * token + h * head for t, h in itertools.product(range(T), range(heads)))
+        meet = any(b - a < D for a, b in zip(at, at[1:]))
+        status = lib.dsv4_rope(rope_call(abi, T, D, (0, 1024, 64, heads), (10 ** 6, token, head, heads)), None)
+        assert status == (-1 if meet else -3), (T, heads, token, head)
+        seen[meet] += 1
+    assert min(seen) > 500
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="calls that pass the check would be launched")
 def test_rope_row_check_against_every_row(abi):  # noqa: F811
     """Parts of one buffer are refused exactly where two rows meet: every pair of rows compared.  A call that passes the
     check ends at the launch, for want of a device."""
